@@ -442,6 +442,161 @@ dion3_status dion3_flush_row_scale(int32_t rows, int32_t cols, int32_t batch,
                                    float* const* momentum, float* row_scale,
                                    dion3_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Layer operators: what makes the gradients the step consumes.  One pre-norm
+ * layer around a matrix W (out_features x in_features, the layout and type of
+ * dion3_group.params / grads): RMS norm, linear layer, their gradients, and
+ * activations kept in 8 bits for the backward pass.  The paper has no
+ * counterpart.
+ *
+ * These entry points follow the conventions above except that matrices may
+ * have any row pitch >= their row length (elements of a row are contiguous) and
+ * any base aligned to its element; 16-byte aligned bases and pitches are
+ * faster.  Results do not depend on the alignment beyond fp32 summation order
+ * and are the same bits from call to call.  A matrix with zero rows (tokens)
+ * is valid and may have a NULL base: forward calls then enqueue nothing, and a
+ * gradient summed over the tokens is zero (or unchanged, when accumulated).
+ * Sums and norms are fp32.  NaN and infinity propagate as in the formulas.
+ * ------------------------------------------------------------------------ */
+
+/* A row-major matrix: rows and columns come from the call. data NULL: absent. */
+typedef struct {
+  void* data;
+  int64_t ld;    /* row pitch in elements */
+  int32_t dtype; /* dion3_dtype */
+} dion3_matrix;
+
+/*
+ * A matrix in 8-bit blocks: every 32 columns of a row (the last block of a row
+ * may be shorter) share one scale byte b and stand for codes x 2^(b - 127).
+ * b is the smallest in [0, 248] that keeps every |code| <= 127 (values beyond
+ * 127 x 2^121 saturate there); b = 255 marks a block that held a NaN or an
+ * infinity, and stands for NaN throughout.  A code has at most 7 significant
+ * bits, so the values are exact in bf16 and fp32; in fp16 those outside its
+ * range round to it.
+ */
+typedef struct {
+  int8_t* codes;     /* [rows][ld_codes], ld_codes >= cols */
+  int64_t ld_codes;
+  uint8_t* scales;   /* [rows][ld_scales], ld_scales >= ceil(cols / 32) */
+  int64_t ld_scales;
+} dion3_packed8;
+
+/* gelu is the tanh form 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum {
+  DION3_ACT_NONE = 0,
+  DION3_ACT_RELU = 1,
+  DION3_ACT_GELU = 2,
+  DION3_ACT_SILU = 3
+} dion3_act;
+
+/* x (any dtype) into 8-bit blocks, and blocks into values of out's dtype. */
+dion3_status dion3_pack8(int32_t rows, int32_t cols, const dion3_matrix* x,
+                         const dion3_packed8* out, dion3_stream_t stream);
+dion3_status dion3_unpack8(int32_t rows, int32_t cols, const dion3_packed8* in,
+                           const dion3_matrix* out, dion3_stream_t stream);
+
+/*
+ * Root-mean-square norm of each row with the residual's addition:
+ *   h = x + residual (h = x without one), rstd = 1 / sqrt(mean(h^2) + eps),
+ *   y = h rstd weight,
+ * computed in fp32 from the unrounded h and rounded once at each output.
+ *   x, residual, h, y  one dtype (fp32, bf16, fp16); residual, h and y may be
+ *                      NULL.  h may be x or residual (in place); y may be x
+ *                      when h is not given.
+ *   weight             [cols] of weight_dtype.
+ *   y8                 y in 8-bit blocks, from the unrounded y, or NULL.  At
+ *                      least one of y and y8.
+ *   rstd               fp32 [rows] for the backward pass, or NULL.
+ * cols <= 49152.
+ */
+dion3_status dion3_rms_norm(int32_t rows, int32_t cols, const dion3_matrix* x,
+                            const dion3_matrix* residual, const void* weight,
+                            int32_t weight_dtype, float eps, const dion3_matrix* h,
+                            const dion3_matrix* y, const dion3_packed8* y8, float* rstd,
+                            dion3_stream_t stream);
+
+/*
+ * Gradient of dion3_rms_norm from its saved h (x itself without a residual)
+ * and rstd: with hn = h rstd and g = dy weight,
+ *   dx = dh + rstd (g - hn mean(g hn)),     dw = sum over rows of dy hn.
+ * dx is the gradient of x and of the residual alike.
+ *   dh  gradient that reaches h along the residual stream, or NULL (0).
+ *   dx  may be dy or dh (in place).
+ *   dw  fp32 [cols], or NULL; accumulate != 0: dw += instead of dw =.
+ */
+dion3_status dion3_rms_norm_backward_workspace_size(int32_t rows, int32_t cols, size_t* bytes);
+dion3_status dion3_rms_norm_backward(int32_t rows, int32_t cols, const dion3_matrix* dy,
+                                     const dion3_matrix* h, const void* weight,
+                                     int32_t weight_dtype, const float* rstd,
+                                     const dion3_matrix* dh, const dion3_matrix* dx, float* dw,
+                                     int32_t accumulate, void* ws, size_t ws_bytes,
+                                     dion3_stream_t stream);
+
+/*
+ * Linear layer with its epilogue on the tensor cores:
+ *   z = x W^T + bias,   y = act(z) + residual.
+ *   x [tokens][in_features], w [out_features][in_features], y, residual and z
+ *   [tokens][out_features]: one dtype, bf16 or fp16 (fp32 returns
+ *   DION3_ERR_UNSUPPORTED).  residual (may be y), z, z8, y8 and bias (any dtype,
+ *   [out_features]) are optional: data / codes / pointer NULL.
+ *   z, z8  the pre-activation for the backward pass, in 16 bits or in blocks.
+ *   y8     y in blocks (the next layer's x in its backward pass).
+ * Products accumulate in fp32 and the epilogue works on the fp32 sums; z, y
+ * and the blocks are each rounded once from them.
+ * The workspace holds copies of operands that TMA cannot read (in_features not
+ * a multiple of 8, or a base or pitch that is not a multiple of 16 bytes);
+ * strided = 0 asks for the bytes that dense, aligned matrices need, strided = 1
+ * for the most that any need.
+ */
+typedef struct {
+  int32_t tokens, in_features, out_features;
+  int32_t act; /* dion3_act */
+  dion3_matrix x, w, y;
+  dion3_matrix residual, z;
+  dion3_packed8 z8, y8;
+  const void* bias;
+  int32_t bias_dtype;
+} dion3_linear_args;
+
+dion3_status dion3_linear_workspace_size(int32_t tokens, int32_t in_features,
+                                         int32_t out_features, int32_t dtype, int32_t strided,
+                                         size_t* bytes);
+dion3_status dion3_linear(const dion3_linear_args* args, void* ws, size_t ws_bytes,
+                          dion3_stream_t stream);
+
+/*
+ * Gradient of dion3_linear from dy [tokens][out_features]:
+ *   dz = dy act'(z),  dx = dz W,  dw = dz^T x,  db = sum over tokens of dz.
+ * (The residual's gradient is dy.)
+ *   z or z8  the saved pre-activation, exactly one of them; unused without an
+ *            activation.
+ *   x or x8  the layer's input, exactly one of them (with dw only).  The
+ *            product with x8 is that of the values the blocks stand for.
+ *   dx, dw, db  each may be absent.  dw [out_features][in_features] is fp32 or
+ *            the layer's dtype, any pitch (dense: a dion3_group gradient);
+ *            db is fp32.  accumulate != 0: dw += and db +=, each sum formed in
+ *            fp32 and rounded once.
+ * Without an activation the products read dy itself; with one, dz is rounded
+ * to the layer's 16-bit type, which the tensor cores take, while db sums the
+ * unrounded dz.
+ */
+typedef struct {
+  int32_t tokens, in_features, out_features;
+  int32_t act;
+  int32_t accumulate;
+  dion3_matrix dy, w, x, z;
+  dion3_packed8 x8, z8;
+  dion3_matrix dx, dw;
+  float* db;
+} dion3_linear_grad_args;
+
+dion3_status dion3_linear_backward_workspace_size(int32_t tokens, int32_t in_features,
+                                                  int32_t out_features, int32_t dtype,
+                                                  int32_t strided, size_t* bytes);
+dion3_status dion3_linear_backward(const dion3_linear_grad_args* args, void* ws, size_t ws_bytes,
+                                   dion3_stream_t stream);
+
 /*
  * The bounded device-side wait of the tensor-core kernels, run on its own (a
  * diagnostic of the timeout path; the paper has no counterpart).  One thread

@@ -40,6 +40,9 @@ EXPORTED = (
     "dion3_trace_collect", "dion3_select_rows_noalloc", "dion3_ns_useful_flops",
     "dion3_ns_workspace_size", "dion3_ns_batched", "dion3_step_lazy", "dion3_flush_row_scale",
     "dion3_step_normuon", "dion3_wait_probe", "dion3_set_overlap",
+    "dion3_pack8", "dion3_unpack8", "dion3_rms_norm", "dion3_rms_norm_backward_workspace_size",
+    "dion3_rms_norm_backward", "dion3_linear_workspace_size", "dion3_linear",
+    "dion3_linear_backward_workspace_size", "dion3_linear_backward",
 )
 
 
@@ -464,3 +467,12 @@ def wait_probe(arrive: bool, limit_ns: int, stream=None):
 def device_status(stream=None):
     """Synchronise and raise if a bounded device-side wait ran out."""
     _check(load_library().dion3_device_status(_stream(stream)))
+
+
+from . import layer as _layer  # noqa: E402
+from .layer import (  # noqa: E402,F401
+    ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, PACK_BLOCK, Packed8, alloc_packed8, linear, linear_backward,
+    linear_backward_workspace_size, linear_workspace_size, pack8, rms_norm, rms_norm_backward,
+    rms_norm_backward_workspace_size, unpack8)
+
+_SIGS.update(_layer.SIGS)

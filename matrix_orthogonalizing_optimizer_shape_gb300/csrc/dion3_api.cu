@@ -692,6 +692,13 @@ dion3_status check_ws(void* ws, size_t ws_bytes, size_t need) {
 
 void set_last_error_message(const char* msg) { t_last_error = msg != nullptr ? msg : ""; }
 
+bool inject_launch_failure() { return inject_launch_fail(); }
+
+cudaError_t traced_launch_impl(const char* name, double flops, double bytes, cudaStream_t s,
+                               cudaError_t (*launch)(void*), void* ctx) {
+  return traced(name, flops, bytes, s, [&] { return launch(ctx); });
+}
+
 }  // namespace dion3
 
 using namespace dion3;

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 namespace dion3 {
 
@@ -261,5 +262,18 @@ unsigned* device_status_ptr();
 
 // Sets the message dion3_last_error() returns on this host thread.
 void set_last_error_message(const char* msg);
+
+// Whether DION3_INJECT=launch_fail is set (fault injection on the host).
+bool inject_launch_failure();
+
+// Runs a launch, recorded in the launch trace while that is enabled (see
+// dion3_trace_enable).
+cudaError_t traced_launch_impl(const char* name, double flops, double bytes, cudaStream_t s,
+                               cudaError_t (*launch)(void*), void* ctx);
+template <class Launch>
+cudaError_t traced_launch(const char* name, double flops, double bytes, cudaStream_t s, Launch&& launch) {
+  using L = std::remove_reference_t<Launch>;
+  return traced_launch_impl(name, flops, bytes, s, [](void* c) { return (*static_cast<L*>(c))(); }, &launch);
+}
 
 }  // namespace dion3

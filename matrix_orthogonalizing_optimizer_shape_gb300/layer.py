@@ -1,0 +1,278 @@
+"""Layer operators: RMS norm, linear layer, their gradients and activations kept
+in 8 bits (binding of the layer part of ``include/dion3.h``).
+
+Arguments are 2-D CUDA tensors [tokens, features] whose rows are contiguous
+(any row pitch); outputs are given by the caller.  Every function enqueues on
+``stream`` (default: the current one) and returns without waiting::
+
+    x8 = d3.alloc_packed8(T, K)
+    d3.rms_norm(x, gain, y, residual=r, h=h, y8=x8, rstd=rstd)
+    d3.linear(y, W, out, bias=b, act=d3.ACT_SILU, z=z8)          # z8: a Packed8
+    d3.linear_backward(dout, x8, W, dx=dy, dw=G, db=db, act=d3.ACT_SILU, z=z8, ws=ws)
+    d3.rms_norm_backward(dy, h, gain, rstd, dx, dh=dh, dw=dgain, ws=ws)
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import matrix_orthogonalizing_optimizer_shape_gb300 as _d3
+
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = range(4)
+
+#: Columns that share one scale byte of a :class:`Packed8`.
+PACK_BLOCK = 32
+
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+
+
+class _Matrix(ctypes.Structure):
+    _fields_ = [("data", _vp), ("ld", _i64), ("dtype", _i32)]
+
+
+class _Packed8(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("ld_codes", _i64), ("scales", _vp), ("ld_scales", _i64)]
+
+
+class _LinearArgs(ctypes.Structure):
+    _fields_ = [("tokens", _i32), ("in_features", _i32), ("out_features", _i32), ("act", _i32),
+                ("x", _Matrix), ("w", _Matrix), ("y", _Matrix), ("residual", _Matrix), ("z", _Matrix),
+                ("z8", _Packed8), ("y8", _Packed8), ("bias", _vp), ("bias_dtype", _i32)]
+
+
+class _LinearGradArgs(ctypes.Structure):
+    _fields_ = [("tokens", _i32), ("in_features", _i32), ("out_features", _i32), ("act", _i32),
+                ("accumulate", _i32),
+                ("dy", _Matrix), ("w", _Matrix), ("x", _Matrix), ("z", _Matrix),
+                ("x8", _Packed8), ("z8", _Packed8), ("dx", _Matrix), ("dw", _Matrix), ("db", _vp)]
+
+
+_pm, _pp, _psz, _int = ctypes.POINTER(_Matrix), ctypes.POINTER(_Packed8), ctypes.POINTER(_sz), ctypes.c_int
+SIGS = {
+    "dion3_pack8": (_int, [_i32, _i32, _pm, _pp, _vp]),
+    "dion3_unpack8": (_int, [_i32, _i32, _pp, _pm, _vp]),
+    "dion3_rms_norm": (_int, [_i32, _i32, _pm, _pm, _vp, _i32, ctypes.c_float, _pm, _pm, _pp, _vp, _vp]),
+    "dion3_rms_norm_backward_workspace_size": (_int, [_i32, _i32, _psz]),
+    "dion3_rms_norm_backward": (_int, [_i32, _i32, _pm, _pm, _vp, _i32, _vp, _pm, _pm, _vp, _i32, _vp, _sz, _vp]),
+    "dion3_linear_workspace_size": (_int, [_i32, _i32, _i32, _i32, _i32, _psz]),
+    "dion3_linear": (_int, [ctypes.POINTER(_LinearArgs), _vp, _sz, _vp]),
+    "dion3_linear_backward_workspace_size": (_int, [_i32, _i32, _i32, _i32, _i32, _psz]),
+    "dion3_linear_backward": (_int, [ctypes.POINTER(_LinearGradArgs), _vp, _sz, _vp]),
+}
+
+_CODES = None
+
+
+def _dtype(t) -> int:
+    """dion3_dtype of a tensor."""
+    global _CODES
+    if _CODES is None:
+        import torch
+        _CODES = {torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16}
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise ValueError(f"dtype {t.dtype} is not float32, bfloat16 or float16") from None
+
+
+def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -> _Matrix:
+    """A 2-D CUDA tensor with contiguous rows as a dion3_matrix; shape checked where given."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} has {len(shape)} dimensions, 2 are wanted")
+    r, c = shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} is {r} x {c}, {rows if rows is not None else r} x "
+                         f"{cols if cols is not None else c} is wanted")
+    ld, inner = t.stride()
+    if inner != 1 and c > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if ld < c:  # one row (any stride), or rows that overlap
+        if r > 1:
+            raise ValueError(f"{name}: rows overlap")
+        ld = c
+    return _Matrix(t.data_ptr(), ld, _dtype(t))
+
+
+def _vec(name: str, t, n: int, f32: bool = False) -> int:
+    if not t.is_cuda or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous CUDA vector of {n}")
+    if f32 and _dtype(t) != _d3.F32:
+        raise ValueError(f"{name} must be float32")
+    return t.data_ptr()
+
+
+class Packed8:
+    """A matrix in 8-bit blocks (``dion3_packed8``): int8 codes [rows, cols] and
+    uint8 scale bytes [rows, ceil(cols / 32)], rows contiguous, any row pitch
+    (multiples of 16 bytes are fastest, see :func:`alloc_packed8`)."""
+
+    __slots__ = ("codes", "scales", "shape", "_c")
+
+    def __init__(self, codes, scales):
+        import torch
+        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
+            raise ValueError("codes must be int8 and scales uint8")
+        if not (codes.is_cuda and scales.is_cuda) or codes.dim() != 2 or scales.dim() != 2:
+            raise ValueError("codes and scales must be 2-D CUDA tensors")
+        rows, cols = codes.shape
+        nb = -(-cols // PACK_BLOCK)
+        if tuple(scales.shape) != (rows, nb):
+            raise ValueError(f"scales must be {rows} x {nb} for codes of {rows} x {cols}")
+        lds = []
+        for t, c in ((codes, cols), (scales, nb)):
+            ld, inner = t.stride()
+            if (inner != 1 and c > 1) or (ld < c and rows > 1):
+                raise ValueError("the rows of codes and scales must be contiguous and not overlap")
+            lds.append(max(ld, c))
+        self.codes, self.scales, self.shape = codes, scales, (rows, cols)
+        self._c = _Packed8(codes.data_ptr(), lds[0], scales.data_ptr(), lds[1])
+
+
+def _packed(name: str, p: Packed8, rows: int, cols: int) -> _Packed8:
+    if p.shape != (rows, cols):
+        raise ValueError(f"{name} is {p.shape[0]} x {p.shape[1]}, {rows} x {cols} is wanted")
+    return p._c
+
+
+def alloc_packed8(rows: int, cols: int, device=None) -> Packed8:
+    """An uninitialised :class:`Packed8` with row pitches that are multiples of 16 bytes."""
+    import torch
+    dev = device if device is not None else "cuda"
+    nb = -(-cols // PACK_BLOCK)
+    codes = torch.empty(rows, -(-cols // 16) * 16, dtype=torch.int8, device=dev)[:, :cols]
+    scales = torch.empty(rows, -(-nb // 16) * 16, dtype=torch.uint8, device=dev)[:, :nb]
+    return Packed8(codes, scales)
+
+
+def _ws(ws, nbytes):
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda:
+        raise ValueError("ws is not a CUDA tensor")
+    return ws.data_ptr(), nbytes if nbytes is not None else ws.numel() * ws.element_size()
+
+
+def pack8(x, out: Packed8, stream=None):
+    """x [rows, cols] into 8-bit blocks (see dion3_pack8)."""
+    m = _mat("x", x)
+    rows, cols = x.shape
+    _d3._check(_d3.load_library().dion3_pack8(rows, cols, m, _packed("out", out, rows, cols), _d3._stream(stream)))
+
+
+def unpack8(src: Packed8, out, stream=None):
+    """The values that 8-bit blocks stand for, in out's dtype (see dion3_unpack8)."""
+    rows, cols = src.shape
+    _d3._check(_d3.load_library().dion3_unpack8(rows, cols, src._c, _mat("out", out, rows, cols),
+                                                _d3._stream(stream)))
+
+
+def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] = None, rstd=None,
+             eps: float = 1e-6, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over each row, y
+    and / or its 8-bit blocks y8, and rstd for the backward pass (see
+    dion3_rms_norm)."""
+    mx = _mat("x", x)
+    rows, cols = x.shape
+    _d3._check(_d3.load_library().dion3_rms_norm(
+        rows, cols, mx, None if residual is None else _mat("residual", residual, rows, cols),
+        _vec("weight", weight, cols), _dtype(weight), eps, None if h is None else _mat("h", h, rows, cols),
+        None if y is None else _mat("y", y, rows, cols), None if y8 is None else _packed("y8", y8, rows, cols),
+        None if rstd is None else _vec("rstd", rstd, rows, f32=True), _d3._stream(stream)))
+
+
+def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    out = _sz(0)
+    _d3._check(_d3.load_library().dion3_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def rms_norm_backward(dy, h, weight, rstd, dx, *, dh=None, dw=None, accumulate: bool = False, ws=None,
+                      ws_bytes: Optional[int] = None, stream=None):
+    """Gradient of :func:`rms_norm`: dx (of x and the residual alike; dh is the
+    gradient that reaches h from elsewhere) and dw, float32 (see
+    dion3_rms_norm_backward)."""
+    mdy = _mat("dy", dy)
+    rows, cols = dy.shape
+    p, n = _ws(ws, ws_bytes)
+    _d3._check(_d3.load_library().dion3_rms_norm_backward(
+        rows, cols, mdy, _mat("h", h, rows, cols), _vec("weight", weight, cols), _dtype(weight),
+        _vec("rstd", rstd, rows, f32=True), None if dh is None else _mat("dh", dh, rows, cols),
+        _mat("dx", dx, rows, cols), None if dw is None else _vec("dw", dw, cols, f32=True), int(accumulate), p, n,
+        _d3._stream(stream)))
+
+
+def _ws_size(fn: str, tokens, in_features, out_features, dtype, strided) -> int:
+    import torch
+    code = {torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16}.get(dtype, -1)
+    out = _sz(0)
+    _d3._check(getattr(_d3.load_library(), fn)(tokens, in_features, out_features, code, int(strided),
+                                               ctypes.byref(out)))
+    return out.value
+
+
+def linear_workspace_size(tokens: int, in_features: int, out_features: int, *, dtype, strided: bool = False) -> int:
+    """Workspace bytes of :func:`linear` (0 for dense tensors with in_features a
+    multiple of 8); ``strided``: for any pitch and base."""
+    return _ws_size("dion3_linear_workspace_size", tokens, in_features, out_features, dtype, strided)
+
+
+def linear_backward_workspace_size(tokens: int, in_features: int, out_features: int, *, dtype,
+                                   strided: bool = False) -> int:
+    """Workspace bytes of :func:`linear_backward`; ``strided``: for any pitch and base."""
+    return _ws_size("dion3_linear_backward_workspace_size", tokens, in_features, out_features, dtype, strided)
+
+
+_NO_MAT, _NO_PACK = _Matrix(), _Packed8()
+
+
+def linear(x, w, y, *, bias=None, residual=None, act: int = ACT_NONE, z=None, y8: Optional[Packed8] = None, ws=None,
+           ws_bytes: Optional[int] = None, stream=None):
+    """y = act(x w^T + bias) + residual.  z (a tensor or a :class:`Packed8`)
+    receives the pre-activation, y8 the output in 8-bit blocks (see
+    dion3_linear)."""
+    mx = _mat("x", x)
+    tokens, k = x.shape
+    mw = _mat("w", w, None, k)
+    n = w.shape[0]
+    z8 = _NO_PACK
+    mz = _NO_MAT
+    if isinstance(z, Packed8):
+        z8 = _packed("z", z, tokens, n)
+    elif z is not None:
+        mz = _mat("z", z, tokens, n)
+    args = _LinearArgs(tokens, k, n, act, mx, mw, _mat("y", y, tokens, n),
+                       _NO_MAT if residual is None else _mat("residual", residual, tokens, n), mz, z8,
+                       _NO_PACK if y8 is None else _packed("y8", y8, tokens, n),
+                       None if bias is None else _vec("bias", bias, n), 0 if bias is None else _dtype(bias))
+    p, nb = _ws(ws, ws_bytes)
+    _d3._check(_d3.load_library().dion3_linear(args, p, nb, _d3._stream(stream)))
+
+
+def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE, z=None, accumulate: bool = False,
+                    ws=None, ws_bytes: Optional[int] = None, stream=None):
+    """Gradient of :func:`linear` from dy: dx, dw (float32 or the layer's dtype)
+    and db (float32), those that are given.  x and z are tensors or
+    :class:`Packed8` checkpoints; ``accumulate`` adds to dw and db (see
+    dion3_linear_backward)."""
+    mdy = _mat("dy", dy)
+    tokens, n = dy.shape
+    mw = _mat("w", w, n)
+    k = w.shape[1]
+    mx, x8, mz, z8 = _NO_MAT, _NO_PACK, _NO_MAT, _NO_PACK
+    if isinstance(x, Packed8):
+        x8 = _packed("x", x, tokens, k)
+    elif x is not None:
+        mx = _mat("x", x, tokens, k)
+    if isinstance(z, Packed8):
+        z8 = _packed("z", z, tokens, n)
+    elif z is not None:
+        mz = _mat("z", z, tokens, n)
+    args = _LinearGradArgs(tokens, k, n, act, int(accumulate), mdy, mw, mx, mz, x8, z8,
+                           _NO_MAT if dx is None else _mat("dx", dx, tokens, k),
+                           _NO_MAT if dw is None else _mat("dw", dw, n, k),
+                           None if db is None else _vec("db", db, n, f32=True))
+    p, nb = _ws(ws, ws_bytes)
+    _d3._check(_d3.load_library().dion3_linear_backward(args, p, nb, _d3._stream(stream)))
