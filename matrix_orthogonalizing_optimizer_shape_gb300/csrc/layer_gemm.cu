@@ -48,6 +48,20 @@ __device__ __forceinline__ float load_bias(const void* b, int dtype, int c) {
   return __half2float(static_cast<const __half*>(b)[c]);
 }
 
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
+  if (act == kActRelu) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_fwd<kActRelu>(v[j]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_fwd<kActGelu>(v[j]);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_fwd<kActSilu>(v[j]);
+  }
+}
+
 // One 8-bit block held by a warp: lane = column of the block (0 past the end).
 __device__ __forceinline__ void store_block_warp(const Pack8& o, long long t, int m, bool in, float v) {
   const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
@@ -76,10 +90,11 @@ __device__ __forceinline__ void epilogue_rows(const Epilogue& e, int t0, int m, 
       const float z = in ? v[j] + bias : 0.f;
       if (e.z != nullptr && in) e.z[t * e.ld_z + m] = pack1<BF16>(z);
       if (e.z8.q != nullptr) store_block_warp(e.z8, t, m, in, z);
-      float y = act_fwd(e.act, z);
-      if (e.res != nullptr) y += unpack1<BF16>(r[j]);
-      if (in) static_cast<uint16_t*>(e.out)[t * e.ld_out + m] = pack1<BF16>(y);
-      if (e.out8.q != nullptr) store_block_warp(e.out8, t, m, in, in ? y : 0.f);
+      float y[1] = {z};
+      apply_act(e.act, y);
+      if (e.res != nullptr) y[0] += unpack1<BF16>(r[j]);
+      if (in) static_cast<uint16_t*>(e.out)[t * e.ld_out + m] = pack1<BF16>(y[0]);
+      if (e.out8.q != nullptr) store_block_warp(e.out8, t, m, in, in ? y[0] : 0.f);
     }
   } else if (e.out_f32) {
     float* o = static_cast<float*>(e.out) + static_cast<long long>(t0) * e.ld_out + m;
@@ -412,10 +427,10 @@ __device__ __forceinline__ void add_bias(const Epilogue& e, int c0, int cols, fl
 
 // One block of 32 columns held by a thread (0 past the last column).
 __device__ __forceinline__ void store_block_row(const Pack8& o, long long r, int c0, int cols, const float (&f)[32]) {
-  uint32_t m = 0;
+  float m = fabsf(f[0]);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  const uint32_t byte = scale_byte(m);
+  for (int j = 1; j < 32; ++j) m = max_mag(m, f[j]);
+  const uint32_t byte = scale_byte(__float_as_uint(m) & 0x7FFFFFFFu);
   const float inv = inv_scale(byte);
   float v[32];
 #pragma unroll
@@ -423,9 +438,7 @@ __device__ __forceinline__ void store_block_row(const Pack8& o, long long r, int
   saturate_block(byte, v);
   uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j] = code_of(v[4 * j], inv) | code_of(v[4 * j + 1], inv) << 8 | code_of(v[4 * j + 2], inv) << 16 |
-           code_of(v[4 * j + 3], inv) << 24;
+  for (int j = 0; j < 8; ++j) w[j] = codes4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv);
   int8_t* q = o.q + r * o.ldq + c0;
   if (c0 + 32 <= cols && ((reinterpret_cast<uintptr_t>(q) & 15u) == 0)) {
     *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -595,10 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
               st.store_plain<2>(e.z, e.ld_z, p.rows, p.cols, w, c0, row0, false);
           }
           if (e.z8.q != nullptr && r < p.rows) store_block_row(e.z8, r, c0, p.cols, f);
-          if (e.act != kActNone) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = act_fwd(e.act, f[j]);
-          }
+          apply_act(e.act, f);
         }
         if (addend != nullptr && r < p.rows) piece.add<BF16>(f);
         if constexpr (OUT == kOut32) {

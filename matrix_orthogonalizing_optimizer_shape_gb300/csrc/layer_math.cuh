@@ -103,25 +103,39 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
 // --------------------------------------------------------------------------
 // Activations.  gelu is its tanh form, 0.5 z (1 + tanh(sqrt(2/pi) (z + c z^3)))
 // = z / (1 + exp(-2 sqrt(2/pi) (z + c z^3))), c = 0.044715: written with the
-// sigmoid it does not cancel at large -z.  The derivatives drop the product of
-// the sigmoid's slope with a power of z where that slope is zero, so they stay
-// finite for every finite z.
+// sigmoid it does not cancel at large -z.  The sigmoid takes two special
+// function instructions, 2^x and 1/x (each within 2 ulp; results below 2^-126
+// become 0), and the slope's cubic term is bounded where the sigmoid's own
+// slope is 0, so derivatives stay finite for every finite z.
 // --------------------------------------------------------------------------
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kLog2E = 1.4426950408889634f;
 
-__device__ __forceinline__ float act_fwd(int act, float z) {
-  if (act == kActNone) return z;
-  if (act == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  const float u = act == kActSilu ? z : kGelu2 * (z + 0.044715f * z * z * z);
-  return __fdividef(z, 1.f + __expf(-u));
+__device__ __forceinline__ float sigmoid(float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2E * u));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
 }
-__device__ __forceinline__ float act_grad(int act, float z) {
-  if (act == kActRelu) return z > 0.f ? 1.f : (z != z ? z : 0.f);
-  const float u = act == kActSilu ? z : kGelu2 * (z + 0.044715f * z * z * z);
-  const float s = __fdividef(1.f, 1.f + __expf(-u));
-  const float d = s * (1.f - s);
-  if (d == 0.f) return s;
-  return act == kActSilu ? fmaf(z, d, s) : fmaf(z * d, kGelu2 * fmaf(0.134145f, z * z, 1.f), s);
+__device__ __forceinline__ float gelu_arg(float z) { return z * fmaf(0.044715f * kGelu2, z * z, kGelu2); }
+
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float z) {
+  if constexpr (ACT == kActNone) return z;
+  if constexpr (ACT == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
+  if constexpr (ACT == kActGelu) return z * sigmoid(gelu_arg(z));
+  return z * sigmoid(z);
+}
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+  if constexpr (ACT == kActNone) return 1.f;
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  if constexpr (ACT == kActGelu) {
+    const float s = sigmoid(gelu_arg(z)), zd = z * fmaf(-s, s, s);
+    return fmaf(zd, kGelu2 * fmaf(0.134145f, fminf(z * z, 1e9f), 1.f), s);
+  }
+  const float s = sigmoid(z);
+  return fmaf(z, fmaf(-s, s, s), s);
 }
 
 // --------------------------------------------------------------------------
@@ -167,6 +181,27 @@ __device__ __forceinline__ void saturate_block(uint32_t byte, float (&v)[N]) {
 __device__ __forceinline__ uint32_t code_of(float v, float inv) {
   const float f = fmaf(v, inv, 12582912.f);
   return inv == 0.f ? 0u : (__float_as_uint(f) & 0xFFu);
+}
+// Four codes in one word.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  const uint32_t x = __float_as_uint(fmaf(a, inv, 12582912.f)), y = __float_as_uint(fmaf(b, inv, 12582912.f));
+  const uint32_t z = __float_as_uint(fmaf(c, inv, 12582912.f)), w = __float_as_uint(fmaf(d, inv, 12582912.f));
+  const uint32_t r = __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+  return inv == 0.f ? 0u : r;
+}
+// The values of four codes: 2^23 + (q + 128) is built from the code's bits and
+// the 2^23 + 128 taken off again, both exact.
+__device__ __forceinline__ void values4(uint32_t w, float scale, float (&v)[4]) {
+  const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + j)) - 8388736.f) * scale;
+}
+// Larger magnitude of two values; NaN if either is.
+__device__ __forceinline__ float max_mag(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 }  // namespace lm

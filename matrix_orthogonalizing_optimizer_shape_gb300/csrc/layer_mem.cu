@@ -2,6 +2,7 @@
 // the RMS norm with the residual's addition and its gradient, and the
 // activation's gradient with the bias gradient's column sums.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "layer_math.cuh"
@@ -17,17 +18,16 @@ __device__ __forceinline__ float load_w(const void* w, int dtype, int c) {
   return __half2float(static_cast<const __half*>(w)[c]);
 }
 
-// Largest |v| bits over the lanes that share a block of 32 columns (VEC
-// columns a lane).  Magnitudes compare as unsigned integers; a NaN compares
-// above every number.
+// Bits of the largest |v| over the lanes that share a block of 32 columns (VEC
+// columns a lane); a NaN is larger than every number.
 template <int VEC>
 __device__ __forceinline__ uint32_t block_amax(const float (&v)[VEC]) {
-  uint32_t m = 0;
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  for (int j = 1; j < VEC; ++j) m = max_mag(m, v[j]);
 #pragma unroll
-  for (int d = 1; d < kPackBlock / VEC; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return m;
+  for (int d = 1; d < kPackBlock / VEC; d *= 2) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
 // Codes (and, from the block's first lane, its scale byte) of VEC columns at
@@ -40,29 +40,96 @@ __device__ __forceinline__ void store_block(const Pack8& o, long long row, int c
   saturate_block(byte, v);
   if (c >= cols) return;
   int8_t* q = o.q + row * o.ldq + c;
-  if constexpr (VEC == 8) {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j / 4] |= code_of(v[j], inv) << (8 * (j % 4));
-    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-  } else {
+  if constexpr (VEC == 8)
+    *reinterpret_cast<uint2*>(q) =
+        make_uint2(codes4(v[0], v[1], v[2], v[3], inv), codes4(v[4], v[5], v[6], v[7], inv));
+  else
     *q = static_cast<int8_t>(code_of(v[0], inv));
-  }
   if (c % kPackBlock == 0) o.s[row * o.lds + c / kPackBlock] = static_cast<uint8_t>(byte);
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_cols(const Mat& m, long long row, int c, int cols, float (&v)[VEC]) {
-  if (c < cols) {
-    load_vec<T, VEC>(static_cast<const T*>(m.p) + row * m.ld + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = 0.f;
+// Raw codes and scale byte of VEC columns, and their values.
+template <int VEC>
+struct Codes {
+  uint2 w;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const Pack8& p, long long row, int c, int cols) {
+    if (c >= cols) return;
+    const int8_t* q = p.q + row * p.ldq + c;
+    if constexpr (VEC == 8)
+      w = *reinterpret_cast<const uint2*>(q);
+    else
+      w.x = static_cast<uint32_t>(static_cast<uint8_t>(*q));
+    byte = p.s[row * p.lds + c / kPackBlock];
   }
-}
+  __device__ __forceinline__ void values(float (&v)[VEC]) const {
+    const float sc = scale_of(byte);
+    float a[4];
+    values4(w.x, sc, a);
+    if constexpr (VEC == 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j];
+      values4(w.y, sc, a);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 + j] = a[j];
+    } else {
+      v[0] = a[0];
+    }
+  }
+};
+
 template <typename T, int VEC>
 __device__ __forceinline__ void store_cols(const Mat& m, long long row, int c, int cols, const float (&v)[VEC]) {
   if (c < cols) store_vec<T, VEC>(static_cast<T*>(m.p) + row * m.ld + c, v);
+}
+// VEC elements as they lie in memory (loaded ahead of their use), zeros past
+// the last column.
+template <typename T, int VEC>
+struct Raw {
+  static constexpr int kWords = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const Mat& m, long long row, int c, int cols) {
+    if (c >= cols) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0u;
+      return;
+    }
+    const T* p = static_cast<const T*>(m.p) + row * m.ld + c;
+    if constexpr (VEC == 1) {
+      if constexpr (sizeof(T) == 2)
+        w[0] = *reinterpret_cast<const uint16_t*>(p);
+      else
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[VEC]) const {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(w[j]);
+    } else if constexpr (VEC == 1) {
+      v[0] = unpack1<kBf>(static_cast<uint16_t>(w[0]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        const float2 f = unpack2<kBf>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void load_cols(const Mat& m, long long row, int c, int cols, float (&v)[VEC]) {
+  Raw<T, VEC> raw;
+  raw.load(m, row, c, cols);
+  raw.values(v);
 }
 
 // Sum over the CTA, the same bits in every thread (blockDim.x a multiple of
@@ -83,63 +150,134 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
 }
 
 // --------------------------------------------------------------------------
-// 8-bit checkpoints
+// 8-bit checkpoints.  Bound by HBM.  blockDim = (lanes along a row, rows): a
+// thread keeps its columns and walks the rows kWalk at a time, all their loads
+// issued before the first is used.
 // --------------------------------------------------------------------------
-template <typename T, int VEC>
-__global__ void __launch_bounds__(256) pack8_kernel(int rows, int cols, Mat x, Pack8 o) {
-  const int per_row = (cols + kPackBlock - 1) / kPackBlock * (kPackBlock / VEC);  // lanes of a row, whole blocks
-  const long long total = (static_cast<long long>(rows) * per_row + 31) / 32 * 32;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const long long row = i / per_row;
-    const int c = row < rows ? static_cast<int>(i - row * per_row) * VEC : cols;
-    float v[VEC];
-    load_cols<T, VEC>(x, row, c, cols, v);
-    store_block<VEC>(o, row, c, cols, v);
-  }
-}
+constexpr int kWalk = 4;
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) unpack8_kernel(int rows, int cols, Pack8 in, Mat out) {
-  const int per_row = (cols + VEC - 1) / VEC;
-  const long long total = static_cast<long long>(rows) * per_row;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const long long row = i / per_row;
-    const int c = static_cast<int>(i - row * per_row) * VEC;
-    const float sc = scale_of(in.s[row * in.lds + c / kPackBlock]);
-    float v[VEC];
-    if constexpr (VEC == 8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(in.q + row * in.ldq + c);
+__global__ void __launch_bounds__(256, 4) pack8_kernel(int rows, int cols, Mat x, Pack8 o) {
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
+  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += kWalk * step) {
+    Raw<T, VEC> raw[kWalk];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? w.x : w.y) >> (8 * (j % 4)))) * sc;
-    } else {
-      v[0] = static_cast<float>(in.q[row * in.ldq + c]) * sc;
+    for (int i = 0; i < kWalk; ++i) raw[i].load(x, row + i * step, row + i * step < rows ? c : cols, cols);
+#pragma unroll
+    for (int i = 0; i < kWalk; ++i) {
+      float v[VEC];
+      raw[i].values(v);
+      store_block<VEC>(o, row + i * step, row + i * step < rows ? c : cols, cols, v);
     }
-    store_cols<T, VEC>(out, row, c, cols, v);
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pack8 in, Mat out) {
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+  if (c >= cols) return;
+  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
+  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += kWalk * step) {
+    Codes<VEC> q[kWalk];
+#pragma unroll
+    for (int i = 0; i < kWalk; ++i)
+      if (row + i * step < rows) q[i].load(in, row + i * step, c, cols);
+#pragma unroll
+    for (int i = 0; i < kWalk; ++i) {
+      if (row + i * step >= rows) break;
+      float v[VEC];
+      q[i].values(v);
+      store_cols<T, VEC>(out, row + i * step, c, cols, v);
+    }
   }
 }
 
 // --------------------------------------------------------------------------
-// RMS norm: one CTA a row at a time, the row read twice (the second time from
-// cache).  h = x + r; rstd = 1 / sqrt(mean(h^2) + eps); y = h rstd w, from the
-// unrounded h.
+// RMS norm: h = x + r; rstd = 1 / sqrt(mean(h^2) + eps); y = h rstd w, from the
+// unrounded h.  Bound by HBM.  blockDim = (lanes of a row, rows): a thread holds
+// NV pieces of VEC columns of its row in registers from the load to the last
+// store and loads the next row's pieces before it waits for this row's sum.
+// The gain stays in registers over the rows.
 // --------------------------------------------------------------------------
+constexpr int kRowThreads = 512;  // most of a row kernel's block (128 registers a thread)
+
+template <typename T, int VEC, int NV, bool RES>
+__global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
+  __shared__ float red[64];
+  int flip = 0;
+  const int span = blockDim.x * VEC;
+  float w[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = threadIdx.x * VEC + i * span + j;
+      w[i][j] = c < a.cols ? load_w(a.w, a.w_dtype, c) : 0.f;
+    }
+  Raw<T, VEC> x[NV], r[RES ? NV : 1];
+  auto load_row = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = row < a.rows ? static_cast<int>(threadIdx.x) * VEC + i * span : a.cols;
+      x[i].load(a.x, row, c, a.cols);
+      if constexpr (RES) r[i].load(a.residual, row, c, a.cols);
+    }
+  };
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  load_row(row);
+  for (; row < a.rows; row += step) {
+    float v[NV][VEC], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i].values(v[i]);
+      if constexpr (RES) {
+        float t[VEC];
+        r[i].values(t);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[i][j] += t[j];
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    load_row(row + step);
+    ss = cta_sum(ss, red, flip);
+    const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = threadIdx.x * VEC + i * span;
+      if (a.h.p) store_cols<T, VEC>(a.h, row, c, a.cols, v[i]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i][j] = c < a.cols ? v[i][j] * rstd * w[i][j] : 0.f;
+      if (a.y.p) store_cols<T, VEC>(a.y, row, c, a.cols, v[i]);
+      if (a.y8.q) store_block<VEC>(a.y8, row, c, a.cols, v[i]);
+    }
+  }
+}
+
+// The same for rows too wide for that: the row is read twice, the second time
+// from cache.
 template <typename T, int VEC>
-__global__ void rms_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
   __shared__ float red[64];
   int flip = 0;
   const int span = blockDim.x * VEC;
   const int padded = (a.cols + span - 1) / span * span;
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float ss = 0.f;
-    for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
-      float v[VEC], r[VEC];
-      load_cols<T, VEC>(a.x, row, c, a.cols, v);
-      if (a.residual.p) {
-        load_cols<T, VEC>(a.residual, row, c, a.cols, r);
+  auto load_h = [&](long long row, int c, float (&v)[VEC]) {
+    load_cols<T, VEC>(a.x, row, c, a.cols, v);
+    if (a.residual.p) {
+      float r[VEC];
+      load_cols<T, VEC>(a.residual, row, c, a.cols, r);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] += r[j];
-      }
+      for (int j = 0; j < VEC; ++j) v[j] += r[j];
+    }
+  };
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float ss = 0.f, v[VEC];
+    for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
+      load_h(row, c, v);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss = fmaf(v[j], v[j], ss);
     }
@@ -147,13 +285,7 @@ __global__ void rms_norm_kernel(NormArgs a) {
     const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int c = threadIdx.x * VEC; c < padded; c += span) {
-      float v[VEC], r[VEC];
-      load_cols<T, VEC>(a.x, row, c, a.cols, v);
-      if (a.residual.p) {
-        load_cols<T, VEC>(a.residual, row, c, a.cols, r);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] += r[j];
-      }
+      load_h(row, c, v);
       if (a.h.p) store_cols<T, VEC>(a.h, row, c, a.cols, v);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] = c < a.cols ? v[j] * rstd * load_w(a.w, a.w_dtype, c + j) : 0.f;
@@ -163,11 +295,100 @@ __global__ void rms_norm_kernel(NormArgs a) {
   }
 }
 
-// Gradient: hn = h rstd, g = dy w; dx = dh + rstd (g - hn mean(g hn)),
-// dw = sum over rows of dy hn.  A CTA takes rows in turn and keeps its column
-// sums of dw in shared memory; column_sum_kernel adds the CTAs' sums in order.
+// Gradient: hn = h rstd, g = dy w; dx = dh + rstd (g - hn mean(g hn)), dw = sum
+// over rows of dy hn.  Bound by HBM.  As the forward kernel, with dw's column
+// sums of the CTA's rows in registers; column_sum_kernel adds the CTAs' sums in
+// order.
+__device__ __forceinline__ float norm_dx(float dy, float w, float hn, float mean, float rstd, float dh) {
+  return fmaf(rstd, fmaf(-hn, mean, __fmul_rn(dy, w)), dh);
+}
+
+template <typename T, int VEC, int NV, bool DH>
+__global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_grad_kernel(NormGradArgs a) {
+  __shared__ float red[64];
+  extern __shared__ float rows_sum[];  // [blockDim.y][span * NV], blockDim.y > 1
+  int flip = 0;
+  const int span = blockDim.x * VEC;
+  float w[NV][VEC], dw[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = threadIdx.x * VEC + i * span + j;
+      w[i][j] = c < a.cols ? load_w(a.w, a.w_dtype, c) : 0.f;
+      dw[i][j] = 0.f;
+    }
+  Raw<T, VEC> dy[NV], h[NV], dh[DH ? NV : 1];
+  float rstd_next = 0.f;
+  auto load_row = [&](long long row) {
+    if (row < a.rows) rstd_next = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = row < a.rows ? static_cast<int>(threadIdx.x) * VEC + i * span : a.cols;
+      dy[i].load(a.dy, row, c, a.cols);
+      h[i].load(a.h, row, c, a.cols);
+    }
+  };
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  load_row(row);
+  for (; row < a.rows; row += step) {
+    const float rstd = rstd_next;
+    float g[NV][VEC], hn[NV][VEC], s = 0.f;
+    if constexpr (DH) {  // not needed before the sum is known
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dh[i].load(a.dh, row, static_cast<int>(threadIdx.x) * VEC + i * span, a.cols);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      dy[i].values(g[i]);
+      h[i].values(hn[i]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        hn[i][j] = __fmul_rn(hn[i][j], rstd);
+        dw[i][j] = fmaf(g[i][j], hn[i][j], dw[i][j]);
+        s = fmaf(__fmul_rn(g[i][j], w[i][j]), hn[i][j], s);
+      }
+    }
+    load_row(row + step);
+    s = cta_sum(s, red, flip) / static_cast<float>(a.cols);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float d[VEC] = {};
+      if constexpr (DH) dh[i].values(d);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) d[j] = norm_dx(g[i][j], w[i][j], hn[i][j], s, rstd, d[j]);
+      store_cols<T, VEC>(a.dx, row, static_cast<int>(threadIdx.x) * VEC + i * span, a.cols, d);
+    }
+  }
+  if (a.dw == nullptr) return;
+  // The rows of the block first, in order.
+  if (blockDim.y > 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) rows_sum[(threadIdx.y * NV + i) * span + threadIdx.x * VEC + j] = dw[i][j];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        for (int y = 1; y < blockDim.y; ++y) dw[i][j] += rows_sum[(y * NV + i) * span + threadIdx.x * VEC + j];
+  }
+  float* part = a.partials + static_cast<long long>(blockIdx.x) * a.cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = threadIdx.x * VEC + i * span;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < a.cols) part[c + j] = dw[i][j];
+  }
+}
+
+// The same for rows too wide for that: read twice, column sums in shared memory.
 template <typename T, int VEC>
-__global__ void rms_norm_grad_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a) {
   extern __shared__ float colsum[];
   __shared__ float red[64];
   int flip = 0;
@@ -178,25 +399,24 @@ __global__ void rms_norm_grad_kernel(NormGradArgs a) {
       for (int j = 0; j < VEC; ++j) colsum[c + j] = 0.f;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float rstd = a.rstd[row];
-    float s = 0.f;
+    float s = 0.f, dy[VEC], h[VEC];
     for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
-      float dy[VEC], h[VEC];
       load_cols<T, VEC>(a.dy, row, c, a.cols, dy);
       load_cols<T, VEC>(a.h, row, c, a.cols, h);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s = fmaf(__fmul_rn(dy[j], load_w(a.w, a.w_dtype, c + j)), __fmul_rn(h[j], rstd), s);
+      for (int j = 0; j < VEC; ++j)
+        s = fmaf(__fmul_rn(dy[j], load_w(a.w, a.w_dtype, c + j)), __fmul_rn(h[j], rstd), s);
     }
     s = cta_sum(s, red, flip) / static_cast<float>(a.cols);
     for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
-      float dy[VEC], h[VEC], d[VEC];
+      float d[VEC];
       load_cols<T, VEC>(a.dy, row, c, a.cols, dy);
       load_cols<T, VEC>(a.h, row, c, a.cols, h);
       if (a.dh.p) load_cols<T, VEC>(a.dh, row, c, a.cols, d);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float hn = __fmul_rn(h[j], rstd);
-        const float g = fmaf(-hn, s, __fmul_rn(dy[j], load_w(a.w, a.w_dtype, c + j)));
-        d[j] = a.dh.p ? fmaf(rstd, g, d[j]) : __fmul_rn(rstd, g);
+        d[j] = norm_dx(dy[j], load_w(a.w, a.w_dtype, c + j), hn, s, rstd, a.dh.p ? d[j] : 0.f);
         if (a.dw != nullptr) colsum[c + j] = fmaf(dy[j], hn, colsum[c + j]);
       }
       store_cols<T, VEC>(a.dx, row, c, a.cols, d);
@@ -208,64 +428,72 @@ __global__ void rms_norm_grad_kernel(NormGradArgs a) {
       for (int j = 0; j < VEC; ++j) a.partials[static_cast<long long>(blockIdx.x) * a.cols + c + j] = colsum[c + j];
 }
 
-// out[c] (+)= sum over p of partials[p][c], in order of p within each of 8
-// interleaved chains and of the chains after that: the same bits every call.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* partials, int nparts, int cols, float* out,
-                                                         int accumulate) {
-  __shared__ float red[8][33];
+// out[c] (+)= sum over p of partials[p][c], in order of p within each of
+// kChains interleaved chains and of the chains after that: the same bits every
+// call.
+constexpr int kChains = 32;
+__global__ void __launch_bounds__(32 * kChains) column_sum_kernel(const float* partials, int nparts, int cols,
+                                                                  float* out, int accumulate) {
+  __shared__ float red[kChains][33];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int p = w; p < nparts; p += 8) s += partials[static_cast<long long>(p) * cols + c];
+#pragma unroll 4
+    for (int p = w; p < nparts; p += kChains) s += partials[static_cast<long long>(p) * cols + c];
   }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < cols) {
     s = red[0][lane];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
+    for (int i = 1; i < kChains; ++i) s += red[i][lane];
     out[c] = accumulate ? out[c] + s : s;
   }
 }
 
 // --------------------------------------------------------------------------
-// Activation gradient and bias gradient: a CTA takes 32 VEC columns (one warp
-// wide) of every 8 gridDim.y-th rows; its 8 warps' column sums meet in shared
-// memory and go to one row of the partials.
+// Activation gradient and bias gradient.  Bound by HBM.  A warp takes 32 VEC
+// columns and walks the rows kWalk at a time; the 8 warps' column sums of a CTA
+// meet in shared memory and go to one row of the partials.
 // --------------------------------------------------------------------------
-template <typename T, int VEC>
-__global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
+template <typename T, int VEC, int ACT, bool Z8>
+__global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
   __shared__ float red[8][32 * VEC];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int c = (blockIdx.x * 32 + lane) * VEC;
+  const long long step = static_cast<long long>(gridDim.y) * 8;
   float sum[VEC] = {};
-  for (long long row = blockIdx.y * 8 + w; row < a.rows; row += gridDim.y * 8) {
-    float d[VEC], z[VEC];
-    if (c >= a.cols) break;
-    load_cols<T, VEC>(a.dy, row, c, a.cols, d);
-    if (a.act != kActNone) {
-      if (a.z.p) {
-        load_cols<T, VEC>(a.z, row, c, a.cols, z);
-      } else {
-        const float sc = scale_of(a.z8.s[row * a.z8.lds + c / kPackBlock]);
-        const int8_t* q = a.z8.q + row * a.z8.ldq + c;
-        if constexpr (VEC == 8) {
-          const uint2 u = *reinterpret_cast<const uint2*>(q);
+  for (long long row = blockIdx.y * 8 + w; row < a.rows; row += kWalk * step) {
+    Raw<T, VEC> dy[kWalk], z[ACT != kActNone && !Z8 ? kWalk : 1];
+    Codes<VEC> z8[Z8 ? kWalk : 1];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            z[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? u.x : u.y) >> (8 * (j % 4)))) * sc;
-        } else {
-          z[0] = static_cast<float>(*q) * sc;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) d[j] *= act_grad(a.act, z[j]);
+    for (int i = 0; i < kWalk; ++i) {
+      const int ci = row + i * step < a.rows ? c : a.cols;
+      dy[i].load(a.dy, row + i * step, ci, a.cols);
+      if constexpr (ACT != kActNone && Z8)
+        z8[i].load(a.z8, row + i * step, ci, a.cols);
+      else if constexpr (ACT != kActNone)
+        z[i].load(a.z, row + i * step, ci, a.cols);
     }
-    if (a.dz.p) store_cols<T, VEC>(a.dz, row, c, a.cols, d);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sum[j] += d[j];
+    for (int i = 0; i < kWalk; ++i) {
+      if (row + i * step >= a.rows || c >= a.cols) break;
+      float d[VEC];
+      dy[i].values(d);
+      if constexpr (ACT != kActNone) {
+        float t[VEC];
+        if constexpr (Z8)
+          z8[i].values(t);
+        else
+          z[i].values(t);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) d[j] = __fmul_rn(d[j], act_grad<ACT>(t[j]));
+      }
+      if (a.dz.p) store_cols<T, VEC>(a.dz, row + i * step, c, a.cols, d);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum[j] += d[j];
+    }
   }
   if (a.db == nullptr) return;
 #pragma unroll
@@ -280,13 +508,29 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
   }
 }
 
+// One element a lane, neighbouring lanes neighbouring elements: source rows may
+// start anywhere.
 __global__ void __launch_bounds__(256) repitch_kernel(int rows, int cols, const uint16_t* src, long long ld_src,
                                                       uint16_t* dst, long long ld_dst) {
-  const long long total = static_cast<long long>(rows) * cols;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const long long r = i / cols;
-    const int c = static_cast<int>(i - r * cols);
-    dst[r * ld_dst + c] = src[r * ld_src + c];
+  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
+  constexpr int kCols = 4;
+  const int c0 = blockIdx.x * blockDim.x * kCols + threadIdx.x;
+  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += 2 * step) {
+    uint16_t v[2][kCols];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = c0 + j * blockDim.x;
+        if (row + i * step < rows && c < cols) v[i][j] = src[(row + i * step) * ld_src + c];
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = c0 + j * blockDim.x;
+        if (row + i * step < rows && c < cols) dst[(row + i * step) * ld_dst + c] = v[i][j];
+      }
   }
 }
 
@@ -338,39 +582,118 @@ cudaError_t by_dtype(int dtype, F&& f) {
   return f(__half{});
 }
 
+// Row kernels: pieces a thread (NV), lanes along a row and rows of a block.
+struct RowShape {
+  int nv = 0;  // 0: too wide
+  dim3 block;
+};
+RowShape row_shape(int lanes, int max_threads, int max_nv) {
+  RowShape r;
+  for (int nv = 1; nv <= max_nv; nv *= 2) {
+    const int tx = ((lanes + nv - 1) / nv + 31) / 32 * 32;
+    if (tx > max_threads) continue;
+    r.nv = nv;
+    r.block = dim3(tx, tx == 32 ? 4 : 1);
+    return r;
+  }
+  return r;
+}
+// Blocks of a kernel that the device holds at once (kept per block size).
+template <typename K>
+int resident(K k, int threads, size_t smem, std::atomic<int>* cache) {
+  std::atomic<int>& c = cache[threads / 32];
+  int n = c.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = 1;
+    }
+    c.store(n, std::memory_order_relaxed);
+  }
+  return n * sm_count();
+}
+
+// Blocks of 8 warps over rows x lanes: a warp takes 32 lanes of a row, the
+// block's warps neighbouring rows, `walk` of them at a time.  One wave: the
+// last blocks of a second one would run alone.
+const dim3 kWalkBlock(32, 8);
+template <typename K>
+dim3 walk_grid(K k, int rows, int lanes, int walk, std::atomic<int>* cache) {
+  const int gx = (lanes + 31) / 32;
+  const int most = (rows + 8 * walk - 1) / (8 * walk);
+  return dim3(gx, std::max(1, std::min({most, resident(k, 256, 0, cache) / gx, 65535})));
+}
+
+// Calls f with nv as a constant.
+template <int MAX, typename F>
+cudaError_t by_nv(int nv, F&& f) {
+  if constexpr (MAX > 1) {
+    if (nv < MAX) return by_nv<MAX / 2>(nv, f);
+  }
+  return f(std::integral_constant<int, MAX>{});
+}
+template <typename F>
+cudaError_t by_act(int act, F&& f) {
+  if (act == kActRelu) return f(std::integral_constant<int, kActRelu>{});
+  if (act == kActGelu) return f(std::integral_constant<int, kActGelu>{});
+  if (act == kActSilu) return f(std::integral_constant<int, kActSilu>{});
+  return f(std::integral_constant<int, kActNone>{});
+}
+
 }  // namespace
 
 cudaError_t launch_pack8(int rows, int cols, int dtype, Mat x, Pack8 out, cudaStream_t s) {
   const bool vec = cols % 8 == 0 && vec_mat(x, elem_bytes(dtype)) && vec_pack(out);
-  const long long lanes = static_cast<long long>(rows) * ((cols + kPackBlock - 1) / kPackBlock) *
-                          (vec ? kPackBlock / 8 : kPackBlock);
+  const int lanes = (cols + kPackBlock - 1) / kPackBlock * (vec ? kPackBlock / 8 : kPackBlock);  // whole blocks
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
+    static std::atomic<int> cache[2][9];
     auto k = vec ? pack8_kernel<T, 8> : pack8_kernel<T, 1>;
-    return launch_kernel(false, k, dim3(flat_grid(lanes)), dim3(256), 0, s, rows, cols, x, out);
+    return launch_kernel(false, k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, x, out);
   });
 }
 
 cudaError_t launch_unpack8(int rows, int cols, Pack8 in, int dtype, Mat out, cudaStream_t s) {
   const bool vec = cols % 8 == 0 && vec_mat(out, elem_bytes(dtype)) && vec_pack(in);
-  const long long lanes = static_cast<long long>(rows) * (vec ? cols / 8 : cols);
+  const int lanes = vec ? cols / 8 : cols;
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
+    static std::atomic<int> cache[2][9];
     auto k = vec ? unpack8_kernel<T, 8> : unpack8_kernel<T, 1>;
-    return launch_kernel(false, k, dim3(flat_grid(lanes)), dim3(256), 0, s, rows, cols, in, out);
+    return launch_kernel(false, k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, in, out);
   });
 }
+
+// Columns of a thread in the register kernels: pieces of 8, or single elements
+// where pitch, base or width rules vectors out.
+template <typename T, int VEC>
+constexpr int kMaxPieces = VEC == 8 ? 2 : 8;
 
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
   const int eb = elem_bytes(a.dtype);
   const bool vec = a.cols % 8 == 0 && vec_mat(a.x, eb) && vec_mat(a.residual, eb) && vec_mat(a.h, eb) &&
                    vec_mat(a.y, eb) && vec_pack(a.y8);
   const int lanes = vec ? a.cols / 8 : a.cols;
-  const int threads = std::min(1024, (lanes + 31) / 32 * 32);
-  return by_dtype(a.dtype, [&](auto t) {
+  auto run = [&](auto t, auto v) {
     using T = decltype(t);
-    auto k = vec ? rms_norm_kernel<T, 8> : rms_norm_kernel<T, 1>;
-    return launch_kernel(false, k, dim3(std::min(a.rows, 8 * sm_count())), dim3(threads), 0, s, a);
+    constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
+    const RowShape r = row_shape(lanes, kRowThreads, MAXV);
+    if (r.nv == 0)
+      return launch_kernel(false, rms_norm_wide_kernel<T, VEC>, dim3(std::min(a.rows, 2 * sm_count())), dim3(1024), 0,
+                           s, a);
+    return by_nv<MAXV>(r.nv, [&](auto n) {
+      constexpr int NV = decltype(n)::value;
+      static std::atomic<int> cache[2][kRowThreads / 32 + 1];
+      const bool res = a.residual.p != nullptr;
+      auto k = res ? rms_norm_kernel<T, VEC, NV, true> : rms_norm_kernel<T, VEC, NV, false>;
+      const int threads = r.block.x * r.block.y;
+      const long long blocks = (static_cast<long long>(a.rows) + r.block.y - 1) / r.block.y;
+      const int grid = static_cast<int>(std::min<long long>(blocks, resident(k, threads, 0, cache[res])));
+      return launch_kernel(false, k, dim3(grid), r.block, 0, s, a);
+    });
+  };
+  return by_dtype(a.dtype, [&](auto t) {
+    return vec ? run(t, std::integral_constant<int, 8>{}) : run(t, std::integral_constant<int, 1>{});
   });
 }
 
@@ -378,43 +701,70 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   const int eb = elem_bytes(a.dtype);
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, eb) && vec_mat(a.h, eb) && vec_mat(a.dh, eb) && vec_mat(a.dx, eb);
   const int lanes = vec ? a.cols / 8 : a.cols;
-  const int threads = std::min(1024, (lanes + 31) / 32 * 32);
-  const int grid = std::max(1, std::min(a.rows, std::min(kMaxPartials, 4 * sm_count())));
-  const size_t smem = a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0;
-  cudaError_t e = by_dtype(a.dtype, [&](auto t) {
+  int parts = 0;  // rows of partial column sums
+  auto run = [&](auto t, auto v) {
     using T = decltype(t);
-    auto k = vec ? rms_norm_grad_kernel<T, 8> : rms_norm_grad_kernel<T, 1>;
-    cudaError_t se = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4);
-    if (se != cudaSuccess) return se;
-    return launch_kernel(false, k, dim3(grid), dim3(threads), smem, s, a);
+    constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
+    const RowShape r = row_shape(lanes, kRowThreads, MAXV);
+    if (r.nv == 0) {
+      auto k = rms_norm_grad_wide_kernel<T, VEC>;
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4);
+      if (e != cudaSuccess) return e;
+      parts = std::min(a.rows, sm_count());
+      return launch_kernel(false, k, dim3(parts), dim3(1024), a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0, s,
+                           a);
+    }
+    return by_nv<MAXV>(r.nv, [&](auto n) {
+      constexpr int NV = decltype(n)::value;
+      static std::atomic<int> cache[2][kRowThreads / 32 + 1];
+      const bool dh = a.dh.p != nullptr;
+      auto k = dh ? rms_norm_grad_kernel<T, VEC, NV, true> : rms_norm_grad_kernel<T, VEC, NV, false>;
+      const int ty = r.block.y, threads = r.block.x * ty;
+      const size_t smem = ty > 1 ? static_cast<size_t>(threads) * VEC * NV * 4 : 0;
+      const long long blocks = (static_cast<long long>(a.rows) + ty - 1) / ty;
+      // One row of partials a block, as many at most as the workspace holds.
+      parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
+                                         static_cast<long long>(kMaxPartials)}));
+      return launch_kernel(false, k, dim3(parts), r.block, smem, s, a);
+    });
+  };
+  const cudaError_t e = by_dtype(a.dtype, [&](auto t) {
+    return vec ? run(t, std::integral_constant<int, 8>{}) : run(t, std::integral_constant<int, 1>{});
   });
   if (e != cudaSuccess || a.dw == nullptr) return e;
-  return launch_kernel(false, column_sum_kernel, dim3((a.cols + 31) / 32), dim3(256), 0, s,
-                       static_cast<const float*>(a.partials), grid, a.cols, a.dw, a.accumulate);
+  return launch_kernel(false, column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
+                       static_cast<const float*>(a.partials), parts, a.cols, a.dw, a.accumulate);
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, 2) && vec_mat(a.z, 2) && vec_mat(a.dz, 2) && vec_pack(a.z8);
-  const int wide = vec ? 256 : 32;
-  const int gx = (a.cols + wide - 1) / wide;
-  const int gy = std::max(1, std::min({kMaxPartials, (a.rows + 7) / 8, (8 * sm_count() + gx - 1) / gx}));
-  cudaError_t e = by_dtype(a.dtype, [&](auto t) {
+  int parts = 0;
+  const cudaError_t e = by_dtype(a.dtype, [&](auto t) {
     using T = decltype(t);
     if constexpr (std::is_same<T, float>::value) {
       return cudaErrorInvalidValue;  // 16-bit types only
     } else {
-      auto k = vec ? act_grad_kernel<T, 8> : act_grad_kernel<T, 1>;
-      return launch_kernel(false, k, dim3(gx, gy), dim3(256), 0, s, a);
+      return by_act(a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        auto k = a.z8.q != nullptr ? (vec ? act_grad_kernel<T, 8, ACT, true> : act_grad_kernel<T, 1, ACT, true>)
+                                   : (vec ? act_grad_kernel<T, 8, ACT, false> : act_grad_kernel<T, 1, ACT, false>);
+        static std::atomic<int> cache[2][2][9];
+        dim3 grid = walk_grid(k, a.rows, vec ? a.cols / 8 : a.cols, kWalk, cache[a.z8.q != nullptr][vec]);
+        grid.y = std::min<unsigned>(grid.y, kMaxPartials);
+        parts = static_cast<int>(grid.y);
+        return launch_kernel(false, k, grid, dim3(256), 0, s, a);
+      });
     }
   });
   if (e != cudaSuccess || a.db == nullptr) return e;
-  return launch_kernel(false, column_sum_kernel, dim3((a.cols + 31) / 32), dim3(256), 0, s,
-                       static_cast<const float*>(a.partials), gy, a.cols, a.db, a.accumulate);
+  return launch_kernel(false, column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
+                       static_cast<const float*>(a.partials), parts, a.cols, a.db, a.accumulate);
 }
 
 cudaError_t launch_repitch(int rows, int cols, Mat src, Mat dst, cudaStream_t s) {
-  return launch_kernel(false, repitch_kernel, dim3(flat_grid(static_cast<long long>(rows) * cols)), dim3(256), 0, s,
-                       rows, cols, static_cast<const uint16_t*>(src.p), src.ld, static_cast<uint16_t*>(dst.p), dst.ld);
+  static std::atomic<int> cache[9];
+  return launch_kernel(false, repitch_kernel, walk_grid(repitch_kernel, rows, (cols + 3) / 4, 2, cache), kWalkBlock, 0, s, rows, cols, static_cast<const uint16_t*>(src.p),
+                       src.ld, static_cast<uint16_t*>(dst.p), dst.ld);
 }
 
 cudaError_t launch_zero(int rows, int cols, int elem_bytes, Mat out, cudaStream_t s) {
