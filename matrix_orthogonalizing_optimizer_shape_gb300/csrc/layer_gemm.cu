@@ -62,82 +62,113 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
   }
 }
 
-// One 8-bit block held by a warp: lane = column of the block (0 past the end).
-__device__ __forceinline__ void store_block_warp(const Pack8& o, long long t, int m, bool in, float v) {
-  const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
-  if (!in) return;
-  float u[1] = {v};
-  saturate_block(byte, u);
-  o.q[t * o.ldq + m] = static_cast<int8_t>(code_of(u[0], inv_scale(byte)));
-  if (m % kPackBlock == 0) o.s[t * o.lds + m / kPackBlock] = static_cast<uint8_t>(byte);
+// The 8-bit blocks of n rows held by a warp: lane = column of the block, 0 past
+// the last column (`in` false there).
+template <int C>
+__device__ __forceinline__ void store_blocks_warp(const Pack8& o, int t0, int n, int m, bool in, const float (&v)[C]) {
+  int8_t* q = o.q + static_cast<long long>(t0) * o.ldq + m;
+  uint8_t* s = o.s + static_cast<long long>(t0) * o.lds + m / kPackBlock;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    if (j >= n) break;
+    const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7FFFFFFFu));
+    float u[1] = {v[j]};
+    saturate_block(byte, u);
+    if (in) q[j * o.ldq] = static_cast<int8_t>(code_of(u[0], inv_scale(byte)));
+    if (in && m % kPackBlock == 0) s[j * o.lds] = static_cast<uint8_t>(byte);
+  }
 }
 
 // Values v[0..C) of output rows t0.. at column m (in: m < M).  Run by a whole
 // warp whose lanes hold 32 consecutive columns.
 template <bool BF16, bool FWD, int C>
 __device__ __forceinline__ void epilogue_rows(const Epilogue& e, int t0, int m, bool in, float bias, float (&v)[C]) {
+  const int n = min(C, e.N - t0);
+  const int nw = in ? n : 0;  // rows this lane writes
+  const long long o = static_cast<long long>(t0) * e.ld_out + m;
   if constexpr (FWD) {
     uint16_t r[C];
     if (e.res != nullptr) {
+      const uint16_t* p = e.res + static_cast<long long>(t0) * e.ld_res + m;
+#pragma unroll
+      for (int j = 0; j < C; ++j) r[j] = j < nw ? p[j * e.ld_res] : uint16_t(0);
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = in ? v[j] + bias : 0.f;
+    if (e.z != nullptr) {
+      uint16_t* p = e.z + static_cast<long long>(t0) * e.ld_z + m;
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        r[j] = in && t0 + j < e.N ? e.res[static_cast<long long>(t0 + j) * e.ld_res + m] : uint16_t(0);
+        if (j < nw) p[j * e.ld_z] = pack1<BF16>(v[j]);
     }
+    if (e.z8.q != nullptr) store_blocks_warp(e.z8, t0, n, m, in, v);
+    apply_act(e.act, v);
+    if (e.res != nullptr) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      if (t0 + j >= e.N) break;
-      const long long t = t0 + j;
-      const float z = in ? v[j] + bias : 0.f;
-      if (e.z != nullptr && in) e.z[t * e.ld_z + m] = pack1<BF16>(z);
-      if (e.z8.q != nullptr) store_block_warp(e.z8, t, m, in, z);
-      float y[1] = {z};
-      apply_act(e.act, y);
-      if (e.res != nullptr) y[0] += unpack1<BF16>(r[j]);
-      if (in) static_cast<uint16_t*>(e.out)[t * e.ld_out + m] = pack1<BF16>(y[0]);
-      if (e.out8.q != nullptr) store_block_warp(e.out8, t, m, in, in ? y[0] : 0.f);
+      for (int j = 0; j < C; ++j) v[j] += unpack1<BF16>(r[j]);
     }
+    uint16_t* p = static_cast<uint16_t*>(e.out) + o;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (j < nw) p[j * e.ld_out] = pack1<BF16>(v[j]);
+    if (e.out8.q != nullptr) store_blocks_warp(e.out8, t0, n, m, in, v);
   } else if (e.out_f32) {
-    float* o = static_cast<float*>(e.out) + static_cast<long long>(t0) * e.ld_out + m;
+    float* p = static_cast<float*>(e.out) + o;
+    if (e.accumulate) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] += j < nw ? p[j * e.ld_out] : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      if (in && t0 + j < e.N) o[j * e.ld_out] = e.accumulate ? o[j * e.ld_out] + v[j] : v[j];
+      if (j < nw) p[j * e.ld_out] = v[j];
   } else {
-    uint16_t* o = static_cast<uint16_t*>(e.out) + static_cast<long long>(t0) * e.ld_out + m;
+    uint16_t* p = static_cast<uint16_t*>(e.out) + o;
+    if (e.accumulate) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] += j < nw ? unpack1<BF16>(p[j * e.ld_out]) : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      if (in && t0 + j < e.N)
-        o[j * e.ld_out] = pack1<BF16>(e.accumulate ? unpack1<BF16>(o[j * e.ld_out]) + v[j] : v[j]);
+      if (j < nw) p[j * e.ld_out] = pack1<BF16>(v[j]);
   }
 }
 
-template <int BN>
+template <int BN, bool DEEP>  // DEEP: one CTA an SM, the ring takes all of it
 struct TileCfg {
   static constexpr int kABytes = BM * BK * 2;
   static constexpr int kBBytes = BN * BK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 96 * 1024 / kStageBytes;  // two CTAs an SM
+  static constexpr int kStages = (DEEP ? 200 : 96) * 1024 / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kTmemCols = BN < 32 ? 32 : BN;
   static constexpr int kBars = (2 * kStages + 2) * 8;
   static constexpr int kDyn = 1024 + kRing + kBars + 16;
+  static_assert(BN * BM * 4 <= kRing, "a tile's partial sums take the ring's place");
 };
 constexpr int kTileThreads = 6 * 32;
+constexpr int kTurn = 8;  // output rows an epilogue warp finishes at a time
 
-template <bool BF16, bool AT, bool BT, int BN, bool FWD>
+// K is split over the CTAs of a cluster when there are few tiles: each CTA
+// multiplies its share of the K slabs, the partial tiles meet in distributed
+// shared memory, and every CTA adds the partials of its share of the rows in
+// rank order (the same bits every call) and finishes them.
+template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP>
 __global__ void __launch_bounds__(kTileThreads)
-    tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, int nkb, int tiles_m,
-                Epilogue e, unsigned* status) {
-  using C = TileCfg<BN>;
+    tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, int nkb_all,
+                int tiles_m, int split, Epilogue e, unsigned* status) {
+  using C = TileCfg<BN, DEEP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t sA = base, sB = base + C::kStages * C::kABytes;
-  const uint32_t bar_full = base + C::kRing, bar_empty = bar_full + 8 * C::kStages, bar_done = bar_empty + 8 * C::kStages,
-                 bar_drain = bar_done + 8;
+  const uint32_t bar_full = base + C::kRing, bar_empty = bar_full + 8 * C::kStages,
+                 bar_done = bar_empty + 8 * C::kStages, bar_drain = bar_done + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + C::kRing + C::kBars);
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
+    prefetch_map(&tmA);
+    prefetch_map(&tmB);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
@@ -152,7 +183,14 @@ __global__ void __launch_bounds__(kTileThreads)
   fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  const int m0 = (blockIdx.x % tiles_m) * BM, t0 = (blockIdx.x / tiles_m) * BN;
+  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = blockIdx.x / split;
+  const int m0 = (tile % tiles_m) * BM, t0 = (tile / tiles_m) * BN;
+  const int kb0 = static_cast<int>(static_cast<long long>(nkb_all) * rank / split);
+  const int nkb = static_cast<int>(static_cast<long long>(nkb_all) * (rank + 1) / split) - kb0;
+  const int quad = warp % 4;
+  const int m = m0 + quad * 32 + lane;
+  const bool in = m < e.M;
 
   if (warp == 0) {
     int kb = 0;
@@ -160,7 +198,7 @@ __global__ void __launch_bounds__(kTileThreads)
       const uint32_t s = kb % C::kStages, ph = (kb / C::kStages) & 1u;
       if (!mbar_wait_warp(bar_empty + 8 * s, ph ^ 1u, status)) break;
       const uint32_t a = sA + s * C::kABytes, b = sB + s * C::kBBytes, full = bar_full + 8 * s;
-      const int k0 = kb * BK;
+      const int k0 = (kb0 + kb) * BK;
       if (elect_one()) {
         mbar_expect(full, C::kStageBytes);
         if constexpr (AT) {
@@ -203,75 +241,102 @@ __global__ void __launch_bounds__(kTileThreads)
     if (elect_one()) mma_commit(bar_drain);
     __syncwarp();
     mbar_wait_warp(bar_drain, 0u, status);
-  } else {
-    const int quad = warp % 4;
-    const int m = m0 + quad * 32 + lane;
-    const bool in = m < e.M;
+  } else if (mbar_wait_warp(bar_done, 0u, status)) {
+    fence_after();
     const float bias = FWD && e.bias != nullptr && in ? load_bias(e.bias, e.bias_dtype, m) : 0.f;
-    if (mbar_wait_warp(bar_done, 0u, status)) {
-      fence_after();
-      constexpr int CH = BN < 32 ? 16 : 32;
-      const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // Eight rows a turn, rolled: this code runs once or a few times a launch,
+    // and fetching it unrolled took longer than running it.  A turn's loads
+    // run under the turn before.
+    uint32_t u[kTurn];
+    tmem_ld8(tb, u);
+    const int n = min(BN, e.N - t0);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += CH) {
-        if (t0 + c >= e.N) break;
-        uint32_t u[CH];
-        if constexpr (CH == 16)
-          tmem_ld16(tb + c, u);
-        else
-          tmem_ld32(tb + c, u);
-        tmem_ld_done(u);
-        float v[CH];
+    for (int c = 0; c < n; c += kTurn) {
+      tmem_ld_done(u);
+      float v[kTurn];
 #pragma unroll
-        for (int j = 0; j < CH; ++j) v[j] = __uint_as_float(u[j]);
-        epilogue_rows<BF16, FWD, CH>(e, t0 + c, m, in, bias, v);
+      for (int j = 0; j < kTurn; ++j) v[j] = __uint_as_float(u[j]);
+      if (c + kTurn < n) tmem_ld8(tb + c + kTurn, u);
+      if (split > 1) {  // every slab has been consumed: the ring is free
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j) st_shared_f32(base + ((c + j) * BM + quad * 32 + lane) * 4, v[j]);
+      } else {
+        epilogue_rows<BF16, FWD, kTurn>(e, t0 + c, m, in, bias, v);
+      }
+    }
+  }
+  if (split > 1) {
+    cluster_sync();
+    if (warp >= 2) {
+      const float bias = FWD && e.bias != nullptr && in ? load_bias(e.bias, e.bias_dtype, m) : 0.f;
+      const int valid = min(BN, e.N - t0), per = (valid + split - 1) / split;
+      const int j1 = min(valid, (rank + 1) * per);
+#pragma unroll 1
+      for (int j0 = rank * per; j0 < j1; j0 += kTurn) {
+        float v[kTurn] = {};
+        const uint32_t at = base + (j0 * BM + quad * 32 + lane) * 4;
+        for (int r = 0; r < split; ++r) {
+          const uint32_t peer = map_to_rank(at, r);
+#pragma unroll
+          for (int j = 0; j < kTurn; ++j)
+            if (j0 + j < j1) v[j] += ld_cluster_f32(peer + j * BM * 4);
+        }
+        // Rows past this CTA's share end at e.N for the epilogue.
+        Epilogue part = e;
+        part.N = t0 + j1;
+        epilogue_rows<BF16, FWD, kTurn>(part, t0 + j0, m, in, bias, v);
       }
     }
   }
   fence_before();
-  __syncthreads();
+  // With a split, no CTA leaves while a peer may still read its partials.
+  if (split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   if (warp == 1) {
     fence_after();
     tmem_free<1>(tmem, C::kTmemCols);
   }
 }
 
-
 // --------------------------------------------------------------------------
 // Large products: persistent clusters of two CTAs on two SMs, each cluster a
-// 256 x 256 tile of the output at a time with the paired-SM MMA (M = 256, N =
-// 256, K = 16).  Here the TMEM lanes are output rows: CTA rank r holds rows
+// 256 x 256 (or 256 x 128) tile of the output at a time with the paired-SM MMA
+// (M = 256, K = 16).  Here the TMEM lanes are output rows: CTA rank r holds rows
 // 128 r .. of the tile and every epilogue thread one row, 32 contiguous
 // columns at a time, so an 8-bit block is one thread's registers.  Two
-// 256-column accumulators let the epilogue of a tile run under the next
+// accumulators let the epilogue of a tile run under the next
 // tile's MMAs.  Warps: 0 TMA producer, 1 MMA issuer (even CTA), 2..9 epilogue
 // (two per TMEM lane quadrant, each half of the columns).
 // --------------------------------------------------------------------------
-constexpr int kPairN = 256;
 constexpr int kPairEpiWarps = 8;
-constexpr int kPairTmem = 512;
+constexpr int kBox = 2048;  // staging box: 32 rows of 64 bytes
 constexpr int kBand = 8;  // row tiles walked together, column by column: operand panels shared through L2
 
 enum PairOut : int { kOutFwd = 0, kOut16 = 1, kOut32 = 2 };
 
 struct PairParams {
   int rows, cols, nkb;         // output rows and columns, K slabs
-  int tiles_r, tiles_c;        // 256 x 256 tiles
+  int tiles_r, tiles_c;        // tiles of 256 rows
   int tma_out, tma_z;          // the output has a store map
   int vec_res;                 // residual (or the accumulated output) readable in 16-byte pieces
   Epilogue e;
   unsigned* status;
 };
 
+template <int PN>  // tile width: 256, or 128 where there are few tiles
 struct PairCfg {
-  static constexpr int kHalf = 128 * BK * 2;  // one operand of one CTA and slab: 16 KB
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 6;
+  static constexpr int kA = 128 * BK * 2;       // one CTA's rows of A, one slab: 16 KB
+  static constexpr int kB = PN / 2 * BK * 2;    // and its half of B
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = PN == 256 ? 6 : 8;
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kBox = 2048;           // staging box: 32 rows of 64 bytes
   static constexpr int kStaging = kPairEpiWarps * 2 * kBox;
   static constexpr int kBars = (2 * kStages + 5) * 8;
   static constexpr int kDyn = 1024 + kRing + kStaging + kBars + 16;
+  static constexpr int kTmem = 2 * PN;          // two accumulators
   static constexpr int kThreads = 32 * (2 + kPairEpiWarps);
 };
 
@@ -291,7 +356,7 @@ struct Stager {
   bool bulk;       // every box is read by a bulk store
   // Writes the thread's row of the next box (64 bytes); returns its address.
   __device__ __forceinline__ uint32_t fill(const uint32_t (&w)[16]) {
-    const uint32_t b = buf + (count & 1u) * PairCfg::kBox;
+    const uint32_t b = buf + (count & 1u) * kBox;
     const uint32_t sw = static_cast<uint32_t>((lane >> 1) & 3);
     if (lane == 0) {  // the store two boxes back has read its box
       if (bulk)
@@ -451,16 +516,16 @@ __device__ __forceinline__ void store_block_row(const Pack8& o, long long r, int
   o.s[r * o.lds + c0 / kPackBlock] = static_cast<uint8_t>(byte);
 }
 
-template <bool BF16, bool AT, bool BT, int OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
+template <bool BF16, bool AT, bool BT, int OUT, int PN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
                 const __grid_constant__ PairParams p) {
-  using C = PairCfg;
+  using C = PairCfg<PN>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t sA = base, sB = base + C::kStages * C::kHalf, staging = base + C::kRing;
+  const uint32_t sA = base, sB = base + C::kStages * C::kA, staging = base + C::kRing;
   const uint32_t bar_full = staging + C::kStaging, bar_empty = bar_full + 8 * C::kStages;
   const uint32_t bar_tfull = bar_empty + 8 * C::kStages, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + C::kRing + C::kStaging + C::kBars);
@@ -471,6 +536,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   const int total = p.tiles_r * p.tiles_c;
   if (threadIdx.x == 0) {
+    prefetch_map(&tmA);
+    prefetch_map(&tmB);
+    if (p.tma_out) prefetch_map(&tmOut);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full + 8 * s, 1);   // in the even CTA: its producer, and both CTAs' bytes
       mbar_init(bar_empty + 8 * s, 1);  // the pair's MMA commit
@@ -482,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     mbar_init(bar_drain, 1);
     mbar_init_fence();
   }
-  if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), kPairTmem);
+  if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), C::kTmem);
   fence_before();
   cluster_sync();
   fence_after();
@@ -495,24 +563,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     for (int u = cluster; u < total && ok; u += nclusters) {
       int R, Cc;
       pair_tile(p, u, R, Cc);
-      const int a_row = R * 256 + static_cast<int>(rank) * 128, b_row = Cc * kPairN + static_cast<int>(rank) * 128;
+      const int a_row = R * 256 + static_cast<int>(rank) * 128, b_row = Cc * PN + static_cast<int>(rank) * (PN / 2);
       for (int kb = 0; kb < p.nkb; ++kb, ++kc) {
         const uint32_t s = kc % C::kStages, ph = (kc / C::kStages) & 1u;
         if (!(ok = mbar_wait_warp(bar_empty + 8 * s, ph ^ 1u, p.status))) break;
-        const uint32_t a = sA + s * C::kHalf, b = sB + s * C::kHalf;
+        const uint32_t a = sA + s * C::kA, b = sB + s * C::kB;
         const int k0 = kb * BK;
         if (elect_one()) {
           if (leader) mbar_expect(bar_full + 8 * s, 2 * C::kStage);
           const uint32_t full = map_to_rank(bar_full + 8 * s, 0);
           if constexpr (AT) {
             tma_load_pair(a, &tmA, full, a_row, k0);
-            tma_load_pair(a + C::kHalf / 2, &tmA, full, a_row + 64, k0);
+            tma_load_pair(a + C::kA / 2, &tmA, full, a_row + 64, k0);
           } else {
             tma_load_pair(a, &tmA, full, k0, a_row);
           }
           if constexpr (BT) {
             tma_load_pair(b, &tmB, full, b_row, k0);
-            tma_load_pair(b + C::kHalf / 2, &tmB, full, b_row + 64, k0);
+            if constexpr (PN == 256) tma_load_pair(b + C::kB / 2, &tmB, full, b_row + 64, k0);
           } else {
             tma_load_pair(b, &tmB, full, k0, b_row);
           }
@@ -528,19 +596,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     }
   } else if (warp == 1) {
     if (leader) {
-      constexpr uint32_t id = instr_desc<BF16, AT, BT>(256, kPairN);
+      constexpr uint32_t id = instr_desc<BF16, AT, BT>(256, PN);
       uint32_t kc = 0, tc = 0;
       bool ok = true;
       for (int u = cluster; u < total && ok; u += nclusters, ++tc) {
         const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
         if (!mbar_wait_warp(bar_tempty + 8 * acc, aph ^ 1u, p.status)) break;
         fence_after();
-        const uint32_t d = tmem + acc * kPairN;
+        const uint32_t d = tmem + acc * PN;
         for (int kb = 0; kb < p.nkb; ++kb, ++kc) {
           const uint32_t s = kc % C::kStages, ph = (kc / C::kStages) & 1u;
           if (!(ok = mbar_wait_warp(bar_full + 8 * s, ph, p.status))) break;
           fence_after();
-          const uint64_t da = smem_desc<AT>(sA + s * C::kHalf), db = smem_desc<BT>(sB + s * C::kHalf);
+          const uint64_t da = smem_desc<AT>(sA + s * C::kA), db = smem_desc<BT>(sB + s * C::kB);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
@@ -560,9 +628,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     }
   } else {
     const int quad = warp % 4;
-    const int col_lo = ((warp - 2) / 4) * 128;
+    const int col_lo = ((warp - 2) / 4) * (PN / 2);
     const Epilogue& e = p.e;
-    Stager st{staging + static_cast<uint32_t>(warp - 2) * 2 * C::kBox, 0u, lane,
+    Stager st{staging + static_cast<uint32_t>(warp - 2) * 2 * kBox, 0u, lane,
               p.tma_out && (e.z == nullptr || p.tma_z)};
     // What is added to the row before it is rounded: the residual, or the
     // output itself.
@@ -575,9 +643,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       pair_tile(p, u, R, Cc);
       const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
       const int row0 = R * 256 + static_cast<int>(rank) * 128 + quad * 32, r = row0 + lane;
-      const int cbase = Cc * kPairN + col_lo;
-      const int nch = row0 < p.rows ? min(4, (p.cols - cbase + 31) / 32) : 0;  // chunks with something to write
-      const uint32_t tb = tmem + acc * kPairN + col_lo + (static_cast<uint32_t>(quad * 32) << 16);
+      const int cbase = Cc * PN + col_lo;
+      const int nch = row0 < p.rows ? min(PN / 64, (p.cols - cbase + 31) / 32) : 0;  // chunks with something to write
+      const uint32_t tb = tmem + acc * PN + col_lo + (static_cast<uint32_t>(quad * 32) << 16);
       RowPiece piece, next;
       if (nch > 0) piece.load(addend, ld_add, p, r, cbase);
       if (!mbar_wait_warp(bar_tfull + 8 * acc, aph, p.status)) break;
@@ -637,8 +705,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       fence_before();
       mbar_arrive_remote_cta(map_to_rank(bar_tempty + 8 * acc, 0));
     }
-    // Every bulk store has finished before shared memory goes away.
-    if (lane == 0) bulk_wait_all();
+    // Every bulk store has read its box before shared memory goes away.
+    if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
   }
   fence_before();
@@ -647,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   cluster_sync();
   if (warp == 1) {
     fence_after();
-    tmem_free<2>(tmem, kPairTmem);
+    tmem_free<2>(tmem, C::kTmem);
   }
 }
 
@@ -731,18 +799,19 @@ int resident_pairs(K kern, int threads, int smem, int dev, int* cached) {
 
 // The pair kernel's A is the operand of the output's rows (Product::B) and its
 // B that of the columns (Product::A).
-template <bool BF16, bool AT, bool BT, int OUT>
+template <bool BF16, bool AT, bool BT, int OUT, int PN>
 cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cudaStream_t s) {
-  auto kern = pair_kernel<BF16, AT, BT, OUT>;
+  using C = PairCfg<PN>;
+  auto kern = pair_kernel<BF16, AT, BT, OUT, PN>;
   static std::once_flag once[64];
   static int pairs[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
-  const cudaError_t err = allow_smem(kern, PairCfg::kDyn, once, dev);
+  const cudaError_t err = allow_smem(kern, C::kDyn, once, dev);
   if (err != cudaSuccess) return err;
   CUtensorMap ta, tb, to, tz;
   if (!operand_map(&ta, g.B, AT ? g.K : g.N, AT ? g.N : g.K, AT ? BK : 128, g.elem)) return cudaErrorInvalidValue;
-  if (!operand_map(&tb, g.A, BT ? g.K : g.M, BT ? g.M : g.K, BT ? BK : 128, g.elem)) return cudaErrorInvalidValue;
+  if (!operand_map(&tb, g.A, BT ? g.K : g.M, BT ? g.M : g.K, BT ? BK : PN / 2, g.elem)) return cudaErrorInvalidValue;
   memset(&to, 0, sizeof to);
   memset(&tz, 0, sizeof tz);
   PairParams p{};
@@ -750,7 +819,7 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   p.cols = g.M;
   p.nkb = (g.K + BK - 1) / BK;
   p.tiles_r = (g.N + 255) / 256;
-  p.tiles_c = (g.M + 255) / 256;
+  p.tiles_c = (g.M + PN - 1) / PN;
   p.tma_out = store_map(&to, e.out, e.ld_out, g.N, g.M, e.out_f32 ? static_cast<int>(kF32) : g.elem);
   p.tma_z = store_map(&tz, e.z, e.ld_z, g.N, g.M, g.elem);
   const uintptr_t add = reinterpret_cast<uintptr_t>(OUT == kOutFwd ? static_cast<const void*>(e.res) : e.out);
@@ -760,15 +829,25 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   const long long total = static_cast<long long>(p.tiles_r) * p.tiles_c;
   if (total > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
   const int clusters =
-      static_cast<int>(std::min<long long>(total, resident_pairs(kern, PairCfg::kThreads, PairCfg::kDyn, dev, pairs)));
-  return launch_kernel(pdl_enabled(), kern, dim3(2 * clusters), dim3(PairCfg::kThreads), PairCfg::kDyn, s, ta, tb, to,
+      static_cast<int>(std::min<long long>(total, resident_pairs(kern, C::kThreads, C::kDyn, dev, pairs)));
+  return launch_kernel(pdl_enabled(), kern, dim3(2 * clusters), dim3(C::kThreads), C::kDyn, s, ta, tb, to,
                        tz, p);
 }
 
-template <bool BF16, bool AT, bool BT, int BN, bool FWD>
-cudaError_t run_tile(const Product& g, const Epilogue& e, unsigned* status, cudaStream_t s) {
-  using C = TileCfg<BN>;
-  auto kern = tile_kernel<BF16, AT, BT, BN, FWD>;
+int sm_count(int dev) {
+  static int cached[64] = {0};
+  if (cached[dev & 63] == 0) {
+    int n = 0;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cached[dev & 63] = n > 0 ? n : 1;
+  }
+  return cached[dev & 63];
+}
+
+template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP>
+cudaError_t run_tile(const Product& g, const Epilogue& e, int split, unsigned* status, cudaStream_t s) {
+  using C = TileCfg<BN, DEEP>;
+  auto kern = tile_kernel<BF16, AT, BT, BN, FWD, DEEP>;
   static std::once_flag once[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -777,30 +856,111 @@ cudaError_t run_tile(const Product& g, const Epilogue& e, unsigned* status, cuda
   CUtensorMap ta, tb;
   if (!operand_map(&ta, g.A, AT ? g.K : g.M, AT ? g.M : g.K, AT ? BK : BM, g.elem)) return cudaErrorInvalidValue;
   if (!operand_map(&tb, g.B, BT ? g.K : g.N, BT ? g.N : g.K, BT ? BK : BN, g.elem)) return cudaErrorInvalidValue;
-  const int tiles_m = (g.M + BM - 1) / BM;
-  const long long tiles = static_cast<long long>(tiles_m) * ((g.N + BN - 1) / BN);
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_kernel(pdl_enabled(), kern, dim3(static_cast<unsigned>(tiles)), dim3(kTileThreads), C::kDyn, s, ta, tb,
-                       (g.K + BK - 1) / BK, tiles_m, e, status);
+  const int tiles_m = (g.M + BM - 1) / BM, nkb = (g.K + BK - 1) / BK;
+  const long long ctas = static_cast<long long>(tiles_m) * ((g.N + BN - 1) / BN) * split;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = C::kDyn;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (pdl_enabled()) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (split > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = split;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, nkb, tiles_m, split, e, status);
 }
 
-// Which kernel a product takes: the pair kernel once both output dimensions
-// fill its tile (16384 x 4096 x 11008 forward: 0.91 ms against 2.00 ms).
-bool use_pair(const Product& g) { return g.N >= 256 && g.M >= 256; }
+// Which kernel a product takes, and how.
+struct Plan {
+  bool pair;
+  int bn, split;  // tile width; CTAs that share a tile's K (tile kernel)
+  bool deep;      // one CTA an SM with a deeper ring (tile kernel)
+};
+
+// The cheapest by an estimate in microseconds.  Short of large products every
+// variant is bound by what an SM takes in: about 105 KB a microsecond with one
+// CTA or a pair's half on it, 135 with two CTAs, while all SMs together take
+// 6500 KB a microsecond from HBM.  To that come a launch's fixed part, the rows
+// that a tile's epilogue writes, and the join of a split.  Measured over 48
+// products (cold caches) of 1 .. 16384 rows and 512 .. 11008 columns, its choice
+// is within 10 % of the best of some 12 variants each: at 256 x 2048 x 2048 (dx)
+// a 64-wide tile with K over 4 CTAs, 11.1 us, where a pair a tile takes 15.9;
+// at 16384 x 512 x 512 (dW) K over 8 CTAs, 22 us, where a pair takes 77.
+Plan plan_product(const Product& g) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int sms = sm_count(dev), pairs = sms / 2;
+  const long long nkb = (g.K + BK - 1) / BK, tm = (g.M + BM - 1) / BM;
+  const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
+  const double hbm = 2.0 * (1.0 * g.M * g.K + 1.0 * g.N * g.K + 1.0 * g.M * g.N) / 1024 / 6500;
+  Plan best{};
+  double least = 1e30;
+  for (int bn : {256, 128}) {
+    const long long waves = ceil_div(ceil_div(g.N, 256) * ceil_div(g.M, bn), pairs);
+    const double t = 6.0 + std::max(hbm, waves * nkb * (16 + bn / 16) / (waves > 1 ? 116.0 : 105.0));
+    if (t < least) least = t, best = {true, bn, 1, false};
+  }
+  for (int bn : {128, 64, 32, 16}) {
+    if (g.b_mn && bn < 64) break;
+    if (bn > 16 && g.N <= bn / 2 && !(g.b_mn && bn == 64)) continue;  // a narrower tile holds every row
+    const long long tiles = tm * ceil_div(g.N, bn);
+    if (tiles > 16 * sms) continue;
+    for (int split = 1; split <= 8 && split * 2 <= std::max(nkb, 2ll); split *= 2) {
+      const long long ctas = tiles * split, rounds = ceil_div(ctas, 2 * sms);
+      const long long on_sm = rounds > 1 ? 2 * rounds : ceil_div(ctas, sms);
+      const double kb = static_cast<double>(on_sm) * ceil_div(nkb, split) * (16 + bn / 8);
+      const double t = 5.0 + 3.0 * (rounds - 1) + std::max(hbm, kb / (on_sm > 1 ? 135.0 : 105.0)) +
+                       (split > 1 ? 0.6 + 0.02 * bn : 0.0) + (split > 4 ? 3.0 : 0.0) +
+                       std::min<long long>(g.N, bn) / split * (g.a_mn ? 0.015 : 0.03);
+      if (t < least) least = t, best = {false, bn, split, ctas <= sms && split <= 4};
+    }
+  }
+  return best;
+}
+
+template <bool BF16, bool AT, bool BT, int BN, bool FWD>
+cudaError_t run_tile_d(const Product& g, const Epilogue& e, const Plan& p, unsigned* status, cudaStream_t s) {
+  return p.deep ? run_tile<BF16, AT, BT, BN, FWD, true>(g, e, p.split, status, s)
+                : run_tile<BF16, AT, BT, BN, FWD, false>(g, e, p.split, status, s);
+}
+template <bool BF16, bool AT, bool BT, bool FWD>
+cudaError_t run_tile_n(const Product& g, const Epilogue& e, const Plan& p, unsigned* status, cudaStream_t s) {
+  if constexpr (!BT) {
+    if (p.bn == 16) return run_tile_d<BF16, AT, BT, 16, FWD>(g, e, p, status, s);
+    if (p.bn == 32) return run_tile_d<BF16, AT, BT, 32, FWD>(g, e, p, status, s);
+  }
+  if (p.bn <= 64) return run_tile_d<BF16, AT, BT, 64, FWD>(g, e, p, status, s);
+  return run_tile_d<BF16, AT, BT, 128, FWD>(g, e, p, status, s);
+}
+
+template <bool BF16, bool AT, bool BT, int OUT>
+cudaError_t run_pair_n(const Product& g, const Epilogue& e, const Plan& p, unsigned* status, cudaStream_t s) {
+  return p.bn == 128 ? run_pair<BF16, AT, BT, OUT, 128>(g, e, status, s)
+                     : run_pair<BF16, AT, BT, OUT, 256>(g, e, status, s);
+}
 
 template <bool BF16>
 cudaError_t run_product(const Product& g, const Epilogue& e, unsigned* status, cudaStream_t s) {
-  const bool pair = use_pair(g);
+  const Plan p = plan_product(g);
   if (!g.a_mn && !g.b_mn)
-    return pair ? run_pair<BF16, false, false, kOutFwd>(g, e, status, s)
-                : run_tile<BF16, false, false, 128, true>(g, e, status, s);
+    return p.pair ? run_pair_n<BF16, false, false, kOutFwd>(g, e, p, status, s)
+                  : run_tile_n<BF16, false, false, true>(g, e, p, status, s);
   if (g.a_mn && !g.b_mn)
-    return pair ? run_pair<BF16, false, true, kOut16>(g, e, status, s)
-                : run_tile<BF16, true, false, 128, false>(g, e, status, s);
+    return p.pair ? run_pair_n<BF16, false, true, kOut16>(g, e, p, status, s)
+                  : run_tile_n<BF16, true, false, false>(g, e, p, status, s);
   if (g.a_mn && g.b_mn) {
-    if (!pair) return run_tile<BF16, true, true, 128, false>(g, e, status, s);
-    return e.out_f32 ? run_pair<BF16, true, true, kOut32>(g, e, status, s)
-                     : run_pair<BF16, true, true, kOut16>(g, e, status, s);
+    if (!p.pair) return run_tile_n<BF16, true, true, false>(g, e, p, status, s);
+    return e.out_f32 ? run_pair_n<BF16, true, true, kOut32>(g, e, p, status, s)
+                     : run_pair_n<BF16, true, true, kOut16>(g, e, p, status, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -14,6 +14,7 @@ Arguments are 2-D CUDA tensors [tokens, features] whose rows are contiguous
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import matrix_orthogonalizing_optimizer_shape_gb300 as _d3
@@ -60,23 +61,49 @@ SIGS = {
     "dion3_linear_backward": (_int, [ctypes.POINTER(_LinearGradArgs), _vp, _sz, _vp]),
 }
 
-_CODES = None
+# A call is marshalled as packed bytes in the layout of the structures above: a
+# small operator's time is its host side, and filling ctypes structures field by
+# field took longer than the rest of the call.
+_MAT = struct.Struct("@Pqi4x")
+_LINEAR = struct.Struct("@4i" + "Pqi4x" * 5 + "PqPq" * 2 + "Pi4x")
+_LINEAR_GRAD = struct.Struct("@5i4x" + "Pqi4x" * 4 + "PqPq" * 2 + "Pqi4x" * 2 + "P")
+assert (_MAT.size, _LINEAR.size, _LINEAR_GRAD.size) == tuple(map(ctypes.sizeof, (_Matrix, _LinearArgs, _LinearGradArgs)))
+_NO_MAT, _NO_PACK = (0, 0, 0), (0, 0, 0, 0)
+
+_DTYPES = {}
+_FNS = {}
+
+
+def _fn(name: str):
+    """The library's entry point, taking structures as bytes."""
+    f = _FNS.get(name)
+    if f is None:
+        res, args = SIGS[name]
+        args = [_vp if isinstance(a, type) and issubclass(a, ctypes._Pointer) else a for a in args]
+        f = _FNS[name] = ctypes.CFUNCTYPE(res, *args)((name, _d3.load_library()))
+    return f
 
 
 def _dtype(t) -> int:
     """dion3_dtype of a tensor."""
-    global _CODES
-    if _CODES is None:
+    if not _DTYPES:
         import torch
-        _CODES = {torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16}
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise ValueError(f"dtype {t.dtype} is not float32, bfloat16 or float16") from None
+        _DTYPES.update({torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"dtype {t.dtype} is not float32, bfloat16 or float16")
+    return code
 
 
-def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -> _Matrix:
-    """A 2-D CUDA tensor with contiguous rows as a dion3_matrix; shape checked where given."""
+def _stream(stream) -> Optional[int]:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    return _d3._stream(stream)
+
+
+def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -> tuple:
+    """(data, ld, dtype) of a 2-D CUDA tensor with contiguous rows; shape checked where given."""
     if not t.is_cuda:
         raise ValueError(f"{name} is not a CUDA tensor")
     shape = t.shape
@@ -93,7 +120,7 @@ def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -
         if r > 1:
             raise ValueError(f"{name}: rows overlap")
         ld = c
-    return _Matrix(t.data_ptr(), ld, _dtype(t))
+    return t.data_ptr(), ld, _dtype(t)
 
 
 def _vec(name: str, t, n: int, f32: bool = False) -> int:
@@ -109,7 +136,7 @@ class Packed8:
     uint8 scale bytes [rows, ceil(cols / 32)], rows contiguous, any row pitch
     (multiples of 16 bytes are fastest, see :func:`alloc_packed8`)."""
 
-    __slots__ = ("codes", "scales", "shape", "_c")
+    __slots__ = ("codes", "scales", "shape", "_fields", "_c")
 
     def __init__(self, codes, scales):
         import torch
@@ -128,13 +155,14 @@ class Packed8:
                 raise ValueError("the rows of codes and scales must be contiguous and not overlap")
             lds.append(max(ld, c))
         self.codes, self.scales, self.shape = codes, scales, (rows, cols)
-        self._c = _Packed8(codes.data_ptr(), lds[0], scales.data_ptr(), lds[1])
+        self._fields = (codes.data_ptr(), lds[0], scales.data_ptr(), lds[1])
+        self._c = struct.pack("@PqPq", *self._fields)
 
 
-def _packed(name: str, p: Packed8, rows: int, cols: int) -> _Packed8:
+def _packed(name: str, p: Packed8, rows: int, cols: int) -> Packed8:
     if p.shape != (rows, cols):
         raise ValueError(f"{name} is {p.shape[0]} x {p.shape[1]}, {rows} x {cols} is wanted")
-    return p._c
+    return p
 
 
 def alloc_packed8(rows: int, cols: int, device=None) -> Packed8:
@@ -157,16 +185,19 @@ def _ws(ws, nbytes):
 
 def pack8(x, out: Packed8, stream=None):
     """x [rows, cols] into 8-bit blocks (see dion3_pack8)."""
-    m = _mat("x", x)
+    m = _MAT.pack(*_mat("x", x))
     rows, cols = x.shape
-    _d3._check(_d3.load_library().dion3_pack8(rows, cols, m, _packed("out", out, rows, cols), _d3._stream(stream)))
+    _d3._check(_fn("dion3_pack8")(rows, cols, m, _packed("out", out, rows, cols)._c, _stream(stream)))
 
 
 def unpack8(src: Packed8, out, stream=None):
     """The values that 8-bit blocks stand for, in out's dtype (see dion3_unpack8)."""
     rows, cols = src.shape
-    _d3._check(_d3.load_library().dion3_unpack8(rows, cols, src._c, _mat("out", out, rows, cols),
-                                                _d3._stream(stream)))
+    _d3._check(_fn("dion3_unpack8")(rows, cols, src._c, _MAT.pack(*_mat("out", out, rows, cols)), _stream(stream)))
+
+
+def _opt(name: str, t, rows: int, cols: int):
+    return None if t is None else _MAT.pack(*_mat(name, t, rows, cols))
 
 
 def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] = None, rstd=None,
@@ -174,13 +205,12 @@ def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] 
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over each row, y
     and / or its 8-bit blocks y8, and rstd for the backward pass (see
     dion3_rms_norm)."""
-    mx = _mat("x", x)
+    mx = _MAT.pack(*_mat("x", x))
     rows, cols = x.shape
-    _d3._check(_d3.load_library().dion3_rms_norm(
-        rows, cols, mx, None if residual is None else _mat("residual", residual, rows, cols),
-        _vec("weight", weight, cols), _dtype(weight), eps, None if h is None else _mat("h", h, rows, cols),
-        None if y is None else _mat("y", y, rows, cols), None if y8 is None else _packed("y8", y8, rows, cols),
-        None if rstd is None else _vec("rstd", rstd, rows, f32=True), _d3._stream(stream)))
+    _d3._check(_fn("dion3_rms_norm")(
+        rows, cols, mx, _opt("residual", residual, rows, cols), _vec("weight", weight, cols), _dtype(weight), eps,
+        _opt("h", h, rows, cols), _opt("y", y, rows, cols), None if y8 is None else _packed("y8", y8, rows, cols)._c,
+        None if rstd is None else _vec("rstd", rstd, rows, f32=True), _stream(stream)))
 
 
 def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -194,14 +224,13 @@ def rms_norm_backward(dy, h, weight, rstd, dx, *, dh=None, dw=None, accumulate: 
     """Gradient of :func:`rms_norm`: dx (of x and the residual alike; dh is the
     gradient that reaches h from elsewhere) and dw, float32 (see
     dion3_rms_norm_backward)."""
-    mdy = _mat("dy", dy)
+    mdy = _MAT.pack(*_mat("dy", dy))
     rows, cols = dy.shape
     p, n = _ws(ws, ws_bytes)
-    _d3._check(_d3.load_library().dion3_rms_norm_backward(
-        rows, cols, mdy, _mat("h", h, rows, cols), _vec("weight", weight, cols), _dtype(weight),
-        _vec("rstd", rstd, rows, f32=True), None if dh is None else _mat("dh", dh, rows, cols),
-        _mat("dx", dx, rows, cols), None if dw is None else _vec("dw", dw, cols, f32=True), int(accumulate), p, n,
-        _d3._stream(stream)))
+    _d3._check(_fn("dion3_rms_norm_backward")(
+        rows, cols, mdy, _opt("h", h, rows, cols), _vec("weight", weight, cols), _dtype(weight),
+        _vec("rstd", rstd, rows, f32=True), _opt("dh", dh, rows, cols), _opt("dx", dx, rows, cols),
+        None if dw is None else _vec("dw", dw, cols, f32=True), int(accumulate), p, n, _stream(stream)))
 
 
 def _ws_size(fn: str, tokens, in_features, out_features, dtype, strided) -> int:
@@ -225,9 +254,6 @@ def linear_backward_workspace_size(tokens: int, in_features: int, out_features: 
     return _ws_size("dion3_linear_backward_workspace_size", tokens, in_features, out_features, dtype, strided)
 
 
-_NO_MAT, _NO_PACK = _Matrix(), _Packed8()
-
-
 def linear(x, w, y, *, bias=None, residual=None, act: int = ACT_NONE, z=None, y8: Optional[Packed8] = None, ws=None,
            ws_bytes: Optional[int] = None, stream=None):
     """y = act(x w^T + bias) + residual.  z (a tensor or a :class:`Packed8`)
@@ -240,15 +266,15 @@ def linear(x, w, y, *, bias=None, residual=None, act: int = ACT_NONE, z=None, y8
     z8 = _NO_PACK
     mz = _NO_MAT
     if isinstance(z, Packed8):
-        z8 = _packed("z", z, tokens, n)
+        z8 = _packed("z", z, tokens, n)._fields
     elif z is not None:
         mz = _mat("z", z, tokens, n)
-    args = _LinearArgs(tokens, k, n, act, mx, mw, _mat("y", y, tokens, n),
-                       _NO_MAT if residual is None else _mat("residual", residual, tokens, n), mz, z8,
-                       _NO_PACK if y8 is None else _packed("y8", y8, tokens, n),
-                       None if bias is None else _vec("bias", bias, n), 0 if bias is None else _dtype(bias))
+    args = _LINEAR.pack(tokens, k, n, act, *mx, *mw, *_mat("y", y, tokens, n),
+                        *(_NO_MAT if residual is None else _mat("residual", residual, tokens, n)), *mz, *z8,
+                        *(_NO_PACK if y8 is None else _packed("y8", y8, tokens, n)._fields),
+                        0 if bias is None else _vec("bias", bias, n), 0 if bias is None else _dtype(bias))
     p, nb = _ws(ws, ws_bytes)
-    _d3._check(_d3.load_library().dion3_linear(args, p, nb, _d3._stream(stream)))
+    _d3._check(_fn("dion3_linear")(args, p, nb, _stream(stream)))
 
 
 def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE, z=None, accumulate: bool = False,
@@ -263,16 +289,16 @@ def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE,
     k = w.shape[1]
     mx, x8, mz, z8 = _NO_MAT, _NO_PACK, _NO_MAT, _NO_PACK
     if isinstance(x, Packed8):
-        x8 = _packed("x", x, tokens, k)
+        x8 = _packed("x", x, tokens, k)._fields
     elif x is not None:
         mx = _mat("x", x, tokens, k)
     if isinstance(z, Packed8):
-        z8 = _packed("z", z, tokens, n)
+        z8 = _packed("z", z, tokens, n)._fields
     elif z is not None:
         mz = _mat("z", z, tokens, n)
-    args = _LinearGradArgs(tokens, k, n, act, int(accumulate), mdy, mw, mx, mz, x8, z8,
-                           _NO_MAT if dx is None else _mat("dx", dx, tokens, k),
-                           _NO_MAT if dw is None else _mat("dw", dw, n, k),
-                           None if db is None else _vec("db", db, n, f32=True))
+    args = _LINEAR_GRAD.pack(tokens, k, n, act, int(accumulate), *mdy, *mw, *mx, *mz, *x8, *z8,
+                             *(_NO_MAT if dx is None else _mat("dx", dx, tokens, k)),
+                             *(_NO_MAT if dw is None else _mat("dw", dw, n, k)),
+                             0 if db is None else _vec("db", db, n, f32=True))
     p, nb = _ws(ws, ws_bytes)
-    _d3._check(_d3.load_library().dion3_linear_backward(args, p, nb, _d3._stream(stream)))
+    _d3._check(_fn("dion3_linear_backward")(args, p, nb, _stream(stream)))

@@ -177,9 +177,9 @@ class Fake:
 
 
 def test_matrix_marshalling():
-    assert (lambda m: (m.ld, m.dtype))(L._mat("x", Fake((4, 8), (11, 1)))) == (11, d3.BF16)
-    assert L._mat("x", Fake((1, 8), (1, 1))).ld == 8  # the stride of a single row says nothing
-    assert L._mat("x", Fake((4, 1), (3, 9))).ld == 3  # nor does that of a single column
+    assert L._mat("x", Fake((4, 8), (11, 1))) == (FAKE, 11, d3.BF16)
+    assert L._mat("x", Fake((1, 8), (1, 1)))[1] == 8  # the stride of a single row says nothing
+    assert L._mat("x", Fake((4, 1), (3, 9)))[1] == 3  # nor does that of a single column
     for bad in (Fake((4, 8), (1, 4)), Fake((4, 8), (4, 1)), Fake((4, 8), (0, 1)), Fake((8,), (1,)),
                 Fake((4, 8), (8, 1), torch.int32)):
         with pytest.raises(ValueError):
