@@ -16,9 +16,10 @@ namespace dion3 {
 // tensor memory), and then wait in pdl_wait() until that kernel has completed
 // and its memory is visible; no global memory is touched before the wait.
 // Every kernel calls pdl_trigger() first, so a following GEMM may be scheduled
-// as soon as all of its CTAs have started.  The memory-bound kernels are
+// as soon as all of its CTAs have started.  The step's memory-bound kernels are
 // launched without the attribute (their early CTAs would sit beside a running
-// GEMM: measured slower), so for them both instructions do nothing.
+// GEMM: measured slower), so for them both instructions do nothing; the layer
+// operators' kernels all carry it.
 // DION3_PDL=0 turns the attribute off everywhere.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -70,8 +70,12 @@ struct ActGradArgs {
 };
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s);
 
-// 16-bit matrix copied to a pitch that TMA takes.
-cudaError_t launch_repitch(int rows, int cols, Mat src, Mat dst, cudaStream_t s);
+// 16-bit matrices (n = 1 or 2) copied to a pitch that TMA takes.
+struct Repitch {
+  int rows, cols;
+  Mat src, dst;
+};
+cudaError_t launch_repitch(const Repitch* jobs, int n, cudaStream_t s);
 // out[rows][cols] = 0 (32- or 16-bit elements, dense), or a 32-bit vector.
 cudaError_t launch_zero(int rows, int cols, int elem_bytes, Mat out, cudaStream_t s);
 

@@ -115,21 +115,24 @@ struct Carve {
 // An operand of a product as TMA takes it (16-byte base and pitch).
 bool tma_ready(const Mat& m) { return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0; }
 
-struct Staged {
-  Mat src, dst;
-  int rows = 0, cols = 0;
-  bool copy = false;
+// The operands of a call that have to be copied first.
+struct Staging {
+  Repitch job[2];
+  int n = 0;
+  // m as the products can read it: itself, or its copy in the workspace.
+  Mat add(Carve& c, const Mat& m, int rows, int cols) {
+    if (tma_ready(m)) return m;
+    const Mat dst{c.take(static_cast<size_t>(rows) * up8(cols) * 2), up8(cols)};
+    job[n++] = {rows, cols, m, dst};
+    return dst;
+  }
+  cudaError_t run(cudaStream_t s) const {
+    if (n == 0) return cudaSuccess;
+    double bytes = 0.0;
+    for (int i = 0; i < n; ++i) bytes += 4.0 * job[i].rows * job[i].cols;
+    return traced_launch("repitch", 0.0, bytes, s, [&] { return launch_repitch(job, n, s); });
+  }
 };
-Staged stage(Carve& c, const Mat& m, int rows, int cols) {
-  Staged s{m, m, rows, cols, !tma_ready(m)};
-  if (s.copy) s.dst = {c.take(static_cast<size_t>(rows) * up8(cols) * 2), up8(cols)};
-  return s;
-}
-cudaError_t run_stage(const Staged& g, cudaStream_t s) {
-  if (!g.copy) return cudaSuccess;
-  return traced_launch("repitch", 0.0, 4.0 * g.rows * g.cols, s,
-                       [&] { return launch_repitch(g.rows, g.cols, g.src, g.dst, s); });
-}
 
 dion3_status check_act(int32_t act) {
   return act < DION3_ACT_NONE || act > DION3_ACT_SILU ? fail(DION3_ERR_INVALID_ARG, "unknown activation %d", act)
@@ -311,22 +314,22 @@ dion3_status dion3_linear(const dion3_linear_args* g, void* ws, size_t ws_bytes,
   if (T > 0 && (g->y.data == g->x.data || g->y.data == g->w.data))
     return fail(DION3_ERR_INVALID_ARG, "y may not be x or w");
   Carve c{static_cast<char*>(ws)};
-  const Staged x = stage(c, mat(g->x), T, K), w = stage(c, mat(g->w), N, K);
+  Staging copies;
+  const Mat x = copies.add(c, mat(g->x), T, K), w = copies.add(c, mat(g->w), N, K);
   DION3_TRY(check_ws(ws, ws_bytes, T > 0 ? c.off : 0));
   DION3_TRY(check_inject());
   if (T == 0) return ok();
   unsigned* st = device_status_ptr();
   if (st == nullptr) return fail(DION3_ERR_CUDA, "cannot resolve the device status word");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  DION3_CUDA(run_stage(x, s), "repitch launch");
-  DION3_CUDA(run_stage(w, s), "repitch launch");
+  DION3_CUDA(copies.run(s), "repitch launch");
   Product p{};
   p.M = N;
   p.N = T;
   p.K = K;
   p.elem = dt;
-  p.A = w.dst;
-  p.B = x.dst;
+  p.A = w;
+  p.B = x;
   p.out = mat(g->y);
   p.out_dtype = dt;
   p.bias = g->bias;
@@ -398,13 +401,14 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
                         : nullptr;
   Mat dz = mat(g->dy);
   if (own_dz) dz = {c.take(static_cast<size_t>(T) * up8(N) * 2), up8(N)};
-  Staged x{}, w{};
+  Staging copies;
+  Mat x{}, w{};
   if (want_dw && x8) {
-    x.dst = {c.take(static_cast<size_t>(T) * up8(K) * 2), up8(K)};
+    x = {c.take(static_cast<size_t>(T) * up8(K) * 2), up8(K)};
   } else if (want_dw) {
-    x = stage(c, mat(g->x), T, K);
+    x = copies.add(c, mat(g->x), T, K);
   }
-  if (want_dx) w = stage(c, mat(g->w), N, K);
+  if (want_dx) w = copies.add(c, mat(g->w), N, K);
   DION3_TRY(check_ws(ws, ws_bytes, T > 0 ? c.off : 0));
   DION3_TRY(check_inject());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -435,14 +439,14 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
                              [&] { return launch_act_grad(a, s); }),
                "activation gradient launch");
   }
+  DION3_CUDA(copies.run(s), "repitch launch");
   if (want_dx) {
-    DION3_CUDA(run_stage(w, s), "repitch launch");
     Product p{};
     p.M = K;
     p.N = T;
     p.K = N;
     p.elem = dt;
-    p.A = w.dst;
+    p.A = w;
     p.a_mn = true;
     p.B = dz;
     p.out = mat(g->dx);
@@ -454,15 +458,14 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
   if (want_dw) {
     if (x8)
       DION3_CUDA(traced_launch("unpack8", 0.0, static_cast<double>(T) * K * (2 + 33.0 / 32), s,
-                               [&] { return launch_unpack8(T, K, pack(g->x8), dt, x.dst, s); }),
+                               [&] { return launch_unpack8(T, K, pack(g->x8), dt, x, s); }),
                  "unpack8 launch");
-    DION3_CUDA(run_stage(x, s), "repitch launch");
     Product p{};
     p.M = K;
     p.N = N;
     p.K = T;
     p.elem = dt;
-    p.A = x.dst;
+    p.A = x;
     p.a_mn = true;
     p.B = dz;
     p.b_mn = true;

@@ -1,6 +1,11 @@
 // Memory-bound kernels of the layer operators on sm_103a: 8-bit checkpoints,
 // the RMS norm with the residual's addition and its gradient, and the
 // activation's gradient with the bias gradient's column sums.
+//
+// All are launched with programmatic stream serialization like the products:
+// a kernel's blocks may be placed while the one before it drains, and read
+// nothing before it has completed (pdl_wait).  The calls of a layer's step are
+// short chains of small kernels, where that takes a microsecond or two off each.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -158,6 +163,8 @@ constexpr int kWalk = 4;
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256, 4) pack8_kernel(int rows, int cols, Mat x, Pack8 o) {
+  pdl_trigger();
+  pdl_wait();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
   const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
   for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += kWalk * step) {
@@ -175,6 +182,8 @@ __global__ void __launch_bounds__(256, 4) pack8_kernel(int rows, int cols, Mat x
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pack8 in, Mat out) {
+  pdl_trigger();
+  pdl_wait();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
   if (c >= cols) return;
   const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
@@ -204,6 +213,8 @@ constexpr int kRowThreads = 512;  // most of a row kernel's block (128 registers
 
 template <typename T, int VEC, int NV, bool RES>
 __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ float red[64];
   int flip = 0;
   const int span = blockDim.x * VEC;
@@ -261,6 +272,8 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
 // from cache.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ float red[64];
   int flip = 0;
   const int span = blockDim.x * VEC;
@@ -305,6 +318,8 @@ __device__ __forceinline__ float norm_dx(float dy, float w, float hn, float mean
 
 template <typename T, int VEC, int NV, bool DH>
 __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_grad_kernel(NormGradArgs a) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ float red[64];
   extern __shared__ float rows_sum[];  // [blockDim.y][span * NV], blockDim.y > 1
   int flip = 0;
@@ -389,6 +404,8 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1
 // The same for rows too wide for that: read twice, column sums in shared memory.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a) {
+  pdl_trigger();
+  pdl_wait();
   extern __shared__ float colsum[];
   __shared__ float red[64];
   int flip = 0;
@@ -434,6 +451,8 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
 constexpr int kChains = 32;
 __global__ void __launch_bounds__(32 * kChains) column_sum_kernel(const float* partials, int nparts, int cols,
                                                                   float* out, int accumulate) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ float red[kChains][33];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
@@ -459,6 +478,8 @@ __global__ void __launch_bounds__(32 * kChains) column_sum_kernel(const float* p
 // --------------------------------------------------------------------------
 template <typename T, int VEC, int ACT, bool Z8>
 __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ float red[8][32 * VEC];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int c = (blockIdx.x * 32 + lane) * VEC;
@@ -504,37 +525,51 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
 #pragma unroll
     for (int k = 1; k < 8; ++k) s += red[k][i];
     const int col = (blockIdx.x * 32 + i % 32) * VEC + i / 32;
-    if (col < a.cols) a.partials[static_cast<long long>(blockIdx.y) * a.cols + col] = s;
+    if (col >= a.cols) continue;
+    if (gridDim.y > 1)
+      a.partials[static_cast<long long>(blockIdx.y) * a.cols + col] = s;
+    else
+      a.db[col] = a.accumulate ? a.db[col] + s : s;
   }
 }
 
-// One element a lane, neighbouring lanes neighbouring elements: source rows may
-// start anywhere.
-__global__ void __launch_bounds__(256) repitch_kernel(int rows, int cols, const uint16_t* src, long long ld_src,
-                                                      uint16_t* dst, long long ld_dst) {
+// Copies up to two matrices (blockIdx.z).  One element a lane, neighbouring lanes
+// neighbouring elements: source rows may start anywhere.
+struct RepitchArgs {
+  Repitch job[2];
+};
+__global__ void __launch_bounds__(256) repitch_kernel(RepitchArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const Repitch& g = a.job[blockIdx.z];
+  const uint16_t* src = static_cast<const uint16_t*>(g.src.p);
+  uint16_t* dst = static_cast<uint16_t*>(g.dst.p);
   const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
   constexpr int kCols = 4;
   const int c0 = blockIdx.x * blockDim.x * kCols + threadIdx.x;
-  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += 2 * step) {
+  if (c0 >= g.cols) return;
+  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < g.rows; row += 2 * step) {
     uint16_t v[2][kCols];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const int c = c0 + j * blockDim.x;
-        if (row + i * step < rows && c < cols) v[i][j] = src[(row + i * step) * ld_src + c];
+        if (row + i * step < g.rows && c < g.cols) v[i][j] = src[(row + i * step) * g.src.ld + c];
       }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const int c = c0 + j * blockDim.x;
-        if (row + i * step < rows && c < cols) dst[(row + i * step) * ld_dst + c] = v[i][j];
+        if (row + i * step < g.rows && c < g.cols) dst[(row + i * step) * g.dst.ld + c] = v[i][j];
       }
   }
 }
 
 __global__ void __launch_bounds__(256) zero_kernel(int rows, int cols, int elem_bytes, uint8_t* out, long long ld) {
+  pdl_trigger();
+  pdl_wait();
   const long long total = static_cast<long long>(rows) * cols;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const long long r = i / cols, at = r * ld + (i - r * cols);
@@ -649,7 +684,7 @@ cudaError_t launch_pack8(int rows, int cols, int dtype, Mat x, Pack8 out, cudaSt
     using T = decltype(t);
     static std::atomic<int> cache[2][9];
     auto k = vec ? pack8_kernel<T, 8> : pack8_kernel<T, 1>;
-    return launch_kernel(false, k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, x, out);
+    return launch_kernel(pdl_enabled(), k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, x, out);
   });
 }
 
@@ -660,7 +695,7 @@ cudaError_t launch_unpack8(int rows, int cols, Pack8 in, int dtype, Mat out, cud
     using T = decltype(t);
     static std::atomic<int> cache[2][9];
     auto k = vec ? unpack8_kernel<T, 8> : unpack8_kernel<T, 1>;
-    return launch_kernel(false, k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, in, out);
+    return launch_kernel(pdl_enabled(), k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, in, out);
   });
 }
 
@@ -679,7 +714,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
     constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
     const RowShape r = row_shape(lanes, kRowThreads, MAXV);
     if (r.nv == 0)
-      return launch_kernel(false, rms_norm_wide_kernel<T, VEC>, dim3(std::min(a.rows, 2 * sm_count())), dim3(1024), 0,
+      return launch_kernel(pdl_enabled(), rms_norm_wide_kernel<T, VEC>, dim3(std::min(a.rows, 2 * sm_count())), dim3(1024), 0,
                            s, a);
     return by_nv<MAXV>(r.nv, [&](auto n) {
       constexpr int NV = decltype(n)::value;
@@ -689,7 +724,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
       const int threads = r.block.x * r.block.y;
       const long long blocks = (static_cast<long long>(a.rows) + r.block.y - 1) / r.block.y;
       const int grid = static_cast<int>(std::min<long long>(blocks, resident(k, threads, 0, cache[res])));
-      return launch_kernel(false, k, dim3(grid), r.block, 0, s, a);
+      return launch_kernel(pdl_enabled(), k, dim3(grid), r.block, 0, s, a);
     });
   };
   return by_dtype(a.dtype, [&](auto t) {
@@ -711,7 +746,7 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4);
       if (e != cudaSuccess) return e;
       parts = std::min(a.rows, sm_count());
-      return launch_kernel(false, k, dim3(parts), dim3(1024), a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0, s,
+      return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(1024), a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0, s,
                            a);
     }
     return by_nv<MAXV>(r.nv, [&](auto n) {
@@ -725,14 +760,14 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
       // One row of partials a block, as many at most as the workspace holds.
       parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
                                          static_cast<long long>(kMaxPartials)}));
-      return launch_kernel(false, k, dim3(parts), r.block, smem, s, a);
+      return launch_kernel(pdl_enabled(), k, dim3(parts), r.block, smem, s, a);
     });
   };
   const cudaError_t e = by_dtype(a.dtype, [&](auto t) {
     return vec ? run(t, std::integral_constant<int, 8>{}) : run(t, std::integral_constant<int, 1>{});
   });
   if (e != cudaSuccess || a.dw == nullptr) return e;
-  return launch_kernel(false, column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
+  return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
                        static_cast<const float*>(a.partials), parts, a.cols, a.dw, a.accumulate);
 }
 
@@ -750,25 +785,34 @@ cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s) {
                                    : (vec ? act_grad_kernel<T, 8, ACT, false> : act_grad_kernel<T, 1, ACT, false>);
         static std::atomic<int> cache[2][2][9];
         dim3 grid = walk_grid(k, a.rows, vec ? a.cols / 8 : a.cols, kWalk, cache[a.z8.q != nullptr][vec]);
-        grid.y = std::min<unsigned>(grid.y, kMaxPartials);
+        // Few rows: one block a column strip, which writes db itself (a second
+        // kernel takes longer than the rows the strip's warps walk instead).
+        grid.y = a.db != nullptr && a.rows <= 256 ? 1 : std::min<unsigned>(grid.y, kMaxPartials);
         parts = static_cast<int>(grid.y);
-        return launch_kernel(false, k, grid, dim3(256), 0, s, a);
+        return launch_kernel(pdl_enabled(), k, grid, dim3(256), 0, s, a);
       });
     }
   });
-  if (e != cudaSuccess || a.db == nullptr) return e;
-  return launch_kernel(false, column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
+  if (e != cudaSuccess || a.db == nullptr || parts == 1) return e;
+  return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
                        static_cast<const float*>(a.partials), parts, a.cols, a.db, a.accumulate);
 }
 
-cudaError_t launch_repitch(int rows, int cols, Mat src, Mat dst, cudaStream_t s) {
+cudaError_t launch_repitch(const Repitch* jobs, int n, cudaStream_t s) {
   static std::atomic<int> cache[9];
-  return launch_kernel(false, repitch_kernel, walk_grid(repitch_kernel, rows, (cols + 3) / 4, 2, cache), kWalkBlock, 0, s, rows, cols, static_cast<const uint16_t*>(src.p),
-                       src.ld, static_cast<uint16_t*>(dst.p), dst.ld);
+  RepitchArgs a{};
+  dim3 grid(1, 1, n);
+  for (int i = 0; i < n; ++i) {
+    a.job[i] = jobs[i];
+    const dim3 g = walk_grid(repitch_kernel, jobs[i].rows, (jobs[i].cols + 3) / 4, 2, cache);
+    grid.x = std::max(grid.x, g.x);
+    grid.y = std::max(grid.y, g.y);
+  }
+  return launch_kernel(pdl_enabled(), repitch_kernel, grid, kWalkBlock, 0, s, a);
 }
 
 cudaError_t launch_zero(int rows, int cols, int elem_bytes, Mat out, cudaStream_t s) {
-  return launch_kernel(false, zero_kernel, dim3(flat_grid(static_cast<long long>(rows) * cols)), dim3(256), 0, s, rows,
+  return launch_kernel(pdl_enabled(), zero_kernel, dim3(flat_grid(static_cast<long long>(rows) * cols)), dim3(256), 0, s, rows,
                        cols, elem_bytes, static_cast<uint8_t*>(out.p), out.ld);
 }
 

@@ -21,7 +21,9 @@ SLOPE, ACT_ERR = 1.13, 2.0 ** -18
 SIZES = [  # tokens, in, out
     (1, 1, 1), (1, 64, 128), (2, 7, 33), (16, 256, 100), (17, 72, 264), (33, 130, 31), (64, 512, 256), (65, 65, 129),
     (127, 1000, 96), (128, 64, 512), (129, 2047, 130), (300, 320, 257), (513, 200, 1030), (1, 4096, 1001),
-    (700, 1032, 776)]
+    (700, 1032, 776),
+    # several large tiles a cluster, in one product of the layer or another; odd widths with them
+    (2100, 72, 2050), (130, 2080, 2201), (257, 2303, 2048), (4100, 40, 300)]
 
 
 def ws_for(fn, t, k, n, dtype, strided):
