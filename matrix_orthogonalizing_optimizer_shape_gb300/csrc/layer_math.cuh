@@ -165,7 +165,7 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {  // 2^e; NaN for byte
                                                                   : __uint_as_float(byte << 23);
 }
 // Values of a block as they are coded: saturated in the one scale where that
-// can matter (a branch that ordinary blocks skip together).
+// can matter.
 template <int N>
 __device__ __forceinline__ void saturate_block(uint32_t byte, float (&v)[N]) {
   if (byte == kTopByte) {
@@ -202,6 +202,20 @@ __device__ __forceinline__ float max_mag(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
+}
+
+// The same for two packed 16-bit values each.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_mag2(uint32_t a, uint32_t b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)),
+                                  __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
 }
 
 }  // namespace lm

@@ -35,22 +35,28 @@ __device__ __forceinline__ uint32_t block_amax(const float (&v)[VEC]) {
   return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
-// Codes (and, from the block's first lane, its scale byte) of VEC columns at
-// column c of a row.  Lanes of a warp hold consecutive columns from a multiple
-// of 32; values of columns past the end are 0 and not written.
+// Codes (and, from the block's first lane, its scale byte) of VEC columns to q
+// (and sb).  Lanes of a warp hold consecutive columns from a multiple of 32;
+// `in` is false past the last column, where the values are 0.  amax: the bits
+// of the block's largest magnitude.  Called by all lanes of a warp together.
 template <int VEC>
-__device__ __forceinline__ void store_block(const Pack8& o, long long row, int c, int cols, float (&v)[VEC]) {
-  const uint32_t byte = scale_byte(block_amax<VEC>(v));
+__device__ __forceinline__ void store_block(int8_t* q, uint8_t* sb, bool in, bool first, uint32_t amax,
+                                            float (&v)[VEC]) {
+  const uint32_t byte = scale_byte(amax);
   const float inv = inv_scale(byte);
-  saturate_block(byte, v);
-  if (c >= cols) return;
-  int8_t* q = o.q + row * o.ldq + c;
+  if (__any_sync(0xffffffffu, byte == kTopByte)) saturate_block(byte, v);  // skipped by the whole warp
+  if (!in) return;
   if constexpr (VEC == 8)
     *reinterpret_cast<uint2*>(q) =
         make_uint2(codes4(v[0], v[1], v[2], v[3], inv), codes4(v[4], v[5], v[6], v[7], inv));
   else
     *q = static_cast<int8_t>(code_of(v[0], inv));
-  if (c % kPackBlock == 0) o.s[row * o.lds + c / kPackBlock] = static_cast<uint8_t>(byte);
+  if (first) *sb = static_cast<uint8_t>(byte);
+}
+template <int VEC>
+__device__ __forceinline__ void store_block(const Pack8& o, long long row, int c, int cols, float (&v)[VEC]) {
+  store_block<VEC>(o.q + row * o.ldq + c, o.s + row * o.lds + c / kPackBlock, c < cols, c % kPackBlock == 0,
+                   block_amax<VEC>(v), v);
 }
 
 // Raw codes and scale byte of VEC columns, and their values.
@@ -58,14 +64,13 @@ template <int VEC>
 struct Codes {
   uint2 w;
   uint32_t byte;
-  __device__ __forceinline__ void load(const Pack8& p, long long row, int c, int cols) {
-    if (c >= cols) return;
-    const int8_t* q = p.q + row * p.ldq + c;
+  __device__ __forceinline__ void load(const int8_t* q, const uint8_t* s, bool in) {
+    if (!in) return;
     if constexpr (VEC == 8)
       w = *reinterpret_cast<const uint2*>(q);
     else
       w.x = static_cast<uint32_t>(static_cast<uint8_t>(*q));
-    byte = p.s[row * p.lds + c / kPackBlock];
+    byte = *s;
   }
   __device__ __forceinline__ void values(float (&v)[VEC]) const {
     const float sc = scale_of(byte);
@@ -94,12 +99,14 @@ struct Raw {
   static constexpr int kWords = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(T)) / 4;
   uint32_t w[kWords];
   __device__ __forceinline__ void load(const Mat& m, long long row, int c, int cols) {
-    if (c >= cols) {
+    load(static_cast<const T*>(m.p) + row * m.ld + c, c < cols);
+  }
+  __device__ __forceinline__ void load(const T* p, bool in) {
+    if (!in) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) w[i] = 0u;
       return;
     }
-    const T* p = static_cast<const T*>(m.p) + row * m.ld + c;
     if constexpr (VEC == 1) {
       if constexpr (sizeof(T) == 2)
         w[0] = *reinterpret_cast<const uint16_t*>(p);
@@ -130,6 +137,22 @@ struct Raw {
     }
   }
 };
+// Bits of the block's largest magnitude, from the elements as loaded.
+template <typename T, int VEC>
+__device__ __forceinline__ uint32_t raw_amax(const Raw<T, VEC>& r) {
+  if constexpr (VEC == 8 && sizeof(T) == 2) {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    uint32_t m = max_mag2<kBf>(max_mag2<kBf>(r.w[0], r.w[1]), max_mag2<kBf>(r.w[2], r.w[3]));
+    m = max_mag2<kBf>(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_mag2<kBf>(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float2 f = unpack2<kBf>(m);
+    return __float_as_uint(max_mag(f.x, f.y)) & 0x7FFFFFFFu;
+  } else {
+    float v[VEC];
+    r.values(v);
+    return block_amax<VEC>(v);
+  }
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void load_cols(const Mat& m, long long row, int c, int cols, float (&v)[VEC]) {
   Raw<T, VEC> raw;
@@ -137,8 +160,9 @@ __device__ __forceinline__ void load_cols(const Mat& m, long long row, int c, in
   raw.values(v);
 }
 
-// Sum over the CTA, the same bits in every thread (blockDim.x a multiple of
-// 32).  `red` alternates between two halves so one barrier a call is enough.
+// Sum over the threads of a row (blockDim.x, a multiple of 32), the same bits in
+// every one.  `red` (16-byte aligned) alternates between two halves so one
+// barrier a call is enough; every thread adds the warps' sums itself.
 __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -148,9 +172,11 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
   flip ^= 1;
   if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = v;
   __syncthreads();
-  v = threadIdx.x % 32 < nw ? r[threadIdx.x % 32] : 0.f;
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  v = 0.f;
+  for (int w = 0; w < nw; w += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(r + w);
+    v += x.x + (w + 1 < nw ? x.y : 0.f) + (w + 2 < nw ? x.z : 0.f) + (w + 3 < nw ? x.w : 0.f);
+  }
   return v;
 }
 
@@ -166,16 +192,22 @@ __global__ void __launch_bounds__(256, 4) pack8_kernel(int rows, int cols, Mat x
   pdl_trigger();
   pdl_wait();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
-  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
-  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += kWalk * step) {
+  const int step = gridDim.y * blockDim.y;
+  int row = blockIdx.y * blockDim.y + threadIdx.y;
+  const T* px = static_cast<const T*>(x.p) + row * x.ld + c;
+  int8_t* pq = o.q + row * o.ldq + c;
+  uint8_t* ps = o.s + row * o.lds + c / kPackBlock;
+  const long long dx = step * x.ld, dq = step * o.ldq, ds = step * o.lds;
+  const bool first = c % kPackBlock == 0;
+  for (; row < rows; row += kWalk * step) {
     Raw<T, VEC> raw[kWalk];
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i) raw[i].load(x, row + i * step, row + i * step < rows ? c : cols, cols);
+    for (int i = 0; i < kWalk; ++i, px += dx) raw[i].load(px, c < cols && row + i * step < rows);
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i) {
+    for (int i = 0; i < kWalk; ++i, pq += dq, ps += ds) {
       float v[VEC];
       raw[i].values(v);
-      store_block<VEC>(o, row + i * step, row + i * step < rows ? c : cols, cols, v);
+      store_block<VEC>(pq, ps, c < cols && row + i * step < rows, first, raw_amax(raw[i]), v);
     }
   }
 }
@@ -186,18 +218,22 @@ __global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pac
   pdl_wait();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
   if (c >= cols) return;
-  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
-  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < rows; row += kWalk * step) {
+  const int step = gridDim.y * blockDim.y;
+  int row = blockIdx.y * blockDim.y + threadIdx.y;
+  const int8_t* pq = in.q + row * in.ldq + c;
+  const uint8_t* ps = in.s + row * in.lds + c / kPackBlock;
+  T* po = static_cast<T*>(out.p) + row * out.ld + c;
+  const long long dq = step * in.ldq, ds = step * in.lds, dst = step * out.ld;
+  for (; row < rows; row += kWalk * step) {
     Codes<VEC> q[kWalk];
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i)
-      if (row + i * step < rows) q[i].load(in, row + i * step, c, cols);
+    for (int i = 0; i < kWalk; ++i, pq += dq, ps += ds) q[i].load(pq, ps, row + i * step < rows);
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i) {
+    for (int i = 0; i < kWalk; ++i, po += dst) {
       if (row + i * step >= rows) break;
       float v[VEC];
       q[i].values(v);
-      store_cols<T, VEC>(out, row + i * step, c, cols, v);
+      store_vec<T, VEC>(po, v);
     }
   }
 }
@@ -215,8 +251,9 @@ template <typename T, int VEC, int NV, bool RES>
 __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float red[64];
+  __shared__ __align__(16) float red[64];
   int flip = 0;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
   float w[NV][VEC];
 #pragma unroll
@@ -254,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
     }
     load_row(row + step);
     ss = cta_sum(ss, red, flip);
-    const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -274,8 +311,9 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float red[64];
+  __shared__ __align__(16) float red[64];
   int flip = 0;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
   const int padded = (a.cols + span - 1) / span * span;
   auto load_h = [&](long long row, int c, float (&v)[VEC]) {
@@ -295,7 +333,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
       for (int j = 0; j < VEC; ++j) ss = fmaf(v[j], v[j], ss);
     }
     ss = cta_sum(ss, red, flip);
-    const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int c = threadIdx.x * VEC; c < padded; c += span) {
       load_h(row, c, v);
@@ -320,9 +358,10 @@ template <typename T, int VEC, int NV, bool DH>
 __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_grad_kernel(NormGradArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float red[64];
+  __shared__ __align__(16) float red[64];
   extern __shared__ float rows_sum[];  // [blockDim.y][span * NV], blockDim.y > 1
   int flip = 0;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
   float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
@@ -366,7 +405,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1
       }
     }
     load_row(row + step);
-    s = cta_sum(s, red, flip) / static_cast<float>(a.cols);
+    s = cta_sum(s, red, flip) * inv_cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float d[VEC] = {};
@@ -407,8 +446,9 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
   pdl_trigger();
   pdl_wait();
   extern __shared__ float colsum[];
-  __shared__ float red[64];
+  __shared__ __align__(16) float red[64];
   int flip = 0;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
   if (a.dw != nullptr)
     for (int c = threadIdx.x * VEC; c < a.cols; c += span)
@@ -424,7 +464,7 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
       for (int j = 0; j < VEC; ++j)
         s = fmaf(__fmul_rn(dy[j], load_w(a.w, a.w_dtype, c + j)), __fmul_rn(h[j], rstd), s);
     }
-    s = cta_sum(s, red, flip) / static_cast<float>(a.cols);
+    s = cta_sum(s, red, flip) * inv_cols;
     for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
       float d[VEC];
       load_cols<T, VEC>(a.dy, row, c, a.cols, dy);
@@ -483,23 +523,31 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
   __shared__ float red[8][32 * VEC];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int c = (blockIdx.x * 32 + lane) * VEC;
-  const long long step = static_cast<long long>(gridDim.y) * 8;
+  const int step = gridDim.y * 8;
+  int row = blockIdx.y * 8 + w;
+  const T* py = static_cast<const T*>(a.dy.p) + row * a.dy.ld + c;
+  const T* pz = static_cast<const T*>(a.z.p) + row * a.z.ld + c;
+  const int8_t* pq = a.z8.q + row * a.z8.ldq + c;
+  const uint8_t* ps = a.z8.s + row * a.z8.lds + c / kPackBlock;
+  T* pd = static_cast<T*>(a.dz.p) + row * a.dz.ld + c;
+  const long long sy = step * a.dy.ld, sz = step * a.z.ld, sq = step * a.z8.ldq, ss = step * a.z8.lds,
+                  sd = step * a.dz.ld;
   float sum[VEC] = {};
-  for (long long row = blockIdx.y * 8 + w; row < a.rows; row += kWalk * step) {
+  for (; row < a.rows && c < a.cols; row += kWalk * step) {
     Raw<T, VEC> dy[kWalk], z[ACT != kActNone && !Z8 ? kWalk : 1];
     Codes<VEC> z8[Z8 ? kWalk : 1];
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i) {
-      const int ci = row + i * step < a.rows ? c : a.cols;
-      dy[i].load(a.dy, row + i * step, ci, a.cols);
+    for (int i = 0; i < kWalk; ++i, py += sy, pz += sz, pq += sq, ps += ss) {
+      const bool in = row + i * step < a.rows;
+      dy[i].load(py, in);
       if constexpr (ACT != kActNone && Z8)
-        z8[i].load(a.z8, row + i * step, ci, a.cols);
+        z8[i].load(pq, ps, in);
       else if constexpr (ACT != kActNone)
-        z[i].load(a.z, row + i * step, ci, a.cols);
+        z[i].load(pz, in);
     }
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i) {
-      if (row + i * step >= a.rows || c >= a.cols) break;
+    for (int i = 0; i < kWalk; ++i, pd += sd) {
+      if (row + i * step >= a.rows) break;
       float d[VEC];
       dy[i].values(d);
       if constexpr (ACT != kActNone) {
@@ -511,7 +559,7 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) d[j] = __fmul_rn(d[j], act_grad<ACT>(t[j]));
       }
-      if (a.dz.p) store_cols<T, VEC>(a.dz, row + i * step, c, a.cols, d);
+      if (a.dz.p) store_vec<T, VEC>(pd, d);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) sum[j] += d[j];
     }
@@ -617,19 +665,24 @@ cudaError_t by_dtype(int dtype, F&& f) {
   return f(__half{});
 }
 
-// Row kernels: pieces a thread (NV), lanes along a row and rows of a block.
+// Row kernels: pieces a thread (NV), lanes along a row and rows of a block; at
+// most few_threads lanes if that can be.  The gradient does best with 256 (its
+// row sum is spread over fewer warps: 16384 x 4096 in 95 us against 114 with
+// 512), the forward kernel with as many as there are (100 us against 103).
 struct RowShape {
   int nv = 0;  // 0: too wide
   dim3 block;
 };
-RowShape row_shape(int lanes, int max_threads, int max_nv) {
+RowShape row_shape(int lanes, int few_threads, int max_threads, int max_nv) {
   RowShape r;
-  for (int nv = 1; nv <= max_nv; nv *= 2) {
-    const int tx = ((lanes + nv - 1) / nv + 31) / 32 * 32;
-    if (tx > max_threads) continue;
-    r.nv = nv;
-    r.block = dim3(tx, tx == 32 ? 4 : 1);
-    return r;
+  for (int most : {few_threads, max_threads}) {
+    for (int nv = 1; nv <= max_nv; nv *= 2) {
+      const int tx = ((lanes + nv - 1) / nv + 31) / 32 * 32;
+      if (tx > most) continue;
+      r.nv = nv;
+      r.block = dim3(tx, tx == 32 ? 4 : 1);
+      return r;
+    }
   }
   return r;
 }
@@ -712,7 +765,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
   auto run = [&](auto t, auto v) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
-    const RowShape r = row_shape(lanes, kRowThreads, MAXV);
+    const RowShape r = row_shape(lanes, kRowThreads, kRowThreads, MAXV);
     if (r.nv == 0)
       return launch_kernel(pdl_enabled(), rms_norm_wide_kernel<T, VEC>, dim3(std::min(a.rows, 2 * sm_count())), dim3(1024), 0,
                            s, a);
@@ -740,7 +793,7 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   auto run = [&](auto t, auto v) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
-    const RowShape r = row_shape(lanes, kRowThreads, MAXV);
+    const RowShape r = row_shape(lanes, 256, kRowThreads, MAXV);
     if (r.nv == 0) {
       auto k = rms_norm_grad_wide_kernel<T, VEC>;
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4);
