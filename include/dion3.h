@@ -577,6 +577,8 @@ dion3_status dion3_linear(const dion3_linear_args* args, void* ws, size_t ws_byt
  *            the layer's dtype, any pitch (dense: a dion3_group gradient);
  *            db is fp32.  accumulate != 0: dw += and db +=, each sum formed in
  *            fp32 and rounded once.
+ * A fp32 dw over more than 4096 tokens is summed in pieces of 4096 (the tensor
+ * cores' fp32 sums truncate; relative error about 4e-6).
  * Without an activation the products read dy itself; with one, dz is rounded
  * to the layer's 16-bit type, which the tensor cores take, while db sums the
  * unrounded dz.

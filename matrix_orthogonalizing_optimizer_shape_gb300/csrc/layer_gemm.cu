@@ -317,6 +317,16 @@ constexpr int kBand = 8;  // row tiles walked together, column by column: operan
 
 enum PairOut : int { kOutFwd = 0, kOut16 = 1, kOut32 = 2 };
 
+// A 32-bit result is summed in pieces of kPiece K slabs: the tensor cores
+// truncate each addition to the accumulator, an error that grows with their
+// number (relative 1.9e-5 over 16384 tokens in one piece, 4.4e-6 over 4096,
+// 1.0e-6 over 1024).  The pieces of a tile follow each other in the same
+// cluster; the first is stored and the others are added to it in place, rounded
+// to nearest, by bulk reductions that find the tile in L2.  Their traffic is why
+// a piece is no shorter: dW of 16384 x 4096 x 11008 takes 818 us in one piece and
+// 1060 in pieces of 16 slabs.  A 16-bit result does not show the error.
+constexpr int kPiece = 64;
+
 struct PairParams {
   int rows, cols, nkb;         // output rows and columns, K slabs
   int tiles_r, tiles_c;        // tiles of 256 rows
@@ -535,6 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   const int total = p.tiles_r * p.tiles_c;
+  const int depth = OUT == kOut32 ? kPiece : p.nkb;  // K slabs of one accumulation
   if (threadIdx.x == 0) {
     prefetch_map(&tmA);
     prefetch_map(&tmB);
@@ -599,12 +610,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
       constexpr uint32_t id = instr_desc<BF16, AT, BT>(256, PN);
       uint32_t kc = 0, tc = 0;
       bool ok = true;
-      for (int u = cluster; u < total && ok; u += nclusters, ++tc) {
+      for (int u = cluster, kb0 = 0; u < total && ok; ++tc) {
         const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
         if (!mbar_wait_warp(bar_tempty + 8 * acc, aph ^ 1u, p.status)) break;
         fence_after();
         const uint32_t d = tmem + acc * PN;
-        for (int kb = 0; kb < p.nkb; ++kb, ++kc) {
+        const int kb1 = min(p.nkb, kb0 + depth);
+        for (int kb = kb0; kb < kb1; ++kb, ++kc) {
           const uint32_t s = kc % C::kStages, ph = (kc / C::kStages) & 1u;
           if (!(ok = mbar_wait_warp(bar_full + 8 * s, ph, p.status))) break;
           fence_after();
@@ -612,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16<2>(d, da + kDescStep<AT> * kk, db + kDescStep<BT> * kk, id, (kb > 0 || kk > 0) ? 1u : 0u);
+              mma_f16<2>(d, da + kDescStep<AT> * kk, db + kDescStep<BT> * kk, id, (kb > kb0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(bar_empty + 8 * s, 0x3);
           }
           __syncwarp();
@@ -620,6 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
         if (!ok) break;
         if (elect_one()) mma_commit_pair(bar_tfull + 8 * acc, 0x3);
         __syncwarp();
+        kb0 = kb1;
+        if (kb0 == p.nkb) kb0 = 0, u += nclusters;
       }
       // All MMAs have completed before TMEM is freed.
       if (elect_one()) mma_commit_pair(bar_drain, 0x1);
@@ -638,10 +652,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
         OUT == kOutFwd ? e.res : (OUT == kOut16 && e.accumulate ? static_cast<const uint16_t*>(e.out) : nullptr);
     const long long ld_add = OUT == kOutFwd ? e.ld_res : e.ld_out;
     uint32_t tc = 0;
-    for (int u = cluster; u < total; u += nclusters, ++tc) {
+    for (int u = cluster, kb0 = 0; u < total; ++tc) {
       int R, Cc;
       pair_tile(p, u, R, Cc);
       const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
+      const bool add = OUT == kOut32 && (e.accumulate != 0 || kb0 > 0);
       const int row0 = R * 256 + static_cast<int>(rank) * 128 + quad * 32, r = row0 + lane;
       const int cbase = Cc * PN + col_lo;
       const int nch = row0 < p.rows ? min(PN / 64, (p.cols - cbase + 31) / 32) : 0;  // chunks with something to write
@@ -650,6 +665,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
       if (nch > 0) piece.load(addend, ld_add, p, r, cbase);
       if (!mbar_wait_warp(bar_tfull + 8 * acc, aph, p.status)) break;
       fence_after();
+      // The previous piece of this tile is in place before this one is added.
+      if (OUT == kOut32 && kb0 > 0 && lane == 0) bulk_wait_all();
       uint32_t v[32];
       if (nch > 0) {
         tmem_ld32(tb, v);
@@ -685,9 +702,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(f[16 * h + j]);
             if (p.tma_out)
-              st.store(&tmOut, w, c0 + 16 * h, row0, e.accumulate != 0);
+              st.store(&tmOut, w, c0 + 16 * h, row0, add);
             else
-              st.store_plain<4>(e.out, e.ld_out, p.rows, p.cols, w, c0 + 16 * h, row0, e.accumulate != 0);
+              st.store_plain<4>(e.out, e.ld_out, p.rows, p.cols, w, c0 + 16 * h, row0, add);
           }
         } else {
           to_words<BF16>(f, w);
@@ -704,6 +721,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
       }
       fence_before();
       mbar_arrive_remote_cta(map_to_rank(bar_tempty + 8 * acc, 0));
+      kb0 += depth;
+      if (kb0 >= p.nkb) kb0 = 0, u += nclusters;
     }
     // Every bulk store has read its box before shared memory goes away.
     if (lane == 0) bulk_wait_read<0>();

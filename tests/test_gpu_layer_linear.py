@@ -226,3 +226,30 @@ def test_linear_parts_match_the_whole(cuda_lib):
         g.replay()
     assert torch.equal(a, dx) and torch.equal(b, dw) and torch.equal(c, db)
     assert float(np.abs(act_ref("silu", host(z))).max()) > 0 and dact_ref("none", host(z)).all()
+
+
+@pytest.mark.parametrize("grad,pad", [("f32", 0), ("f32", 1), ("bf16", 0), ("bf16", 3)])
+def test_weight_gradient_over_many_tokens(cuda_lib, grad, pad):
+    """A 32-bit gradient is summed in pieces over the tokens; written, then added to."""
+    t, k, n = 9000, 2080, 2201
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(t, k, generator=g, device="cuda").bfloat16()
+    dy = torch.randn(t, n, generator=g, device="cuda").bfloat16()
+    w = torch.zeros(n, k, dtype=torch.bfloat16, device="cuda")
+    dw, buf = out(n, k, grad, pad)
+    ws = ws_for(d3.linear_backward_workspace_size, t, k, n, "bf16", False)
+    want, size = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+    d3.linear_backward(dy, x, w, dw=dw, ws=ws)
+    d3.device_status()
+    tol = size * sum_bound(t) + want.abs() * (U[grad] * 1.01)
+    assert bool(((dw.double() - want).abs() <= tol).all()) and untouched(dw, buf)
+    # 9000 tokens in 3 pieces of at most 64 x 4 accumulations: 2^-23 of a partial sum each, whose
+    # root mean square grows to the result's
+    if grad == "f32":
+        assert float((dw.double() - want).norm() / want.norm()) <= 256 * 2.0 ** -23
+    first = dw.clone()
+    d3.linear_backward(dy, x, w, dw=dw, ws=ws)
+    assert torch.equal(dw, first), "the same bits every call"
+    d3.linear_backward(dy, x, w, dw=dw, ws=ws, accumulate=True)
+    tol = size * sum_bound(t) + (want.abs() + first.double().abs()) * (U[grad] * 1.01)
+    assert bool(((dw.double() - first.double() - want).abs() <= tol).all()) and untouched(dw, buf)
