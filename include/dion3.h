@@ -573,8 +573,8 @@ dion3_status dion3_linear(const dion3_linear_args* args, void* ws, size_t ws_byt
  *            activation.
  *   x or x8  the layer's input, exactly one of them (with dw only).  The
  *            product with x8 is that of the values the blocks stand for.
- *   dx, dw, db  each may be absent.  dw [out_features][in_features] is fp32 or
- *            the layer's dtype, any pitch (dense: a dion3_group gradient);
+ *   dx, dw, db  each may be absent.  dw [out_features][in_features] has any
+ *            dtype and pitch (dense bf16 or fp32: a dion3_group gradient);
  *            db is fp32.  accumulate != 0: dw += and db +=, each sum formed in
  *            fp32 and rounded once.
  * A fp32 dw over more than 4096 tokens is summed in pieces of 4096 (the tensor

@@ -90,7 +90,7 @@ struct Product {
   int elem;                   // kBF16 or kF16: operands, 16-bit outputs, residual
   Mat A, B;
   bool a_mn, b_mn;
-  Mat out; int out_dtype;     // elem or kF32
+  Mat out; int out_dtype;     // elem; of a gradient (a_mn, b_mn) any dtype
   int accumulate;             // out += ...
   // Forward epilogue: z = v + bias, out = act(z) + residual.
   const void* bias; int bias_dtype;

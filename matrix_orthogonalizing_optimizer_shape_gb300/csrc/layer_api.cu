@@ -370,8 +370,7 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
   DION3_TRY(check_mat("w", g->w, N, K, dt));
   if (want_dx) DION3_TRY(check_mat("dx", g->dx, T, K, dt));
   if (want_dw) {
-    if (g->dw.dtype != DION3_F32 && g->dw.dtype != dt)
-      return fail(DION3_ERR_INVALID_ARG, "dw has dtype %d: fp32 or the layer's type is wanted", g->dw.dtype);
+    if (!known_dtype(g->dw.dtype)) return fail(DION3_ERR_INVALID_ARG, "dw: unknown dtype %d", g->dw.dtype);
     DION3_TRY(check_mat("dw", g->dw, N, K, g->dw.dtype));
     if (x8 && g->x.data != nullptr) return fail(DION3_ERR_INVALID_ARG, "x and x8 are both given");
     if (x8) {

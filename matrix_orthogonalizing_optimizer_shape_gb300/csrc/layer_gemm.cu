@@ -34,7 +34,7 @@ constexpr int BK = 64;  // 16-bit elements of one 128-byte swizzle row
 
 struct Epilogue {
   int M, N;
-  void* out; long long ld_out; int out_f32, accumulate;
+  void* out; long long ld_out; int out_f32, out_bf16, accumulate;
   const void* bias; int bias_dtype;
   int act;
   const uint16_t* res; long long ld_res;
@@ -125,11 +125,14 @@ __device__ __forceinline__ void epilogue_rows(const Epilogue& e, int t0, int m, 
     uint16_t* p = static_cast<uint16_t*>(e.out) + o;
     if (e.accumulate) {
 #pragma unroll
-      for (int j = 0; j < C; ++j) v[j] += j < nw ? unpack1<BF16>(p[j * e.ld_out]) : 0.f;
+      for (int j = 0; j < C; ++j) {
+        const uint16_t old = j < nw ? p[j * e.ld_out] : uint16_t(0);
+        v[j] += e.out_bf16 ? unpack1<true>(old) : unpack1<false>(old);
+      }
     }
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      if (j < nw) p[j * e.ld_out] = pack1<BF16>(v[j]);
+      if (j < nw) p[j * e.ld_out] = e.out_bf16 ? pack1<true>(v[j]) : pack1<false>(v[j]);
   }
 }
 
@@ -315,7 +318,8 @@ constexpr int kPairEpiWarps = 8;
 constexpr int kBox = 2048;  // staging box: 32 rows of 64 bytes
 constexpr int kBand = 8;  // row tiles walked together, column by column: operand panels shared through L2
 
-enum PairOut : int { kOutFwd = 0, kOut16 = 1, kOut32 = 2 };
+// kOutOther: 16 bits, of the type that the operands do not have.
+enum PairOut : int { kOutFwd = 0, kOut16 = 1, kOut32 = 2, kOutOther = 3 };
 
 // A 32-bit result is summed in pieces of kPiece K slabs: the tensor cores
 // truncate each addition to the accumulator, an error that grows with their
@@ -644,12 +648,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
     const int quad = warp % 4;
     const int col_lo = ((warp - 2) / 4) * (PN / 2);
     const Epilogue& e = p.e;
+    constexpr bool kOutBf = OUT == kOutOther ? !BF16 : BF16;
     Stager st{staging + static_cast<uint32_t>(warp - 2) * 2 * kBox, 0u, lane,
               p.tma_out && (e.z == nullptr || p.tma_z)};
     // What is added to the row before it is rounded: the residual, or the
     // output itself.
     const uint16_t* addend =
-        OUT == kOutFwd ? e.res : (OUT == kOut16 && e.accumulate ? static_cast<const uint16_t*>(e.out) : nullptr);
+        OUT == kOutFwd ? e.res : (OUT != kOut32 && e.accumulate ? static_cast<const uint16_t*>(e.out) : nullptr);
     const long long ld_add = OUT == kOutFwd ? e.ld_res : e.ld_out;
     uint32_t tc = 0;
     for (int u = cluster, kb0 = 0; u < total; ++tc) {
@@ -695,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
           if (e.z8.q != nullptr && r < p.rows) store_block_row(e.z8, r, c0, p.cols, f);
           apply_act(e.act, f);
         }
-        if (addend != nullptr && r < p.rows) piece.add<BF16>(f);
+        if (addend != nullptr && r < p.rows) piece.add<kOutBf>(f);
         if constexpr (OUT == kOut32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // 16 columns a box
@@ -707,7 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PN>::kThread
               st.store_plain<4>(e.out, e.ld_out, p.rows, p.cols, w, c0 + 16 * h, row0, add);
           }
         } else {
-          to_words<BF16>(f, w);
+          to_words<kOutBf>(f, w);
           if (p.tma_out)
             st.store(&tmOut, w, c0, row0, false);
           else
@@ -839,7 +844,7 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   p.nkb = (g.K + BK - 1) / BK;
   p.tiles_r = (g.N + 255) / 256;
   p.tiles_c = (g.M + PN - 1) / PN;
-  p.tma_out = store_map(&to, e.out, e.ld_out, g.N, g.M, e.out_f32 ? static_cast<int>(kF32) : g.elem);
+  p.tma_out = store_map(&to, e.out, e.ld_out, g.N, g.M, g.out_dtype);
   p.tma_z = store_map(&tz, e.z, e.ld_z, g.N, g.M, g.elem);
   const uintptr_t add = reinterpret_cast<uintptr_t>(OUT == kOutFwd ? static_cast<const void*>(e.res) : e.out);
   p.vec_res = add % 16 == 0 && (OUT == kOutFwd ? e.ld_res : e.ld_out) % 8 == 0;
@@ -978,8 +983,9 @@ cudaError_t run_product(const Product& g, const Epilogue& e, unsigned* status, c
                   : run_tile_n<BF16, true, false, false>(g, e, p, status, s);
   if (g.a_mn && g.b_mn) {
     if (!p.pair) return run_tile_n<BF16, true, true, false>(g, e, p, status, s);
-    return e.out_f32 ? run_pair_n<BF16, true, true, kOut32>(g, e, p, status, s)
-                     : run_pair_n<BF16, true, true, kOut16>(g, e, p, status, s);
+    if (e.out_f32) return run_pair_n<BF16, true, true, kOut32>(g, e, p, status, s);
+    return g.out_dtype == g.elem ? run_pair_n<BF16, true, true, kOut16>(g, e, p, status, s)
+                                 : run_pair_n<BF16, true, true, kOutOther>(g, e, p, status, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -993,6 +999,7 @@ cudaError_t launch_product(const Product& g, unsigned* status, cudaStream_t s) {
   e.out = g.out.p;
   e.ld_out = g.out.ld;
   e.out_f32 = g.out_dtype == kF32;
+  e.out_bf16 = g.out_dtype == kBF16;
   e.accumulate = g.accumulate;
   e.bias = g.bias;
   e.bias_dtype = g.bias_dtype;

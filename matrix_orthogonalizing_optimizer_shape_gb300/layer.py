@@ -279,8 +279,8 @@ def linear(x, w, y, *, bias=None, residual=None, act: int = ACT_NONE, z=None, y8
 
 def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE, z=None, accumulate: bool = False,
                     ws=None, ws_bytes: Optional[int] = None, stream=None):
-    """Gradient of :func:`linear` from dy: dx, dw (float32 or the layer's dtype)
-    and db (float32), those that are given.  x and z are tensors or
+    """Gradient of :func:`linear` from dy: dx, dw (any dtype) and db (float32),
+    those that are given.  x and z are tensors or
     :class:`Packed8` checkpoints; ``accumulate`` adds to dw and db (see
     dion3_linear_backward)."""
     mdy = _mat("dy", dy)

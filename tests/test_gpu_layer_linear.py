@@ -86,7 +86,7 @@ def test_linear_backward(cuda_lib, dtype, t, k, n, form):
         x, z, hx, hz = x8, z8, pack_host(x8), pack_host(z8)
         if dtype == "f16":  # a block's value in fp16
             hx = torch.from_numpy(hx).half().double().numpy()
-    grad = "f32" if (t + n) % 2 else dtype
+    grad = ("f32", "bf16", "f16")[(t + n + len(form)) % 3]
     dx, dxbuf = out(t, k, dtype, pad, shift)
     dw, dwbuf = out(n, k, grad, pad, shift)
     db = torch.full((n,), 3.0, device="cuda")

@@ -64,7 +64,7 @@ def test_linear_refuses(lib, kw, status, word):
 
 @pytest.mark.parametrize("kw,status,word", [
     (dict(tokens=-5), INV, b"rows"), (dict(act=9), INV, b"activation"), (dict(w=M(dtype=d3.F32)), UNS, b"fp32"),
-    (dict(dw=M(dtype=d3.F16)), INV, b"dw"), (dict(x=L._Matrix()), INV, b"x is NULL"),
+    (dict(dw=M(dtype=5)), INV, b"dw"), (dict(x=L._Matrix()), INV, b"x is NULL"),
     (dict(x8=P()), INV, b"x and x8"), (dict(act=1), INV, b"z is NULL"), (dict(act=1, z=M(), z8=P()), INV, b"z and z8"),
     (dict(dx=M()), INV, b"dx may not be dy"), (dict(db=FAKE + 2), INV, b"db"), (dict(act=2, z=M()), WS, b"NULL"),
     (dict(x=L._Matrix(), x8=P(lds=1)), INV, b"x8"), (dict(dy=M(ld=60)), INV, b"dy"),
