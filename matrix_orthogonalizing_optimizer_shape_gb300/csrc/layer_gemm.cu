@@ -406,23 +406,26 @@ struct Stager {
                                               int x, int y, bool add) {
     const uint32_t b = fill(w);
     __syncwarp();
-    constexpr int kCols = 64 / BYTES, kRows = 32 / kCols;  // rows a pass
-    const int c = lane % kCols;
-#pragma unroll 4
-    for (int r0 = 0; r0 < 32; r0 += kRows) {
-      const int r = r0 + lane / kCols;
-      const uint32_t at = b + r * 64 + ((((c * BYTES) >> 4) ^ ((r >> 1) & 3)) << 4) + ((c * BYTES) & 15);
-      if (y + r < rows && x + c < cols) {
-        const long long o = static_cast<long long>(y + r) * ld + x + c;
+    constexpr int kCols = 64 / BYTES, kPass = 32 / kCols;  // columns of the box, rows a pass
+    const int c = lane % kCols, r0 = lane / kCols, n = x + c < cols ? rows - y - r0 : 0;
+    const uint32_t sw = static_cast<uint32_t>(c * BYTES), at = b + r0 * 64;
+    uint8_t* d = static_cast<uint8_t*>(out) + (static_cast<long long>(y + r0) * ld + x + c) * BYTES;
+    const long long step = ld * (kPass * BYTES);
+#pragma unroll 1
+    for (int r = 0; r < 32; r += 8) {
+#pragma unroll
+      for (int j = 0; j < 8; j += kPass, d += step) {
+        if (r + j >= n) continue;
+        const uint32_t src = at + (r + j) * 64 + (sw ^ ((j / 2 & 3) << 4));
         if constexpr (BYTES == 2) {
           uint16_t v;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
-          static_cast<uint16_t*>(out)[o] = v;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src) : "memory");
+          *reinterpret_cast<uint16_t*>(d) = v;
         } else {
           float v;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-          float* d = static_cast<float*>(out) + o;
-          *d = add ? *d + v : v;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(src) : "memory");
+          float* f = reinterpret_cast<float*>(d);
+          *f = add ? *f + v : v;
         }
       }
     }

@@ -23,10 +23,179 @@ __device__ __forceinline__ float load_w(const void* w, int dtype, int c) {
   return __half2float(static_cast<const __half*>(w)[c]);
 }
 
+// The gain of VEC columns from c, 0 past the last.
+template <int VEC>
+__device__ __forceinline__ void load_gain(const void* w, int dtype, int c, int cols, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
+      if (dtype == kF32)
+        load_vec<float, 8>(static_cast<const float*>(w) + c, v);
+      else if (dtype == kBF16)
+        load_vec<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16*>(w) + c, v);
+      else
+        load_vec<__half, 8>(static_cast<const __half*>(w) + c, v);
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = c + j < cols ? load_w(w, dtype, c + j) : 0.f;
+}
+
+// --------------------------------------------------------------------------
+// Access.  A thread holds VEC consecutive columns: 8, or 1 for fp32 rows that
+// are not a multiple of 8 columns or not 16-byte aligned.  16-bit rows of any
+// width and alignment are taken 8 columns a thread too (ANY): a thread reads the
+// two aligned 16-byte pieces that its columns lie in and shifts, and a warp
+// writes its 256 columns through shared memory as consecutive 4-byte words.
+// --------------------------------------------------------------------------
+
+// A matrix that is read, and (ANY) the bytes that its rows span: 16-byte pieces
+// inside it may be read whole, whatever columns they hold.
+template <typename T, bool ANY>
+struct Reader {
+  const T* p;
+  long long ld;
+  uintptr_t lo = 0, hi = 0;
+  __device__ __forceinline__ Reader(const Mat& m, int rows, int cols) : p(static_cast<const T*>(m.p)), ld(m.ld) {
+    if constexpr (ANY) {
+      lo = reinterpret_cast<uintptr_t>(p);
+      hi = lo + ((static_cast<long long>(rows) - 1) * ld + cols) * sizeof(T);
+    }
+  }
+  __device__ __forceinline__ const T* at(long long row, int c) const { return p + row * ld + c; }
+};
+
+// VEC elements as they lie in memory, loaded ahead of their use.
+template <typename T, int VEC, bool ANY>
+struct Raw {
+  static constexpr int kWords = VEC == 1 ? 1 : (ANY ? 2 : 1) * VEC * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[kWords];
+  uint32_t meta;  // ANY: elements to shift by, and columns inside the row << 8
+  // p: the element at column c of the row; `in` false or c past the end: zeros.
+  __device__ __forceinline__ void load(const Reader<T, ANY>& r, const T* p, int c, int cols, bool in) {
+    if (!in || c >= cols) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0u;
+      meta = 0u;
+      return;
+    }
+    if constexpr (ANY) {
+      static_assert(VEC == 8 && sizeof(T) == 2, "16-bit types, 8 columns");
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p), lo = at & ~static_cast<uintptr_t>(15);
+      const uint32_t n = static_cast<uint32_t>(min(8, cols - c));
+      if (lo >= r.lo && lo + 32 <= r.hi) {
+        const uint4 u = reinterpret_cast<const uint4*>(lo)[0], v = reinterpret_cast<const uint4*>(lo)[1];
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+        meta = static_cast<uint32_t>(at & 15) / 2 | n << 8;
+      } else {  // the first or last columns of the whole matrix
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = (2 * i < n ? q[2 * i] : 0u) | (2 * i + 1 < n ? static_cast<uint32_t>(q[2 * i + 1]) << 16 : 0u);
+        w[4] = w[5] = w[6] = w[7] = 0u;
+        meta = n << 8;
+      }
+    } else if constexpr (VEC == 1) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const Reader<T, ANY>& r, long long row, int c, int cols, bool in = true) {
+    load(r, r.at(row, c), c, cols, in);
+  }
+  // ANY: the elements in the first four words, zeros past the end of the row.
+  __device__ __forceinline__ void align() {
+    if constexpr (ANY) {
+      const uint32_t n = meta >> 8;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = meta & 4 ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = meta & 2 ? w[i + 1] : w[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = meta & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+      if (n < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xFFFFu : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[VEC]) {
+    align();
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(w[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        const float2 f = unpack2<kBf>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void load_cols(const Reader<T, ANY>& r, long long row, int c, int cols, float (&v)[VEC]) {
+  Raw<T, VEC, ANY> raw;
+  raw.load(r, row, c, cols);
+  raw.values(v);
+}
+
+// Writes VEC columns from p (the element at column c; nothing past the end of
+// the row).  ANY: called by all lanes of a warp, which hold consecutive columns
+// of one row; buf is the warp's 33 pieces of shared memory.
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void store_cols(T* p, int c, int cols, const float (&v)[VEC], uint4* buf) {
+  if constexpr (!ANY) {
+    if (c < cols) store_vec<T, VEC>(p, v);
+  } else {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    const int lane = threadIdx.x % 32;
+    const int n = min(256, cols - (c - 8 * lane));  // columns of the warp
+    uint16_t* out = reinterpret_cast<uint16_t*>(p) - 8 * lane;
+    __syncwarp();
+    buf[lane] = make_uint4(pack2<kBf>(v[0], v[1]), pack2<kBf>(v[2], v[3]), pack2<kBf>(v[4], v[5]),
+                           pack2<kBf>(v[6], v[7]));
+    __syncwarp();
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(buf);
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(out) >> 1) & 1;  // the same in every lane
+    if (odd && lane == 0 && n > 0) out[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 32 * j + lane, e = 2 * i + odd;
+      const uint32_t x = odd ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];  // w[128] is beyond the row's data
+      if (e + 1 < n)
+        *reinterpret_cast<uint32_t*>(out + e) = x;
+      else if (e < n)
+        out[e] = static_cast<uint16_t>(x);
+    }
+  }
+}
+// Its shared memory.
+template <bool ANY, int WARPS>
+struct StoreBuf {
+  uint4 piece[ANY ? WARPS : 1][33];
+  __device__ __forceinline__ uint4* mine() {
+    return ANY ? piece[(threadIdx.y * blockDim.x + threadIdx.x) / 32] : piece[0];
+  }
+};
+
+// --------------------------------------------------------------------------
+// 8-bit blocks
+// --------------------------------------------------------------------------
+
 // Bits of the largest |v| over the lanes that share a block of 32 columns (VEC
 // columns a lane); a NaN is larger than every number.
 template <int VEC>
 __device__ __forceinline__ uint32_t block_amax(const float (&v)[VEC]) {
+  if constexpr (VEC == 1) return __reduce_max_sync(0xffffffffu, __float_as_uint(v[0]) & 0x7FFFFFFFu);
   float m = fabsf(v[0]);
 #pragma unroll
   for (int j = 1; j < VEC; ++j) m = max_mag(m, v[j]);
@@ -34,42 +203,73 @@ __device__ __forceinline__ uint32_t block_amax(const float (&v)[VEC]) {
   for (int d = 1; d < kPackBlock / VEC; d *= 2) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, d));
   return __float_as_uint(m) & 0x7FFFFFFFu;
 }
+// The same from 16-bit elements as loaded (and aligned).
+template <bool BF16>
+__device__ __forceinline__ uint32_t block_amax16(const uint32_t* w) {
+  uint32_t m = max_mag2<BF16>(max_mag2<BF16>(w[0], w[1]), max_mag2<BF16>(w[2], w[3]));
+  m = max_mag2<BF16>(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_mag2<BF16>(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const float2 f = unpack2<BF16>(m);
+  return __float_as_uint(max_mag(f.x, f.y)) & 0x7FFFFFFFu;
+}
 
-// Codes (and, from the block's first lane, its scale byte) of VEC columns to q
-// (and sb).  Lanes of a warp hold consecutive columns from a multiple of 32;
-// `in` is false past the last column, where the values are 0.  amax: the bits
-// of the block's largest magnitude.  Called by all lanes of a warp together.
-template <int VEC>
-__device__ __forceinline__ void store_block(int8_t* q, uint8_t* sb, bool in, bool first, uint32_t amax,
+// Codes (and, from the block's first lane, its scale byte) of VEC columns from
+// column c to q (and sb).  Lanes of a warp hold consecutive columns from a
+// multiple of 32; n: how many of the thread's columns are in the row (the values
+// of the others are 0).  amax: the bits of the block's largest magnitude.
+// Without ANY eight codes are one aligned piece; with it `aligned` says whether
+// they are where the row has them all.  Called by all lanes of a warp together.
+template <int VEC, bool ANY>
+__device__ __forceinline__ void store_block(int8_t* q, uint8_t* sb, int n, bool first, bool aligned, uint32_t amax,
                                             float (&v)[VEC]) {
   const uint32_t byte = scale_byte(amax);
   const float inv = inv_scale(byte);
   if (__any_sync(0xffffffffu, byte == kTopByte)) saturate_block(byte, v);  // skipped by the whole warp
-  if (!in) return;
-  if constexpr (VEC == 8)
-    *reinterpret_cast<uint2*>(q) =
-        make_uint2(codes4(v[0], v[1], v[2], v[3], inv), codes4(v[4], v[5], v[6], v[7], inv));
-  else
+  if (n <= 0) return;
+  if constexpr (VEC == 8) {
+    const uint32_t w[2] = {codes4(v[0], v[1], v[2], v[3], inv), codes4(v[4], v[5], v[6], v[7], inv)};
+    if (!ANY || (aligned && n >= 8)) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) q[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j % 4)));
+    }
+  } else {
     *q = static_cast<int8_t>(code_of(v[0], inv));
+  }
   if (first) *sb = static_cast<uint8_t>(byte);
 }
-template <int VEC>
-__device__ __forceinline__ void store_block(const Pack8& o, long long row, int c, int cols, float (&v)[VEC]) {
-  store_block<VEC>(o.q + row * o.ldq + c, o.s + row * o.lds + c / kPackBlock, c < cols, c % kPackBlock == 0,
+__device__ __forceinline__ bool codes_aligned(const Pack8& p) {
+  return ((reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.ldq)) & 7u) == 0;
+}
+template <int VEC, bool ANY>
+__device__ __forceinline__ void store_block(const Pack8& o, long long row, int c, int cols, bool aligned,
+                                            float (&v)[VEC]) {
+  store_block<VEC, ANY>(o.q + row * o.ldq + c, o.s + row * o.lds + c / kPackBlock, cols - c, c % kPackBlock == 0, aligned,
                    block_amax<VEC>(v), v);
 }
 
 // Raw codes and scale byte of VEC columns, and their values.
-template <int VEC>
+template <int VEC, bool ANY>
 struct Codes {
   uint2 w;
   uint32_t byte;
-  __device__ __forceinline__ void load(const int8_t* q, const uint8_t* s, bool in) {
-    if (!in) return;
-    if constexpr (VEC == 8)
+  // n: columns in the row from this one; ANY and `aligned` as for store_block.
+  __device__ __forceinline__ void load(const int8_t* q, const uint8_t* s, int n, bool aligned) {
+    if (n <= 0) return;
+    if constexpr (VEC == 1) {
+      w.x = static_cast<uint8_t>(*q);
+    } else if (!ANY || (aligned && n >= 8)) {
       w = *reinterpret_cast<const uint2*>(q);
-    else
-      w.x = static_cast<uint32_t>(static_cast<uint8_t>(*q));
+    } else {
+      w = make_uint2(0u, 0u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = j < n ? static_cast<uint8_t>(q[j]) : 0u;
+        (j < 4 ? w.x : w.y) |= x << (8 * (j % 4));
+      }
+    }
     byte = *s;
   }
   __device__ __forceinline__ void values(float (&v)[VEC]) const {
@@ -87,78 +287,6 @@ struct Codes {
     }
   }
 };
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_cols(const Mat& m, long long row, int c, int cols, const float (&v)[VEC]) {
-  if (c < cols) store_vec<T, VEC>(static_cast<T*>(m.p) + row * m.ld + c, v);
-}
-// VEC elements as they lie in memory (loaded ahead of their use), zeros past
-// the last column.
-template <typename T, int VEC>
-struct Raw {
-  static constexpr int kWords = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(T)) / 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const Mat& m, long long row, int c, int cols) {
-    load(static_cast<const T*>(m.p) + row * m.ld + c, c < cols);
-  }
-  __device__ __forceinline__ void load(const T* p, bool in) {
-    if (!in) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = 0u;
-      return;
-    }
-    if constexpr (VEC == 1) {
-      if constexpr (sizeof(T) == 2)
-        w[0] = *reinterpret_cast<const uint16_t*>(p);
-      else
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 u = reinterpret_cast<const uint4*>(p)[i];
-        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-      }
-    }
-  }
-  __device__ __forceinline__ void values(float (&v)[VEC]) const {
-    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(w[j]);
-    } else if constexpr (VEC == 1) {
-      v[0] = unpack1<kBf>(static_cast<uint16_t>(w[0]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) {
-        const float2 f = unpack2<kBf>(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
-    }
-  }
-};
-// Bits of the block's largest magnitude, from the elements as loaded.
-template <typename T, int VEC>
-__device__ __forceinline__ uint32_t raw_amax(const Raw<T, VEC>& r) {
-  if constexpr (VEC == 8 && sizeof(T) == 2) {
-    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    uint32_t m = max_mag2<kBf>(max_mag2<kBf>(r.w[0], r.w[1]), max_mag2<kBf>(r.w[2], r.w[3]));
-    m = max_mag2<kBf>(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max_mag2<kBf>(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const float2 f = unpack2<kBf>(m);
-    return __float_as_uint(max_mag(f.x, f.y)) & 0x7FFFFFFFu;
-  } else {
-    float v[VEC];
-    r.values(v);
-    return block_amax<VEC>(v);
-  }
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void load_cols(const Mat& m, long long row, int c, int cols, float (&v)[VEC]) {
-  Raw<T, VEC> raw;
-  raw.load(m, row, c, cols);
-  raw.values(v);
-}
 
 // Sum over the threads of a row (blockDim.x, a multiple of 32), the same bits in
 // every one.  `red` (16-byte aligned) alternates between two halves so one
@@ -187,53 +315,61 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
 // --------------------------------------------------------------------------
 constexpr int kWalk = 4;
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(256, 4) pack8_kernel(int rows, int cols, Mat x, Pack8 o) {
+template <typename T, int VEC, bool ANY>
+__global__ void __launch_bounds__(256, ANY ? 3 : 4) pack8_kernel(int rows, int cols, Mat x, Pack8 o) {
   pdl_trigger();
   pdl_wait();
+  const Reader<T, ANY> rx(x, rows, cols);
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
   const int step = gridDim.y * blockDim.y;
   int row = blockIdx.y * blockDim.y + threadIdx.y;
-  const T* px = static_cast<const T*>(x.p) + row * x.ld + c;
+  const T* px = rx.at(row, c);
   int8_t* pq = o.q + row * o.ldq + c;
   uint8_t* ps = o.s + row * o.lds + c / kPackBlock;
   const long long dx = step * x.ld, dq = step * o.ldq, ds = step * o.lds;
-  const bool first = c % kPackBlock == 0;
+  const bool first = c % kPackBlock == 0, aligned = codes_aligned(o);
   for (; row < rows; row += kWalk * step) {
-    Raw<T, VEC> raw[kWalk];
+    Raw<T, VEC, ANY> raw[kWalk];
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i, px += dx) raw[i].load(px, c < cols && row + i * step < rows);
+    for (int i = 0; i < kWalk; ++i, px += dx) raw[i].load(rx, px, c, cols, row + i * step < rows);
 #pragma unroll
     for (int i = 0; i < kWalk; ++i, pq += dq, ps += ds) {
       float v[VEC];
       raw[i].values(v);
-      store_block<VEC>(pq, ps, c < cols && row + i * step < rows, first, raw_amax(raw[i]), v);
+      uint32_t amax;
+      if constexpr (sizeof(T) == 2)
+        amax = block_amax16<std::is_same<T, __nv_bfloat16>::value>(raw[i].w);
+      else
+        amax = block_amax<VEC>(v);
+      store_block<VEC, ANY>(pq, ps, row + i * step < rows ? cols - c : 0, first, aligned, amax, v);
     }
   }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 __global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pack8 in, Mat out) {
   pdl_trigger();
   pdl_wait();
+  __shared__ StoreBuf<ANY, 8> sbuf;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
-  if (c >= cols) return;
   const int step = gridDim.y * blockDim.y;
   int row = blockIdx.y * blockDim.y + threadIdx.y;
   const int8_t* pq = in.q + row * in.ldq + c;
   const uint8_t* ps = in.s + row * in.lds + c / kPackBlock;
   T* po = static_cast<T*>(out.p) + row * out.ld + c;
   const long long dq = step * in.ldq, ds = step * in.lds, dst = step * out.ld;
+  const bool aligned = codes_aligned(in);
   for (; row < rows; row += kWalk * step) {
-    Codes<VEC> q[kWalk];
+    Codes<VEC, ANY> q[kWalk];
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i, pq += dq, ps += ds) q[i].load(pq, ps, row + i * step < rows);
+    for (int i = 0; i < kWalk; ++i, pq += dq, ps += ds)
+      q[i].load(pq, ps, row + i * step < rows ? cols - c : 0, aligned);
 #pragma unroll
     for (int i = 0; i < kWalk; ++i, po += dst) {
       if (row + i * step >= rows) break;
       float v[VEC];
       q[i].values(v);
-      store_vec<T, VEC>(po, v);
+      store_cols<T, VEC, ANY>(po, c, cols, v, sbuf.mine());
     }
   }
 }
@@ -247,7 +383,7 @@ __global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pac
 // --------------------------------------------------------------------------
 constexpr int kRowThreads = 512;  // most of a row kernel's block (128 registers a thread)
 
-template <typename T, int VEC, int NV, bool RES>
+template <typename T, int VEC, bool ANY, int NV, bool RES>
 __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -255,21 +391,24 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
   int flip = 0;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
-  float w[NV][VEC];
+  // Where registers are short (twice the words a piece), the gain is read again
+  // for each row and the next row's pieces after this one.
+  constexpr bool kAhead = !(ANY && NV > 1);
+  float w[kAhead ? NV : 1][VEC];
+  if constexpr (kAhead) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = threadIdx.x * VEC + i * span + j;
-      w[i][j] = c < a.cols ? load_w(a.w, a.w_dtype, c) : 0.f;
-    }
-  Raw<T, VEC> x[NV], r[RES ? NV : 1];
+    for (int i = 0; i < NV; ++i) load_gain<VEC>(a.w, a.w_dtype, threadIdx.x * VEC + i * span, a.cols, w[i]);
+  }
+  __shared__ StoreBuf<ANY, kRowThreads / 32> sbuf;
+  const Reader<T, ANY> rx(a.x, a.rows, a.cols), rr(a.residual, a.rows, a.cols);
+  const bool aligned = codes_aligned(a.y8);
+  Raw<T, VEC, ANY> x[NV], r[RES ? NV : 1];
   auto load_row = [&](long long row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = row < a.rows ? static_cast<int>(threadIdx.x) * VEC + i * span : a.cols;
-      x[i].load(a.x, row, c, a.cols);
-      if constexpr (RES) r[i].load(a.residual, row, c, a.cols);
+      const int c = static_cast<int>(threadIdx.x) * VEC + i * span;
+      x[i].load(rx, row, c, a.cols, row < a.rows);
+      if constexpr (RES) r[i].load(rr, row, c, a.cols, row < a.rows);
     }
   };
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
@@ -289,25 +428,30 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     }
-    load_row(row + step);
+    if constexpr (kAhead) load_row(row + step);
     ss = cta_sum(ss, red, flip);
     const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x * VEC + i * span;
-      if (a.h.p) store_cols<T, VEC>(a.h, row, c, a.cols, v[i]);
+      if (a.h.p)
+        store_cols<T, VEC, ANY>(static_cast<T*>(a.h.p) + row * a.h.ld + c, c, a.cols, v[i], sbuf.mine());
+      float (&g)[VEC] = w[kAhead ? i : 0];
+      if constexpr (!kAhead) load_gain<VEC>(a.w, a.w_dtype, c, a.cols, g);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = c < a.cols ? v[i][j] * rstd * w[i][j] : 0.f;
-      if (a.y.p) store_cols<T, VEC>(a.y, row, c, a.cols, v[i]);
-      if (a.y8.q) store_block<VEC>(a.y8, row, c, a.cols, v[i]);
+      for (int j = 0; j < VEC; ++j) v[i][j] = c + j < a.cols ? v[i][j] * rstd * g[j] : 0.f;
+      if (a.y.p)
+        store_cols<T, VEC, ANY>(static_cast<T*>(a.y.p) + row * a.y.ld + c, c, a.cols, v[i], sbuf.mine());
+      if (a.y8.q) store_block<VEC, ANY>(a.y8, row, c, a.cols, aligned, v[i]);
     }
+    if constexpr (!kAhead) load_row(row + step);
   }
 }
 
 // The same for rows too wide for that: the row is read twice, the second time
 // from cache.
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -316,11 +460,14 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
   const int padded = (a.cols + span - 1) / span * span;
+  __shared__ StoreBuf<ANY, 32> sbuf;
+  const Reader<T, ANY> rx(a.x, a.rows, a.cols), rr(a.residual, a.rows, a.cols);
+  const bool aligned = codes_aligned(a.y8);
   auto load_h = [&](long long row, int c, float (&v)[VEC]) {
-    load_cols<T, VEC>(a.x, row, c, a.cols, v);
+    load_cols<T, VEC, ANY>(rx, row, c, a.cols, v);
     if (a.residual.p) {
       float r[VEC];
-      load_cols<T, VEC>(a.residual, row, c, a.cols, r);
+      load_cols<T, VEC, ANY>(rr, row, c, a.cols, r);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] += r[j];
     }
@@ -337,11 +484,13 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int c = threadIdx.x * VEC; c < padded; c += span) {
       load_h(row, c, v);
-      if (a.h.p) store_cols<T, VEC>(a.h, row, c, a.cols, v);
+      if (a.h.p) store_cols<T, VEC, ANY>(static_cast<T*>(a.h.p) + row * a.h.ld + c, c, a.cols, v, sbuf.mine());
+      float g[VEC];
+      load_gain<VEC>(a.w, a.w_dtype, c, a.cols, g);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = c < a.cols ? v[j] * rstd * load_w(a.w, a.w_dtype, c + j) : 0.f;
-      if (a.y.p) store_cols<T, VEC>(a.y, row, c, a.cols, v);
-      if (a.y8.q) store_block<VEC>(a.y8, row, c, a.cols, v);
+      for (int j = 0; j < VEC; ++j) v[j] = c + j < a.cols ? v[j] * rstd * g[j] : 0.f;
+      if (a.y.p) store_cols<T, VEC, ANY>(static_cast<T*>(a.y.p) + row * a.y.ld + c, c, a.cols, v, sbuf.mine());
+      if (a.y8.q) store_block<VEC, ANY>(a.y8, row, c, a.cols, aligned, v);
     }
   }
 }
@@ -350,12 +499,13 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
 // over rows of dy hn.  Bound by HBM.  As the forward kernel, with dw's column
 // sums of the CTA's rows in registers; column_sum_kernel adds the CTAs' sums in
 // order.
-__device__ __forceinline__ float norm_dx(float dy, float w, float hn, float mean, float rstd, float dh) {
-  return fmaf(rstd, fmaf(-hn, mean, __fmul_rn(dy, w)), dh);
+__device__ __forceinline__ float norm_dx(float g, float hn, float mean, float rstd, float dh) {
+  return fmaf(rstd, fmaf(-hn, mean, g), dh);
 }
 
-template <typename T, int VEC, int NV, bool DH>
-__global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_grad_kernel(NormGradArgs a) {
+template <typename T, int VEC, bool ANY, int NV, bool DH>
+__global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY ? 2 : 1)
+    rms_norm_grad_kernel(NormGradArgs a) {
   pdl_trigger();
   pdl_wait();
   __shared__ __align__(16) float red[64];
@@ -363,24 +513,23 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1
   int flip = 0;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
-  float w[NV][VEC], dw[NV][VEC];
+  constexpr bool kAhead = !(ANY && NV > 1);  // as in the forward kernel
+  float w[kAhead ? NV : 1][VEC], dw[NV][VEC] = {};
+  if constexpr (kAhead) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = threadIdx.x * VEC + i * span + j;
-      w[i][j] = c < a.cols ? load_w(a.w, a.w_dtype, c) : 0.f;
-      dw[i][j] = 0.f;
-    }
-  Raw<T, VEC> dy[NV], h[NV], dh[DH ? NV : 1];
+    for (int i = 0; i < NV; ++i) load_gain<VEC>(a.w, a.w_dtype, threadIdx.x * VEC + i * span, a.cols, w[i]);
+  }
+  __shared__ StoreBuf<ANY, kRowThreads / 32> sbuf;
+  const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rh(a.h, a.rows, a.cols), rd(a.dh, a.rows, a.cols);
+  Raw<T, VEC, ANY> dy[NV], h[NV], dh[DH ? NV : 1];
   float rstd_next = 0.f;
   auto load_row = [&](long long row) {
     if (row < a.rows) rstd_next = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = row < a.rows ? static_cast<int>(threadIdx.x) * VEC + i * span : a.cols;
-      dy[i].load(a.dy, row, c, a.cols);
-      h[i].load(a.h, row, c, a.cols);
+      const int c = static_cast<int>(threadIdx.x) * VEC + i * span;
+      dy[i].load(ry, row, c, a.cols, row < a.rows);
+      h[i].load(rh, row, c, a.cols, row < a.rows);
     }
   };
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
@@ -391,29 +540,34 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1
     float g[NV][VEC], hn[NV][VEC], s = 0.f;
     if constexpr (DH) {  // not needed before the sum is known
 #pragma unroll
-      for (int i = 0; i < NV; ++i) dh[i].load(a.dh, row, static_cast<int>(threadIdx.x) * VEC + i * span, a.cols);
+      for (int i = 0; i < NV; ++i) dh[i].load(rd, row, static_cast<int>(threadIdx.x) * VEC + i * span, a.cols);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       dy[i].values(g[i]);
       h[i].values(hn[i]);
+      float (&gain)[VEC] = w[kAhead ? i : 0];
+      if constexpr (!kAhead) load_gain<VEC>(a.w, a.w_dtype, threadIdx.x * VEC + i * span, a.cols, gain);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         hn[i][j] = __fmul_rn(hn[i][j], rstd);
         dw[i][j] = fmaf(g[i][j], hn[i][j], dw[i][j]);
-        s = fmaf(__fmul_rn(g[i][j], w[i][j]), hn[i][j], s);
+        g[i][j] = __fmul_rn(g[i][j], gain[j]);
+        s = fmaf(g[i][j], hn[i][j], s);
       }
     }
-    load_row(row + step);
+    if constexpr (kAhead) load_row(row + step);
     s = cta_sum(s, red, flip) * inv_cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float d[VEC] = {};
       if constexpr (DH) dh[i].values(d);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) d[j] = norm_dx(g[i][j], w[i][j], hn[i][j], s, rstd, d[j]);
-      store_cols<T, VEC>(a.dx, row, static_cast<int>(threadIdx.x) * VEC + i * span, a.cols, d);
+      for (int j = 0; j < VEC; ++j) d[j] = norm_dx(g[i][j], hn[i][j], s, rstd, d[j]);
+      const int c = static_cast<int>(threadIdx.x) * VEC + i * span;
+      store_cols<T, VEC, ANY>(static_cast<T*>(a.dx.p) + row * a.dx.ld + c, c, a.cols, d, sbuf.mine());
     }
+    if constexpr (!kAhead) load_row(row + step);
   }
   if (a.dw == nullptr) return;
   // The rows of the block first, in order.
@@ -441,7 +595,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 ? 2 : 1
 }
 
 // The same for rows too wide for that: read twice, column sums in shared memory.
-template <typename T, int VEC>
+template <typename T, int VEC, bool ANY>
 __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -449,40 +603,43 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
   __shared__ __align__(16) float red[64];
   int flip = 0;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
+  __shared__ StoreBuf<ANY, 32> sbuf;
+  const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rh(a.h, a.rows, a.cols), rd(a.dh, a.rows, a.cols);
   const int span = blockDim.x * VEC;
+  const int padded = (a.cols + span - 1) / span * span;
   if (a.dw != nullptr)
-    for (int c = threadIdx.x * VEC; c < a.cols; c += span)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) colsum[c + j] = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) colsum[c] = 0.f;
+  __syncthreads();
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float rstd = a.rstd[row];
-    float s = 0.f, dy[VEC], h[VEC];
+    float s = 0.f, dy[VEC], h[VEC], w[VEC];
     for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
-      load_cols<T, VEC>(a.dy, row, c, a.cols, dy);
-      load_cols<T, VEC>(a.h, row, c, a.cols, h);
+      load_cols<T, VEC, ANY>(ry, row, c, a.cols, dy);
+      load_cols<T, VEC, ANY>(rh, row, c, a.cols, h);
+      load_gain<VEC>(a.w, a.w_dtype, c, a.cols, w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        s = fmaf(__fmul_rn(dy[j], load_w(a.w, a.w_dtype, c + j)), __fmul_rn(h[j], rstd), s);
+      for (int j = 0; j < VEC; ++j) s = fmaf(__fmul_rn(dy[j], w[j]), __fmul_rn(h[j], rstd), s);
     }
     s = cta_sum(s, red, flip) * inv_cols;
-    for (int c = threadIdx.x * VEC; c < a.cols; c += span) {
-      float d[VEC];
-      load_cols<T, VEC>(a.dy, row, c, a.cols, dy);
-      load_cols<T, VEC>(a.h, row, c, a.cols, h);
-      if (a.dh.p) load_cols<T, VEC>(a.dh, row, c, a.cols, d);
+    for (int c = threadIdx.x * VEC; c < padded; c += span) {
+      float d[VEC] = {};
+      load_cols<T, VEC, ANY>(ry, row, c, a.cols, dy);
+      load_cols<T, VEC, ANY>(rh, row, c, a.cols, h);
+      if (a.dh.p) load_cols<T, VEC, ANY>(rd, row, c, a.cols, d);
+      load_gain<VEC>(a.w, a.w_dtype, c, a.cols, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float hn = __fmul_rn(h[j], rstd);
-        d[j] = norm_dx(dy[j], load_w(a.w, a.w_dtype, c + j), hn, s, rstd, a.dh.p ? d[j] : 0.f);
-        if (a.dw != nullptr) colsum[c + j] = fmaf(dy[j], hn, colsum[c + j]);
+        d[j] = norm_dx(__fmul_rn(dy[j], w[j]), hn, s, rstd, d[j]);
+        if (a.dw != nullptr && c + j < a.cols) colsum[c + j] = fmaf(dy[j], hn, colsum[c + j]);
       }
-      store_cols<T, VEC>(a.dx, row, c, a.cols, d);
+      store_cols<T, VEC, ANY>(static_cast<T*>(a.dx.p) + row * a.dx.ld + c, c, a.cols, d, sbuf.mine());
     }
   }
+  __syncthreads();
   if (a.dw != nullptr)
-    for (int c = threadIdx.x * VEC; c < a.cols; c += span)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) a.partials[static_cast<long long>(blockIdx.x) * a.cols + c + j] = colsum[c + j];
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x)
+      a.partials[static_cast<long long>(blockIdx.x) * a.cols + c] = colsum[c];
 }
 
 // out[c] (+)= sum over p of partials[p][c], in order of p within each of
@@ -516,8 +673,9 @@ __global__ void __launch_bounds__(32 * kChains) column_sum_kernel(const float* p
 // columns and walks the rows kWalk at a time; the 8 warps' column sums of a CTA
 // meet in shared memory and go to one row of the partials.
 // --------------------------------------------------------------------------
-template <typename T, int VEC, int ACT, bool Z8>
-__global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
+template <typename T, bool ANY, int ACT, bool Z8>
+__global__ void __launch_bounds__(256, ANY ? 2 : 3) act_grad_kernel(ActGradArgs a) {
+  constexpr int VEC = 8;
   pdl_trigger();
   pdl_wait();
   __shared__ float red[8][32 * VEC];
@@ -525,8 +683,9 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
   const int c = (blockIdx.x * 32 + lane) * VEC;
   const int step = gridDim.y * 8;
   int row = blockIdx.y * 8 + w;
-  const T* py = static_cast<const T*>(a.dy.p) + row * a.dy.ld + c;
-  const T* pz = static_cast<const T*>(a.z.p) + row * a.z.ld + c;
+  const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rz(a.z, a.rows, a.cols);
+  const T *py = ry.at(row, c), *pz = rz.at(row, c);
+  const bool aligned = codes_aligned(a.z8);
   const int8_t* pq = a.z8.q + row * a.z8.ldq + c;
   const uint8_t* ps = a.z8.s + row * a.z8.lds + c / kPackBlock;
   T* pd = static_cast<T*>(a.dz.p) + row * a.dz.ld + c;
@@ -534,16 +693,16 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
                   sd = step * a.dz.ld;
   float sum[VEC] = {};
   for (; row < a.rows && c < a.cols; row += kWalk * step) {
-    Raw<T, VEC> dy[kWalk], z[ACT != kActNone && !Z8 ? kWalk : 1];
-    Codes<VEC> z8[Z8 ? kWalk : 1];
+    Raw<T, VEC, ANY> dy[kWalk], z[ACT != kActNone && !Z8 ? kWalk : 1];
+    Codes<VEC, ANY> z8[Z8 ? kWalk : 1];
 #pragma unroll
     for (int i = 0; i < kWalk; ++i, py += sy, pz += sz, pq += sq, ps += ss) {
       const bool in = row + i * step < a.rows;
-      dy[i].load(py, in);
+      dy[i].load(ry, py, c, a.cols, in);
       if constexpr (ACT != kActNone && Z8)
-        z8[i].load(pq, ps, in);
+        z8[i].load(pq, ps, in ? a.cols - c : 0, aligned);
       else if constexpr (ACT != kActNone)
-        z[i].load(pz, in);
+        z[i].load(rz, pz, c, a.cols, in);
     }
 #pragma unroll
     for (int i = 0; i < kWalk; ++i, pd += sd) {
@@ -559,7 +718,7 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) d[j] = __fmul_rn(d[j], act_grad<ACT>(t[j]));
       }
-      if (a.dz.p) store_vec<T, VEC>(pd, d);
+      if (a.dz.p) store_vec<T, VEC>(pd, d);  // the workspace's pitch holds whole pieces
 #pragma unroll
       for (int j = 0; j < VEC; ++j) sum[j] += d[j];
     }
@@ -581,37 +740,35 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(ActGradArgs a) {
   }
 }
 
-// Copies up to two matrices (blockIdx.z).  One element a lane, neighbouring lanes
-// neighbouring elements: source rows may start anywhere.
+// Copies up to two matrices (blockIdx.z) to pitches that hold whole 16-byte
+// pieces.  Bound by HBM.
 struct RepitchArgs {
   Repitch job[2];
 };
-__global__ void __launch_bounds__(256) repitch_kernel(RepitchArgs a) {
+__global__ void __launch_bounds__(256, 4) repitch_kernel(RepitchArgs a) {
   pdl_trigger();
   pdl_wait();
+  using T = __nv_bfloat16;  // any 16-bit type: nothing is computed
   const Repitch& g = a.job[blockIdx.z];
-  const uint16_t* src = static_cast<const uint16_t*>(g.src.p);
-  uint16_t* dst = static_cast<uint16_t*>(g.dst.p);
-  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
-  constexpr int kCols = 4;
-  const int c0 = blockIdx.x * blockDim.x * kCols + threadIdx.x;
-  if (c0 >= g.cols) return;
-  for (long long row = blockIdx.y * blockDim.y + threadIdx.y; row < g.rows; row += 2 * step) {
-    uint16_t v[2][kCols];
+  const int rows = g.rows, cols = g.cols;
+  const Reader<T, true> r(g.src, rows, cols);
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (c >= cols) return;
+  const int step = gridDim.y * blockDim.y;
+  int row = blockIdx.y * blockDim.y + threadIdx.y;
+  const T* p = r.at(row, c);
+  T* d = static_cast<T*>(g.dst.p) + row * g.dst.ld + c;
+  const long long ds = step * g.src.ld, dd = step * g.dst.ld;
+  for (; row < rows; row += kWalk * step) {
+    Raw<T, 8, true> raw[kWalk];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kWalk; ++i, p += ds) raw[i].load(r, p, c, cols, row + i * step < rows);
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) {
-        const int c = c0 + j * blockDim.x;
-        if (row + i * step < g.rows && c < g.cols) v[i][j] = src[(row + i * step) * g.src.ld + c];
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) {
-        const int c = c0 + j * blockDim.x;
-        if (row + i * step < g.rows && c < g.cols) dst[(row + i * step) * g.dst.ld + c] = v[i][j];
-      }
+    for (int i = 0; i < kWalk; ++i, d += dd) {
+      if (row + i * step >= rows) break;
+      raw[i].align();
+      *reinterpret_cast<uint4*>(d) = make_uint4(raw[i].w[0], raw[i].w[1], raw[i].w[2], raw[i].w[3]);
+    }
   }
 }
 
@@ -657,13 +814,6 @@ bool vec_pack(const Pack8& p) {
   return p.q == nullptr || (reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.ldq % 8 == 0);
 }
 int elem_bytes(int dtype) { return dtype == kF32 ? 4 : 2; }
-
-template <typename F>
-cudaError_t by_dtype(int dtype, F&& f) {
-  if (dtype == kF32) return f(float{});
-  if (dtype == kBF16) return f(__nv_bfloat16{});
-  return f(__half{});
-}
 
 // Row kernels: pieces a thread (NV), lanes along a row and rows of a block; at
 // most few_threads lanes if that can be.  The gradient does best with 256 (its
@@ -712,6 +862,24 @@ dim3 walk_grid(K k, int rows, int lanes, int walk, std::atomic<int>* cache) {
   return dim3(gx, std::max(1, std::min({most, resident(k, 256, 0, cache) / gx, 65535})));
 }
 
+// How the columns are taken: type, columns a thread, any alignment.
+template <typename T_, int VEC_, bool ANY_>
+struct Access {
+  using T = T_;
+  static constexpr int VEC = VEC_;
+  static constexpr bool ANY = ANY_;
+  // Pieces a thread of the norm's kernels (and its gradient's) holds at most.
+  static constexpr int kPieces = VEC == 8 ? 4 : 8, kGradPieces = VEC == 8 ? 2 : 8;
+  static int lanes(int cols) { return (cols + VEC - 1) / VEC; }
+};
+// Calls f with the access for rows of `dtype`; vec: all of them are 16-byte
+// aligned and a multiple of 8 columns long.
+template <typename F>
+cudaError_t by_access(int dtype, bool vec, F&& f) {
+  if (dtype == kF32) return vec ? f(Access<float, 8, false>{}) : f(Access<float, 1, false>{});
+  if (dtype == kBF16) return vec ? f(Access<__nv_bfloat16, 8, false>{}) : f(Access<__nv_bfloat16, 8, true>{});
+  return vec ? f(Access<__half, 8, false>{}) : f(Access<__half, 8, true>{});
+}
 // Calls f with nv as a constant.
 template <int MAX, typename F>
 cudaError_t by_nv(int nv, F&& f) {
@@ -731,93 +899,78 @@ cudaError_t by_act(int act, F&& f) {
 }  // namespace
 
 cudaError_t launch_pack8(int rows, int cols, int dtype, Mat x, Pack8 out, cudaStream_t s) {
-  const bool vec = cols % 8 == 0 && vec_mat(x, elem_bytes(dtype)) && vec_pack(out);
-  const int lanes = (cols + kPackBlock - 1) / kPackBlock * (vec ? kPackBlock / 8 : kPackBlock);  // whole blocks
-  return by_dtype(dtype, [&](auto t) {
-    using T = decltype(t);
-    static std::atomic<int> cache[2][9];
-    auto k = vec ? pack8_kernel<T, 8> : pack8_kernel<T, 1>;
-    return launch_kernel(pdl_enabled(), k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, x, out);
+  return by_access(dtype, cols % 8 == 0 && vec_mat(x, elem_bytes(dtype)) && vec_pack(out), [&](auto acc) {
+    using A = decltype(acc);
+    static std::atomic<int> cache[9];
+    auto k = pack8_kernel<typename A::T, A::VEC, A::ANY>;
+    return launch_kernel(pdl_enabled(), k, walk_grid(k, rows, A::lanes(cols), kWalk, cache), kWalkBlock, 0, s, rows,
+                         cols, x, out);
   });
 }
 
 cudaError_t launch_unpack8(int rows, int cols, Pack8 in, int dtype, Mat out, cudaStream_t s) {
-  const bool vec = cols % 8 == 0 && vec_mat(out, elem_bytes(dtype)) && vec_pack(in);
-  const int lanes = vec ? cols / 8 : cols;
-  return by_dtype(dtype, [&](auto t) {
-    using T = decltype(t);
-    static std::atomic<int> cache[2][9];
-    auto k = vec ? unpack8_kernel<T, 8> : unpack8_kernel<T, 1>;
-    return launch_kernel(pdl_enabled(), k, walk_grid(k, rows, lanes, kWalk, cache[vec]), kWalkBlock, 0, s, rows, cols, in, out);
+  return by_access(dtype, cols % 8 == 0 && vec_mat(out, elem_bytes(dtype)) && vec_pack(in), [&](auto acc) {
+    using A = decltype(acc);
+    static std::atomic<int> cache[9];
+    auto k = unpack8_kernel<typename A::T, A::VEC, A::ANY>;
+    return launch_kernel(pdl_enabled(), k, walk_grid(k, rows, A::lanes(cols), kWalk, cache), kWalkBlock, 0, s, rows,
+                         cols, in, out);
   });
 }
-
-// Columns of a thread in the register kernels: pieces of 8, or single elements
-// where pitch, base or width rules vectors out.
-template <typename T, int VEC>
-constexpr int kMaxPieces = VEC == 8 ? 2 : 8;
 
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
   const int eb = elem_bytes(a.dtype);
   const bool vec = a.cols % 8 == 0 && vec_mat(a.x, eb) && vec_mat(a.residual, eb) && vec_mat(a.h, eb) &&
                    vec_mat(a.y, eb) && vec_pack(a.y8);
-  const int lanes = vec ? a.cols / 8 : a.cols;
-  auto run = [&](auto t, auto v) {
-    using T = decltype(t);
-    constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
-    const RowShape r = row_shape(lanes, kRowThreads, kRowThreads, MAXV);
+  return by_access(a.dtype, vec, [&](auto acc) {
+    using A = decltype(acc);
+    using T = typename A::T;
+    const RowShape r = row_shape(A::lanes(a.cols), kRowThreads, kRowThreads, A::kPieces);
     if (r.nv == 0)
-      return launch_kernel(pdl_enabled(), rms_norm_wide_kernel<T, VEC>, dim3(std::min(a.rows, 2 * sm_count())), dim3(1024), 0,
-                           s, a);
-    return by_nv<MAXV>(r.nv, [&](auto n) {
+      return launch_kernel(pdl_enabled(), rms_norm_wide_kernel<T, A::VEC, A::ANY>,
+                           dim3(std::min(a.rows, 2 * sm_count())), dim3(1024), 0, s, a);
+    return by_nv<A::kPieces>(r.nv, [&](auto n) {
       constexpr int NV = decltype(n)::value;
       static std::atomic<int> cache[2][kRowThreads / 32 + 1];
       const bool res = a.residual.p != nullptr;
-      auto k = res ? rms_norm_kernel<T, VEC, NV, true> : rms_norm_kernel<T, VEC, NV, false>;
+      auto k = res ? rms_norm_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_kernel<T, A::VEC, A::ANY, NV, false>;
       const int threads = r.block.x * r.block.y;
       const long long blocks = (static_cast<long long>(a.rows) + r.block.y - 1) / r.block.y;
       const int grid = static_cast<int>(std::min<long long>(blocks, resident(k, threads, 0, cache[res])));
       return launch_kernel(pdl_enabled(), k, dim3(grid), r.block, 0, s, a);
     });
-  };
-  return by_dtype(a.dtype, [&](auto t) {
-    return vec ? run(t, std::integral_constant<int, 8>{}) : run(t, std::integral_constant<int, 1>{});
   });
 }
 
 cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   const int eb = elem_bytes(a.dtype);
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, eb) && vec_mat(a.h, eb) && vec_mat(a.dh, eb) && vec_mat(a.dx, eb);
-  const int lanes = vec ? a.cols / 8 : a.cols;
   int parts = 0;  // rows of partial column sums
-  auto run = [&](auto t, auto v) {
-    using T = decltype(t);
-    constexpr int VEC = decltype(v)::value, MAXV = kMaxPieces<T, VEC>;
-    const RowShape r = row_shape(lanes, 256, kRowThreads, MAXV);
+  const cudaError_t e = by_access(a.dtype, vec, [&](auto acc) {
+    using A = decltype(acc);
+    using T = typename A::T;
+    const RowShape r = row_shape(A::lanes(a.cols), 256, kRowThreads, A::kGradPieces);
     if (r.nv == 0) {
-      auto k = rms_norm_grad_wide_kernel<T, VEC>;
+      auto k = rms_norm_grad_wide_kernel<T, A::VEC, A::ANY>;
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4);
       if (e != cudaSuccess) return e;
       parts = std::min(a.rows, sm_count());
-      return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(1024), a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0, s,
-                           a);
+      return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(1024),
+                           a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0, s, a);
     }
-    return by_nv<MAXV>(r.nv, [&](auto n) {
+    return by_nv<A::kGradPieces>(r.nv, [&](auto n) {
       constexpr int NV = decltype(n)::value;
       static std::atomic<int> cache[2][kRowThreads / 32 + 1];
       const bool dh = a.dh.p != nullptr;
-      auto k = dh ? rms_norm_grad_kernel<T, VEC, NV, true> : rms_norm_grad_kernel<T, VEC, NV, false>;
+      auto k = dh ? rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, false>;
       const int ty = r.block.y, threads = r.block.x * ty;
-      const size_t smem = ty > 1 ? static_cast<size_t>(threads) * VEC * NV * 4 : 0;
+      const size_t smem = ty > 1 ? static_cast<size_t>(threads) * A::VEC * NV * 4 : 0;
       const long long blocks = (static_cast<long long>(a.rows) + ty - 1) / ty;
       // One row of partials a block, as many at most as the workspace holds.
       parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
                                          static_cast<long long>(kMaxPartials)}));
       return launch_kernel(pdl_enabled(), k, dim3(parts), r.block, smem, s, a);
     });
-  };
-  const cudaError_t e = by_dtype(a.dtype, [&](auto t) {
-    return vec ? run(t, std::integral_constant<int, 8>{}) : run(t, std::integral_constant<int, 1>{});
   });
   if (e != cudaSuccess || a.dw == nullptr) return e;
   return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
@@ -825,19 +978,19 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s) {
-  const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, 2) && vec_mat(a.z, 2) && vec_mat(a.dz, 2) && vec_pack(a.z8);
+  const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, 2) && vec_mat(a.z, 2) && vec_pack(a.z8);
   int parts = 0;
-  const cudaError_t e = by_dtype(a.dtype, [&](auto t) {
-    using T = decltype(t);
-    if constexpr (std::is_same<T, float>::value) {
+  const cudaError_t e = by_access(a.dtype, vec, [&](auto acc) {
+    using A = decltype(acc);
+    if constexpr (sizeof(typename A::T) == 4) {
       return cudaErrorInvalidValue;  // 16-bit types only
     } else {
       return by_act(a.act, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        auto k = a.z8.q != nullptr ? (vec ? act_grad_kernel<T, 8, ACT, true> : act_grad_kernel<T, 1, ACT, true>)
-                                   : (vec ? act_grad_kernel<T, 8, ACT, false> : act_grad_kernel<T, 1, ACT, false>);
-        static std::atomic<int> cache[2][2][9];
-        dim3 grid = walk_grid(k, a.rows, vec ? a.cols / 8 : a.cols, kWalk, cache[a.z8.q != nullptr][vec]);
+        const bool z8 = a.z8.q != nullptr;
+        auto k = z8 ? act_grad_kernel<typename A::T, A::ANY, ACT, true> : act_grad_kernel<typename A::T, A::ANY, ACT, false>;
+        static std::atomic<int> cache[2][9];
+        dim3 grid = walk_grid(k, a.rows, A::lanes(a.cols), kWalk, cache[z8]);
         // Few rows: one block a column strip, which writes db itself (a second
         // kernel takes longer than the rows the strip's warps walk instead).
         grid.y = a.db != nullptr && a.rows <= 256 ? 1 : std::min<unsigned>(grid.y, kMaxPartials);
@@ -857,7 +1010,7 @@ cudaError_t launch_repitch(const Repitch* jobs, int n, cudaStream_t s) {
   dim3 grid(1, 1, n);
   for (int i = 0; i < n; ++i) {
     a.job[i] = jobs[i];
-    const dim3 g = walk_grid(repitch_kernel, jobs[i].rows, (jobs[i].cols + 3) / 4, 2, cache);
+    const dim3 g = walk_grid(repitch_kernel, jobs[i].rows, (jobs[i].cols + 7) / 8, kWalk, cache);
     grid.x = std::max(grid.x, g.x);
     grid.y = std::max(grid.y, g.y);
   }
