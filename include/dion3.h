@@ -545,9 +545,10 @@ dion3_status dion3_rms_norm_backward(int32_t rows, int32_t cols, const dion3_mat
  * Products accumulate in fp32 and the epilogue works on the fp32 sums; z, y
  * and the blocks are each rounded once from them.
  * The workspace holds copies of operands that TMA cannot read (in_features not
- * a multiple of 8, or a base or pitch that is not a multiple of 16 bytes);
- * strided = 0 asks for the bytes that dense, aligned matrices need, strided = 1
- * for the most that any need.
+ * a multiple of 8, or a base or pitch that is not a multiple of 16 bytes), or,
+ * for large products, reads slowly (rows off the 128-byte lines; without the
+ * room dion3_linear does without that copy).  strided = 0 asks for the bytes
+ * that dense, aligned matrices need, strided = 1 for the most that any need.
  */
 typedef struct {
   int32_t tokens, in_features, out_features;
