@@ -23,7 +23,9 @@ SIZES = [  # tokens, in, out
     (127, 1000, 96), (128, 64, 512), (129, 2047, 130), (300, 320, 257), (513, 200, 1030), (1, 4096, 1001),
     (700, 1032, 776),
     # several large tiles a cluster, in one product of the layer or another; odd widths with them
-    (2100, 72, 2050), (130, 2080, 2201), (257, 2303, 2048), (4100, 40, 300)]
+    (2100, 72, 2050), (130, 2080, 2201), (257, 2303, 2048), (4100, 40, 300),
+    # a few tokens through many rows
+    (1, 520, 2100), (2, 8, 2048), (3, 264, 2077), (4, 1032, 2049), (5, 1032, 2049)]
 
 
 def ws_for(fn, t, k, n, dtype, strided):
