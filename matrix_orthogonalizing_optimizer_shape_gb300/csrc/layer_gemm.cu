@@ -369,7 +369,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // --------------------------------------------------------------------------
-// Large products: persistent clusters of two CTAs on two SMs, each cluster a
+// Large products: bound by the tensor cores, and back to back by the board's
+// power.  16384 x 4096 x 11008 forward (silu, pre-activation kept): 0.79 ms on a
+// cool board (1.87 PFLOP/s), 0.88 under the power cap; dx 0.77, dW 0.80.
+// Persistent clusters of two CTAs on two SMs, each cluster a
 // 256 x 256 (or 256 x 128) tile of the output at a time with the paired-SM MMA
 // (M = 256, K = 16).  Here the TMEM lanes are output rows: CTA rank r holds rows
 // 128 r .. of the tile and every epilogue thread one row, 32 contiguous

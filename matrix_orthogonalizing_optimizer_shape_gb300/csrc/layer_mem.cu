@@ -311,7 +311,8 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
 // --------------------------------------------------------------------------
 // 8-bit checkpoints.  Bound by HBM.  blockDim = (lanes along a row, rows): a
 // thread keeps its columns and walks the rows kWalk at a time, all their loads
-// issued before the first is used.
+// issued before the first is used.  16384 x 11008 bf16: 94 us written (5.8 TB/s),
+// 89 us read back (6.1 TB/s).
 // --------------------------------------------------------------------------
 constexpr int kWalk = 4;
 
@@ -379,7 +380,8 @@ __global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pac
 // unrounded h.  Bound by HBM.  blockDim = (lanes of a row, rows): a thread holds
 // NV pieces of VEC columns of its row in registers from the load to the last
 // store and loads the next row's pieces before it waits for this row's sum.
-// The gain stays in registers over the rows.
+// The gain stays in registers over the rows.  16384 x 4096 bf16 with residual
+// and blocks: 100 us, 6.1 TB/s.
 // --------------------------------------------------------------------------
 constexpr int kRowThreads = 512;  // most of a row kernel's block (128 registers a thread)
 
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
 // Gradient: hn = h rstd, g = dy w; dx = dh + rstd (g - hn mean(g hn)), dw = sum
 // over rows of dy hn.  Bound by HBM.  As the forward kernel, with dw's column
 // sums of the CTA's rows in registers; column_sum_kernel adds the CTAs' sums in
-// order.
+// order.  16384 x 4096 bf16 with dh: 95 us, 5.7 TB/s.
 __device__ __forceinline__ float norm_dx(float g, float hn, float mean, float rstd, float dh) {
   return fmaf(rstd, fmaf(-hn, mean, g), dh);
 }
@@ -671,7 +673,8 @@ __global__ void __launch_bounds__(32 * kChains) column_sum_kernel(const float* p
 // --------------------------------------------------------------------------
 // Activation gradient and bias gradient.  Bound by HBM.  A warp takes 32 VEC
 // columns and walks the rows kWalk at a time; the 8 warps' column sums of a CTA
-// meet in shared memory and go to one row of the partials.
+// meet in shared memory and go to one row of the partials.  16384 x 11008, silu
+// from blocks: 152 us, 6.0 TB/s.
 // --------------------------------------------------------------------------
 template <typename T, bool ANY, int ACT, bool Z8>
 __global__ void __launch_bounds__(256, ANY ? 2 : 3) act_grad_kernel(ActGradArgs a) {
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(256, ANY ? 2 : 3) act_grad_kernel(ActGradArgs 
 }
 
 // Copies up to two matrices (blockIdx.z) to pitches that hold whole 16-byte
-// pieces.  Bound by HBM.
+// pieces.  Bound by HBM: 15448 x 7164 in 70 us, 6.3 TB/s.
 struct RepitchArgs {
   Repitch job[2];
 };

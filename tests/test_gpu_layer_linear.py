@@ -255,3 +255,31 @@ def test_weight_gradient_over_many_tokens(cuda_lib, grad, pad):
     d3.linear_backward(dy, x, w, dw=dw, ws=ws, accumulate=True)
     tol = size * sum_bound(t) + (want.abs() + first.double().abs()) * (U[grad] * 1.01)
     assert bool(((dw.double() - first.double() - want).abs() <= tol).all()) and untouched(dw, buf)
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """More than 2^31 elements in x's blocks, y, z and dz: the last rows are right."""
+    t, k, n = 140_000, 64, 16_384
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(t, k, generator=g, device="cuda").bfloat16()
+    w = torch.randn(n, k, generator=g, device="cuda").bfloat16() / 8
+    y = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    y8 = d3.alloc_packed8(t, n)
+    d3.linear(x, w, y, act=d3.ACT_RELU, y8=y8)
+    rows = torch.tensor([0, 1, 131_071, 131_072, t - 2, t - 1], device="cuda")
+    want = torch.relu(x[rows].double() @ w.double().t())
+    size = x[rows].double().abs() @ w.double().abs().t()
+    tol = size * sum_bound(k) + want * (U["bf16"] * 1.001)
+    assert bool(((y[rows].double() - want).abs() <= tol).all())
+    back = torch.empty_like(y)
+    d3.unpack8(y8, back)
+    step = torch.exp2(y8.scales[rows].double() - 127).repeat_interleave(32, dim=1)
+    assert bool(((back[rows].double() - want).abs() <= 0.5 * step + size * sum_bound(k)).all())
+    dx = torch.empty_like(x)  # act' of relu from the blocks is 1 where the code is not 0
+    ws = ws_for(d3.linear_backward_workspace_size, t, k, n, "bf16", False)
+    d3.linear_backward(y, None, w, dx=dx, act=d3.ACT_RELU, z=y8, ws=ws)
+    dz = y[rows].double() * (back[rows] > 0)
+    tol = (dz.abs() @ w.double().abs()) * sum_bound(n)
+    want = dz @ w.double()
+    assert bool(((dx[rows].double() - want).abs() <= tol + (want.abs() + tol) * U["bf16"]).all())
+    d3.device_status()
