@@ -69,6 +69,8 @@ struct ActGradArgs {
   float* partials;            // [<= kMaxPartials][cols]
 };
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s);
+// Up to this many rows one block takes all of a strip of columns.
+constexpr int kFewRowsOfDz = 256;
 
 // 16-bit matrices (n = 1 or 2) copied to a pitch that TMA takes.
 struct Repitch {
@@ -76,6 +78,10 @@ struct Repitch {
   Mat src, dst;
 };
 cudaError_t launch_repitch(const Repitch* jobs, int n, cudaStream_t s);
+// launch_act_grad, launch_repitch and, if x8 is given, launch_unpack8 into x
+// (16-byte aligned, whole pieces) in one launch, for small matrices.
+cudaError_t launch_prepare(const ActGradArgs& act, const Repitch* copies, int ncopies, int rows, int cols, Pack8 x8,
+                           Mat x, cudaStream_t s);
 // out[rows][cols] = 0 (32- or 16-bit elements, dense), or a 32-bit vector.
 cudaError_t launch_zero(int rows, int cols, int elem_bytes, Mat out, cudaStream_t s);
 

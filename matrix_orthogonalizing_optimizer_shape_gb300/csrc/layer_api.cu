@@ -139,11 +139,14 @@ struct Staging {
     job[n++] = {rows, cols, m, dst};
     return dst;
   }
+  double bytes() const {
+    double b = 0.0;
+    for (int i = 0; i < n; ++i) b += 4.0 * job[i].rows * job[i].cols;
+    return b;
+  }
   cudaError_t run(cudaStream_t s) const {
     if (n == 0) return cudaSuccess;
-    double bytes = 0.0;
-    for (int i = 0; i < n; ++i) bytes += 4.0 * job[i].rows * job[i].cols;
-    return traced_launch("repitch", 0.0, bytes, s, [&] { return launch_repitch(job, n, s); });
+    return traced_launch("repitch", 0.0, bytes(), s, [&] { return launch_repitch(job, n, s); });
   }
 };
 
@@ -443,6 +446,8 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
   unsigned* st = device_status_ptr();
   if (st == nullptr) return fail(DION3_ERR_CUDA, "cannot resolve the device status word");
 
+  const bool unpack = want_dw && x8;
+  bool unpacked = false;
   if (own_dz || g->db != nullptr) {
     ActGradArgs a{};
     a.rows = T;
@@ -456,10 +461,27 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
     a.db = g->db;
     a.accumulate = g->accumulate != 0;
     a.partials = partials;
-    const double n = static_cast<double>(T) * N;
-    DION3_CUDA(traced_launch("act_grad", 0.0, n * (2 + (act ? (z8 ? 33.0 / 32 : 2.0) : 0.0) + (own_dz ? 2 : 0)), s,
-                             [&] { return launch_act_grad(a, s); }),
-               "activation gradient launch");
+    const double n = static_cast<double>(T) * N, xn = unpack ? static_cast<double>(T) * K : 0.0;
+    const double bytes = n * (2 + (act ? (z8 ? 33.0 / 32 : 2.0) : 0.0) + (own_dz ? 2 : 0));
+    // Small ones in one launch (x8, z8: 1003 x 1544 x 988 24.5 -> 21.7 us, 9864 x
+    // 493 x 81 37.4 -> 32.8); at 16 M elements each in its own kernel, whose
+    // registers and grid are for what it reads (4000 x 2000 x 2000 65.2 against
+    // 67.0, 15448 x 7164 x 88 260 against 306).
+    const bool small = T <= kFewRowsOfDz || n + xn + copies.bytes() / 4 < 12e6;
+    if (small && (copies.n > 0 || unpack)) {
+      const Pack8 none{};
+      DION3_CUDA(traced_launch("prepare", 0.0, bytes + copies.bytes() + xn * (2 + 33.0 / 32), s,
+                               [&] {
+                                 return launch_prepare(a, copies.job, copies.n, T, K, unpack ? pack(g->x8) : none, x,
+                                                       s);
+                               }),
+                 "gradient preparation launch");
+      copies.n = 0;
+      unpacked = true;
+    } else {
+      DION3_CUDA(traced_launch("act_grad", 0.0, bytes, s, [&] { return launch_act_grad(a, s); }),
+                 "activation gradient launch");
+    }
   }
   DION3_CUDA(copies.run(s), "repitch launch");
   if (want_dx) {
@@ -478,7 +500,7 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
                "dx launch");
   }
   if (want_dw) {
-    if (x8)
+    if (unpack && !unpacked)
       DION3_CUDA(traced_launch("unpack8", 0.0, static_cast<double>(T) * K * (2 + 33.0 / 32), s,
                                [&] { return launch_unpack8(T, K, pack(g->x8), dt, x, s); }),
                  "unpack8 launch");

@@ -347,21 +347,20 @@ __global__ void __launch_bounds__(256, ANY ? 3 : 4) pack8_kernel(int rows, int c
   }
 }
 
-template <typename T, int VEC, bool ANY>
-__global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pack8 in, Mat out) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ StoreBuf<ANY, 8> sbuf;
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
-  const int step = gridDim.y * blockDim.y;
-  int row = blockIdx.y * blockDim.y + threadIdx.y;
+// Blocks of 8 warps in x strips of 32 VEC columns, y deep in rows.
+template <typename T, int VEC, bool ANY, bool ANY_CODES>
+__device__ __forceinline__ void unpack_rows(int rows, int cols, const Pack8& in, const Mat& out, int x, int y, int ny,
+                                            uint4* buf) {
+  const int c = (x * 32 + threadIdx.x % 32) * VEC;
+  const int step = ny * 8;
+  int row = y * 8 + (threadIdx.y * blockDim.x + threadIdx.x) / 32;
   const int8_t* pq = in.q + row * in.ldq + c;
   const uint8_t* ps = in.s + row * in.lds + c / kPackBlock;
   T* po = static_cast<T*>(out.p) + row * out.ld + c;
   const long long dq = step * in.ldq, ds = step * in.lds, dst = step * out.ld;
   const bool aligned = codes_aligned(in);
   for (; row < rows; row += kWalk * step) {
-    Codes<VEC, ANY> q[kWalk];
+    Codes<VEC, ANY_CODES> q[kWalk];
 #pragma unroll
     for (int i = 0; i < kWalk; ++i, pq += dq, ps += ds)
       q[i].load(pq, ps, row + i * step < rows ? cols - c : 0, aligned);
@@ -370,9 +369,16 @@ __global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pac
       if (row + i * step >= rows) break;
       float v[VEC];
       q[i].values(v);
-      store_cols<T, VEC, ANY>(po, c, cols, v, sbuf.mine());
+      store_cols<T, VEC, ANY>(po, c, cols, v, buf);
     }
   }
+}
+template <typename T, int VEC, bool ANY>
+__global__ void __launch_bounds__(256, 4) unpack8_kernel(int rows, int cols, Pack8 in, Mat out) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ StoreBuf<ANY, 8> sbuf;
+  unpack_rows<T, VEC, ANY, ANY>(rows, cols, in, out, blockIdx.x, blockIdx.y, gridDim.y, sbuf.mine());
 }
 
 // --------------------------------------------------------------------------
@@ -674,18 +680,20 @@ __global__ void __launch_bounds__(32 * kChains) column_sum_kernel(const float* p
 // Activation gradient and bias gradient.  Bound by HBM.  A warp takes 32 VEC
 // columns and walks the rows kWalk at a time; the 8 warps' column sums of a CTA
 // meet in shared memory and go to one row of the partials.  16384 x 11008, silu
-// from blocks: 152 us, 6.0 TB/s.
+// from blocks: 152 us, 6.0 TB/s.  The arguments are read where the launch put
+// them: with a copy of them, rows of any alignment take 231 us instead of 139
+// (15448 x 7164, silu).
 // --------------------------------------------------------------------------
+struct StripSums {
+  float warp[8][256];
+};
 template <typename T, bool ANY, int ACT, bool Z8>
-__global__ void __launch_bounds__(256, ANY ? 2 : 3) act_grad_kernel(ActGradArgs a) {
+__device__ __forceinline__ void act_grad_rows(const ActGradArgs& a, int x, int y, int ny, StripSums& sums) {
   constexpr int VEC = 8;
-  pdl_trigger();
-  pdl_wait();
-  __shared__ float red[8][32 * VEC];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-  const int c = (blockIdx.x * 32 + lane) * VEC;
-  const int step = gridDim.y * 8;
-  int row = blockIdx.y * 8 + w;
+  const int c = (x * 32 + lane) * VEC;
+  const int step = ny * 8;
+  int row = y * 8 + w;
   const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rz(a.z, a.rows, a.cols);
   const T *py = ry.at(row, c), *pz = rz.at(row, c);
   const bool aligned = codes_aligned(a.z8);
@@ -728,37 +736,37 @@ __global__ void __launch_bounds__(256, ANY ? 2 : 3) act_grad_kernel(ActGradArgs 
   }
   if (a.db == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) red[w][lane + 32 * j] = sum[j];
+  for (int j = 0; j < VEC; ++j) sums.warp[w][lane + 32 * j] = sum[j];
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * VEC; i += 256) {
-    float s = red[0][i];
+  const int i = threadIdx.x;
+  float s = sums.warp[0][i];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += red[k][i];
-    const int col = (blockIdx.x * 32 + i % 32) * VEC + i / 32;
-    if (col >= a.cols) continue;
-    if (gridDim.y > 1)
-      a.partials[static_cast<long long>(blockIdx.y) * a.cols + col] = s;
-    else
-      a.db[col] = a.accumulate ? a.db[col] + s : s;
-  }
+  for (int k = 1; k < 8; ++k) s += sums.warp[k][i];
+  const int col = (x * 32 + i % 32) * VEC + i / 32;
+  if (col >= a.cols) return;
+  if (ny > 1)
+    a.partials[static_cast<long long>(y) * a.cols + col] = s;
+  else
+    a.db[col] = a.accumulate ? a.db[col] + s : s;
 }
-
-// Copies up to two matrices (blockIdx.z) to pitches that hold whole 16-byte
-// pieces.  Bound by HBM: 15448 x 7164 in 70 us, 6.3 TB/s.
-struct RepitchArgs {
-  Repitch job[2];
-};
-__global__ void __launch_bounds__(256, 4) repitch_kernel(RepitchArgs a) {
+template <typename T, bool ANY, int ACT, bool Z8>
+__global__ void __launch_bounds__(256, ANY ? 2 : 3) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
   pdl_trigger();
   pdl_wait();
+  __shared__ StripSums sums;
+  act_grad_rows<T, ANY, ACT, Z8>(a, blockIdx.x, blockIdx.y, gridDim.y, sums);
+}
+
+// Copies a matrix to a pitch that holds whole 16-byte pieces.  Bound by HBM:
+// 15448 x 7164 in 70 us, 6.3 TB/s.
+__device__ __forceinline__ void repitch_rows(const Repitch& g, int x, int y, int ny) {
   using T = __nv_bfloat16;  // any 16-bit type: nothing is computed
-  const Repitch& g = a.job[blockIdx.z];
   const int rows = g.rows, cols = g.cols;
   const Reader<T, true> r(g.src, rows, cols);
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const int c = (x * 32 + threadIdx.x % 32) * 8;
   if (c >= cols) return;
-  const int step = gridDim.y * blockDim.y;
-  int row = blockIdx.y * blockDim.y + threadIdx.y;
+  const int step = ny * 8;
+  int row = y * 8 + (threadIdx.y * blockDim.x + threadIdx.x) / 32;
   const T* p = r.at(row, c);
   T* d = static_cast<T*>(g.dst.p) + row * g.dst.ld + c;
   const long long ds = step * g.src.ld, dd = step * g.dst.ld;
@@ -773,6 +781,43 @@ __global__ void __launch_bounds__(256, 4) repitch_kernel(RepitchArgs a) {
       *reinterpret_cast<uint4*>(d) = make_uint4(raw[i].w[0], raw[i].w[1], raw[i].w[2], raw[i].w[3]);
     }
   }
+}
+struct RepitchArgs {
+  Repitch job[2];  // by blockIdx.z
+};
+__global__ void __launch_bounds__(256, 4) repitch_kernel(const __grid_constant__ RepitchArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  repitch_rows(a.job[blockIdx.z], blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+// What a small gradient needs before its products, in one launch (each launch
+// less takes some 3 us off it): dz and db, the copies, and x from its blocks,
+// every one over its own run of blocks.
+struct PrepareArgs {
+  ActGradArgs act;
+  Repitch copy[2];
+  int rows, cols;   // x
+  Pack8 x8;
+  Mat x;
+  int first[5];     // blocks before dz, the copies, x, and in all
+  int strips[4];    // strips of each
+};
+template <typename T, int ACT, bool Z8>
+__global__ void __launch_bounds__(256, 2) prepare_kernel(const __grid_constant__ PrepareArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ StripSums sums;
+  int k = 0;
+  while (static_cast<int>(blockIdx.x) >= a.first[k + 1]) ++k;
+  const int at = blockIdx.x - a.first[k], n = a.first[k + 1] - a.first[k];
+  const int x = at % a.strips[k], y = at / a.strips[k], ny = n / a.strips[k];
+  if (k == 0)
+    act_grad_rows<T, true, ACT, Z8>(a.act, x, y, ny, sums);
+  else if (k < 3)
+    repitch_rows(a.copy[k - 1], x, y, ny);
+  else
+    unpack_rows<T, 8, false, true>(a.rows, a.cols, a.x8, a.x, x, y, ny, nullptr);
 }
 
 __global__ void __launch_bounds__(256) zero_kernel(int rows, int cols, int elem_bytes, uint8_t* out, long long ld) {
@@ -980,6 +1025,15 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
                        static_cast<const float*>(a.partials), parts, a.cols, a.dw, a.accumulate);
 }
 
+namespace {
+// db from the activation gradient's partials; one row of them was written to db.
+cudaError_t sum_columns(const float* partials, int parts, int cols, float* db, int accumulate, cudaStream_t s) {
+  if (parts == 1) return cudaSuccess;
+  return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((cols + 31) / 32), dim3(32 * kChains), 0, s, partials,
+                       parts, cols, db, accumulate);
+}
+}  // namespace
+
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, 2) && vec_mat(a.z, 2) && vec_pack(a.z8);
   int parts = 0;
@@ -996,15 +1050,50 @@ cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t s) {
         dim3 grid = walk_grid(k, a.rows, A::lanes(a.cols), kWalk, cache[z8]);
         // Few rows: one block a column strip, which writes db itself (a second
         // kernel takes longer than the rows the strip's warps walk instead).
-        grid.y = a.db != nullptr && a.rows <= 256 ? 1 : std::min<unsigned>(grid.y, kMaxPartials);
+        grid.y = a.db != nullptr && a.rows <= kFewRowsOfDz ? 1 : std::min<unsigned>(grid.y, kMaxPartials);
         parts = static_cast<int>(grid.y);
         return launch_kernel(pdl_enabled(), k, grid, dim3(256), 0, s, a);
       });
     }
   });
-  if (e != cudaSuccess || a.db == nullptr || parts == 1) return e;
-  return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
-                       static_cast<const float*>(a.partials), parts, a.cols, a.db, a.accumulate);
+  return e != cudaSuccess || a.db == nullptr ? e : sum_columns(a.partials, parts, a.cols, a.db, a.accumulate, s);
+}
+
+cudaError_t launch_prepare(const ActGradArgs& act, const Repitch* copies, int ncopies, int rows, int cols, Pack8 x8,
+                           Mat x, cudaStream_t s) {
+  PrepareArgs a{};
+  a.act = act;
+  a.rows = rows;
+  a.cols = cols;
+  a.x8 = x8;
+  a.x = x;
+  // Blocks of a job: whole strips, a wave of the device at most.
+  int n = 0;
+  const auto add = [&](int k, int r, int c, int most) {
+    if (r > 0) {
+      a.strips[k] = (c + 255) / 256;
+      n += a.strips[k] * std::max(1, std::min({(r + 8 * kWalk - 1) / (8 * kWalk), 2 * sm_count() / a.strips[k], most}));
+    }
+    a.first[k + 1] = n;
+  };
+  add(0, act.rows, act.cols, act.db != nullptr && act.rows <= kFewRowsOfDz ? 1 : kMaxPartials);
+  const int parts = n / a.strips[0];
+  for (int k = 0; k < 2; ++k) {
+    if (k < ncopies) a.copy[k] = copies[k];
+    add(1 + k, k < ncopies ? copies[k].rows : 0, k < ncopies ? copies[k].cols : 0, 1 << 30);
+  }
+  add(3, x8.q != nullptr ? rows : 0, cols, 1 << 30);
+  const cudaError_t e = by_act(act.act, [&](auto t) {
+    constexpr int ACT = decltype(t)::value;
+    const bool z8 = act.z8.q != nullptr;
+    auto run = [&](auto v) {
+      using T = decltype(v);
+      auto k = z8 ? prepare_kernel<T, ACT, ACT != kActNone> : prepare_kernel<T, ACT, false>;
+      return launch_kernel(pdl_enabled(), k, dim3(n), dim3(256), 0, s, a);
+    };
+    return act.dtype == kBF16 ? run(__nv_bfloat16{}) : run(__half{});
+  });
+  return e != cudaSuccess || act.db == nullptr ? e : sum_columns(act.partials, parts, act.cols, act.db, act.accumulate, s);
 }
 
 cudaError_t launch_repitch(const Repitch* jobs, int n, cudaStream_t s) {

@@ -70,14 +70,26 @@ _LINEAR_GRAD = struct.Struct("@5i4x" + "Pqi4x" * 4 + "PqPq" * 2 + "Pqi4x" * 2 + 
 assert (_MAT.size, _LINEAR.size, _LINEAR_GRAD.size) == tuple(map(ctypes.sizeof, (_Matrix, _LinearArgs, _LinearGradArgs)))
 _NO_MAT, _NO_PACK = (0, 0, 0), (0, 0, 0, 0)
 
-_DTYPES = {}
 _FNS = {}
+_torch = None
+_DTYPES = {}
+
+
+def _load_torch():
+    """torch, and the dtypes' codes (on first use: importing this module needs neither)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16})
+        _torch = torch
+    return _torch
 
 
 def _fn(name: str):
     """The library's entry point, taking structures as bytes."""
     f = _FNS.get(name)
     if f is None:
+        _load_torch()
         res, args = SIGS[name]
         args = [_vp if isinstance(a, type) and issubclass(a, ctypes._Pointer) else a for a in args]
         f = _FNS[name] = ctypes.CFUNCTYPE(res, *args)((name, _d3.load_library()))
@@ -86,24 +98,36 @@ def _fn(name: str):
 
 def _dtype(t) -> int:
     """dion3_dtype of a tensor."""
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16})
-    code = _DTYPES.get(t.dtype)
-    if code is None:
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        pass
+    _load_torch()
+    if t.dtype not in _DTYPES:
         raise ValueError(f"dtype {t.dtype} is not float32, bfloat16 or float16")
-    return code
+    return _DTYPES[t.dtype]
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        t = _torch or _load_torch()
+        return t._C._cuda_getCurrentRawStream(t._C._cuda_getDevice()) or None
     return _d3._stream(stream)
 
 
 def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -> tuple:
     """(data, ld, dtype) of a 2-D CUDA tensor with contiguous rows; shape checked where given."""
+    try:
+        (r, c), (ld, inner) = t.shape, t.stride()
+        if t.is_cuda and inner == 1 and ld >= c and (rows is None or r == rows) and (cols is None or c == cols):
+            return t.data_ptr(), ld, _DTYPES[t.dtype]
+    except (ValueError, KeyError):
+        pass
+    return _mat_checked(name, t, rows, cols)
+
+
+def _mat_checked(name: str, t, rows, cols) -> tuple:
+    """The same, case by case: what is wrong, or the layouts whose strides say nothing."""
     if not t.is_cuda:
         raise ValueError(f"{name} is not a CUDA tensor")
     shape = t.shape
@@ -124,7 +148,7 @@ def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -
 
 
 def _vec(name: str, t, n: int, f32: bool = False) -> int:
-    if not t.is_cuda or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ValueError(f"{name} must be a contiguous CUDA vector of {n}")
     if f32 and _dtype(t) != _d3.F32:
         raise ValueError(f"{name} must be float32")
