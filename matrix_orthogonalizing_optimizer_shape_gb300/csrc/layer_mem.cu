@@ -8,6 +8,7 @@
 // short chains of small kernels, where that takes a microsecond or two off each.
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "layer_math.cuh"
@@ -23,11 +24,12 @@ __device__ __forceinline__ float load_w(const void* w, int dtype, int c) {
   return __half2float(static_cast<const __half*>(w)[c]);
 }
 
-// The gain of VEC columns from c, 0 past the last.
+// The gain of VEC columns from c, 0 outside the row.
 template <int VEC>
 __device__ __forceinline__ void load_gain(const void* w, int dtype, int c, int cols, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
-    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
+    if (c + 8 <= cols && ((reinterpret_cast<uintptr_t>(w) | static_cast<uintptr_t>(c)) & 7u) == 0 &&
+        (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
       if (dtype == kF32)
         load_vec<float, 8>(static_cast<const float*>(w) + c, v);
       else if (dtype == kBF16)
@@ -38,7 +40,7 @@ __device__ __forceinline__ void load_gain(const void* w, int dtype, int c, int c
     }
   }
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) v[j] = c + j < cols ? load_w(w, dtype, c + j) : 0.f;
+  for (int j = 0; j < VEC; ++j) v[j] = c + j >= 0 && c + j < cols ? load_w(w, dtype, c + j) : 0.f;
 }
 
 // --------------------------------------------------------------------------
@@ -602,6 +604,244 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
   }
 }
 
+// --------------------------------------------------------------------------
+// Norms of rows through shared memory: rows are copied ahead of their use, as the
+// aligned 16-byte pieces of memory that they lie in, so that registers hold no
+// row but the block's own.  A thread holds columns 8 t - lead and the seven after
+// it, where lead is what the rows begin after a 16-byte boundary: whole pieces of
+// memory, of which only a row's first and last are taken element by element.  All
+// matrices have to be misaligned alike (tensors of one shape are), and a block's
+// rows are a multiple of 8 apart, which keeps its lead the same.  bf16, against
+// the shifted access of the kernels above: 16384 x 4095 with residual 101 us for
+// 161, 12000 x 11007 193 for 387; gradient of 6568 x 4353 60 for 107, of 12000 x
+// 11007 216 for 734.  Two thirds of the issue slots are used by the barriers' and
+// conversions' instructions: the gradient gains from more pieces a thread (16384
+// x 4095 124 us with 256 threads, 185 with 512).
+// --------------------------------------------------------------------------
+__device__ __forceinline__ void copy_piece(uint4* dst, uintptr_t src, int bytes) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `behind` (0 to 2) of the thread's groups are unfinished.
+__device__ __forceinline__ void copies_wait(int behind) {
+  if (behind == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (behind == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+// Rows of up to three matrices in a ring of `depth` (2 to 4) in shared memory.
+template <typename T, int MATS>
+struct Staged {
+  uintptr_t base[MATS];
+  long long step[MATS];  // bytes from a row of the block to the next
+  uintptr_t next[MATS];  // the next row to copy
+  long long ahead;       // its number
+  int rows, bytes, depth, pitch, to = 0, from = 0;
+  uint4* ring;  // [depth][MATS][pitch]
+  __device__ __forceinline__ Staged(uint4* ring_, int depth_, int pitch_, int rows_, int cols)
+      : ahead(blockIdx.x), rows(rows_), bytes(cols * static_cast<int>(sizeof(T))), depth(depth_), pitch(pitch_),
+        ring(ring_) {}
+  __device__ __forceinline__ void add(int k, const Mat& m) {
+    base[k] = reinterpret_cast<uintptr_t>(m.p);
+    next[k] = base[k] + blockIdx.x * m.ld * static_cast<long long>(sizeof(T));
+    step[k] = gridDim.x * m.ld * static_cast<long long>(sizeof(T));
+  }
+  // Begins the copy of the block's next row; nothing outside the matrix is read.
+  __device__ __forceinline__ void copy() {
+    if (ahead < rows) {
+#pragma unroll
+      for (int k = 0; k < MATS; ++k) {
+        uint4* dst = ring + (to * MATS + k) * pitch;
+        const int lead = static_cast<int>(next[k] & 15u), all = lead + bytes;
+        const uintptr_t lo = next[k] - lead;
+        // Past the row's last element is another row, but for the last row.
+        const int end = ahead + 1 < rows ? (all + 15) / 16 * 16 : all;
+        for (int o = static_cast<int>(threadIdx.x) * 16; o < all; o += static_cast<int>(blockDim.x) * 16) {
+          if (lo + o >= base[k]) {
+            copy_piece(dst + o / 16, lo + o, min(16, end - o));
+          } else {  // the first row of an unaligned matrix
+            for (int j = lead; j < 16 && j < all; j += sizeof(T))
+              reinterpret_cast<T*>(dst)[j / sizeof(T)] = *reinterpret_cast<const T*>(lo + j);
+          }
+        }
+        next[k] += step[k];
+      }
+    }
+    copies_commit();
+    ahead += gridDim.x;
+    to = to + 1 == depth ? 0 : to + 1;
+  }
+  __device__ __forceinline__ void begin() {
+    for (int i = 1; i < depth; ++i) copy();
+  }
+  // Waits for the block's next row, frees the one before it and copies ahead.
+  __device__ __forceinline__ const uint4* row() {
+    copies_wait(depth - 2);
+    __syncthreads();
+    copy();
+    const uint4* r = ring + from * MATS * pitch;
+    from = from + 1 == depth ? 0 : from + 1;
+    return r;
+  }
+};
+// The eight columns from c of a copied row, zeros outside it (without EDGE: the
+// row begins on a boundary and is a multiple of 8 columns long).
+template <typename T, bool EDGE>
+__device__ __forceinline__ void staged_cols(const uint4* row, int c, int lead, int cols, float (&v)[8]) {
+  Raw<T, 8, false> raw;
+  const uint4* p = row + (c + lead) * static_cast<int>(sizeof(T)) / 16;
+#pragma unroll
+  for (int i = 0; i < Raw<T, 8, false>::kWords / 4; ++i) {
+    const uint4 u = c < cols ? p[i] : make_uint4(0u, 0u, 0u, 0u);
+    raw.w[4 * i] = u.x, raw.w[4 * i + 1] = u.y, raw.w[4 * i + 2] = u.z, raw.w[4 * i + 3] = u.w;
+  }
+  raw.values(v);
+  if (!EDGE || (c >= 0 && c + 8 <= cols)) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < 0 || c + j >= cols) v[j] = 0.f;
+}
+template <typename T, bool EDGE>
+__device__ __forceinline__ void store_staged(const Mat& m, long long row, int c, int cols, const float (&v)[8]) {
+  T* p = static_cast<T*>(m.p) + row * m.ld + c;
+  if (c >= 0 && c + 8 <= cols) {
+    store_vec<T, 8>(p, v);
+    return;
+  }
+  if (!EDGE) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j >= 0 && c + j < cols) p[j] = from_f32<T>(v[j]);
+}
+// Elements between a 16-byte boundary and the block's rows.
+template <typename T>
+__device__ __forceinline__ int lead_of(const Mat& m) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(m.p) + blockIdx.x * m.ld) % 16 / sizeof(T));
+}
+
+template <typename T, int NV, bool RES>
+__global__ void __launch_bounds__(kRowThreads) rms_norm_staged_kernel(const __grid_constant__ NormArgs a, int depth,
+                                                                      int pitch) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ __align__(16) float red[64];
+  extern __shared__ uint4 ring[];
+  int flip = 0;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
+  const int span = blockDim.x * 8, lead = lead_of<T>(a.x), first = static_cast<int>(threadIdx.x) * 8 - lead;
+  Staged<T, 1 + RES> rows(ring, depth, pitch, a.rows, a.cols);
+  rows.add(0, a.x);
+  if constexpr (RES) rows.add(1, a.residual);
+  rows.begin();
+  float w[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load_gain<8>(a.w, a.w_dtype, first + i * span, a.cols, w[i]);
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const uint4* st = rows.row();
+    float v[NV][8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * span;
+      staged_cols<T, true>(st, c, lead, a.cols, v[i]);
+      if constexpr (RES) {
+        float t[8];
+        staged_cols<T, true>(st + pitch, c, lead, a.cols, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += t[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    ss = cta_sum(ss, red, flip);
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
+    if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * span;
+      if (a.h.p) store_staged<T, true>(a.h, row, c, a.cols, v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[i][j];
+      if (a.y.p) store_staged<T, true>(a.y, row, c, a.cols, v[i]);
+    }
+  }
+  copies_wait(0);
+}
+
+template <typename T, bool EDGE, int NV, bool DH>
+__global__ void __launch_bounds__(kRowThreads) rms_norm_grad_staged_kernel(const __grid_constant__ NormGradArgs a,
+                                                                           int depth, int pitch) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ __align__(16) float red[64];
+  extern __shared__ uint4 ring[];
+  constexpr bool kKeep = NV <= 2;  // the row's values stay in registers until its sum is known
+  int flip = 0;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
+  const int span = blockDim.x * 8, lead = EDGE ? lead_of<T>(a.h) : 0, first = static_cast<int>(threadIdx.x) * 8 - lead;
+  Staged<T, 2 + DH> rows(ring, depth, pitch, a.rows, a.cols);
+  rows.add(0, a.dy);
+  rows.add(1, a.h);
+  if constexpr (DH) rows.add(2, a.dh);
+  rows.begin();
+  float w[NV][8], dw[NV][8] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load_gain<8>(a.w, a.w_dtype, first + i * span, a.cols, w[i]);
+  float rstd_next = a.rstd[blockIdx.x];
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float rstd = rstd_next;
+    if (row + gridDim.x < a.rows) rstd_next = a.rstd[row + gridDim.x];
+    const uint4* st = rows.row();
+    float g[kKeep ? NV : 1][8], hn[kKeep ? NV : 1][8], s = 0.f;
+    auto load = [&](int i, float (&gi)[8], float (&hi)[8]) {
+      const int c = first + i * span;
+      staged_cols<T, EDGE>(st, c, lead, a.cols, gi);
+      staged_cols<T, EDGE>(st + pitch, c, lead, a.cols, hi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hi[j] = __fmul_rn(hi[j], rstd);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float (&gi)[8] = g[kKeep ? i : 0], (&hi)[8] = hn[kKeep ? i : 0];
+      load(i, gi, hi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[i][j] = fmaf(gi[j], hi[j], dw[i][j]);
+        gi[j] = __fmul_rn(gi[j], w[i][j]);
+        s = fmaf(gi[j], hi[j], s);
+      }
+    }
+    s = cta_sum(s, red, flip) * inv_cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * span;
+      float (&gi)[8] = g[kKeep ? i : 0], (&hi)[8] = hn[kKeep ? i : 0], d[8] = {};
+      if constexpr (!kKeep) {
+        load(i, gi, hi);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gi[j] = __fmul_rn(gi[j], w[i][j]);
+      }
+      if constexpr (DH) staged_cols<T, EDGE>(st + 2 * pitch, c, lead, a.cols, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = norm_dx(gi[j], hi[j], s, rstd, d[j]);
+      store_staged<T, EDGE>(a.dx, row, c, a.cols, d);
+    }
+  }
+  copies_wait(0);
+  if (a.dw == nullptr) return;
+  float* part = a.partials + static_cast<long long>(blockIdx.x) * a.cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * span;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j >= 0 && c + j < a.cols) part[c + j] = dw[i][j];
+  }
+}
+
 // The same for rows too wide for that: read twice, column sums in shared memory.
 template <typename T, int VEC, bool ANY>
 __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a) {
@@ -615,9 +855,9 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
   const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rh(a.h, a.rows, a.cols), rd(a.dh, a.rows, a.cols);
   const int span = blockDim.x * VEC;
   const int padded = (a.cols + span - 1) / span * span;
+  // A thread's own slots: the words of a piece blockDim.x apart.
   if (a.dw != nullptr)
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) colsum[c] = 0.f;
-  __syncthreads();
+    for (int c = threadIdx.x; c < padded; c += blockDim.x) colsum[c] = 0.f;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float rstd = a.rstd[row];
     float s = 0.f, dy[VEC], h[VEC], w[VEC];
@@ -630,7 +870,7 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
     }
     s = cta_sum(s, red, flip) * inv_cols;
     for (int c = threadIdx.x * VEC; c < padded; c += span) {
-      float d[VEC] = {};
+      float d[VEC] = {}, *sums = colsum + (c - threadIdx.x * VEC) + threadIdx.x;
       load_cols<T, VEC, ANY>(ry, row, c, a.cols, dy);
       load_cols<T, VEC, ANY>(rh, row, c, a.cols, h);
       if (a.dh.p) load_cols<T, VEC, ANY>(rd, row, c, a.cols, d);
@@ -639,15 +879,18 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_wide_kernel(NormGradArgs a
       for (int j = 0; j < VEC; ++j) {
         const float hn = __fmul_rn(h[j], rstd);
         d[j] = norm_dx(__fmul_rn(dy[j], w[j]), hn, s, rstd, d[j]);
-        if (a.dw != nullptr && c + j < a.cols) colsum[c + j] = fmaf(dy[j], hn, colsum[c + j]);
+        if (a.dw != nullptr) sums[j * blockDim.x] = fmaf(dy[j], hn, sums[j * blockDim.x]);
       }
       store_cols<T, VEC, ANY>(static_cast<T*>(a.dx.p) + row * a.dx.ld + c, c, a.cols, d, sbuf.mine());
     }
   }
-  __syncthreads();
-  if (a.dw != nullptr)
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x)
-      a.partials[static_cast<long long>(blockIdx.x) * a.cols + c] = colsum[c];
+  if (a.dw == nullptr) return;
+  for (int c = threadIdx.x * VEC; c < a.cols; c += span)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < a.cols)
+        a.partials[static_cast<long long>(blockIdx.x) * a.cols + c + j] =
+            colsum[(c - threadIdx.x * VEC) + threadIdx.x + j * blockDim.x];
 }
 
 // out[c] (+)= sum over p of partials[p][c], in order of p within each of
@@ -966,10 +1209,89 @@ cudaError_t launch_unpack8(int rows, int cols, Pack8 in, int dtype, Mat out, cud
   });
 }
 
+namespace {
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <typename K>
+cudaError_t allow_smem(K k, int bytes, std::once_flag* once) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess)
+    std::call_once(once[dev & 63],
+                   [&] { err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  return err;
+}
+
+// Whether rows of both are misaligned alike.
+bool alike(const Mat& a, const Mat& b, int elem_bytes) {
+  return b.p == nullptr || ((reinterpret_cast<uintptr_t>(a.p) - reinterpret_cast<uintptr_t>(b.p)) % 16 == 0 &&
+                            (a.ld - b.ld) * elem_bytes % 16 == 0);
+}
+
+// Rows of `mats` matrices through shared memory: pieces a thread (NV, 0: they do
+// not fit), threads, rows in shared memory and pieces of a row there.
+constexpr int kStagedBytes = 220 * 1024;  // of a block at most
+struct StagedPlan {
+  int nv = 0, threads, depth, pitch, row;
+  StagedPlan(int cols, int elem_bytes, int mats) {
+    pitch = cols * elem_bytes / 16 + 3;
+    row = mats * pitch * 16;
+    const RowShape r = row_shape((cols + 16 / elem_bytes - 1 + 7) / 8, 256, kRowThreads, 4);
+    threads = r.block.x;
+    if (2 * row <= kStagedBytes) nv = r.nv;
+  }
+  // Blocks the device holds, of the most an SM has registers for: as many as
+  // leave each two rows.
+  int blocks(int most) {
+    for (int n = std::max(1, most / sm_count());; --n) {
+      depth = std::min(4, (kStagedBytes / n - 2 * 1024) / row);
+      if (depth >= 2 || n == 1) {
+        depth = std::max(depth, 2);
+        return n * sm_count();
+      }
+    }
+  }
+};
+template <typename F>
+cudaError_t by_type(int dtype, F&& f) {
+  if (dtype == kF32) return f(0.f);
+  if (dtype == kBF16) return f(__nv_bfloat16{});
+  return f(__half{});
+}
+// Launches kernel k (one of nkernels) over rows of a staged plan; `grid` gets
+// the blocks: a multiple of 8 that are at most `most`, unless every row has one.
+template <typename K, typename A>
+cudaError_t launch_staged(K k, StagedPlan p, const A& a, int most, int* grid, std::once_flag* once,
+                          std::atomic<int>* cache, cudaStream_t s) {
+  const cudaError_t e = allow_smem(k, kStagedBytes, once);
+  if (e != cudaSuccess) return e;
+  *grid = std::min(p.blocks(resident(k, p.threads, 0, cache)), most);
+  *grid = a.rows <= *grid ? a.rows : std::max(8, *grid / 8 * 8);
+  return launch_kernel(pdl_enabled(), k, dim3(*grid), dim3(p.threads), static_cast<size_t>(p.depth) * p.row, s, a,
+                       p.depth, p.pitch);
+}
+}  // namespace
+
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
   const int eb = elem_bytes(a.dtype);
   const bool vec = a.cols % 8 == 0 && vec_mat(a.x, eb) && vec_mat(a.residual, eb) && vec_mat(a.h, eb) &&
                    vec_mat(a.y, eb) && vec_pack(a.y8);
+  const bool res = a.residual.p != nullptr;
+  // Misaligned rows (up to 240 columns no faster).  Blocks of 8 bits are 32 columns
+  // of a row, wherever it begins.
+  const StagedPlan p(a.cols, eb, 1 + res);
+  if (!vec && a.y8.q == nullptr && a.cols > 240 && p.nv > 0 && alike(a.x, a.residual, eb) && alike(a.x, a.h, eb) &&
+      alike(a.x, a.y, eb))
+    return by_type(a.dtype, [&](auto t) {
+      return by_nv<4>(p.nv, [&](auto n) {
+        using T = decltype(t);
+        constexpr int NV = decltype(n)::value;
+        static std::once_flag once[2][64];
+        static std::atomic<int> cache[2][kRowThreads / 32 + 1];
+        auto k = res ? rms_norm_staged_kernel<T, NV, true> : rms_norm_staged_kernel<T, NV, false>;
+        int grid;
+        return launch_staged(k, p, a, 1 << 30, &grid, once[res], cache[res], s);
+      });
+    });
   return by_access(a.dtype, vec, [&](auto acc) {
     using A = decltype(acc);
     using T = typename A::T;
@@ -980,7 +1302,6 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
     return by_nv<A::kPieces>(r.nv, [&](auto n) {
       constexpr int NV = decltype(n)::value;
       static std::atomic<int> cache[2][kRowThreads / 32 + 1];
-      const bool res = a.residual.p != nullptr;
       auto k = res ? rms_norm_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_kernel<T, A::VEC, A::ANY, NV, false>;
       const int threads = r.block.x * r.block.y;
       const long long blocks = (static_cast<long long>(a.rows) + r.block.y - 1) / r.block.y;
@@ -993,33 +1314,61 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
 cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   const int eb = elem_bytes(a.dtype);
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, eb) && vec_mat(a.h, eb) && vec_mat(a.dh, eb) && vec_mat(a.dx, eb);
-  int parts = 0;  // rows of partial column sums
-  const cudaError_t e = by_access(a.dtype, vec, [&](auto acc) {
-    using A = decltype(acc);
-    using T = typename A::T;
-    const RowShape r = row_shape(A::lanes(a.cols), 256, kRowThreads, A::kGradPieces);
-    if (r.nv == 0) {
-      auto k = rms_norm_grad_wide_kernel<T, A::VEC, A::ANY>;
-      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4);
-      if (e != cudaSuccess) return e;
-      parts = std::min(a.rows, sm_count());
-      return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(1024),
-                           a.dw != nullptr ? static_cast<size_t>(a.cols) * 4 : 0, s, a);
-    }
-    return by_nv<A::kGradPieces>(r.nv, [&](auto n) {
-      constexpr int NV = decltype(n)::value;
-      static std::atomic<int> cache[2][kRowThreads / 32 + 1];
-      const bool dh = a.dh.p != nullptr;
-      auto k = dh ? rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, false>;
-      const int ty = r.block.y, threads = r.block.x * ty;
-      const size_t smem = ty > 1 ? static_cast<size_t>(threads) * A::VEC * NV * 4 : 0;
-      const long long blocks = (static_cast<long long>(a.rows) + ty - 1) / ty;
-      // One row of partials a block, as many at most as the workspace holds.
-      parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
-                                         static_cast<long long>(kMaxPartials)}));
-      return launch_kernel(pdl_enabled(), k, dim3(parts), r.block, smem, s, a);
+  const bool dh = a.dh.p != nullptr;
+  const StagedPlan p(a.cols, eb, 2 + dh);
+  // Where one piece a thread is enough the registers' kernel is as fast or faster
+  // (16384 x 1021 bf16: 37 us against 45; 16384 x 4095 fp32 153 against 155).
+  const bool edge = !vec && a.cols > (eb == 2 ? 1024 : 4096) && alike(a.h, a.dy, eb) && alike(a.h, a.dh, eb) &&
+                    alike(a.h, a.dx, eb);
+  int parts = 0;  // rows of partial column sums, as many at most as the workspace holds
+  cudaError_t e;
+  // Aligned rows of more than two pieces a thread: 16384 x 11008 230 us, read twice
+  // from memory and cache 678.
+  if (p.nv > 0 && (edge || (vec && a.cols > 16 * kRowThreads)))
+    e = by_type(a.dtype, [&](auto t) {
+      return by_nv<4>(p.nv, [&](auto n) {
+        using T = decltype(t);
+        constexpr int NV = decltype(n)::value;
+        static std::once_flag once[4][64];
+        static std::atomic<int> cache[4][kRowThreads / 32 + 1];
+        const auto launch = [&](auto k, int i) {
+          return launch_staged(k, p, a, kMaxPartials, &parts, once[i], cache[i], s);
+        };
+        if constexpr (NV == 4)  // aligned rows that narrow are in registers
+          if (vec)
+            return dh ? launch(rms_norm_grad_staged_kernel<T, false, NV, true>, 0)
+                      : launch(rms_norm_grad_staged_kernel<T, false, NV, false>, 1);
+        return dh ? launch(rms_norm_grad_staged_kernel<T, true, NV, true>, 2)
+                  : launch(rms_norm_grad_staged_kernel<T, true, NV, false>, 3);
+      });
     });
-  });
+  else
+    e = by_access(a.dtype, vec, [&](auto acc) {
+      using A = decltype(acc);
+      using T = typename A::T;
+      const RowShape r = row_shape(A::lanes(a.cols), 256, kRowThreads, A::kGradPieces);
+      if (r.nv == 0) {
+        auto k = rms_norm_grad_wide_kernel<T, A::VEC, A::ANY>;
+        static std::once_flag once[64];
+        const cudaError_t e = allow_smem(k, kNormMaxCols * 4, once);
+        if (e != cudaSuccess) return e;
+        const int span = 1024 * A::VEC;
+        parts = std::min(a.rows, sm_count());
+        return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(1024),
+                             a.dw != nullptr ? static_cast<size_t>(a.cols + span - 1) / span * span * 4 : 0, s, a);
+      }
+      return by_nv<A::kGradPieces>(r.nv, [&](auto n) {
+        constexpr int NV = decltype(n)::value;
+        static std::atomic<int> cache[2][kRowThreads / 32 + 1];
+        auto k = dh ? rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, false>;
+        const int ty = r.block.y, threads = r.block.x * ty;
+        const size_t smem = ty > 1 ? static_cast<size_t>(threads) * A::VEC * NV * 4 : 0;
+        const long long blocks = (static_cast<long long>(a.rows) + ty - 1) / ty;
+        parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
+                                           static_cast<long long>(kMaxPartials)}));
+        return launch_kernel(pdl_enabled(), k, dim3(parts), r.block, smem, s, a);
+      });
+    });
   if (e != cudaSuccess || a.dw == nullptr) return e;
   return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
                        static_cast<const float*>(a.partials), parts, a.cols, a.dw, a.accumulate);

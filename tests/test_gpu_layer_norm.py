@@ -186,6 +186,73 @@ def test_rms_norm_backward(cuda_lib, dtype, rows, cols, strided):
         dh.copy_(keep)
 
 
+def among_nans(rng, rows, cols, dtype, scale, pad, shift):
+    """As dev, with NaN in everything that is not the matrix."""
+    buf = torch.full((rows * (cols + pad) + shift + 8,), float("nan"), dtype=torch_dtype(dtype), device="cuda")
+    v = buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    v.copy_(torch.from_numpy(rng.standard_normal((rows, cols)) * scale))
+    return v
+
+
+# Rows misaligned alike are copied ahead through shared memory: enough of them that a block takes several, of every
+# number of pieces a thread, and aligned ones too wide for registers.  The last form's results are aligned otherwise.
+LONG = [(4000, 250), (4000, 1031), (1500, 2049), (900, 5003), (640, 9001), (320, 8208), (7, 12001), (9, 301)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", LONG)
+@pytest.mark.parametrize("pad,shift,other", [(0, 0, 0), (3, 1, 0), (6, 5, 1)])
+def test_rms_norm_of_many_rows(cuda_lib, dtype, rows, cols, pad, shift, other):
+    rng = np.random.default_rng(rows + cols + pad)
+    x, r = (among_nans(rng, rows, cols, dtype, s, pad, shift) for s in (0.7, 2.0))
+    w = vec(rng, cols, dtype)
+    slack = norm_slack(cols)
+    for res in (None, r):
+        y, ybuf = out(rows, cols, dtype, pad, shift + other)
+        h, hbuf = out(rows, cols, dtype, pad, shift) if res is not None else (None, None)
+        rstd = torch.empty(rows, dtype=torch.float32, device="cuda")
+        d3.rms_norm(x, w, y, residual=res, h=h, rstd=rstd, eps=1e-5)
+        hr, sr, yr = norm_ref(host(x), None if res is None else host(res), host(w), 1e-5)
+        check(host(rstd), sr, sr * slack, "rstd")
+        err = np.abs(yr) * (slack + 3 * 2.0 ** -24)
+        check(host(y), yr, err + np.abs(yr) * U[dtype] * (1 + slack) + TINY[dtype], "y")
+        assert untouched(y, ybuf)
+        if h is not None:
+            check(host(h), hr, np.abs(hr) * (U[dtype] + 2.0 ** -24) + TINY[dtype], "h")
+            assert untouched(h, hbuf)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", LONG)
+@pytest.mark.parametrize("pad,shift,other", [(0, 0, 0), (3, 1, 0), (6, 5, 1)])
+def test_rms_norm_backward_of_many_rows(cuda_lib, dtype, rows, cols, pad, shift, other):
+    rng = np.random.default_rng(rows * 3 + cols + pad)
+    h, dy, stream = (among_nans(rng, rows, cols, dtype, s, pad, shift) for s in (1.5, 0.1, 0.1))
+    w = vec(rng, cols, dtype)
+    rstd = torch.from_numpy(1 / np.sqrt((host(h) ** 2).mean(1) + 1e-6)).to("cuda").float()
+    ws = d3.alloc_workspace(d3.rms_norm_backward_workspace_size(rows, cols))
+    for dh in (None, stream):
+        dx, buf = out(rows, cols, dtype, pad, shift + other)
+        dw = torch.full((cols,), 3.0, device="cuda")
+        d3.rms_norm_backward(dy, h, w, rstd, dx, dh=dh, dw=dw, ws=ws)
+        a = [host(dy), host(h), host(w), host(rstd), None if dh is None else host(dh)]
+        dxr, dwr = norm_grad_ref(*a)
+        hn = np.abs(a[1] * a[3][:, None])
+        mean = (np.abs(a[0] * a[2]) * hn).mean(1, keepdims=True)
+        err = (np.abs(a[0] * a[2]) * 4 + hn * mean * (128 + 16)) * a[3][:, None] * 2.0 ** -24
+        err = err + (0 if dh is None else np.abs(dxr) * 2.0 ** -23)
+        check(host(dx), dxr, err + (np.abs(dxr) + err) * U[dtype] + TINY[dtype], "dx")
+        assert untouched(dx, buf)
+        check(host(dw), dwr, (np.abs(a[0]) * hn).sum(0) * (min(rows, 640) + 8) * 2.0 ** -24, "dw")
+        first = dw.clone()
+        d3.rms_norm_backward(dy, h, w, rstd, dx, dh=dh, dw=dw, ws=ws)
+        assert torch.equal(dw, first), "the same call gives the same bits"
+    same = dx.clone()
+    d3.rms_norm_backward(dy, h, w, rstd, stream, dh=stream)  # in place over dh, without dw and its workspace
+    if not other:
+        assert torch.equal(stream, same)
+
+
 def test_rms_norm_backward_against_differences(cuda_lib):
     rng = np.random.default_rng(2)
     x, w, c = rng.standard_normal((3, 24)), 1 + 0.3 * rng.standard_normal(24), rng.standard_normal((3, 24))
