@@ -292,16 +292,22 @@ struct Codes {
 
 // Sum over the threads of a row (blockDim.x, a multiple of 32), the same bits in
 // every one.  `red` (16-byte aligned) alternates between two halves so one
-// barrier a call is enough; every thread adds the warps' sums itself.
+// barrier a call is enough; every thread adds the warps' sums itself.  ROWS: the
+// rows of a block (threadIdx.y) wait for their own threads alone, at barriers of
+// their own (of which an SM has few: only where few blocks are wanted).
+template <bool ROWS = false>
 __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
   const int nw = blockDim.x / 32;
   if (nw == 1) return v;
-  float* r = red + 32 * flip;
+  float* r = red + 32 * flip + (ROWS ? threadIdx.y * ((nw + 3) / 4 * 4) : 0);
   flip ^= 1;
   if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = v;
-  __syncthreads();
+  if constexpr (ROWS)
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+  else
+    __syncthreads();
   v = 0.f;
   for (int w = 0; w < nw; w += 4) {
     const float4 x = *reinterpret_cast<const float4*>(r + w);
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
       }
     }
     if constexpr (kAhead) load_row(row + step);
-    s = cta_sum(s, red, flip) * inv_cols;
+    s = cta_sum<true>(s, red, flip) * inv_cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float d[VEC] = {};
@@ -614,9 +620,9 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
 // rows are a multiple of 8 apart, which keeps its lead the same.  bf16, against
 // the shifted access of the kernels above: 16384 x 4095 with residual 101 us for
 // 161, 12000 x 11007 193 for 387; gradient of 6568 x 4353 60 for 107, of 12000 x
-// 11007 216 for 734.  Two thirds of the issue slots are used by the barriers' and
-// conversions' instructions: the gradient gains from more pieces a thread (16384
-// x 4095 124 us with 256 threads, 185 with 512).
+// 11007 216 for 734.  The gradient is held up by its instructions and barriers
+// (58 % of the issue slots used): more pieces a thread help (16384 x 4095 124 us
+// with 256 threads, 185 with 512).
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void copy_piece(uint4* dst, uintptr_t src, int bytes) {
   const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
@@ -1361,12 +1367,15 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
         constexpr int NV = decltype(n)::value;
         static std::atomic<int> cache[2][kRowThreads / 32 + 1];
         auto k = dh ? rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, false>;
-        const int ty = r.block.y, threads = r.block.x * ty;
+        // Rows of a block: what makes it 256 threads, as the partials allow few blocks
+        // (16384 x 1024 bf16: 27.5 us against 33.5), where there are rows for it.
+        const int tx = r.block.x, ty = std::max<int>(r.block.y, std::min(256 / tx, a.rows / (2 * sm_count())));
+        const int threads = tx * ty;
         const size_t smem = ty > 1 ? static_cast<size_t>(threads) * A::VEC * NV * 4 : 0;
         const long long blocks = (static_cast<long long>(a.rows) + ty - 1) / ty;
         parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
                                            static_cast<long long>(kMaxPartials)}));
-        return launch_kernel(pdl_enabled(), k, dim3(parts), r.block, smem, s, a);
+        return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(tx, ty), smem, s, a);
       });
     });
   if (e != cudaSuccess || a.dw == nullptr) return e;
