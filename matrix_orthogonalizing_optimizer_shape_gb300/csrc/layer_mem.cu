@@ -1322,10 +1322,13 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, eb) && vec_mat(a.h, eb) && vec_mat(a.dh, eb) && vec_mat(a.dx, eb);
   const bool dh = a.dh.p != nullptr;
   const StagedPlan p(a.cols, eb, 2 + dh);
-  // Where one piece a thread is enough the registers' kernel is as fast or faster
-  // (16384 x 1021 bf16: 37 us against 45; 16384 x 4095 fp32 153 against 155).
-  const bool edge = !vec && a.cols > (eb == 2 ? 1024 : 4096) && alike(a.h, a.dy, eb) && alike(a.h, a.dh, eb) &&
-                    alike(a.h, a.dx, eb);
+  // Misaligned rows where registers hold them only with a lot of instructions, and
+  // there are enough of them to be copied ahead (8005 columns of bf16: 608 rows
+  // 27.2 us for 22.5, 1500 34.0 for 35.4, 5000 69.7 for 102; 9001: 8 rows 14.8 for
+  // 17.0, 608 24.9 for 37.4).
+  const bool some = a.rows >= 6 * sm_count();
+  const bool edge = !vec && (eb == 2 ? a.cols > 16 * kRowThreads || (a.cols > 2048 && some) : a.cols > 4096 && some) &&
+                    alike(a.h, a.dy, eb) && alike(a.h, a.dh, eb) && alike(a.h, a.dx, eb);
   int parts = 0;  // rows of partial column sums, as many at most as the workspace holds
   cudaError_t e;
   // Aligned rows of more than two pieces a thread: 16384 x 11008 230 us, read twice
@@ -1340,12 +1343,14 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
         const auto launch = [&](auto k, int i) {
           return launch_staged(k, p, a, kMaxPartials, &parts, once[i], cache[i], s);
         };
-        if constexpr (NV == 4)  // aligned rows that narrow are in registers
+        if constexpr (NV == 4)
           if (vec)
             return dh ? launch(rms_norm_grad_staged_kernel<T, false, NV, true>, 0)
                       : launch(rms_norm_grad_staged_kernel<T, false, NV, false>, 1);
-        return dh ? launch(rms_norm_grad_staged_kernel<T, true, NV, true>, 2)
-                  : launch(rms_norm_grad_staged_kernel<T, true, NV, false>, 3);
+        if constexpr (NV == 4 || (NV == 2 && sizeof(T) == 2))
+          return dh ? launch(rms_norm_grad_staged_kernel<T, true, NV, true>, 2)
+                    : launch(rms_norm_grad_staged_kernel<T, true, NV, false>, 3);
+        return cudaErrorInvalidValue;  // rows that narrow are in registers
       });
     });
   else

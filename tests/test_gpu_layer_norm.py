@@ -196,7 +196,7 @@ def among_nans(rng, rows, cols, dtype, scale, pad, shift):
 
 # Rows misaligned alike are copied ahead through shared memory: enough of them that a block takes several, of every
 # number of pieces a thread, and aligned ones too wide for registers.  The last form's results are aligned otherwise.
-LONG = [(4000, 250), (4000, 1031), (1500, 2049), (900, 5003), (640, 9001), (320, 8208), (7, 12001), (9, 301)]
+LONG = [(4000, 250), (4000, 1031), (1500, 2049), (900, 5003), (1300, 5003), (640, 9001), (1100, 8300), (320, 8208), (7, 12001), (9, 301)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
