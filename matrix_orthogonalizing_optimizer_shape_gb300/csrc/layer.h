@@ -55,6 +55,7 @@ struct NormGradArgs {
   float* dw;                  // null: not wanted
   int accumulate;
   float* partials;            // [<= kMaxPartials][cols]
+  int strips = 0;             // blocks that give dw themselves
 };
 cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s);
 

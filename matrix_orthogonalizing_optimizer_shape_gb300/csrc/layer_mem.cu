@@ -519,13 +519,63 @@ __device__ __forceinline__ float norm_dx(float g, float hn, float mean, float rs
   return fmaf(rstd, fmaf(-hn, mean, g), dh);
 }
 
+// dw of a strip of columns over all rows, by a block: it does not need the rows'
+// sums, so that few rows' dw comes from blocks beside those of dx, which read the
+// rows once more (from L2), and not from a second launch.
+constexpr int kStripLanes = 8;  // of VEC = 8; a warp's lanes for single columns
+template <int VEC>
+__host__ __device__ constexpr int strip_cols() {
+  return VEC == 8 ? 8 * kStripLanes : 32;
+}
+template <typename T, int VEC, bool ANY>
+__device__ __forceinline__ void strip_dw(const NormGradArgs& a, const Reader<T, ANY>& ry, const Reader<T, ANY>& rh,
+                                         int strip, float* sums) {
+  constexpr int kCols = strip_cols<VEC>(), kLanes = kCols / VEC, kRows = 4;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, groups = blockDim.x * blockDim.y / kLanes;
+  const int c = strip * kCols + tid % kLanes * VEC;
+  float dw[VEC] = {};
+  for (int row = tid / kLanes; row < a.rows; row += kRows * groups) {
+    Raw<T, VEC, ANY> dy[kRows], h[kRows];
+    float rstd[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row + i * groups;
+      dy[i].load(ry, r, c, a.cols, r < a.rows);
+      h[i].load(rh, r, c, a.cols, r < a.rows);
+      rstd[i] = r < a.rows ? a.rstd[r] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float g[VEC], hn[VEC];
+      dy[i].values(g);
+      h[i].values(hn);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) dw[j] = fmaf(g[j], __fmul_rn(hn[j], rstd[i]), dw[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) sums[tid * VEC + j] = dw[j];
+  __syncthreads();
+  const int col = strip * kCols + tid;
+  if (tid >= kCols || col >= a.cols) return;
+  float v = 0.f;
+  for (int k = 0; k < groups; ++k) v += sums[k * kCols + tid];
+  a.dw[col] = a.accumulate ? a.dw[col] + v : v;
+}
+
 template <typename T, int VEC, bool ANY, int NV, bool DH>
 __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY ? 2 : 1)
     rms_norm_grad_kernel(NormGradArgs a) {
   pdl_trigger();
   pdl_wait();
   __shared__ __align__(16) float red[64];
-  extern __shared__ float rows_sum[];  // [blockDim.y][span * NV], blockDim.y > 1
+  extern __shared__ float rows_sum[];  // [blockDim.y][span * NV], blockDim.y > 1, or a strip's
+  const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rh(a.h, a.rows, a.cols), rd(a.dh, a.rows, a.cols);
+  if (static_cast<int>(blockIdx.x) < a.strips) {
+    strip_dw<T, VEC, ANY>(a, ry, rh, blockIdx.x, rows_sum);
+    return;
+  }
+  const int block = blockIdx.x - a.strips;
   int flip = 0;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   const int span = blockDim.x * VEC;
@@ -536,7 +586,6 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
     for (int i = 0; i < NV; ++i) load_gain<VEC>(a.w, a.w_dtype, threadIdx.x * VEC + i * span, a.cols, w[i]);
   }
   __shared__ StoreBuf<ANY, kRowThreads / 32> sbuf;
-  const Reader<T, ANY> ry(a.dy, a.rows, a.cols), rh(a.h, a.rows, a.cols), rd(a.dh, a.rows, a.cols);
   Raw<T, VEC, ANY> dy[NV], h[NV], dh[DH ? NV : 1];
   float rstd_next = 0.f;
   auto load_row = [&](long long row) {
@@ -548,8 +597,8 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
       h[i].load(rh, row, c, a.cols, row < a.rows);
     }
   };
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const long long step = static_cast<long long>(gridDim.x - a.strips) * blockDim.y;
+  long long row = static_cast<long long>(block) * blockDim.y + threadIdx.y;
   load_row(row);
   for (; row < a.rows; row += step) {
     const float rstd = rstd_next;
@@ -585,7 +634,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
     }
     if constexpr (!kAhead) load_row(row + step);
   }
-  if (a.dw == nullptr) return;
+  if (a.dw == nullptr || a.strips > 0) return;
   // The rows of the block first, in order.
   if (blockDim.y > 1) {
 #pragma unroll
@@ -600,7 +649,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
       for (int j = 0; j < VEC; ++j)
         for (int y = 1; y < blockDim.y; ++y) dw[i][j] += rows_sum[(y * NV + i) * span + threadIdx.x * VEC + j];
   }
-  float* part = a.partials + static_cast<long long>(blockIdx.x) * a.cols;
+  float* part = a.partials + static_cast<long long>(block) * a.cols;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = threadIdx.x * VEC + i * span;
@@ -1233,6 +1282,14 @@ bool alike(const Mat& a, const Mat& b, int elem_bytes) {
                             (a.ld - b.ld) * elem_bytes % 16 == 0);
 }
 
+// Whether the memory of two of a gradient's matrices may overlap.
+bool overlap(const NormGradArgs& a, const Mat& x, const Mat& y, int elem_bytes) {
+  const auto end = [&](const Mat& m) {
+    return reinterpret_cast<uintptr_t>(m.p) + ((a.rows - 1LL) * m.ld + a.cols) * elem_bytes;
+  };
+  return reinterpret_cast<uintptr_t>(x.p) < end(y) && reinterpret_cast<uintptr_t>(y.p) < end(x);
+}
+
 // Rows of `mats` matrices through shared memory: pieces a thread (NV, 0: they do
 // not fit), threads, rows in shared memory and pieces of a row there.
 constexpr int kStagedBytes = 220 * 1024;  // of a block at most
@@ -1374,16 +1431,29 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
         auto k = dh ? rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, true> : rms_norm_grad_kernel<T, A::VEC, A::ANY, NV, false>;
         // Rows of a block: what makes it 256 threads, as the partials allow few blocks
         // (16384 x 1024 bf16: 27.5 us against 33.5), where there are rows for it.
-        const int tx = r.block.x, ty = std::max<int>(r.block.y, std::min(256 / tx, a.rows / (2 * sm_count())));
+        // Few rows in one launch: 512 x 4096 bf16 9.8 us for 15.4, as much at 640 x 8000
+        // (16.4 for 17.7).  Misaligned 512 x 2047 12.4 us for 13.3, but 512 x 301 12.3
+        // for 10.4, where few strips have it all to shift (304 x 301 10.3 for 9.6).
+        // What is written must not be what the strips' blocks read.
+        const int few = vec ? 640 : eb == 2 && a.cols >= 1000 ? 512 : 256;
+        const bool strips = a.dw != nullptr && a.rows <= few && !overlap(a, a.dx, a.dy, eb) && !overlap(a, a.dx, a.h, eb);
+        const int tx = r.block.x,
+                  ty = std::max<int>(r.block.y, strips ? 256 / tx : std::min(256 / tx, a.rows / (2 * sm_count())));
         const int threads = tx * ty;
-        const size_t smem = ty > 1 ? static_cast<size_t>(threads) * A::VEC * NV * 4 : 0;
         const long long blocks = (static_cast<long long>(a.rows) + ty - 1) / ty;
+        if (strips) {
+          NormGradArgs b = a;
+          b.strips = (a.cols + strip_cols<A::VEC>() - 1) / strip_cols<A::VEC>();
+          const size_t smem = static_cast<size_t>(threads) * A::VEC * 4;
+          return launch_kernel(pdl_enabled(), k, dim3(b.strips + static_cast<unsigned>(blocks)), dim3(tx, ty), smem, s, b);
+        }
+        const size_t smem = ty > 1 ? static_cast<size_t>(threads) * A::VEC * NV * 4 : 0;
         parts = static_cast<int>(std::min({blocks, static_cast<long long>(resident(k, threads, smem, cache[dh])),
                                            static_cast<long long>(kMaxPartials)}));
         return launch_kernel(pdl_enabled(), k, dim3(parts), dim3(tx, ty), smem, s, a);
       });
     });
-  if (e != cudaSuccess || a.dw == nullptr) return e;
+  if (e != cudaSuccess || a.dw == nullptr || parts == 0) return e;
   return launch_kernel(pdl_enabled(), column_sum_kernel, dim3((a.cols + 31) / 32), dim3(32 * kChains), 0, s,
                        static_cast<const float*>(a.partials), parts, a.cols, a.dw, a.accumulate);
 }

@@ -253,6 +253,26 @@ def test_rms_norm_backward_of_many_rows(cuda_lib, dtype, rows, cols, pad, shift,
         assert torch.equal(stream, same)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(300, 2048), (319, 1031), (640, 512), (70, 8192)])
+def test_rms_norm_backward_in_place_over_dy(cuda_lib, dtype, rows, cols):
+    """dw of few rows is summed beside dx, but not where dx takes dy's place."""
+    rng = np.random.default_rng(rows)
+    h, dy, w = dev(rng, rows, cols, dtype), dev(rng, rows, cols, dtype), vec(rng, cols, dtype)
+    rstd = torch.from_numpy(1 / np.sqrt((host(h) ** 2).mean(1))).to("cuda").float()
+    ws = d3.alloc_workspace(d3.rms_norm_backward_workspace_size(rows, cols))
+    dx, dw, dw2 = torch.empty_like(dy), torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    d3.rms_norm_backward(dy, h, w, rstd, dx, dw=dw, ws=ws)
+    hn = np.abs(host(h) * host(rstd)[:, None])
+    tol = (np.abs(host(dy)) * hn).sum(0) * (rows + 8) * 2.0 ** -24  # of either sum, in any order
+    want = norm_grad_ref(host(dy), host(h), host(w), host(rstd), None)[1]
+    check(host(dw), want, tol, "dw")
+    d3.rms_norm_backward(dy, h, w, rstd, dy, dw=dw2, ws=ws)
+    check(host(dw2), want, tol, "dw in place")
+    rel = torch.linalg.vector_norm((dy - dx).double()) / torch.linalg.vector_norm(dx.double())
+    assert float(rel) <= U[dtype], "dx: at most a rounding apart"
+
+
 def test_rms_norm_backward_against_differences(cuda_lib):
     rng = np.random.default_rng(2)
     x, w, c = rng.standard_normal((3, 24)), 1 + 0.3 * rng.standard_normal(24), rng.standard_normal((3, 24))
