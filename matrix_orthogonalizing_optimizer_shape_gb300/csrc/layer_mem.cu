@@ -667,11 +667,13 @@ __global__ void __launch_bounds__(kRowThreads, NV == 1 && sizeof(T) == 2 && !ANY
 // memory, of which only a row's first and last are taken element by element.  All
 // matrices have to be misaligned alike (tensors of one shape are), and a block's
 // rows are a multiple of 8 apart, which keeps its lead the same.  bf16, against
-// the shifted access of the kernels above: 16384 x 4095 with residual 101 us for
-// 161, 12000 x 11007 193 for 387; gradient of 6568 x 4353 60 for 107, of 12000 x
+// the shifted access of the kernels above: 16384 x 4095 with residual 97 us for
+// 161, 12000 x 11007 193 for 387; gradient of 6568 x 4353 52 for 107, of 12000 x
 // 11007 216 for 734.  The gradient is held up by its instructions and barriers
-// (58 % of the issue slots used): more pieces a thread help (16384 x 4095 124 us
-// with 256 threads, 185 with 512).
+// (62 % of the issue slots used): two pieces a thread do better than one (9000 x
+// 2041 35 us for 41, the norm itself 21 for 25) and than four (47), at 96 registers,
+// with which two blocks of up to 320 threads share an SM (6568 x 4353 52 us; 67 at
+// 118).
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void copy_piece(uint4* dst, uintptr_t src, int bytes) {
   const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
@@ -827,7 +829,7 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_staged_kernel(const __gr
 }
 
 template <typename T, bool EDGE, int NV, bool DH>
-__global__ void __launch_bounds__(kRowThreads) rms_norm_grad_staged_kernel(const __grid_constant__ NormGradArgs a,
+__global__ void __maxnreg__(NV == 2 ? 96 : 128) rms_norm_grad_staged_kernel(const __grid_constant__ NormGradArgs a,
                                                                            int depth, int pitch) {
   pdl_trigger();
   pdl_wait();
@@ -1298,9 +1300,14 @@ struct StagedPlan {
   StagedPlan(int cols, int elem_bytes, int mats) {
     pitch = cols * elem_bytes / 16 + 3;
     row = mats * pitch * 16;
-    const RowShape r = row_shape((cols + 16 / elem_bytes - 1 + 7) / 8, 256, kRowThreads, 4);
-    threads = r.block.x;
-    if (2 * row <= kStagedBytes) nv = r.nv;
+    const int lanes = (cols + 16 / elem_bytes - 1 + 7) / 8;
+    for (int k : {2, 4}) {
+      threads = ((lanes + k - 1) / k + 31) / 32 * 32;
+      if (threads <= kRowThreads) {
+        if (2 * row <= kStagedBytes) nv = k;
+        return;
+      }
+    }
   }
   // Blocks the device holds, of the most an SM has registers for: as many as
   // leave each two rows.
@@ -1314,6 +1321,10 @@ struct StagedPlan {
     }
   }
 };
+template <typename F>
+cudaError_t by_staged_nv(int nv, F&& f) {
+  return nv == 2 ? f(std::integral_constant<int, 2>{}) : f(std::integral_constant<int, 4>{});
+}
 template <typename F>
 cudaError_t by_type(int dtype, F&& f) {
   if (dtype == kF32) return f(0.f);
@@ -1345,7 +1356,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
   if (!vec && a.y8.q == nullptr && a.cols > 240 && p.nv > 0 && alike(a.x, a.residual, eb) && alike(a.x, a.h, eb) &&
       alike(a.x, a.y, eb))
     return by_type(a.dtype, [&](auto t) {
-      return by_nv<4>(p.nv, [&](auto n) {
+      return by_staged_nv(p.nv, [&](auto n) {
         using T = decltype(t);
         constexpr int NV = decltype(n)::value;
         static std::once_flag once[2][64];
@@ -1379,12 +1390,13 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && vec_mat(a.dy, eb) && vec_mat(a.h, eb) && vec_mat(a.dh, eb) && vec_mat(a.dx, eb);
   const bool dh = a.dh.p != nullptr;
   const StagedPlan p(a.cols, eb, 2 + dh);
-  // Misaligned rows where registers hold them only with a lot of instructions, and
-  // there are enough of them to be copied ahead (8005 columns of bf16: 608 rows
-  // 27.2 us for 22.5, 1500 34.0 for 35.4, 5000 69.7 for 102; 9001: 8 rows 14.8 for
-  // 17.0, 608 24.9 for 37.4).
+  // Misaligned rows that registers hold only with many instructions, where there
+  // are enough of them to be copied ahead.  bf16: 9000 x 1531 33 us for 36, but 16384
+  // x 1009 43 for 37; 5000 x 8005 70 for 102, but 608 x 8005 27 for 23; 9001 columns,
+  // which registers do not hold: 8 rows 14.8 for 17.0, 608 24.9 for 37.4.  fp32: 16384
+  // x 4095 152 for 154, but 1500 x 4089 27 for 19; 2500 x 6001 49 for 89.
   const bool some = a.rows >= 6 * sm_count();
-  const bool edge = !vec && (eb == 2 ? a.cols > 16 * kRowThreads || (a.cols > 2048 && some) : a.cols > 4096 && some) &&
+  const bool edge = !vec && (eb == 2 ? a.cols > 16 * kRowThreads || (a.cols > 1280 && some) : a.cols > 4096 && some) &&
                     alike(a.h, a.dy, eb) && alike(a.h, a.dh, eb) && alike(a.h, a.dx, eb);
   int parts = 0;  // rows of partial column sums, as many at most as the workspace holds
   cudaError_t e;
@@ -1392,7 +1404,7 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
   // from memory and cache 678.
   if (p.nv > 0 && (edge || (vec && a.cols > 16 * kRowThreads)))
     e = by_type(a.dtype, [&](auto t) {
-      return by_nv<4>(p.nv, [&](auto n) {
+      return by_staged_nv(p.nv, [&](auto n) {
         using T = decltype(t);
         constexpr int NV = decltype(n)::value;
         static std::once_flag once[4][64];
@@ -1404,10 +1416,8 @@ cudaError_t launch_rms_norm_grad(const NormGradArgs& a, cudaStream_t s) {
           if (vec)
             return dh ? launch(rms_norm_grad_staged_kernel<T, false, NV, true>, 0)
                       : launch(rms_norm_grad_staged_kernel<T, false, NV, false>, 1);
-        if constexpr (NV == 4 || (NV == 2 && sizeof(T) == 2))
-          return dh ? launch(rms_norm_grad_staged_kernel<T, true, NV, true>, 2)
-                    : launch(rms_norm_grad_staged_kernel<T, true, NV, false>, 3);
-        return cudaErrorInvalidValue;  // rows that narrow are in registers
+        return dh ? launch(rms_norm_grad_staged_kernel<T, true, NV, true>, 2)
+                  : launch(rms_norm_grad_staged_kernel<T, true, NV, false>, 3);
       });
     });
   else
