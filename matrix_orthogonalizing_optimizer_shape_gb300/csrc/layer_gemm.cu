@@ -379,15 +379,9 @@ __global__ void __launch_bounds__(256)
 // columns at a time, so an 8-bit block is one thread's registers.  Two
 // accumulators let the epilogue of a tile run under the next
 // tile's MMAs.  Warps: 0 TMA producer, 1 MMA issuer (even CTA), 2..9 epilogue
-// (two per TMEM lane quadrant, each half of the columns).
-//
-// QUAD: a cluster of four CTAs, two pairs, takes two neighbouring tiles of one
-// row of tiles.  They have the operand rows in common, so each pair loads half
-// of them and multicasts it to both: what an SM's copy engine can issue (a
-// 128-byte row every 2.2 cycles, measured) bounds narrow tiles, and this takes a
-// third off.  A ring slot is then free once both pairs have read it.  (Clusters
-// of four leave 8 of the 152 SMs idle, so wide tiles, which the tensor cores
-// bound, go without.)
+// (two per TMEM lane quadrant, each half of the columns).  Each CTA loads its own
+// rows of both operands: what an SM's copy engine can issue (a 128-byte row every
+// 2.2 cycles, measured) bounds the narrow tiles.
 // --------------------------------------------------------------------------
 constexpr int kPairEpiWarps = 8;
 constexpr int kBox = 2048;  // staging box: 32 rows of 64 bytes
@@ -408,7 +402,7 @@ constexpr int kPiece = 64;
 
 struct PairParams {
   int rows, cols, nkb;         // output rows and columns, K slabs
-  int tiles_r, tiles_c;        // tiles of 256 rows; QUAD: tiles_c counts pairs of tiles
+  int tiles_r, tiles_c;        // tiles of 256 rows
   int tma_out, tma_z;          // the output has a store map
   int vec_res;                 // residual (or the accumulated output) readable in 16-byte pieces
   Epilogue e;
@@ -608,7 +602,7 @@ __device__ __forceinline__ void store_block_row(const Pack8& o, long long r, int
   o.s[r * o.lds + c0 / kPackBlock] = static_cast<uint8_t>(byte);
 }
 
-template <bool BF16, bool AT, bool BT, int OUT, int PN, bool QUAD>
+template <bool BF16, bool AT, bool BT, int OUT, int PN>
 __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
@@ -623,11 +617,11 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + C::kRing + C::kStaging + C::kBars);
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr int kCtas = QUAD ? 4 : 2;
-  const uint32_t crank = cluster_rank(), rank = crank & 1u, pair = crank >> 1, even = crank & ~1u;
-  const bool leader = rank == 0;  // of the pair
-  const int cluster = blockIdx.x / kCtas, nclusters = gridDim.x / kCtas;
-  const uint16_t both = static_cast<uint16_t>(0x3 << even);  // the CTAs of the pair
+  constexpr uint32_t even = 0;    // rank of the CTA that issues the MMAs
+  constexpr uint16_t both = 0x3;  // the CTAs of the pair
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == even;
+  const int cluster = blockIdx.x / 2, nclusters = gridDim.x / 2;
   const int total = p.tiles_r * p.tiles_c;
   const int depth = OUT == kOut32 ? kPiece : p.nkb;  // K slabs of one accumulation
   if (threadIdx.x == 0) {
@@ -636,7 +630,7 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
     if (p.tma_out) prefetch_map(&tmOut);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full + 8 * s, 1);   // in the even CTA: its producer, and both CTAs' bytes
-      mbar_init(bar_empty + 8 * s, kCtas / 2);  // the MMA commits of the pairs that read the slot
+      mbar_init(bar_empty + 8 * s, 1);  // the MMA commit that frees the slot
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_tfull + 8 * a, 1);
@@ -658,7 +652,6 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
     for (int u = cluster; u < total && ok; u += nclusters) {
       int R, Cc;
       pair_tile(p, u, R, Cc);
-      if constexpr (QUAD) Cc = 2 * Cc + pair;
       const int a_row = R * 256 + static_cast<int>(rank) * 128, b_row = Cc * PN + static_cast<int>(rank) * (PN / 2);
       for (int kb = 0; kb < p.nkb; ++kb, ++kc) {
         const uint32_t s = kc % C::kStages, ph = (kc / C::kStages) & 1u;
@@ -668,15 +661,7 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
         if (elect_one()) {
           if (leader) mbar_expect(bar_full + 8 * s, 2 * C::kStage);
           const uint32_t full = map_to_rank(bar_full + 8 * s, even);
-          if constexpr (QUAD) {  // the pair's half of the rows, to both pairs
-            const int half = 64 * static_cast<int>(pair);
-            const uint32_t dst = a + static_cast<uint32_t>(pair) * (C::kA / 2);
-            const uint16_t mask = static_cast<uint16_t>(0x5 << rank);
-            if constexpr (AT)
-              tma_load_pair_multicast(dst, &tmA, full, a_row + half, k0, mask);
-            else
-              tma_load_pair_multicast(dst, &tmA, full, k0, a_row + half, mask);
-          } else if constexpr (AT) {
+          if constexpr (AT) {
             tma_load_pair(a, &tmA, full, a_row, k0);
             tma_load_pair(a + C::kA / 2, &tmA, full, a_row + 64, k0);
           } else {
@@ -718,7 +703,7 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               mma_f16<2>(d, da + kDescStep<AT> * kk, db + kDescStep<BT> * kk, id, (kb > kb0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(bar_empty + 8 * s, QUAD ? 0xF : 0x3);
+            mma_commit_pair(bar_empty + 8 * s, both);
           }
           __syncwarp();
         }
@@ -729,7 +714,7 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
         if (kb0 == p.nkb) kb0 = 0, u += nclusters;
       }
       // All MMAs have completed before TMEM is freed.
-      if (elect_one()) mma_commit_pair(bar_drain, static_cast<uint16_t>(1u << even));
+      if (elect_one()) mma_commit_pair(bar_drain, 1u << even);
       __syncwarp();
       mbar_wait_warp(bar_drain, 0u, p.status);
     }
@@ -749,7 +734,6 @@ __global__ void __launch_bounds__(PairCfg<PN>::kThreads, 1)
     for (int u = cluster, kb0 = 0; u < total; ++tc) {
       int R, Cc;
       pair_tile(p, u, R, Cc);
-      if constexpr (QUAD) Cc = 2 * Cc + pair;
       const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
       const bool add = OUT == kOut32 && (e.accumulate != 0 || kb0 > 0);
       const int row0 = R * 256 + static_cast<int>(rank) * 128 + quad * 32, r = row0 + lane;
@@ -933,10 +917,10 @@ int resident_clusters(K kern, int threads, int smem, int size, int dev, int* cac
 
 // The pair kernel's A is the operand of the output's rows (Product::B) and its
 // B that of the columns (Product::A).
-template <bool BF16, bool AT, bool BT, int OUT, int PN, bool QUAD>
+template <bool BF16, bool AT, bool BT, int OUT, int PN>
 cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cudaStream_t s) {
   using C = PairCfg<PN>;
-  auto kern = pair_kernel<BF16, AT, BT, OUT, PN, QUAD>;
+  auto kern = pair_kernel<BF16, AT, BT, OUT, PN>;
   static std::once_flag once[64];
   static int pairs[64] = {0};
   int dev = 0;
@@ -944,7 +928,7 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   const cudaError_t err = allow_smem(kern, C::kDyn, once, dev);
   if (err != cudaSuccess) return err;
   CUtensorMap ta, tb, to, tz;
-  if (!operand_map(&ta, g.B, AT ? g.K : g.N, AT ? g.N : g.K, AT ? BK : QUAD ? 64 : 128, g.elem)) return cudaErrorInvalidValue;
+  if (!operand_map(&ta, g.B, AT ? g.K : g.N, AT ? g.N : g.K, AT ? BK : 128, g.elem)) return cudaErrorInvalidValue;
   if (!operand_map(&tb, g.A, BT ? g.K : g.M, BT ? g.M : g.K, BT ? BK : PN / 2, g.elem)) return cudaErrorInvalidValue;
   memset(&to, 0, sizeof to);
   memset(&tz, 0, sizeof tz);
@@ -953,8 +937,7 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   p.cols = g.M;
   p.nkb = (g.K + BK - 1) / BK;
   p.tiles_r = (g.N + 255) / 256;
-  constexpr int kWide = QUAD ? 2 * PN : PN, kCtas = QUAD ? 4 : 2;
-  p.tiles_c = (g.M + kWide - 1) / kWide;
+  p.tiles_c = (g.M + PN - 1) / PN;
   p.tma_out = store_map(&to, e.out, e.ld_out, g.N, g.M, g.out_dtype);
   p.tma_z = store_map(&tz, e.z, e.ld_z, g.N, g.M, g.elem);
   const uintptr_t add = reinterpret_cast<uintptr_t>(OUT == kOutFwd ? static_cast<const void*>(e.res) : e.out);
@@ -964,9 +947,9 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   const long long total = static_cast<long long>(p.tiles_r) * p.tiles_c;
   if (total > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
   const int clusters = static_cast<int>(
-      std::min<long long>(total, resident_clusters(kern, C::kThreads, C::kDyn, kCtas, dev, pairs)));
+      std::min<long long>(total, resident_clusters(kern, C::kThreads, C::kDyn, 2, dev, pairs)));
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = cluster_config(kCtas * clusters, C::kThreads, C::kDyn, kCtas, pdl_enabled(), s, attr);
+  const cudaLaunchConfig_t cfg = cluster_config(2 * clusters, C::kThreads, C::kDyn, 2, pdl_enabled(), s, attr);
   return cudaLaunchKernelEx(&cfg, kern, ta, tb, to, tz, p);
 }
 
@@ -1006,7 +989,6 @@ struct Plan {
   bool pair;
   int bn, split;  // tile width; CTAs that share a tile's K (tile kernel)
   bool deep;      // one CTA an SM with a deeper ring (tile kernel)
-  bool quad;      // two 128-wide tiles by clusters of four (pair kernel)
 };
 
 // The cheapest by an estimate in microseconds.  Short of large products every
@@ -1017,10 +999,10 @@ struct Plan {
 // 128-byte row of a box then lies in two lines).  To that come a launch's fixed
 // part, the rows that a tile's epilogue writes, and the join of a split.
 // Measured over 64 products of 1 .. 16384 rows and 512 .. 11008 columns, the
-// choice is mostly within 10 % of the best of some 12 variants each: at 256 x
-// 2048 x 2048 (dx) a 64-wide tile with K over 4 CTAs, 11.1 us, where a pair a
-// tile takes 15.9; at 16384 x 512 x 512 (dW) K over 8 CTAs, 22 us, where a pair
-// takes 77; at 427 x 4840 x 1848 clusters of four, 21 us, where pairs take 27.
+// choice is mostly within 10 % of the best of the up to 18 variants that each
+// can take: at 256 x 2048 x 2048 (dx) a 64-wide tile with K over 4 CTAs, 11.1 us,
+// where a pair a tile takes 15.9; at 16384 x 512 x 512 (dW) K over 8 CTAs, 22 us,
+// where a pair takes 77.
 Plan plan_product(const Product& g) {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1037,12 +1019,7 @@ Plan plan_product(const Product& g) {
     const long long waves = ceil_div(ceil_div(g.N, 256) * ceil_div(g.M, bn), pairs);
     const double kb = static_cast<double>(waves) * nkb * (16 + bn / 16) * (bn == 256 ? slow256 : slow128)[off];
     const double t = 6.0 + std::max(hbm, kb / (waves > 1 ? 116.0 : 105.0));
-    if (t < least) least = t, best = {true, bn, 1, false, false};
-  }
-  if (g.M > 128) {
-    const long long waves = ceil_div(ceil_div(g.N, 256) * ceil_div(g.M, 256), sms / 4 - 2);
-    const double t = 6.3 + std::max(hbm, static_cast<double>(waves) * nkb * (0.185 + 0.005 * off));
-    if (t < least) least = t, best = {true, 128, 1, false, true};
+    if (t < least) least = t, best = {true, bn, 1, false};
   }
   for (int bn : {128, 64, 32, 16}) {
     if (g.b_mn && bn < 64) break;
@@ -1056,7 +1033,7 @@ Plan plan_product(const Product& g) {
       const double t = 5.0 + 3.0 * (rounds - 1) + std::max(hbm, kb / (on_sm > 1 ? 135.0 : 105.0)) +
                        (split > 1 ? 0.6 + 0.02 * bn : 0.0) + (split > 4 ? 3.0 : 0.0) +
                        std::min<long long>(g.N, bn) / split * (g.a_mn ? 0.015 : 0.03);
-      if (t < least) least = t, best = {false, bn, split, ctas <= sms && split <= 4, false};
+      if (t < least) least = t, best = {false, bn, split, ctas <= sms && split <= 4};
     }
   }
   return best;
@@ -1079,9 +1056,8 @@ cudaError_t run_tile_n(const Product& g, const Epilogue& e, const Plan& p, unsig
 
 template <bool BF16, bool AT, bool BT, int OUT>
 cudaError_t run_pair_n(const Product& g, const Epilogue& e, const Plan& p, unsigned* status, cudaStream_t s) {
-  if (p.quad) return run_pair<BF16, AT, BT, OUT, 128, true>(g, e, status, s);
-  return p.bn == 128 ? run_pair<BF16, AT, BT, OUT, 128, false>(g, e, status, s)
-                     : run_pair<BF16, AT, BT, OUT, 256, false>(g, e, status, s);
+  return p.bn == 128 ? run_pair<BF16, AT, BT, OUT, 128>(g, e, status, s)
+                     : run_pair<BF16, AT, BT, OUT, 256>(g, e, status, s);
 }
 
 // Whether a forward product goes to few_tokens_kernel: enough rows of W for its

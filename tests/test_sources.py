@@ -1,0 +1,26 @@
+"""Properties of the kernels' sources that no run on one GPU shows."""
+import glob
+import os
+import re
+
+import matrix_orthogonalizing_optimizer_shape_gb300 as d3
+
+CSRC = os.path.join(os.path.dirname(d3.__file__), "csrc")
+
+
+def sources():
+    files = [f for pat in ("*.cu", "*.cuh", "*.h") for f in sorted(glob.glob(os.path.join(CSRC, pat)))]
+    assert files
+    return {os.path.basename(f): open(f).read() for f in files}
+
+
+def test_only_commits_reach_several_ctas():
+    """The library is loaded by one process a GPU: each CTA loads its own operands,
+    and only the tensor cores' commits signal several CTAs of a cluster."""
+    commits = 0
+    for name, text in sources().items():
+        for stmt in re.findall(r"\basm\b[^;]*?\(.*?\)\s*;", text, flags=re.S):
+            if "multicast" in stmt:
+                assert "tcgen05.commit" in stmt, f"{name}: {stmt[:200]}"
+                commits += 1
+    assert commits > 0
