@@ -578,8 +578,12 @@ dion3_status dion3_linear(const dion3_linear_args* args, void* ws, size_t ws_byt
  *            dtype and pitch (dense bf16 or fp32: a dion3_group gradient);
  *            db is fp32.  accumulate != 0: dw += and db +=, each sum formed in
  *            fp32 and rounded once.
- * A fp32 dw over more than 4096 tokens is summed in pieces of 4096 (the tensor
- * cores' fp32 sums truncate; relative error about 4e-6).
+ * A fp32 dw over more than 4096 tokens is summed in pieces of at most 4096, which
+ * are added rounded to nearest: the tensor cores' fp32 sums truncate, so that the
+ * error of one sum grows with its length.  Relative error about 4e-6 over random
+ * signs, up to 3e-5 where all terms have one sign, at any number of tokens.  A
+ * 16-bit dw is not: its sums may be one piece, off by another 1.2e-9 per token over
+ * random signs, which its own rounding covers up to some 10^5 tokens.
  * Without an activation the products read dy itself; with one, dz is rounded
  * to the layer's 16-bit type, which the tensor cores take, while db sums the
  * unrounded dz.

@@ -136,36 +136,86 @@ __device__ __forceinline__ void epilogue_rows(const Epilogue& e, int t0, int m, 
   }
 }
 
-template <int BN, bool DEEP>  // DEEP: one CTA an SM, the ring takes all of it
+// A 32-bit result is summed in pieces of kPiece K slabs: the tensor cores
+// truncate each addition to the accumulator, an error that grows with their
+// number (relative 1.9e-5 over 16384 tokens in one piece, 4.4e-6 over 4096,
+// 1.0e-6 over 1024).  The pieces are added in fp32, rounded to nearest, in order:
+// by the tile kernel to a second set of TMEM columns, by the paired kernel, which
+// has none to spare, to the output in place, by bulk reductions that find the tile
+// in L2.  Their traffic is why a piece is no shorter: dW of 16384 x 4096 x 11008
+// takes 818 us in one piece and 1060 in pieces of 16 slabs.  A 16-bit result does
+// not show the error.
+constexpr int kPiece = 64;
+
+template <int BN, bool DEEP, bool SUM>  // DEEP: one CTA an SM, the ring takes all of it; SUM: a sum of pieces
 struct TileCfg {
   static constexpr int kABytes = BM * BK * 2;
   static constexpr int kBBytes = BN * BK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = (DEEP ? 200 : 96) * 1024 / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kTmemCols = BN < 32 ? 32 : BN;
-  static constexpr int kBars = (2 * kStages + 2) * 8;
+  // Two CTAs of an SM hold 512 columns at most: all there are, so that a CTA
+  // placed early never keeps them from one that has to finish first.
+  static constexpr int kTmemCols = SUM ? 2 * BN : BN < 32 ? 32 : BN;
+  static constexpr int kBars = (2 * kStages + 3) * 8;
   static constexpr int kDyn = 1024 + kRing + kBars + 16;
   static_assert(BN * BM * 4 <= kRing, "a tile's partial sums take the ring's place");
 };
 constexpr int kTileThreads = 6 * 32;
 constexpr int kTurn = 8;  // output rows an epilogue warp finishes at a time
 
+// v += eight TMEM columns of the thread's lane.
+__device__ __forceinline__ void add_columns(uint32_t taddr, float (&v)[kTurn]) {
+  uint32_t u[kTurn];
+  tmem_ld8(taddr, u);
+  tmem_ld_done(u);
+#pragma unroll
+  for (int j = 0; j < kTurn; ++j) v[j] += __uint_as_float(u[j]);
+}
+// Adds all pieces but the last, n columns each, from the accumulator at tb to the
+// sum BN columns after it.  True (to every lane) once the last is in the accumulator.
+template <int BN>
+__device__ __forceinline__ bool take_pieces(uint32_t tb, int pieces, int n, uint32_t bar_done, uint32_t bar_taken,
+                                            unsigned* status) {
+  for (int p = 0;; ++p) {
+    if (!mbar_wait_warp(bar_done, p & 1u, status)) return false;
+    fence_after();
+    if (p == pieces - 1) return true;
+#pragma unroll 1
+    for (int c = 0; c < n; c += kTurn) {
+      float v[kTurn] = {};
+      add_columns(tb + c, v);
+      if (p > 0) add_columns(tb + BN + c, v);
+      uint32_t u[kTurn];
+#pragma unroll
+      for (int j = 0; j < kTurn; ++j) u[j] = __float_as_uint(v[j]);
+      tmem_st8(tb + BN + c, u);
+    }
+    tmem_st_done();
+    fence_before();
+    mbar_arrive(bar_taken);
+  }
+}
+
 // K is split over the CTAs of a cluster when there are few tiles: each CTA
 // multiplies its share of the K slabs, the partial tiles meet in distributed
 // shared memory, and every CTA adds the partials of its share of the rows in
-// rank order (the same bits every call) and finishes them.
-template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP>
+// rank order (the same bits every call) and finishes them.  SUM: a share of
+// more than kPiece slabs, for a 32-bit output.  After each piece the epilogue warps
+// add the accumulator to the running sum in the BN columns beside it, while the
+// MMAs wait: 65536 x 1024 x 1024 (dW) takes 116 us where one piece takes 114.  (A
+// form of its own: shares of one piece take 0.8 us more with its code.)
+template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP, bool SUM>
 __global__ void __launch_bounds__(kTileThreads)
     tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, int nkb_all,
                 int tiles_m, int split, Epilogue e, unsigned* status) {
-  using C = TileCfg<BN, DEEP>;
+  using C = TileCfg<BN, DEEP, SUM>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t sA = base, sB = base + C::kStages * C::kABytes;
   const uint32_t bar_full = base + C::kRing, bar_empty = bar_full + 8 * C::kStages,
-                 bar_done = bar_empty + 8 * C::kStages, bar_drain = bar_done + 8;
+                 bar_done = bar_empty + 8 * C::kStages, bar_drain = bar_done + 8, bar_taken = bar_drain + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + C::kRing + C::kBars);
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -176,8 +226,9 @@ __global__ void __launch_bounds__(kTileThreads)
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
-    mbar_init(bar_done, 1);
+    mbar_init(bar_done, 1);    // a piece is in the accumulator
     mbar_init(bar_drain, 1);
+    mbar_init(bar_taken, 128);  // the epilogue's threads have added it to the sum
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), C::kTmemCols);
@@ -191,6 +242,7 @@ __global__ void __launch_bounds__(kTileThreads)
   const int m0 = (tile % tiles_m) * BM, t0 = (tile / tiles_m) * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(nkb_all) * rank / split);
   const int nkb = static_cast<int>(static_cast<long long>(nkb_all) * (rank + 1) / split) - kb0;
+  const int pieces = SUM ? (nkb + kPiece - 1) / kPiece : 1;
   const int quad = warp % 4;
   const int m = m0 + quad * 32 + lane;
   const bool in = m < e.M;
@@ -225,26 +277,33 @@ __global__ void __launch_bounds__(kTileThreads)
       mbar_wait_warp(bar_full + 8 * (i % C::kStages), (i / C::kStages) & 1u, status);
   } else if (warp == 1) {
     constexpr uint32_t id = instr_desc<BF16, AT, BT>(BM, BN);
-    bool ok = true;
-    for (int kb = 0; kb < nkb && ok; ++kb) {
+    int at = 0, piece = 0;  // slabs in the accumulator, pieces before it
+    for (int kb = 0; kb < nkb; ++kb) {
       const uint32_t s = kb % C::kStages, ph = (kb / C::kStages) & 1u;
-      if (!(ok = mbar_wait_warp(bar_full + 8 * s, ph, status))) break;
+      if (SUM && at == kPiece) {
+        if (!mbar_wait_warp(bar_taken, piece & 1u, status)) break;
+        at = 0, ++piece;
+      }
+      if (!mbar_wait_warp(bar_full + 8 * s, ph, status)) break;
       fence_after();
       const uint64_t da = smem_desc<AT>(sA + s * C::kABytes), db = smem_desc<BT>(sB + s * C::kBBytes);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          mma_f16<1>(tmem, da + kDescStep<AT> * kk, db + kDescStep<BT> * kk, id, (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_f16<1>(tmem, da + kDescStep<AT> * kk, db + kDescStep<BT> * kk, id, (at > 0 || kk > 0) ? 1u : 0u);
         mma_commit(bar_empty + 8 * s);
-        if (kb == nkb - 1) mma_commit(bar_done);
+        if (kb == nkb - 1 || (SUM && at + 1 == kPiece)) mma_commit(bar_done);
       }
+      ++at;
       __syncwarp();
     }
     // All MMAs have completed before TMEM is freed.
     if (elect_one()) mma_commit(bar_drain);
     __syncwarp();
     mbar_wait_warp(bar_drain, 0u, status);
-  } else if (mbar_wait_warp(bar_done, 0u, status)) {
+  } else if (SUM ? take_pieces<BN>(tmem + (static_cast<uint32_t>(quad * 32) << 16), pieces, min(BN, e.N - t0), bar_done,
+                                   bar_taken, status)
+                 : mbar_wait_warp(bar_done, 0u, status)) {
     fence_after();
     const float bias = FWD && e.bias != nullptr && in ? load_bias(e.bias, e.bias_dtype, m) : 0.f;
     const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -260,6 +319,7 @@ __global__ void __launch_bounds__(kTileThreads)
       float v[kTurn];
 #pragma unroll
       for (int j = 0; j < kTurn; ++j) v[j] = __uint_as_float(u[j]);
+      if (SUM && pieces > 1) add_columns(tb + BN + c, v);
       if (c + kTurn < n) tmem_ld8(tb + c + kTurn, u);
       if (split > 1) {  // every slab has been consumed: the ring is free
 #pragma unroll
@@ -389,16 +449,6 @@ constexpr int kBand = 8;  // row tiles walked together, column by column: operan
 
 // kOutOther: 16 bits, of the type that the operands do not have.
 enum PairOut : int { kOutFwd = 0, kOut16 = 1, kOut32 = 2, kOutOther = 3 };
-
-// A 32-bit result is summed in pieces of kPiece K slabs: the tensor cores
-// truncate each addition to the accumulator, an error that grows with their
-// number (relative 1.9e-5 over 16384 tokens in one piece, 4.4e-6 over 4096,
-// 1.0e-6 over 1024).  The pieces of a tile follow each other in the same
-// cluster; the first is stored and the others are added to it in place, rounded
-// to nearest, by bulk reductions that find the tile in L2.  Their traffic is why
-// a piece is no shorter: dW of 16384 x 4096 x 11008 takes 818 us in one piece and
-// 1060 in pieces of 16 slabs.  A 16-bit result does not show the error.
-constexpr int kPiece = 64;
 
 struct PairParams {
   int rows, cols, nkb;         // output rows and columns, K slabs
@@ -963,10 +1013,10 @@ int sm_count(int dev) {
   return cached[dev & 63];
 }
 
-template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP>
+template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP, bool SUM>
 cudaError_t run_tile(const Product& g, const Epilogue& e, int split, unsigned* status, cudaStream_t s) {
-  using C = TileCfg<BN, DEEP>;
-  auto kern = tile_kernel<BF16, AT, BT, BN, FWD, DEEP>;
+  using C = TileCfg<BN, DEEP, SUM>;
+  auto kern = tile_kernel<BF16, AT, BT, BN, FWD, DEEP, SUM>;
   static std::once_flag once[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1041,8 +1091,13 @@ Plan plan_product(const Product& g) {
 
 template <bool BF16, bool AT, bool BT, int BN, bool FWD>
 cudaError_t run_tile_d(const Product& g, const Epilogue& e, const Plan& p, unsigned* status, cudaStream_t s) {
-  return p.deep ? run_tile<BF16, AT, BT, BN, FWD, true>(g, e, p.split, status, s)
-                : run_tile<BF16, AT, BT, BN, FWD, false>(g, e, p.split, status, s);
+  if constexpr (BT) {
+    if (e.out_f32 && g.K > kPiece * BK * p.split)  // a share is longer than a piece
+      return p.deep ? run_tile<BF16, AT, BT, BN, FWD, true, true>(g, e, p.split, status, s)
+                    : run_tile<BF16, AT, BT, BN, FWD, false, true>(g, e, p.split, status, s);
+  }
+  return p.deep ? run_tile<BF16, AT, BT, BN, FWD, true, false>(g, e, p.split, status, s)
+                : run_tile<BF16, AT, BT, BN, FWD, false, false>(g, e, p.split, status, s);
 }
 template <bool BF16, bool AT, bool BT, bool FWD>
 cudaError_t run_tile_n(const Product& g, const Epilogue& e, const Plan& p, unsigned* status, cudaStream_t s) {
