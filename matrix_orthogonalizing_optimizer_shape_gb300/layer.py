@@ -65,21 +65,24 @@ SIGS = {
 # small operator's time is its host side, and filling ctypes structures field by
 # field took longer than the rest of the call.
 _MAT = struct.Struct("@Pqi4x")
+_PACK = struct.Struct("@PqPq")
 _LINEAR = struct.Struct("@4i" + "Pqi4x" * 5 + "PqPq" * 2 + "Pi4x")
 _LINEAR_GRAD = struct.Struct("@5i4x" + "Pqi4x" * 4 + "PqPq" * 2 + "Pqi4x" * 2 + "P")
-assert (_MAT.size, _LINEAR.size, _LINEAR_GRAD.size) == tuple(map(ctypes.sizeof, (_Matrix, _LinearArgs, _LinearGradArgs)))
+assert (_MAT.size, _PACK.size, _LINEAR.size, _LINEAR_GRAD.size) == tuple(
+    map(ctypes.sizeof, (_Matrix, _Packed8, _LinearArgs, _LinearGradArgs)))
 _NO_MAT, _NO_PACK = (0, 0, 0), (0, 0, 0, 0)
 
 _FNS = {}
-_torch = None
+_torch = _I8 = _U8 = None
 _DTYPES = {}
 
 
 def _load_torch():
     """torch, and the dtypes' codes (on first use: importing this module needs neither)."""
-    global _torch
+    global _torch, _I8, _U8
     if _torch is None:
         import torch
+        _I8, _U8 = torch.int8, torch.uint8
         _DTYPES.update({torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16})
         _torch = torch
     return _torch
@@ -158,35 +161,54 @@ def _vec(name: str, t, n: int, f32: bool = False) -> int:
 class Packed8:
     """A matrix in 8-bit blocks (``dion3_packed8``): int8 codes [rows, cols] and
     uint8 scale bytes [rows, ceil(cols / 32)], rows contiguous, any row pitch
-    (multiples of 16 bytes are fastest, see :func:`alloc_packed8`)."""
+    (multiples of 16 bytes are fastest, see :func:`alloc_packed8`).  A call reads
+    the addresses that ``codes`` and ``scales`` have when it is made, so both may
+    be replaced (moved to the host and back, for instance)."""
 
-    __slots__ = ("codes", "scales", "shape", "_fields", "_c")
+    __slots__ = ("codes", "scales")
 
     def __init__(self, codes, scales):
-        import torch
-        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
-            raise ValueError("codes must be int8 and scales uint8")
-        if not (codes.is_cuda and scales.is_cuda) or codes.dim() != 2 or scales.dim() != 2:
-            raise ValueError("codes and scales must be 2-D CUDA tensors")
-        rows, cols = codes.shape
-        nb = -(-cols // PACK_BLOCK)
-        if tuple(scales.shape) != (rows, nb):
-            raise ValueError(f"scales must be {rows} x {nb} for codes of {rows} x {cols}")
-        lds = []
-        for t, c in ((codes, cols), (scales, nb)):
-            ld, inner = t.stride()
-            if (inner != 1 and c > 1) or (ld < c and rows > 1):
-                raise ValueError("the rows of codes and scales must be contiguous and not overlap")
-            lds.append(max(ld, c))
-        self.codes, self.scales, self.shape = codes, scales, (rows, cols)
-        self._fields = (codes.data_ptr(), lds[0], scales.data_ptr(), lds[1])
-        self._c = struct.pack("@PqPq", *self._fields)
+        self.codes, self.scales = codes, scales
+        _packed("Packed8", self)
+
+    @property
+    def shape(self):
+        return tuple(self.codes.shape)
 
 
-def _packed(name: str, p: Packed8, rows: int, cols: int) -> Packed8:
-    if p.shape != (rows, cols):
-        raise ValueError(f"{name} is {p.shape[0]} x {p.shape[1]}, {rows} x {cols} is wanted")
-    return p
+def _packed(name: str, p: Packed8, rows: Optional[int] = None, cols: Optional[int] = None) -> tuple:
+    """(codes, ld_codes, scales, ld_scales); shape checked where given."""
+    q, s = p.codes, p.scales
+    try:
+        (r, c), (sr, nb), (lq, qi), (ls, si) = q.shape, s.shape, q.stride(), s.stride()
+        if (q.is_cuda and s.is_cuda and qi == 1 and si == 1 and lq >= c and ls >= nb and sr == r and nb == (c + 31) // 32
+                and (rows is None or (r == rows and c == cols)) and q.dtype is _I8 and s.dtype is _U8):
+            return q.data_ptr(), lq, s.data_ptr(), ls
+    except ValueError:
+        pass
+    return _packed_checked(name, q, s, rows, cols)
+
+
+def _packed_checked(name: str, q, s, rows, cols) -> tuple:
+    """The same, case by case (see _mat_checked)."""
+    t = _load_torch()
+    if q.dtype != t.int8 or s.dtype != t.uint8:
+        raise ValueError(f"{name}: codes must be int8 and scales uint8")
+    if not (q.is_cuda and s.is_cuda) or q.dim() != 2 or s.dim() != 2:
+        raise ValueError(f"{name}: codes and scales must be 2-D CUDA tensors")
+    r, c = q.shape
+    if rows is not None and (r, c) != (rows, cols):
+        raise ValueError(f"{name} is {r} x {c}, {rows} x {cols} is wanted")
+    nb = -(-c // PACK_BLOCK)
+    if tuple(s.shape) != (r, nb):
+        raise ValueError(f"{name}: scales must be {r} x {nb} for codes of {r} x {c}")
+    lds = []
+    for m, n in ((q, c), (s, nb)):
+        ld, inner = m.stride()
+        if (inner != 1 and n > 1) or (ld < n and r > 1):
+            raise ValueError(f"{name}: the rows of codes and scales must be contiguous and not overlap")
+        lds.append(max(ld, n))
+    return q.data_ptr(), lds[0], s.data_ptr(), lds[1]
 
 
 def alloc_packed8(rows: int, cols: int, device=None) -> Packed8:
@@ -211,13 +233,14 @@ def pack8(x, out: Packed8, stream=None):
     """x [rows, cols] into 8-bit blocks (see dion3_pack8)."""
     m = _MAT.pack(*_mat("x", x))
     rows, cols = x.shape
-    _d3._check(_fn("dion3_pack8")(rows, cols, m, _packed("out", out, rows, cols)._c, _stream(stream)))
+    _d3._check(_fn("dion3_pack8")(rows, cols, m, _PACK.pack(*_packed("out", out, rows, cols)), _stream(stream)))
 
 
 def unpack8(src: Packed8, out, stream=None):
     """The values that 8-bit blocks stand for, in out's dtype (see dion3_unpack8)."""
-    rows, cols = src.shape
-    _d3._check(_fn("dion3_unpack8")(rows, cols, src._c, _MAT.pack(*_mat("out", out, rows, cols)), _stream(stream)))
+    p = _PACK.pack(*_packed("src", src))
+    rows, cols = src.codes.shape
+    _d3._check(_fn("dion3_unpack8")(rows, cols, p, _MAT.pack(*_mat("out", out, rows, cols)), _stream(stream)))
 
 
 def _opt(name: str, t, rows: int, cols: int):
@@ -233,7 +256,7 @@ def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] 
     rows, cols = x.shape
     _d3._check(_fn("dion3_rms_norm")(
         rows, cols, mx, _opt("residual", residual, rows, cols), _vec("weight", weight, cols), _dtype(weight), eps,
-        _opt("h", h, rows, cols), _opt("y", y, rows, cols), None if y8 is None else _packed("y8", y8, rows, cols)._c,
+        _opt("h", h, rows, cols), _opt("y", y, rows, cols), None if y8 is None else _PACK.pack(*_packed("y8", y8, rows, cols)),
         None if rstd is None else _vec("rstd", rstd, rows, f32=True), _stream(stream)))
 
 
@@ -290,12 +313,12 @@ def linear(x, w, y, *, bias=None, residual=None, act: int = ACT_NONE, z=None, y8
     z8 = _NO_PACK
     mz = _NO_MAT
     if isinstance(z, Packed8):
-        z8 = _packed("z", z, tokens, n)._fields
+        z8 = _packed("z", z, tokens, n)
     elif z is not None:
         mz = _mat("z", z, tokens, n)
     args = _LINEAR.pack(tokens, k, n, act, *mx, *mw, *_mat("y", y, tokens, n),
                         *(_NO_MAT if residual is None else _mat("residual", residual, tokens, n)), *mz, *z8,
-                        *(_NO_PACK if y8 is None else _packed("y8", y8, tokens, n)._fields),
+                        *(_NO_PACK if y8 is None else _packed("y8", y8, tokens, n)),
                         0 if bias is None else _vec("bias", bias, n), 0 if bias is None else _dtype(bias))
     p, nb = _ws(ws, ws_bytes)
     _d3._check(_fn("dion3_linear")(args, p, nb, _stream(stream)))
@@ -313,11 +336,11 @@ def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE,
     k = w.shape[1]
     mx, x8, mz, z8 = _NO_MAT, _NO_PACK, _NO_MAT, _NO_PACK
     if isinstance(x, Packed8):
-        x8 = _packed("x", x, tokens, k)._fields
+        x8 = _packed("x", x, tokens, k)
     elif x is not None:
         mx = _mat("x", x, tokens, k)
     if isinstance(z, Packed8):
-        z8 = _packed("z", z, tokens, n)._fields
+        z8 = _packed("z", z, tokens, n)
     elif z is not None:
         mz = _mat("z", z, tokens, n)
     args = _LINEAR_GRAD.pack(tokens, k, n, act, int(accumulate), *mdy, *mw, *mx, *mz, *x8, *z8,
