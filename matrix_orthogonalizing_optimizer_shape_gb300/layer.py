@@ -2,8 +2,9 @@
 in 8 bits (binding of the layer part of ``include/dion3.h``).
 
 Arguments are 2-D CUDA tensors [tokens, features] whose rows are contiguous
-(any row pitch); outputs are given by the caller.  Every function enqueues on
-``stream`` (default: the current one) and returns without waiting::
+(any row pitch), all on the current device; outputs are given by the caller.
+Every function enqueues on ``stream`` (default: the current one) and returns
+without waiting::
 
     x8 = d3.alloc_packed8(T, K)
     d3.rms_norm(x, gain, y, residual=r, h=h, y8=x8, rstd=rstd)
@@ -111,28 +112,44 @@ def _dtype(t) -> int:
     return _DTYPES[t.dtype]
 
 
-def _stream(stream) -> Optional[int]:
+def _device() -> int:
+    """The current device, where the kernels run."""
+    return (_torch or _load_torch())._C._cuda_getDevice()
+
+
+def _stream(stream, dev: int) -> Optional[int]:
+    """The stream of a call whose tensors are on device `dev`."""
+    current = _device()
+    if dev != current:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{current}")
     if stream is None:
-        t = _torch or _load_torch()
-        return t._C._cuda_getCurrentRawStream(t._C._cuda_getDevice()) or None
+        return _torch._C._cuda_getCurrentRawStream(current) or None
     return _d3._stream(stream)
 
 
-def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None) -> tuple:
-    """(data, ld, dtype) of a 2-D CUDA tensor with contiguous rows; shape checked where given."""
+def _on(name: str, t, dev: Optional[int]):
+    """Refuses a tensor that is not on device `dev` (None: any CUDA device)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's other tensors are on device cuda:{dev}")
+
+
+def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None, dev: Optional[int] = None) -> tuple:
+    """(data, ld, dtype) of a 2-D CUDA tensor with contiguous rows; shape and device checked where given."""
     try:
         (r, c), (ld, inner) = t.shape, t.stride()
-        if t.is_cuda and inner == 1 and ld >= c and (rows is None or r == rows) and (cols is None or c == cols):
+        if ((t.is_cuda if dev is None else t.get_device() == dev) and inner == 1 and ld >= c
+                and (rows is None or r == rows) and (cols is None or c == cols)):
             return t.data_ptr(), ld, _DTYPES[t.dtype]
     except (ValueError, KeyError):
         pass
-    return _mat_checked(name, t, rows, cols)
+    return _mat_checked(name, t, rows, cols, dev)
 
 
-def _mat_checked(name: str, t, rows, cols) -> tuple:
+def _mat_checked(name: str, t, rows, cols, dev) -> tuple:
     """The same, case by case: what is wrong, or the layouts whose strides say nothing."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} is not a CUDA tensor")
+    _on(name, t, dev)
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} has {len(shape)} dimensions, 2 are wanted")
@@ -150,8 +167,10 @@ def _mat_checked(name: str, t, rows, cols) -> tuple:
     return t.data_ptr(), ld, _dtype(t)
 
 
-def _vec(name: str, t, n: int, f32: bool = False) -> int:
-    if not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+def _vec(name: str, t, n: int, dev: Optional[int] = None, f32: bool = False) -> int:
+    if not t.is_cuda if dev is None else t.get_device() != dev:
+        _on(name, t, dev)
+    if t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ValueError(f"{name} must be a contiguous CUDA vector of {n}")
     if f32 and _dtype(t) != _d3.F32:
         raise ValueError(f"{name} must be float32")
@@ -176,26 +195,30 @@ class Packed8:
         return tuple(self.codes.shape)
 
 
-def _packed(name: str, p: Packed8, rows: Optional[int] = None, cols: Optional[int] = None) -> tuple:
-    """(codes, ld_codes, scales, ld_scales); shape checked where given."""
+def _packed(name: str, p: Packed8, rows: Optional[int] = None, cols: Optional[int] = None,
+            dev: Optional[int] = None) -> tuple:
+    """(codes, ld_codes, scales, ld_scales); shape and device checked where given."""
     q, s = p.codes, p.scales
     try:
-        (r, c), (sr, nb), (lq, qi), (ls, si) = q.shape, s.shape, q.stride(), s.stride()
-        if (q.is_cuda and s.is_cuda and qi == 1 and si == 1 and lq >= c and ls >= nb and sr == r and nb == (c + 31) // 32
-                and (rows is None or (r == rows and c == cols)) and q.dtype is _I8 and s.dtype is _U8):
+        (r, c), (sr, nb), (lq, qi), (ls, si), d = q.shape, s.shape, q.stride(), s.stride(), q.get_device()
+        if (qi == 1 and si == 1 and lq >= c and ls >= nb and sr == r and nb == (c + 31) // 32
+                and (rows is None or (r == rows and c == cols)) and q.dtype is _I8 and s.dtype is _U8
+                and d >= 0 and s.get_device() == d and (dev is None or d == dev)):
             return q.data_ptr(), lq, s.data_ptr(), ls
     except ValueError:
         pass
-    return _packed_checked(name, q, s, rows, cols)
+    return _packed_checked(name, q, s, rows, cols, dev)
 
 
-def _packed_checked(name: str, q, s, rows, cols) -> tuple:
+def _packed_checked(name: str, q, s, rows, cols, dev) -> tuple:
     """The same, case by case (see _mat_checked)."""
     t = _load_torch()
     if q.dtype != t.int8 or s.dtype != t.uint8:
         raise ValueError(f"{name}: codes must be int8 and scales uint8")
     if not (q.is_cuda and s.is_cuda) or q.dim() != 2 or s.dim() != 2:
         raise ValueError(f"{name}: codes and scales must be 2-D CUDA tensors")
+    _on(f"{name}: codes", q, s.get_device() if dev is None else dev)
+    _on(f"{name}: scales", s, q.get_device())
     r, c = q.shape
     if rows is not None and (r, c) != (rows, cols):
         raise ValueError(f"{name} is {r} x {c}, {rows} x {cols} is wanted")
@@ -221,30 +244,32 @@ def alloc_packed8(rows: int, cols: int, device=None) -> Packed8:
     return Packed8(codes, scales)
 
 
-def _ws(ws, nbytes):
+def _ws(ws, nbytes, dev):
     if ws is None:
         return None, 0
-    if not ws.is_cuda:
-        raise ValueError("ws is not a CUDA tensor")
+    if ws.get_device() != dev:
+        _on("ws", ws, dev)
     return ws.data_ptr(), nbytes if nbytes is not None else ws.numel() * ws.element_size()
 
 
 def pack8(x, out: Packed8, stream=None):
     """x [rows, cols] into 8-bit blocks (see dion3_pack8)."""
     m = _MAT.pack(*_mat("x", x))
-    rows, cols = x.shape
-    _d3._check(_fn("dion3_pack8")(rows, cols, m, _PACK.pack(*_packed("out", out, rows, cols)), _stream(stream)))
+    (rows, cols), dev = x.shape, x.get_device()
+    _d3._check(_fn("dion3_pack8")(rows, cols, m, _PACK.pack(*_packed("out", out, rows, cols, dev)),
+                                  _stream(stream, dev)))
 
 
 def unpack8(src: Packed8, out, stream=None):
     """The values that 8-bit blocks stand for, in out's dtype (see dion3_unpack8)."""
     p = _PACK.pack(*_packed("src", src))
-    rows, cols = src.codes.shape
-    _d3._check(_fn("dion3_unpack8")(rows, cols, p, _MAT.pack(*_mat("out", out, rows, cols)), _stream(stream)))
+    (rows, cols), dev = src.codes.shape, src.codes.get_device()
+    _d3._check(_fn("dion3_unpack8")(rows, cols, p, _MAT.pack(*_mat("out", out, rows, cols, dev)),
+                                    _stream(stream, dev)))
 
 
-def _opt(name: str, t, rows: int, cols: int):
-    return None if t is None else _MAT.pack(*_mat(name, t, rows, cols))
+def _opt(name: str, t, rows: int, cols: int, dev: int):
+    return None if t is None else _MAT.pack(*_mat(name, t, rows, cols, dev))
 
 
 def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] = None, rstd=None,
@@ -253,11 +278,12 @@ def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] 
     and / or its 8-bit blocks y8, and rstd for the backward pass (see
     dion3_rms_norm)."""
     mx = _MAT.pack(*_mat("x", x))
-    rows, cols = x.shape
+    (rows, cols), dev = x.shape, x.get_device()
     _d3._check(_fn("dion3_rms_norm")(
-        rows, cols, mx, _opt("residual", residual, rows, cols), _vec("weight", weight, cols), _dtype(weight), eps,
-        _opt("h", h, rows, cols), _opt("y", y, rows, cols), None if y8 is None else _PACK.pack(*_packed("y8", y8, rows, cols)),
-        None if rstd is None else _vec("rstd", rstd, rows, f32=True), _stream(stream)))
+        rows, cols, mx, _opt("residual", residual, rows, cols, dev), _vec("weight", weight, cols, dev), _dtype(weight),
+        eps, _opt("h", h, rows, cols, dev), _opt("y", y, rows, cols, dev),
+        None if y8 is None else _PACK.pack(*_packed("y8", y8, rows, cols, dev)),
+        None if rstd is None else _vec("rstd", rstd, rows, dev, f32=True), _stream(stream, dev)))
 
 
 def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -272,12 +298,12 @@ def rms_norm_backward(dy, h, weight, rstd, dx, *, dh=None, dw=None, accumulate: 
     gradient that reaches h from elsewhere) and dw, float32 (see
     dion3_rms_norm_backward)."""
     mdy = _MAT.pack(*_mat("dy", dy))
-    rows, cols = dy.shape
-    p, n = _ws(ws, ws_bytes)
+    (rows, cols), dev = dy.shape, dy.get_device()
+    p, n = _ws(ws, ws_bytes, dev)
     _d3._check(_fn("dion3_rms_norm_backward")(
-        rows, cols, mdy, _opt("h", h, rows, cols), _vec("weight", weight, cols), _dtype(weight),
-        _vec("rstd", rstd, rows, f32=True), _opt("dh", dh, rows, cols), _opt("dx", dx, rows, cols),
-        None if dw is None else _vec("dw", dw, cols, f32=True), int(accumulate), p, n, _stream(stream)))
+        rows, cols, mdy, _opt("h", h, rows, cols, dev), _vec("weight", weight, cols, dev), _dtype(weight),
+        _vec("rstd", rstd, rows, dev, f32=True), _opt("dh", dh, rows, cols, dev), _opt("dx", dx, rows, cols, dev),
+        None if dw is None else _vec("dw", dw, cols, dev, f32=True), int(accumulate), p, n, _stream(stream, dev)))
 
 
 def _ws_size(fn: str, tokens, in_features, out_features, dtype, strided) -> int:
@@ -307,21 +333,21 @@ def linear(x, w, y, *, bias=None, residual=None, act: int = ACT_NONE, z=None, y8
     receives the pre-activation, y8 the output in 8-bit blocks (see
     dion3_linear)."""
     mx = _mat("x", x)
-    tokens, k = x.shape
-    mw = _mat("w", w, None, k)
+    (tokens, k), dev = x.shape, x.get_device()
+    mw = _mat("w", w, None, k, dev)
     n = w.shape[0]
     z8 = _NO_PACK
     mz = _NO_MAT
     if isinstance(z, Packed8):
-        z8 = _packed("z", z, tokens, n)
+        z8 = _packed("z", z, tokens, n, dev)
     elif z is not None:
-        mz = _mat("z", z, tokens, n)
-    args = _LINEAR.pack(tokens, k, n, act, *mx, *mw, *_mat("y", y, tokens, n),
-                        *(_NO_MAT if residual is None else _mat("residual", residual, tokens, n)), *mz, *z8,
-                        *(_NO_PACK if y8 is None else _packed("y8", y8, tokens, n)),
-                        0 if bias is None else _vec("bias", bias, n), 0 if bias is None else _dtype(bias))
-    p, nb = _ws(ws, ws_bytes)
-    _d3._check(_fn("dion3_linear")(args, p, nb, _stream(stream)))
+        mz = _mat("z", z, tokens, n, dev)
+    args = _LINEAR.pack(tokens, k, n, act, *mx, *mw, *_mat("y", y, tokens, n, dev),
+                        *(_NO_MAT if residual is None else _mat("residual", residual, tokens, n, dev)), *mz, *z8,
+                        *(_NO_PACK if y8 is None else _packed("y8", y8, tokens, n, dev)),
+                        0 if bias is None else _vec("bias", bias, n, dev), 0 if bias is None else _dtype(bias))
+    p, nb = _ws(ws, ws_bytes, dev)
+    _d3._check(_fn("dion3_linear")(args, p, nb, _stream(stream, dev)))
 
 
 def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE, z=None, accumulate: bool = False,
@@ -331,21 +357,21 @@ def linear_backward(dy, x, w, *, dx=None, dw=None, db=None, act: int = ACT_NONE,
     :class:`Packed8` checkpoints; ``accumulate`` adds to dw and db (see
     dion3_linear_backward)."""
     mdy = _mat("dy", dy)
-    tokens, n = dy.shape
-    mw = _mat("w", w, n)
+    (tokens, n), dev = dy.shape, dy.get_device()
+    mw = _mat("w", w, n, None, dev)
     k = w.shape[1]
     mx, x8, mz, z8 = _NO_MAT, _NO_PACK, _NO_MAT, _NO_PACK
     if isinstance(x, Packed8):
-        x8 = _packed("x", x, tokens, k)
+        x8 = _packed("x", x, tokens, k, dev)
     elif x is not None:
-        mx = _mat("x", x, tokens, k)
+        mx = _mat("x", x, tokens, k, dev)
     if isinstance(z, Packed8):
-        z8 = _packed("z", z, tokens, n)
+        z8 = _packed("z", z, tokens, n, dev)
     elif z is not None:
-        mz = _mat("z", z, tokens, n)
+        mz = _mat("z", z, tokens, n, dev)
     args = _LINEAR_GRAD.pack(tokens, k, n, act, int(accumulate), *mdy, *mw, *mx, *mz, *x8, *z8,
-                             *(_NO_MAT if dx is None else _mat("dx", dx, tokens, k)),
-                             *(_NO_MAT if dw is None else _mat("dw", dw, n, k)),
-                             0 if db is None else _vec("db", db, n, f32=True))
-    p, nb = _ws(ws, ws_bytes)
-    _d3._check(_fn("dion3_linear_backward")(args, p, nb, _stream(stream)))
+                             *(_NO_MAT if dx is None else _mat("dx", dx, tokens, k, dev)),
+                             *(_NO_MAT if dw is None else _mat("dw", dw, n, k, dev)),
+                             0 if db is None else _vec("db", db, n, dev, f32=True))
+    p, nb = _ws(ws, ws_bytes, dev)
+    _d3._check(_fn("dion3_linear_backward")(args, p, nb, _stream(stream, dev)))

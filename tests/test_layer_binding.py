@@ -13,8 +13,8 @@ class Fake:
     """What the binding reads of a tensor, on no device."""
     is_cuda = True
 
-    def __init__(self, shape, dtype, address, pitch=None):
-        self.shape, self.dtype, self.address = torch.Size(shape), dtype, address
+    def __init__(self, shape, dtype, address, pitch=None, device=0):
+        self.shape, self.dtype, self.address, self.device = torch.Size(shape), dtype, address, device
         self.pitch = shape[-1] if pitch is None else pitch
 
     def stride(self, i=None):
@@ -28,7 +28,13 @@ class Fake:
         return self.address
 
     def get_device(self):
-        return 0
+        return self.device
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return 4
 
 
 @pytest.fixture
@@ -87,6 +93,56 @@ def test_replaced_blocks_are_checked(calls, codes, scales):
     with pytest.raises(ValueError):
         d3.unpack8(p, Fake((4, 40), torch.bfloat16, 0x8000), stream=1)
     assert not calls
+
+
+def all_calls():
+    """Every entry point with every tensor that it takes, as (call, names of the tensors)."""
+    bf, f32 = torch.bfloat16, torch.float32
+
+    def mat(rows, cols, dtype=bf):
+        return lambda d: Fake((rows, cols), dtype, 0x100, device=d)
+
+    def vec(n):
+        return lambda d: Fake((n,), f32, 0x100, device=d)
+
+    def pack(rows, cols):
+        def make(d):
+            return d3.Packed8(Fake((rows, cols), torch.int8, 0x100, device=d),
+                              Fake((rows, -(-cols // 32)), torch.uint8, 0x100, device=d))
+        return make
+    big = vec(1 << 20)
+    return [(d3.pack8, dict(x=mat(4, 40), out=pack(4, 40))), (d3.unpack8, dict(src=pack(4, 40), out=mat(4, 40))),
+            (d3.rms_norm, dict(x=mat(4, 40), weight=vec(40), y=mat(4, 40), residual=mat(4, 40), h=mat(4, 40),
+                               y8=pack(4, 40), rstd=vec(4))),
+            (d3.rms_norm_backward, dict(dy=mat(4, 40), h=mat(4, 40), weight=vec(40), rstd=vec(4), dx=mat(4, 40),
+                                        dh=mat(4, 40), dw=vec(40), ws=big)),
+            (d3.linear, dict(x=mat(4, 8), w=mat(40, 8), y=mat(4, 40), bias=vec(40), residual=mat(4, 40), z=mat(4, 40),
+                             y8=pack(4, 40), ws=big)),
+            (d3.linear, dict(x=mat(4, 8), w=mat(40, 8), y=mat(4, 40), z=pack(4, 40))),
+            (d3.linear_backward, dict(dy=mat(4, 40), x=mat(4, 8), w=mat(40, 8), dx=mat(4, 8), dw=mat(40, 8, f32),
+                                      db=vec(40), z=mat(4, 40), ws=big)),
+            (d3.linear_backward, dict(dy=mat(4, 40), x=pack(4, 8), w=mat(40, 8), dw=mat(40, 8, f32), z=pack(4, 40)))]
+
+
+@pytest.mark.parametrize("case", range(8))
+def test_tensors_on_another_device_are_refused(calls, monkeypatch, case):
+    call, tensors = all_calls()[case]
+    for stream in (None, 1):
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1, raising=False)
+        call(**{k: t(0) for k, t in tensors.items()}, stream=stream)
+        assert len(calls) == 1
+        calls.clear()
+        for other in tensors:  # one of them is on the other device, and all are while the first is current
+            with pytest.raises(ValueError, match="device|cuda:1"):
+                call(**{k: t(int(k == other)) for k, t in tensors.items()}, stream=stream)
+        with pytest.raises(ValueError, match="cuda:1"):
+            call(**{k: t(1) for k, t in tensors.items()}, stream=stream)
+        assert not calls
+
+
+def test_blocks_on_two_devices_are_refused(calls):
+    with pytest.raises(ValueError, match="device"):
+        d3.Packed8(Fake((4, 40), torch.int8, 1), Fake((4, 2), torch.uint8, 1, device=1))
 
 
 @pytest.mark.gpu
