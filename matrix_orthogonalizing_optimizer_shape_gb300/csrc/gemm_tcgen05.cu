@@ -88,6 +88,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -1072,22 +1073,23 @@ bool diag_full_enabled() {
 
 // Clusters of this kernel that fit on the device at once (persistent grid).
 int max_active_clusters(int dev) {
-  static int cached[64] = {0};
-  if (cached[dev & 63] == 0) {
+  static std::atomic<int> cached[64];
+  std::atomic<int>& c = cached[dev & 63];
+  int n = c.load(std::memory_order_relaxed);
+  if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = Smem::kDyn;
-    int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, gemm_tcgen05_kernel<false>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       int sms = 0;
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
       n = sms > 1 ? sms / 2 : 1;
     }
-    cached[dev & 63] = n;
+    c.store(n, std::memory_order_relaxed);
   }
-  return cached[dev & 63];
+  return n;
 }
 
 }  // namespace

@@ -26,6 +26,9 @@ struct Pack8 {
 
 enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 
+// SMs of the current device.
+int sm_count();
+
 // ---------------------------------------------------------------------------
 // Memory-bound kernels (layer_mem.cu)
 // ---------------------------------------------------------------------------

@@ -17,6 +17,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -949,20 +950,19 @@ cudaLaunchConfig_t cluster_config(int ctas, int threads, int smem, int size, boo
 
 // Clusters of `kern` that the device runs at once.
 template <typename K>
-int resident_clusters(K kern, int threads, int smem, int size, int dev, int* cached) {
-  if (cached[dev & 63] == 0) {
+int resident_clusters(K kern, int threads, int smem, int size, int dev, std::atomic<int>* cached) {
+  std::atomic<int>& c = cached[dev & 63];
+  int n = c.load(std::memory_order_relaxed);
+  if (n == 0) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(size, threads, smem, size, false, nullptr, attr);
-    int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
-      int sms = 0;
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-      n = sms > size ? sms / size : 1;
+      n = std::max(1, sm_count() / size);
     }
-    cached[dev & 63] = n;
+    c.store(n, std::memory_order_relaxed);
   }
-  return cached[dev & 63];
+  return n;
 }
 
 // The pair kernel's A is the operand of the output's rows (Product::B) and its
@@ -972,7 +972,7 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   using C = PairCfg<PN>;
   auto kern = pair_kernel<BF16, AT, BT, OUT, PN>;
   static std::once_flag once[64];
-  static int pairs[64] = {0};
+  static std::atomic<int> pairs[64];
   int dev = 0;
   cudaGetDevice(&dev);
   const cudaError_t err = allow_smem(kern, C::kDyn, once, dev);
@@ -1001,16 +1001,6 @@ cudaError_t run_pair(const Product& g, const Epilogue& e, unsigned* status, cuda
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = cluster_config(2 * clusters, C::kThreads, C::kDyn, 2, pdl_enabled(), s, attr);
   return cudaLaunchKernelEx(&cfg, kern, ta, tb, to, tz, p);
-}
-
-int sm_count(int dev) {
-  static int cached[64] = {0};
-  if (cached[dev & 63] == 0) {
-    int n = 0;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    cached[dev & 63] = n > 0 ? n : 1;
-  }
-  return cached[dev & 63];
 }
 
 template <bool BF16, bool AT, bool BT, int BN, bool FWD, bool DEEP, bool SUM>
@@ -1054,9 +1044,7 @@ struct Plan {
 // where a pair a tile takes 15.9; at 16384 x 512 x 512 (dW) K over 8 CTAs, 22 us,
 // where a pair takes 77.
 Plan plan_product(const Product& g) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const int sms = sm_count(dev), pairs = sms / 2;
+  const int sms = sm_count(), pairs = sms / 2;
   const long long nkb = (g.K + BK - 1) / BK, tm = (g.M + BM - 1) / BM;
   const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
   const auto off_line = [](const Mat& m) { return m.ld % 64 != 0 || reinterpret_cast<uintptr_t>(m.p) % 128 != 0; };

@@ -1136,18 +1136,23 @@ __global__ void __launch_bounds__(256) zero_kernel(int rows, int cols, int elem_
 // --------------------------------------------------------------------------
 // Host side
 // --------------------------------------------------------------------------
+}  // namespace
+
 int sm_count() {
-  static int cached[64] = {0};
+  static std::atomic<int> cached[64];
   int dev = 0;
   cudaGetDevice(&dev);
-  if (cached[dev & 63] == 0) {
-    int n = 0;
+  std::atomic<int>& c = cached[dev & 63];
+  int n = c.load(std::memory_order_relaxed);
+  if (n == 0) {
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    cached[dev & 63] = n > 0 ? n : 1;
+    n = n > 0 ? n : 1;
+    c.store(n, std::memory_order_relaxed);
   }
-  return cached[dev & 63];
+  return n;
 }
 
+namespace {
 // Blocks for `work` items of 256 threads, enough to fill the device.
 unsigned flat_grid(long long threads) {
   const long long want = (threads + 255) / 256;

@@ -24,3 +24,14 @@ def test_only_commits_reach_several_ctas():
                 assert "tcgen05.commit" in stmt, f"{name}: {stmt[:200]}"
                 commits += 1
     assert commits > 0
+
+
+def test_cached_values_are_atomic():
+    """Host threads may make their first calls together: what a function keeps in a
+    static is an atomic, a once_flag, constant, or written under one of them."""
+    guarded = re.compile(r"std::(atomic|once_flag|mutex)|const(expr)? |\bPFN_|\(")
+    for name, text in sources().items():
+        for m in re.finditer(r"^ +static (?!_)[^;{]*", text, flags=re.M):
+            decl = m.group(0)
+            locked = "std::mutex" in text[max(0, m.start() - 200):m.start()]  # declared right after its lock
+            assert locked or guarded.search(decl), f"{name}: {decl.strip()}"
