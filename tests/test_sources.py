@@ -35,3 +35,14 @@ def test_cached_values_are_atomic():
             decl = m.group(0)
             locked = "std::mutex" in text[max(0, m.start() - 200):m.start()]  # declared right after its lock
             assert locked or guarded.search(decl), f"{name}: {decl.strip()}"
+
+
+def test_every_wrapper_is_used():
+    """tc_ops.cuh holds the instructions that the kernels issue, and no others."""
+    texts = sources()
+    names = re.findall(r"__forceinline__ \w+ (\w+)\(|constexpr \w+ (\w+)\(", texts["tc_ops.cuh"])
+    assert len(names) > 20
+    users = [texts["tc_ops.cuh"]] + [t for n, t in texts.items() if '"tc_ops.cuh"' in t]
+    for name in (a or b for a, b in names):
+        uses = sum(len(re.findall(rf"\b{name}\b", t)) for t in users)
+        assert uses > 1, f"{name} is not used"
