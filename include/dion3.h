@@ -540,6 +540,7 @@ dion3_status dion3_rms_norm_backward(int32_t rows, int32_t cols, const dion3_mat
  *   [tokens][out_features]: one dtype, bf16 or fp16 (fp32 returns
  *   DION3_ERR_UNSUPPORTED).  residual (may be y), z, z8, y8 and bias (any dtype,
  *   [out_features]) are optional: data / codes / pointer NULL.
+ *   y may not be x or w.
  *   z, z8  the pre-activation for the backward pass, in 16 bits or in blocks.
  *   y8     y in blocks (the next layer's x in its backward pass).
  * Products accumulate in fp32 and the epilogue works on the fp32 sums; z, y
@@ -574,7 +575,8 @@ dion3_status dion3_linear(const dion3_linear_args* args, void* ws, size_t ws_byt
  *            activation.
  *   x or x8  the layer's input, exactly one of them (with dw only).  The
  *            product with x8 is that of the values the blocks stand for.
- *   dx, dw, db  each may be absent.  dw [out_features][in_features] has any
+ *   dx, dw, db  each may be absent.  dx may not be dy or w, nor x where dw is
+ *            wanted.  dw [out_features][in_features] has any
  *            dtype and pitch (dense bf16 or fp32: a dion3_group gradient);
  *            db is fp32.  accumulate != 0: dw += and db +=, each sum formed in
  *            fp32 and rounded once.

@@ -413,8 +413,8 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
     }
   }
   DION3_TRY(check_f32("db", g->db));
-  if (T > 0 && want_dx && (g->dx.data == g->dy.data || g->dx.data == g->w.data || g->dx.data == g->x.data))
-    return fail(DION3_ERR_INVALID_ARG, "dx may not be dy, w or x");
+  if (T > 0 && want_dx && (g->dx.data == g->dy.data || g->dx.data == g->w.data || (want_dw && g->dx.data == g->x.data)))
+    return fail(DION3_ERR_INVALID_ARG, "dx may not be dy, w or (with dw) x");
 
   // dz is dy itself without an activation, if the products can read it well.
   const bool products = want_dx || want_dw;
