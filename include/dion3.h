@@ -588,7 +588,7 @@ dion3_status dion3_linear(const dion3_linear_args* args, void* ws, size_t ws_byt
  * random signs, which its own rounding covers up to some 10^5 tokens.
  * Without an activation the products read dy itself; with one, dz is rounded
  * to the layer's 16-bit type, which the tensor cores take, while db sums the
- * unrounded dz.
+ * unrounded dz.  A fp32 dw behind an activation carries that rounding.
  */
 typedef struct {
   int32_t tokens, in_features, out_features;

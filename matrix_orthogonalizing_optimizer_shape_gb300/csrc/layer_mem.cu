@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a) {
 // Gradient: hn = h rstd, g = dy w; dx = dh + rstd (g - hn mean(g hn)), dw = sum
 // over rows of dy hn.  Bound by HBM.  As the forward kernel, with dw's column
 // sums of the CTA's rows in registers; column_sum_kernel adds the CTAs' sums in
-// order.  16384 x 4096 bf16 with dh: 95 us, 5.7 TB/s.
+// order.  16384 x 4096 bf16 with dh: 91 us, 5.9 TB/s.
 __device__ __forceinline__ float norm_dx(float g, float hn, float mean, float rstd, float dh) {
   return fmaf(rstd, fmaf(-hn, mean, g), dh);
 }

@@ -317,7 +317,8 @@ def _ws_size(fn: str, tokens, in_features, out_features, dtype, strided) -> int:
 
 def linear_workspace_size(tokens: int, in_features: int, out_features: int, *, dtype, strided: bool = False) -> int:
     """Workspace bytes of :func:`linear` (0 for dense tensors with in_features a
-    multiple of 8); ``strided``: for any pitch and base."""
+    multiple of 64; needed only where it is no multiple of 8, and else a help to
+    large products); ``strided``: for any pitch and base."""
     return _ws_size("dion3_linear_workspace_size", tokens, in_features, out_features, dtype, strided)
 
 
