@@ -606,6 +606,46 @@ dion3_status dion3_linear_backward_workspace_size(int32_t tokens, int32_t in_fea
 dion3_status dion3_linear_backward(const dion3_linear_grad_args* args, void* ws, size_t ws_bytes,
                                    dion3_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Model operators: what stands around a stack of layers in a language model
+ * that is trained with the operators above and the step.  Token embedding, a
+ * recurrence along the tokens, log probabilities, and the clipping of all
+ * gradients, with their backward passes.  The paper has no counterpart.
+ *
+ * The conventions of the layer operators hold: matrices of any row pitch and
+ * element-aligned base, fp32 sums and statistics, the same bits from call to
+ * call.  Token numbers (ids, targets) are device vectors of 4- or 8-byte signed
+ * integers (id_bytes).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Token embedding, y[t] = scale table[ids[t]].
+ *   ids    [tokens]; a position whose id lies outside [0, vocab) (padding, -1 by
+ *          custom) gets a row of zeros.
+ *   table  [vocab][cols], y [tokens][cols], any two dtypes.  y may not be table.
+ * cols <= 2^20 here and in the gradient.
+ */
+dion3_status dion3_embedding(int32_t tokens, int32_t vocab, int32_t cols, const void* ids,
+                             int32_t id_bytes, const dion3_matrix* table, float scale,
+                             const dion3_matrix* y, dion3_stream_t stream);
+
+/*
+ * Gradient of dion3_embedding for its table,
+ *   dtable[v] = scale (sum of dy[t] over the positions t with ids[t] = v),
+ * summed in fp32 in an order that depends on the ids alone and rounded once.
+ * Rows of tokens that do not occur are set to 0.  accumulate != 0: dtable +=
+ * instead, and the rows of tokens that do not occur are not touched.
+ *   dy      [tokens][cols], dtable [vocab][cols], any two dtypes.  dtable may not
+ *           be dy.
+ *   tokens  at most 2^27.
+ */
+dion3_status dion3_embedding_backward_workspace_size(int32_t tokens, int32_t vocab, int32_t cols,
+                                                     size_t* bytes);
+dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t cols,
+                                      const dion3_matrix* dy, const void* ids, int32_t id_bytes,
+                                      float scale, const dion3_matrix* dtable, int32_t accumulate,
+                                      void* ws, size_t ws_bytes, dion3_stream_t stream);
+
 /*
  * The bounded device-side wait of the tensor-core kernels, run on its own (a
  * diagnostic of the timeout path; the paper has no counterpart).  One thread

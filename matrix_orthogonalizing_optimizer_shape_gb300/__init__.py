@@ -43,6 +43,7 @@ EXPORTED = (
     "dion3_pack8", "dion3_unpack8", "dion3_rms_norm", "dion3_rms_norm_backward_workspace_size",
     "dion3_rms_norm_backward", "dion3_linear_workspace_size", "dion3_linear",
     "dion3_linear_backward_workspace_size", "dion3_linear_backward",
+    "dion3_embedding", "dion3_embedding_backward_workspace_size", "dion3_embedding_backward",
 )
 
 
@@ -474,5 +475,9 @@ from .layer import (  # noqa: E402,F401
     ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, PACK_BLOCK, Packed8, alloc_packed8, linear, linear_backward,
     linear_backward_workspace_size, linear_workspace_size, pack8, rms_norm, rms_norm_backward,
     rms_norm_backward_workspace_size, unpack8)
+from . import model as _model  # noqa: E402
+from .model import (  # noqa: E402,F401
+    embedding, embedding_backward, embedding_backward_workspace_size)
 
 _SIGS.update(_layer.SIGS)
+_SIGS.update(_model.SIGS)

@@ -1,0 +1,364 @@
+// Token embedding and its gradient on sm_103a.  Both are bound by HBM.
+//
+// The gradient sums the rows of dy that belong to one token.  Which rows those
+// are is found without a sort of the whole vocabulary: the tokens are grouped by
+// the low bits of their number, a block a group (group_kernel), then summed in
+// windows of equal numbers of positions (window_kernel), so that a token that
+// makes up a tenth of the batch costs no block more than any other, and runs that
+// cross windows are joined in order (join_kernel).  No atomic touches a sum: the
+// result's bits depend on the ids alone.
+#include <algorithm>
+#include <type_traits>
+
+#include "layer_math.cuh"
+#include "model.h"
+
+namespace dion3 {
+namespace {
+
+using namespace lm;
+
+__device__ __forceinline__ long long id_at(const Ids& ids, long long i) {
+  return ids.bytes == 8 ? static_cast<const long long*>(ids.p)[i] : static_cast<const int*>(ids.p)[i];
+}
+
+// --------------------------------------------------------------------------
+// Lookup.  blockDim = (lanes along a row, rows); a thread keeps its columns and
+// walks kWalk rows, all their loads issued before the first is used.  VEC = 8
+// columns a thread, or 1 where rows are not whole aligned pieces.
+// --------------------------------------------------------------------------
+constexpr int kWalk = 4;
+
+template <typename W, typename T, int VEC>
+__global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+  if (c >= a.cols) return;
+  const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
+  for (long long t = static_cast<long long>(blockIdx.y) * blockDim.y + threadIdx.y; t < a.tokens; t += kWalk * step) {
+    long long id[kWalk];
+    float v[kWalk][VEC];
+#pragma unroll
+    for (int i = 0; i < kWalk; ++i) id[i] = t + i * step < a.tokens ? id_at(a.ids, t + i * step) : -1;
+#pragma unroll
+    for (int i = 0; i < kWalk; ++i) {
+      if (id[i] >= 0 && id[i] < a.vocab) {
+        load_vec<W, VEC>(static_cast<const W*>(a.table.p) + id[i] * a.table.ld + c, v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kWalk; ++i) {
+      if (t + i * step >= a.tokens) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i][j] *= a.scale;
+      store_vec<T, VEC>(static_cast<T*>(a.y.p) + (t + i * step) * a.y.ld + c, v[i]);
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// Groups.  Block b takes the tokens with id mod blocks = b (a power of two):
+// frequent tokens have neighbouring numbers in most vocabularies, and land in
+// different blocks.  Every block reads all ids (from L2: 64 kB at 16384 tokens),
+// counts its own by token and warp, and lays their positions out behind those of
+// the blocks before it, which it counts on the way.  A warp takes a contiguous
+// part of the positions in order, so a token's positions end up ascending.
+// Rows of tokens that do not occur are zeroed here too.
+// --------------------------------------------------------------------------
+constexpr int kGroupWarps = 16, kGroupThreads = 32 * kGroupWarps;
+constexpr int kMaxLocals = 512;  // tokens of a block: counters in 34 kB of shared memory
+constexpr int kMinGroups = 256;
+
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+__global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, int log_groups, int locals) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ int cnt[];  // [kGroupWarps][locals], then [locals] totals
+  __shared__ int before_s, wsum[kGroupWarps];
+  int* total = cnt + kGroupWarps * locals;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int mine = blockIdx.x, mask = (1 << log_groups) - 1;
+  for (int i = threadIdx.x; i < kGroupWarps * locals; i += kGroupThreads) cnt[i] = 0;
+  if (threadIdx.x == 0) before_s = 0;
+  __syncthreads();
+
+  const int slice = ((a.tokens + kGroupWarps - 1) / kGroupWarps + 127) / 128 * 128;
+  const long long lo = static_cast<long long>(warp) * slice, hi = min(lo + slice, static_cast<long long>(a.tokens));
+  int* own = cnt + warp * locals;
+  int before = 0;
+  auto load = [&](long long i0, int (&id)[4]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const long long i = i0 + 32 * u + lane, v = i < hi ? id_at(a.ids, i) : -1;
+      id[u] = v >= 0 && v < a.vocab ? static_cast<int>(v) : -1;
+    }
+  };
+  for (long long i0 = lo; i0 < hi; i0 += 128) {
+    int id[4];
+    load(i0, id);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (id[u] < 0) continue;
+      const int g = id[u] & mask;
+      before += g < mine;
+      if (g == mine) atomicAdd(own + (id[u] >> log_groups), 1);
+    }
+  }
+  before = warp_sum(before);
+  if (lane == 0) atomicAdd(&before_s, before);
+  __syncthreads();
+
+  // Where each warp's part of each token starts.
+  int sum = 0;
+  if (threadIdx.x < locals) {
+    for (int w = 0; w < kGroupWarps; ++w) {
+      const int n = cnt[w * locals + threadIdx.x];
+      cnt[w * locals + threadIdx.x] = sum;
+      sum += n;
+    }
+    total[threadIdx.x] = sum;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += n;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int base = before_s + incl - sum;
+  for (int w = 0; w < warp; ++w) base += wsum[w];
+  if (threadIdx.x < locals)
+    for (int w = 0; w < kGroupWarps; ++w) cnt[w * locals + threadIdx.x] += base;
+  if (threadIdx.x == kGroupThreads - 1 && mine == mask) *a.count = base + sum;
+  __syncthreads();
+
+  for (long long i0 = lo; i0 < hi; i0 += 128) {
+    int id[4];
+    load(i0, id);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool hit = id[u] >= 0 && (id[u] & mask) == mine;
+      const unsigned hits = __ballot_sync(0xffffffffu, hit);
+      if (hits == 0u) continue;
+      if (hit) {
+        const int local = id[u] >> log_groups;
+        const unsigned same = __match_any_sync(hits, local);
+        const int at = own[local] + __popc(same & ((1u << lane) - 1u));
+        a.order[at] = static_cast<int>(i0) + 32 * u + lane;
+        a.token[at] = id[u];
+        __syncwarp(hits);
+        if ((same >> lane) == 1u) own[local] = at + 1;  // the last of them
+      }
+      __syncwarp();
+    }
+  }
+  if (a.accumulate) return;
+  const int es = a.table_dtype == kF32 ? 4 : 2;
+  const long long bytes = static_cast<long long>(a.cols) * es, pitch = a.dtable.ld * es;
+  uint8_t* out = static_cast<uint8_t*>(a.dtable.p);
+  const bool pieces = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(bytes) | static_cast<uintptr_t>(pitch)) & 15u) == 0;
+  for (int l = warp; l < locals; l += kGroupWarps) {
+    const long long row = (static_cast<long long>(l) << log_groups) + mine;
+    if (row >= a.vocab || total[l] != 0) continue;
+    uint8_t* p = out + row * pitch;
+    if (pieces) {
+      for (long long i = 16 * lane; i < bytes; i += 512) *reinterpret_cast<uint4*>(p + i) = make_uint4(0u, 0u, 0u, 0u);
+    } else if (es == 4) {
+      for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint32_t*>(p)[i] = 0u;
+    } else {
+      for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0u;
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// Sums.  A window is `window` grouped positions; a block takes one window of one
+// strip of columns, walks its rows kBatch at a time with all their loads in
+// flight, and writes a token's row when its run ends.  A run that reaches over
+// the window's first or last position leaves its sum in fp32 instead: slot 0 of
+// the window if it began before, else slot 1.
+// --------------------------------------------------------------------------
+constexpr int kBatch = 8, kMaxWindow = 512;
+
+template <int VEC>
+__device__ __forceinline__ void put_row(const EmbedGradArgs& a, int token, int c, const float (&sum)[VEC]) {
+  const long long at = static_cast<long long>(token) * a.dtable.ld + c;
+  auto put = [&](auto* p) {
+    using T = std::remove_pointer_t<decltype(p)>;
+    float v[VEC];
+    if (a.accumulate) {
+      load_vec<T, VEC>(p + at, v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = fmaf(sum[j], a.scale, v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = sum[j] * a.scale;
+    }
+    store_vec<T, VEC>(p + at, v);
+  };
+  if (a.table_dtype == kF32)
+    put(static_cast<float*>(a.dtable.p));
+  else if (a.table_dtype == kBF16)
+    put(static_cast<__nv_bfloat16*>(a.dtable.p));
+  else
+    put(static_cast<__half*>(a.dtable.p));
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) window_kernel(EmbedGradArgs a, int window) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ int pos[kMaxWindow], tok[kMaxWindow + 2];
+  const int n = *a.count, s0 = blockIdx.x * window, s1 = min(s0 + window, n);
+  if (s0 >= n) return;
+  for (int i = threadIdx.x; i < s1 - s0; i += blockDim.x) pos[i] = a.order[s0 + i];
+  for (int i = static_cast<int>(threadIdx.x) - 1; i <= s1 - s0; i += blockDim.x)
+    tok[i + 1] = s0 + i >= 0 && s0 + i < n ? a.token[s0 + i] : -1;
+  __syncthreads();
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  if (c >= a.cols) return;
+  const T* dy = static_cast<const T*>(a.dy.p) + c;
+  float* part = a.partials + 2ll * blockIdx.x * a.cols + c;
+  bool began_before = tok[0] == tok[1];
+  float sum[VEC] = {};
+  const int len = s1 - s0;
+  for (int i0 = 0; i0 < len; i0 += kBatch) {
+    float v[kBatch][VEC];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (i0 + i < len) load_vec<T, VEC>(dy + static_cast<long long>(pos[i0 + i]) * a.dy.ld, v[i]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i >= len) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum[j] += v[i][j];
+      const int t = tok[i0 + i + 1];
+      const bool last = i0 + i == len - 1, goes_on = t == tok[i0 + i + 2];
+      if (goes_on && !last) continue;
+      if (!goes_on && !began_before)
+        put_row<VEC>(a, t, c, sum);
+      else
+        store_vec<float, VEC>(part + (began_before ? 0 : a.cols), sum);
+      began_before = false;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum[j] = 0.f;
+    }
+  }
+}
+
+// A run that begins in window w and reaches over its end: its sums in slot 1 of w
+// and slot 0 of the windows after it, added by 8 rows of threads that take every
+// eighth and then in order.
+constexpr int kJoinRows = 8;
+
+template <int VEC>
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(EmbedGradArgs a, int window) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ float red[kJoinRows][32][VEC + 1];
+  const int n = *a.count;
+  const int s0 = blockIdx.x * window, s1 = s0 + window;
+  if (s1 >= n) return;
+  const int t = a.token[s1 - 1];
+  if (a.token[s1] != t || (s0 > 0 && a.token[s0 - 1] == t)) return;
+  const int windows = (n + window - 1) / window;
+  int more = 0;  // windows after this one that the run reaches
+  for (;;) {
+    const int w = blockIdx.x + 1 + more + threadIdx.y * 32 + threadIdx.x;
+    const int got = __syncthreads_count(w < windows && a.token[min(w, windows - 1) * window] == t);
+    more += got;
+    if (got < 32 * kJoinRows) break;
+  }
+  const int c = (blockIdx.y * 32 + threadIdx.x) * VEC;
+  const bool in = c < a.cols;
+  float sum[VEC] = {};
+  if (in) {
+    for (int i = threadIdx.y; i <= more; i += kJoinRows) {
+      float v[VEC];
+      load_vec<float, VEC>(a.partials + (2ll * (static_cast<int>(blockIdx.x) + i) + (i == 0)) * a.cols + c, v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum[j] += v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) red[threadIdx.y][threadIdx.x][j] = sum[j];
+  __syncthreads();
+  if (threadIdx.y != 0 || !in) return;
+  for (int r = 1; r < kJoinRows; ++r)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sum[j] += red[r][threadIdx.x][j];
+  put_row<VEC>(a, t, c, sum);
+}
+
+// --------------------------------------------------------------------------
+// Host side
+// --------------------------------------------------------------------------
+bool pieces_of(const Mat& m, int dtype, int cols) {  // whole aligned pieces of 8 columns
+  const int es = dtype == kF32 ? 4 : 2;
+  return cols % 8 == 0 && (reinterpret_cast<uintptr_t>(m.p) & 15u) == 0 && m.ld * es % 16 == 0;
+}
+int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+// Calls f with a null pointer of the element type.
+template <class F>
+cudaError_t with_type(int dtype, F&& f) {
+  if (dtype == kF32) return f(static_cast<float*>(nullptr));
+  if (dtype == kBF16) return f(static_cast<__nv_bfloat16*>(nullptr));
+  return f(static_cast<__half*>(nullptr));
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s) {
+  const bool vec = pieces_of(a.table, a.table_dtype, a.cols) && pieces_of(a.y, a.dtype, a.cols);
+  const int pieces = vec ? a.cols / 8 : a.cols;
+  int lanes = 32;
+  while (lanes < 256 && lanes < pieces) lanes *= 2;
+  const dim3 block(lanes, 256 / lanes);
+  const dim3 grid(ceil_div(pieces, lanes), std::min(65535, ceil_div(a.tokens, kWalk * block.y)));
+  return with_type(a.table_dtype, [&](auto* w) {
+    return with_type(a.dtype, [&](auto* t) {
+      using W = std::remove_pointer_t<decltype(w)>;
+      using T = std::remove_pointer_t<decltype(t)>;
+      return launch_kernel(pdl_enabled(), vec ? embedding_kernel<W, T, 8> : embedding_kernel<W, T, 1>, grid, block, 0, s,
+                           a);
+    });
+  });
+}
+
+// Windows enough for every SM, sums of several rows each: 32 positions at 16384.
+int embed_window(int tokens) {
+  int w = 8;
+  while (w < kMaxWindow && w < (tokens + 511) / 512) w *= 2;
+  return w;
+}
+
+cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s) {
+  int log_groups = 8;
+  static_assert(kMinGroups == 1 << 8, "256 blocks");
+  while (ceil_div(a.vocab, 1ll << log_groups) > kMaxLocals) ++log_groups;
+  const int locals = ceil_div(a.vocab, 1ll << log_groups);
+  cudaError_t e = launch_kernel(pdl_enabled(), group_kernel, dim3(1u << log_groups), dim3(kGroupThreads),
+                                (kGroupWarps + 1) * locals * sizeof(int), s, a, log_groups, locals);
+  if (e != cudaSuccess) return e;
+  const bool vec = pieces_of(a.dy, a.dtype, a.cols) && pieces_of(a.dtable, a.table_dtype, a.cols);
+  const int window = embed_window(a.tokens), windows = ceil_div(a.tokens, window);
+  const int pieces = vec ? a.cols / 8 : a.cols;
+  const int threads = vec ? 128 : 256;
+  e = with_type(a.dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_kernel(pdl_enabled(), vec ? window_kernel<T, 8> : window_kernel<T, 1>,
+                         dim3(windows, ceil_div(pieces, threads)), dim3(threads), 0, s, a, window);
+  });
+  if (e != cudaSuccess || windows == 1) return e;
+  return launch_kernel(pdl_enabled(), vec ? join_kernel<8> : join_kernel<1>, dim3(windows, ceil_div(pieces, 32)),
+                       dim3(32, kJoinRows), 0, s, a, window);
+}
+
+}  // namespace dion3

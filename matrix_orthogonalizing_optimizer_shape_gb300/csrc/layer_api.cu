@@ -1,66 +1,17 @@
 // C ABI of the layer operators (include/dion3.h): argument validation,
 // workspace carving and launch order.
-#include "../../include/dion3.h"
-#include "layer.h"
+#include "api_util.h"
 
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 
 namespace dion3 {
 namespace {
 
-dion3_status fail(dion3_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-dion3_status fail(dion3_status st, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_last_error_message(buf);
-  return st;
-}
-dion3_status ok() {
-  set_last_error_message("");
-  return DION3_OK;
-}
-dion3_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(DION3_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-constexpr int32_t kMaxRows = 1 << 30, kMaxCols = 1 << 24;
-
-bool known_dtype(int32_t d) { return d == DION3_F32 || d == DION3_BF16 || d == DION3_F16; }
-int bytes_of(int32_t d) { return d == DION3_F32 ? 4 : 2; }
 // Pitch of a 16-bit matrix in the workspace: rows start on 128-byte lines, which
 // TMA reads fastest.
 long long line_pitch(long long n) { return (n + 63) / 64 * 64; }
 size_t matrix_bytes(long long rows, long long cols) { return static_cast<size_t>(rows) * line_pitch(cols) * 2; }
 
-dion3_status check_dims(int32_t rows, int32_t cols, int32_t max_cols) {
-  if (rows < 0 || cols < 1) return fail(DION3_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1 (got %d x %d)", rows, cols);
-  if (rows > kMaxRows || cols > max_cols)
-    return fail(DION3_ERR_UNSUPPORTED, "%d x %d is larger than this operator takes (%d x %d)", rows, cols, kMaxRows,
-                max_cols);
-  return DION3_OK;
-}
-
-// A matrix of `rows` rows that must be there (its data may be NULL if it has
-// no rows).
-dion3_status check_mat(const char* name, const dion3_matrix& m, int32_t rows, int32_t cols, int32_t dtype) {
-  if (rows == 0) return DION3_OK;
-  if (m.data == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
-  if (m.dtype != dtype) return fail(DION3_ERR_INVALID_ARG, "%s has dtype %d, %d is wanted", name, m.dtype, dtype);
-  if (m.ld < cols) return fail(DION3_ERR_INVALID_ARG, "%s: pitch %lld is smaller than its row of %d", name,
-                               static_cast<long long>(m.ld), cols);
-  if (m.ld > (1ll << 38)) return fail(DION3_ERR_INVALID_ARG, "%s: pitch too large", name);
-  if (reinterpret_cast<uintptr_t>(m.data) % bytes_of(dtype))
-    return fail(DION3_ERR_INVALID_ARG, "%s is not aligned to its element", name);
-  return DION3_OK;
-}
-dion3_status check_opt(const char* name, const dion3_matrix* m, int32_t rows, int32_t cols, int32_t dtype) {
-  return m == nullptr || m->data == nullptr ? DION3_OK : check_mat(name, *m, rows, cols, dtype);
-}
 dion3_status check_pack(const char* name, const dion3_packed8& p, int32_t rows, int32_t cols) {
   if (rows == 0) return DION3_OK;
   if (p.codes == nullptr || p.scales == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s: codes or scales NULL", name);
@@ -74,46 +25,8 @@ dion3_status check_pack(const char* name, const dion3_packed8& p, int32_t rows, 
 }
 bool present(const dion3_packed8* p) { return p != nullptr && (p->codes != nullptr || p->scales != nullptr); }
 
-dion3_status check_vector(const char* name, const void* w, int32_t dtype) {
-  if (!known_dtype(dtype)) return fail(DION3_ERR_INVALID_ARG, "%s: unknown dtype %d", name, dtype);
-  if (w == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(w) % bytes_of(dtype))
-    return fail(DION3_ERR_INVALID_ARG, "%s is not aligned to its element", name);
-  return DION3_OK;
-}
-dion3_status check_f32(const char* name, const float* p) {
-  if (reinterpret_cast<uintptr_t>(p) % 4) return fail(DION3_ERR_INVALID_ARG, "%s is not aligned to its element", name);
-  return DION3_OK;
-}
-dion3_status check_ws(void* ws, size_t bytes, size_t need) {
-  if (need == 0) return DION3_OK;
-  if (ws == nullptr) return fail(DION3_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
-  if (reinterpret_cast<uintptr_t>(ws) & 255u)
-    return fail(DION3_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (bytes < need) return fail(DION3_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", bytes, need);
-  return DION3_OK;
-}
-dion3_status check_inject() {
-  return inject_launch_failure() ? fail(DION3_ERR_CUDA, "injected launch failure (DION3_INJECT=launch_fail)")
-                                 : DION3_OK;
-}
-
-Mat mat(const dion3_matrix& m) { return {m.data, m.ld}; }
-Mat mat(const dion3_matrix* m) { return m == nullptr ? Mat{} : mat(*m); }
 Pack8 pack(const dion3_packed8& p) { return {p.codes, p.ld_codes, p.scales, p.ld_scales}; }
 Pack8 pack(const dion3_packed8* p) { return p == nullptr ? Pack8{} : pack(*p); }
-
-// Hands out 256-byte aligned pieces of a workspace (base NULL: sizes only).
-struct Carve {
-  char* base;
-  size_t off = 0;
-  void* take(size_t bytes) {
-    off = (off + 255) / 256 * 256;
-    void* p = base != nullptr ? base + off : nullptr;
-    off += bytes;
-    return p;
-  }
-};
 
 // An operand of a product as TMA takes it (16-byte base and pitch), and as it
 // reads it fastest.
@@ -165,17 +78,6 @@ dion3_status check_linear_dims(int32_t tokens, int32_t in, int32_t out, int32_t 
 }  // namespace dion3
 
 using namespace dion3;
-
-#define DION3_TRY(call)                    \
-  do {                                     \
-    const dion3_status rc_ = (call);       \
-    if (rc_ != DION3_OK) return rc_;       \
-  } while (0)
-#define DION3_CUDA(call, what)                       \
-  do {                                               \
-    const cudaError_t e_ = (call);                   \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
 
 extern "C" {
 

@@ -1,0 +1,43 @@
+// Internal launcher interface of the model operators (embedding, recurrence,
+// log probabilities, gradient norm).  Nothing here crosses the C ABI.
+#pragma once
+
+#include "layer.h"
+
+namespace dion3 {
+
+// Token numbers: signed integers of 4 or 8 bytes.
+struct Ids {
+  const void* p = nullptr;
+  int bytes = 8;
+};
+
+// ---------------------------------------------------------------------------
+// Embedding (embedding.cu)
+// ---------------------------------------------------------------------------
+struct EmbedArgs {
+  int tokens, vocab, cols;
+  Ids ids;
+  Mat table; int table_dtype;
+  Mat y; int dtype;
+  float scale;
+};
+cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s);
+
+// Positions of a window of the grouped tokens, and the workspace's pieces.
+int embed_window(int tokens);
+struct EmbedGradArgs {
+  int tokens, vocab, cols;
+  Ids ids;
+  Mat dy; int dtype;
+  Mat dtable; int table_dtype;
+  float scale;
+  int accumulate;
+  int* order;       // [tokens] positions, grouped by token
+  int* token;       // [tokens] their tokens
+  int* count;       // [1] positions that have a token
+  float* partials;  // [2 windows][cols]
+};
+cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s);
+
+}  // namespace dion3

@@ -1,0 +1,109 @@
+// C ABI of the model operators (include/dion3.h): argument validation,
+// workspace carving and launch order.
+#include "api_util.h"
+#include "model.h"
+
+#include <algorithm>
+
+namespace dion3 {
+namespace {
+
+constexpr int32_t kMaxGrouped = 1 << 27;    // tokens whose positions are grouped
+constexpr int32_t kMaxEmbedCols = 1 << 20;
+
+dion3_status check_any(const char* name, const dion3_matrix* m, int32_t rows, int32_t cols) {
+  if (m == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!known_dtype(m->dtype)) return fail(DION3_ERR_INVALID_ARG, "%s: unknown dtype %d", name, m->dtype);
+  return check_mat(name, *m, rows, cols, m->dtype);
+}
+dion3_status check_ids(const char* name, const void* p, int32_t bytes, int32_t n) {
+  if (bytes != 4 && bytes != 8) return fail(DION3_ERR_INVALID_ARG, "%s: numbers of %d bytes, 4 or 8 are wanted", name, bytes);
+  if (n > 0 && p == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) % bytes)
+    return fail(DION3_ERR_INVALID_ARG, "%s is not aligned to its element", name);
+  return DION3_OK;
+}
+dion3_status check_finite(const char* name, float v) {
+  return v - v == 0.f ? DION3_OK : fail(DION3_ERR_INVALID_ARG, "%s must be finite", name);
+}
+
+}  // namespace
+}  // namespace dion3
+
+using namespace dion3;
+
+extern "C" {
+
+dion3_status dion3_embedding(int32_t tokens, int32_t vocab, int32_t cols, const void* ids, int32_t id_bytes,
+                             const dion3_matrix* table, float scale, const dion3_matrix* y, dion3_stream_t stream) {
+  DION3_TRY(check_dims(tokens, cols, kMaxEmbedCols));
+  DION3_TRY(check_dims(vocab, cols, kMaxEmbedCols));
+  DION3_TRY(check_ids("ids", ids, id_bytes, tokens));
+  DION3_TRY(check_any("table", table, vocab, cols));
+  DION3_TRY(check_any("y", y, tokens, cols));
+  DION3_TRY(check_finite("scale", scale));
+  if (tokens > 0 && y->data == table->data) return fail(DION3_ERR_INVALID_ARG, "y may not be table");
+  DION3_TRY(check_inject());
+  if (tokens == 0) return ok();
+  EmbedArgs a{tokens, vocab, cols, {ids, id_bytes}, mat(table), table->dtype, mat(y), y->dtype, scale};
+  const double n = static_cast<double>(tokens) * cols;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DION3_CUDA(traced_launch("embedding", 0.0, n * (bytes_of(table->dtype) + bytes_of(y->dtype)), s,
+                           [&] { return launch_embedding(a, s); }),
+             "embedding launch");
+  return ok();
+}
+
+dion3_status dion3_embedding_backward_workspace_size(int32_t tokens, int32_t vocab, int32_t cols, size_t* bytes) {
+  if (bytes == nullptr) return fail(DION3_ERR_INVALID_ARG, "bytes is NULL");
+  DION3_TRY(check_dims(tokens, cols, kMaxEmbedCols));
+  DION3_TRY(check_dims(vocab, cols, kMaxEmbedCols));
+  if (tokens > kMaxGrouped) return fail(DION3_ERR_UNSUPPORTED, "more than %d tokens", kMaxGrouped);
+  Carve c{nullptr};
+  if (tokens > 0) {
+    const size_t n = tokens, w = embed_window(tokens);
+    c.take(4 * n);
+    c.take(4 * n);
+    c.take(4);
+    c.take(2 * ((n + w - 1) / w) * cols * 4);
+  }
+  *bytes = c.off;
+  return ok();
+}
+
+dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t cols, const dion3_matrix* dy,
+                                      const void* ids, int32_t id_bytes, float scale, const dion3_matrix* dtable,
+                                      int32_t accumulate, void* ws, size_t ws_bytes, dion3_stream_t stream) {
+  size_t need = 0;
+  DION3_TRY(dion3_embedding_backward_workspace_size(tokens, vocab, cols, &need));
+  DION3_TRY(check_ids("ids", ids, id_bytes, tokens));
+  DION3_TRY(check_any("dy", dy, tokens, cols));
+  DION3_TRY(check_any("dtable", dtable, vocab, cols));
+  DION3_TRY(check_finite("scale", scale));
+  if (tokens > 0 && dtable->data != nullptr && dy->data == dtable->data)
+    return fail(DION3_ERR_INVALID_ARG, "dtable may not be dy");
+  DION3_TRY(check_ws(ws, ws_bytes, need));
+  DION3_TRY(check_inject());
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (vocab == 0) return ok();
+  if (tokens == 0) {
+    if (!accumulate)
+      DION3_CUDA(launch_zero(vocab, cols, bytes_of(dtable->dtype), mat(dtable), s), "zero launch");
+    return ok();
+  }
+  EmbedGradArgs a{tokens, vocab,         cols, {ids, id_bytes}, mat(dy), dy->dtype, mat(dtable), dtable->dtype,
+                  scale,  accumulate != 0};
+  const size_t n = tokens, w = embed_window(tokens);
+  Carve c{static_cast<char*>(ws)};
+  a.order = static_cast<int*>(c.take(4 * n));
+  a.token = static_cast<int*>(c.take(4 * n));
+  a.count = static_cast<int*>(c.take(4));
+  a.partials = static_cast<float*>(c.take(2 * ((n + w - 1) / w) * cols * 4));
+  DION3_CUDA(traced_launch("embedding_backward", 0.0,
+                           1.0 * tokens * cols * bytes_of(dy->dtype) + 1.0 * vocab * cols * bytes_of(dtable->dtype), s,
+                           [&] { return launch_embedding_grad(a, s); }),
+             "embedding_backward launch");
+  return ok();
+}
+
+}  // extern "C"

@@ -94,7 +94,7 @@ def _fn(name: str):
     f = _FNS.get(name)
     if f is None:
         _load_torch()
-        res, args = SIGS[name]
+        res, args = _d3._SIGS[name]
         args = [_vp if isinstance(a, type) and issubclass(a, ctypes._Pointer) else a for a in args]
         f = _FNS[name] = ctypes.CFUNCTYPE(res, *args)((name, _d3.load_library()))
     return f

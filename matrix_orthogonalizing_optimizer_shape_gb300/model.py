@@ -1,0 +1,71 @@
+"""Model operators: what stands around a stack of layers in a language model
+(binding of the model part of ``include/dion3.h``).
+
+Matrices are 2-D CUDA tensors whose rows are contiguous (any row pitch), token
+numbers contiguous int32 or int64 vectors, all on the current device; outputs
+are given by the caller.  Every function enqueues on ``stream`` (default: the
+current one) and returns without waiting::
+
+    d3.embedding(ids, table, x)
+    d3.embedding_backward(dx, ids, dtable, ws=ws)
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import matrix_orthogonalizing_optimizer_shape_gb300 as _d3
+
+from . import layer as _l
+from .layer import _MAT, _i32, _mat, _pm, _psz, _stream, _sz, _vp, _ws
+
+_int, _f32 = ctypes.c_int, ctypes.c_float
+SIGS = {
+    "dion3_embedding": (_int, [_i32, _i32, _i32, _vp, _i32, _pm, _f32, _pm, _vp]),
+    "dion3_embedding_backward_workspace_size": (_int, [_i32, _i32, _i32, _psz]),
+    "dion3_embedding_backward": (_int, [_i32, _i32, _i32, _pm, _vp, _i32, _f32, _pm, _i32, _vp, _sz, _vp]),
+}
+
+
+def _ids(name: str, t, n: Optional[int], dev: int) -> tuple:
+    """(data, bytes of a number) of a contiguous vector of token numbers on device `dev`."""
+    if t.get_device() != dev or not t.is_cuda:
+        _l._on(name, t, dev)
+    if len(t.shape) != 1 or (n is not None and t.shape[0] != n) or (t.shape[0] > 1 and t.stride() != (1,)):
+        raise ValueError(f"{name} must be a contiguous CUDA vector" + ("" if n is None else f" of {n}"))
+    torch = _l._load_torch()
+    if t.dtype is torch.int64:
+        return t.data_ptr(), 8
+    if t.dtype is torch.int32:
+        return t.data_ptr(), 4
+    raise ValueError(f"{name} must be int32 or int64, not {t.dtype}")
+
+
+def embedding(ids, table, y, *, scale: float = 1.0, stream=None):
+    """y[t] = scale * table[ids[t]]; zeros where ids[t] lies outside the table
+    (see dion3_embedding)."""
+    my = _MAT.pack(*_mat("y", y))
+    (tokens, cols), dev = y.shape, y.get_device()
+    mt = _MAT.pack(*_mat("table", table, None, cols, dev))
+    p, b = _ids("ids", ids, tokens, dev)
+    _d3._check(_l._fn("dion3_embedding")(tokens, table.shape[0], cols, p, b, mt, scale, my, _stream(stream, dev)))
+
+
+def embedding_backward_workspace_size(tokens: int, vocab: int, cols: int) -> int:
+    out = _sz(0)
+    _d3._check(_d3.load_library().dion3_embedding_backward_workspace_size(tokens, vocab, cols, ctypes.byref(out)))
+    return out.value
+
+
+def embedding_backward(dy, ids, dtable, *, scale: float = 1.0, accumulate: bool = False, ws=None,
+                       ws_bytes: Optional[int] = None, stream=None):
+    """Gradient of :func:`embedding` for its table: dtable[v] = scale * the sum of
+    dy[t] over the positions of token v, 0 where it does not occur; ``accumulate``
+    adds to dtable instead (see dion3_embedding_backward)."""
+    md = _MAT.pack(*_mat("dy", dy))
+    (tokens, cols), dev = dy.shape, dy.get_device()
+    mt = _MAT.pack(*_mat("dtable", dtable, None, cols, dev))
+    p, b = _ids("ids", ids, tokens, dev)
+    w, n = _ws(ws, ws_bytes, dev)
+    _d3._check(_l._fn("dion3_embedding_backward")(tokens, dtable.shape[0], cols, md, p, b, scale, mt, int(accumulate),
+                                                  w, n, _stream(stream, dev)))

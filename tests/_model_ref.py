@@ -1,0 +1,59 @@
+"""Plain float64 forms of the model operators, tensors with marked surroundings,
+and the error bounds the tests hold the kernels to.  Nothing here comes from the
+package."""
+from __future__ import annotations
+
+import numpy as np
+import torch
+
+from _harness import torch_dtype
+from _layer_ref import TINY, U, check, sum_bound  # noqa: F401
+
+TYPES = ("f32", "bf16", "f16")
+
+
+def host(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def dev(a, dtype, pad=0, shift=0):
+    """A matrix on the GPU with `pad` spare columns of NaN in its pitch, `shift`
+    elements into its buffer, NaN before and behind."""
+    rows, cols = a.shape
+    buf = torch.full((rows * (cols + pad) + shift + 8,), float("nan"), dtype=torch_dtype(dtype), device="cuda")
+    v = buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    v.copy_(torch.from_numpy(np.asarray(a, dtype=np.float64)))
+    return v
+
+
+def out(rows, cols, dtype, pad=0, shift=0, fill=7.0):
+    """An output filled with a marker, and its whole buffer."""
+    buf = torch.full((rows * (cols + pad) + shift + 8,), fill, dtype=torch_dtype(dtype), device="cuda")
+    return buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols], buf
+
+
+def untouched(v, buf, fill=7.0):
+    """Nothing outside v's rows was written."""
+    keep = torch.ones_like(buf, dtype=torch.bool)
+    keep.as_strided(v.shape, v.stride(), v.storage_offset()).fill_(False)
+    return bool((buf[keep] == fill).all())
+
+
+def numbers(a, bits=64):
+    return torch.from_numpy(np.asarray(a, dtype=np.int64)).to("cuda").to(torch.int64 if bits == 64 else torch.int32)
+
+
+def embedding_ref(ids, table, scale):
+    ok = (ids >= 0) & (ids < table.shape[0])
+    return np.where(ok[:, None], table[np.where(ok, ids, 0)], 0.0) * scale if len(table) else np.zeros(
+        (len(ids), table.shape[1]))
+
+
+def embedding_grad_ref(dy, ids, vocab, scale):
+    """dtable, the sums of magnitudes and the numbers of terms behind it."""
+    ok = (ids >= 0) & (ids < vocab)
+    d, mag, n = np.zeros((vocab, dy.shape[1])), np.zeros((vocab, dy.shape[1])), np.zeros(vocab)
+    np.add.at(d, ids[ok], dy[ok] * scale)
+    np.add.at(mag, ids[ok], np.abs(dy[ok] * scale))
+    np.add.at(n, ids[ok], 1)
+    return d, mag, n
