@@ -647,6 +647,47 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
                                       void* ws, size_t ws_bytes, dion3_stream_t stream);
 
 /*
+ * Gated linear recurrence along the tokens, each channel on its own:
+ *   a = sigmoid(z_t),   h_t = a h_{t-1} + (1 - a) x_t,
+ * with the state in fp32 and h_t rounded once.  Sequences are packed one behind the
+ * other: rows offsets[i] .. offsets[i + 1] - 1 are sequence i.
+ *   z, x, h    [tokens][channels], one dtype.  h may be z or x (in place).
+ *   offsets    device int32 [sequences + 1], ascending, from 0 to tokens at most, or
+ *              NULL: all rows are one sequence (sequences = 1).  Rows that belong to
+ *              none are not touched, nor are the others' results theirs.
+ *   first      fp32 [sequences][channels], dense: the states before each sequence,
+ *              or NULL (0).
+ *   last       fp32 [sequences][channels], dense: receives the states after each
+ *              sequence (those before it where it has no rows), or NULL.  May be
+ *              first.
+ * z = -infinity forgets (h_t = x_t), z = +infinity keeps (h_t = h_{t-1}).
+ * channels <= 2^20, sequences <= 2^27.  Offsets that do not ascend give undefined
+ * values in the rows, but no access outside the matrices.
+ */
+dion3_status dion3_recurrence(int32_t tokens, int32_t channels, const dion3_matrix* z,
+                              const dion3_matrix* x, const int32_t* offsets, int32_t sequences,
+                              const float* first, const dion3_matrix* h, float* last,
+                              dion3_stream_t stream);
+
+/*
+ * Gradient of dion3_recurrence from its inputs and its saved h: with g_t the
+ * gradient that reaches h_t, g_t = dh_t + a_{t+1} g_{t+1} (a sequence's last row:
+ * + dlast instead),
+ *   dx_t = (1 - a_t) g_t,   dz_t = g_t (h_{t-1} - x_t) a_t (1 - a_t),
+ *   dfirst = a g of the sequence's first row (dlast where it has no rows).
+ *   dh, z, x, h, dz, dx  [tokens][channels], one dtype.  dz and dx may each be z, x
+ *              or dh (in place), but not h nor one another.
+ *   first, dlast, dfirst  fp32 [sequences][channels], dense, or NULL (first: 0,
+ *              dlast: 0).  dfirst may be dlast.
+ */
+dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const dion3_matrix* dh,
+                                       const dion3_matrix* z, const dion3_matrix* x,
+                                       const dion3_matrix* h, const int32_t* offsets,
+                                       int32_t sequences, const float* first, const float* dlast,
+                                       const dion3_matrix* dz, const dion3_matrix* dx,
+                                       float* dfirst, dion3_stream_t stream);
+
+/*
  * The bounded device-side wait of the tensor-core kernels, run on its own (a
  * diagnostic of the timeout path; the paper has no counterpart).  One thread
  * initialises an mbarrier in shared memory and waits for its first phase with

@@ -40,4 +40,21 @@ struct EmbedGradArgs {
 };
 cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Recurrence (recurrence.cu): the forward pass, or the gradient.
+// ---------------------------------------------------------------------------
+struct RecurrenceArgs {
+  int tokens, channels, dtype;
+  Mat z, x, h;
+  const int* offsets;  // [sequences + 1], or null: one sequence
+  int sequences;       // >= 1
+  const float* first;  // [sequences][channels], may be null
+  float* last;         // forward, may be null
+  Mat dh, dz, dx;      // gradient
+  const float* dlast;  // may be null
+  float* dfirst;       // may be null
+  bool grad;
+};
+cudaError_t launch_recurrence(const RecurrenceArgs& a, cudaStream_t s);
+
 }  // namespace dion3

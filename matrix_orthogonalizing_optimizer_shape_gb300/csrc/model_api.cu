@@ -10,6 +10,8 @@ namespace {
 
 constexpr int32_t kMaxGrouped = 1 << 27;    // tokens whose positions are grouped
 constexpr int32_t kMaxEmbedCols = 1 << 20;
+constexpr int32_t kMaxChannels = 1 << 20;
+constexpr int32_t kMaxSequences = 1 << 27;
 
 dion3_status check_any(const char* name, const dion3_matrix* m, int32_t rows, int32_t cols) {
   if (m == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
@@ -26,6 +28,21 @@ dion3_status check_ids(const char* name, const void* p, int32_t bytes, int32_t n
 dion3_status check_finite(const char* name, float v) {
   return v - v == 0.f ? DION3_OK : fail(DION3_ERR_INVALID_ARG, "%s must be finite", name);
 }
+
+dion3_status check_mat_ptr(const char* name, const dion3_matrix* m, int32_t rows, int32_t cols, int32_t dtype) {
+  if (m == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
+  return check_mat(name, *m, rows, cols, dtype);
+}
+dion3_status check_sequences(const int32_t* offsets, int32_t sequences) {
+  if (sequences < 0) return fail(DION3_ERR_INVALID_ARG, "sequences must be >= 0 (got %d)", sequences);
+  if (sequences > kMaxSequences) return fail(DION3_ERR_UNSUPPORTED, "more than %d sequences", kMaxSequences);
+  if (offsets == nullptr && sequences != 1)
+    return fail(DION3_ERR_INVALID_ARG, "offsets is NULL with %d sequences", sequences);
+  if (reinterpret_cast<uintptr_t>(offsets) % 4) return fail(DION3_ERR_INVALID_ARG, "offsets is not aligned to its element");
+  return DION3_OK;
+}
+// Whether two matrices of a call start at the same address.
+bool same(const dion3_matrix* a, const dion3_matrix* b) { return a->data != nullptr && a->data == b->data; }
 
 }  // namespace
 }  // namespace dion3
@@ -103,6 +120,87 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
                            1.0 * tokens * cols * bytes_of(dy->dtype) + 1.0 * vocab * cols * bytes_of(dtable->dtype), s,
                            [&] { return launch_embedding_grad(a, s); }),
              "embedding_backward launch");
+  return ok();
+}
+
+dion3_status dion3_recurrence(int32_t tokens, int32_t channels, const dion3_matrix* z, const dion3_matrix* x,
+                              const int32_t* offsets, int32_t sequences, const float* first, const dion3_matrix* h,
+                              float* last, dion3_stream_t stream) {
+  DION3_TRY(check_dims(tokens, channels, kMaxChannels));
+  DION3_TRY(check_any("z", z, tokens, channels));
+  DION3_TRY(check_mat_ptr("x", x, tokens, channels, z->dtype));
+  DION3_TRY(check_mat_ptr("h", h, tokens, channels, z->dtype));
+  DION3_TRY(check_sequences(offsets, sequences));
+  DION3_TRY(check_f32("first", first));
+  DION3_TRY(check_f32("last", last));
+  if ((same(h, z) && h->ld != z->ld) || (same(h, x) && h->ld != x->ld))
+    return fail(DION3_ERR_INVALID_ARG, "h in the place of z or x needs its pitch");
+  DION3_TRY(check_inject());
+  if (sequences == 0 || (tokens == 0 && last == nullptr)) return ok();
+  RecurrenceArgs a{};
+  a.tokens = tokens;
+  a.channels = channels;
+  a.dtype = z->dtype;
+  a.z = mat(z);
+  a.x = mat(x);
+  a.h = mat(h);
+  a.offsets = offsets;
+  a.sequences = sequences;
+  a.first = first;
+  a.last = last;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DION3_CUDA(traced_launch("recurrence", 0.0, 3.0 * tokens * channels * bytes_of(z->dtype), s,
+                           [&] { return launch_recurrence(a, s); }),
+             "recurrence launch");
+  return ok();
+}
+
+dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const dion3_matrix* dh, const dion3_matrix* z,
+                                       const dion3_matrix* x, const dion3_matrix* h, const int32_t* offsets,
+                                       int32_t sequences, const float* first, const float* dlast,
+                                       const dion3_matrix* dz, const dion3_matrix* dx, float* dfirst,
+                                       dion3_stream_t stream) {
+  DION3_TRY(check_dims(tokens, channels, kMaxChannels));
+  DION3_TRY(check_any("dh", dh, tokens, channels));
+  const struct {
+    const char* name;
+    const dion3_matrix* m;
+  } rest[] = {{"z", z}, {"x", x}, {"h", h}, {"dz", dz}, {"dx", dx}};
+  for (const auto& r : rest) DION3_TRY(check_mat_ptr(r.name, r.m, tokens, channels, dh->dtype));
+  DION3_TRY(check_sequences(offsets, sequences));
+  DION3_TRY(check_f32("first", first));
+  DION3_TRY(check_f32("dlast", dlast));
+  DION3_TRY(check_f32("dfirst", dfirst));
+  if (same(dz, h) || same(dx, h) || same(dz, dx))
+    return fail(DION3_ERR_INVALID_ARG, "dz and dx may not be h nor one another");
+  for (const dion3_matrix* in : {z, x, dh})
+    for (const dion3_matrix* o : {dz, dx})
+      if (same(in, o) && in->ld != o->ld)
+        return fail(DION3_ERR_INVALID_ARG, "dz or dx in the place of an input needs its pitch");
+  if (first != nullptr && (first == dfirst))
+    return fail(DION3_ERR_INVALID_ARG, "dfirst may not be first");
+  DION3_TRY(check_inject());
+  if (sequences == 0 || (tokens == 0 && dfirst == nullptr)) return ok();
+  RecurrenceArgs a{};
+  a.tokens = tokens;
+  a.channels = channels;
+  a.dtype = dh->dtype;
+  a.z = mat(z);
+  a.x = mat(x);
+  a.h = mat(h);
+  a.offsets = offsets;
+  a.sequences = sequences;
+  a.first = first;
+  a.dh = mat(dh);
+  a.dz = mat(dz);
+  a.dx = mat(dx);
+  a.dlast = dlast;
+  a.dfirst = dfirst;
+  a.grad = true;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DION3_CUDA(traced_launch("recurrence_backward", 0.0, 6.0 * tokens * channels * bytes_of(dh->dtype), s,
+                           [&] { return launch_recurrence(a, s); }),
+             "recurrence_backward launch");
   return ok();
 }
 

@@ -7,6 +7,8 @@ are given by the caller.  Every function enqueues on ``stream`` (default: the
 current one) and returns without waiting::
 
     d3.embedding(ids, table, x)
+    d3.recurrence(z, x, h, offsets=offsets, first=state, last=state)
+    d3.recurrence_backward(dh, z, x, h, dz, dx, offsets=offsets)
     d3.embedding_backward(dx, ids, dtable, ws=ws)
 """
 from __future__ import annotations
@@ -24,6 +26,8 @@ SIGS = {
     "dion3_embedding": (_int, [_i32, _i32, _i32, _vp, _i32, _pm, _f32, _pm, _vp]),
     "dion3_embedding_backward_workspace_size": (_int, [_i32, _i32, _i32, _psz]),
     "dion3_embedding_backward": (_int, [_i32, _i32, _i32, _pm, _vp, _i32, _f32, _pm, _i32, _vp, _sz, _vp]),
+    "dion3_recurrence": (_int, [_i32, _i32, _pm, _pm, _vp, _i32, _vp, _pm, _vp, _vp]),
+    "dion3_recurrence_backward": (_int, [_i32, _i32, _pm, _pm, _pm, _pm, _vp, _i32, _vp, _vp, _pm, _pm, _vp, _vp]),
 }
 
 
@@ -69,3 +73,53 @@ def embedding_backward(dy, ids, dtable, *, scale: float = 1.0, accumulate: bool 
     w, n = _ws(ws, ws_bytes, dev)
     _d3._check(_l._fn("dion3_embedding_backward")(tokens, dtable.shape[0], cols, md, p, b, scale, mt, int(accumulate),
                                                   w, n, _stream(stream, dev)))
+
+
+def _offsets(t, dev: int) -> tuple:
+    """(data, sequences) of the offsets of packed sequences."""
+    if t is None:
+        return None, 1
+    p, b = _ids("offsets", t, None, dev)
+    if b != 4:
+        raise ValueError("offsets must be int32")
+    if t.shape[0] < 1:
+        raise ValueError("offsets must hold one number more than there are sequences")
+    return p, t.shape[0] - 1
+
+
+def _states(name: str, t, n: int, channels: int, dev: int) -> Optional[int]:
+    """Address of a dense float32 [sequences, channels] tensor."""
+    if t is None:
+        return None
+    p, ld, dtype = _mat(name, t, n, channels, dev)
+    if dtype != _d3.F32 or (ld != channels and n > 1):
+        raise ValueError(f"{name} must be float32 and dense")
+    return p
+
+
+def recurrence(z, x, h, *, offsets=None, first=None, last=None, stream=None):
+    """h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(z), along the rows of each
+    sequence: rows offsets[i] to offsets[i + 1], int32 (None: all rows are one).
+    ``first`` and ``last`` are the states before and after each sequence, float32
+    [sequences, channels] (see dion3_recurrence)."""
+    mz = _MAT.pack(*_mat("z", z))
+    (tokens, channels), dev = z.shape, z.get_device()
+    mx, mh = (_MAT.pack(*_mat(name, t, tokens, channels, dev)) for name, t in (("x", x), ("h", h)))
+    p, n = _offsets(offsets, dev)
+    _d3._check(_l._fn("dion3_recurrence")(tokens, channels, mz, mx, p, n, _states("first", first, n, channels, dev), mh,
+                                          _states("last", last, n, channels, dev), _stream(stream, dev)))
+
+
+def recurrence_backward(dh, z, x, h, dz, dx, *, offsets=None, first=None, dlast=None, dfirst=None, stream=None):
+    """Gradient of :func:`recurrence` from dh and the saved z, x and h: dz, dx and
+    dfirst; dlast is the gradient that reaches the states after the sequences (see
+    dion3_recurrence_backward)."""
+    md = _MAT.pack(*_mat("dh", dh))
+    (tokens, channels), dev = dh.shape, dh.get_device()
+    mz, mx, mh, mdz, mdx = (_MAT.pack(*_mat(name, t, tokens, channels, dev)) for name, t in (
+        ("z", z), ("x", x), ("h", h), ("dz", dz), ("dx", dx)))
+    p, n = _offsets(offsets, dev)
+    _d3._check(_l._fn("dion3_recurrence_backward")(
+        tokens, channels, md, mz, mx, mh, p, n, _states("first", first, n, channels, dev),
+        _states("dlast", dlast, n, channels, dev), mdz, mdx, _states("dfirst", dfirst, n, channels, dev),
+        _stream(stream, dev)))

@@ -57,3 +57,46 @@ def embedding_grad_ref(dy, ids, vocab, scale):
     np.add.at(mag, ids[ok], np.abs(dy[ok] * scale))
     np.add.at(n, ids[ok], 1)
     return d, mag, n
+
+
+def _gates(z):
+    e = np.exp(-np.abs(z))
+    big, small = 1 / (1 + e), e / (1 + e)
+    return np.where(z >= 0, big, small), np.where(z >= 0, small, big)
+
+
+def recurrence_ref(z, x, offsets, first):
+    """h, the states after each sequence, and a bound on the error of a state whose
+    step is off by one unit: e_t = a e_{t-1} + |h_{t-1}| + |x_t|."""
+    a, na = _gates(z)
+    h, err = np.full_like(x, np.nan), np.zeros_like(x)
+    n = len(offsets) - 1
+    last = np.zeros((n, x.shape[1])) if first is None else first.copy()
+    last_err = np.zeros_like(last)
+    for i in range(n):
+        s, e = last[i], np.zeros(x.shape[1])
+        for t in range(offsets[i], offsets[i + 1]):
+            e = a[t] * e + np.abs(s) + np.abs(x[t])
+            s = a[t] * s + na[t] * x[t]
+            h[t], err[t] = s, e
+        last[i], last_err[i] = s, e
+    return h, last, err, last_err
+
+
+def recurrence_grad_ref(dh, z, x, h, offsets, first, dlast):
+    """dz, dx, dfirst, and the same kind of bound on the error of g."""
+    a, na = _gates(z)
+    n = len(offsets) - 1
+    dz, dx, err = np.full_like(x, np.nan), np.full_like(x, np.nan), np.zeros_like(x)
+    dfirst = np.zeros((n, x.shape[1])) if dlast is None else dlast.copy()
+    first_err = np.zeros_like(dfirst)
+    for i in range(n):
+        s, e = dfirst[i], np.zeros(x.shape[1])
+        for t in range(offsets[i + 1] - 1, offsets[i] - 1, -1):
+            prev = h[t - 1] if t > offsets[i] else 0.0 if first is None else first[i]
+            e = e + np.abs(s) + np.abs(dh[t])
+            g = dh[t] + s
+            dz[t], dx[t], err[t] = g * (prev - x[t]) * a[t] * na[t], g * na[t], e
+            s, e = a[t] * g, a[t] * e
+        dfirst[i], first_err[i] = s, e
+    return dz, dx, dfirst, err, first_err
