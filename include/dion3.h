@@ -688,6 +688,47 @@ dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const d
                                        float* dfirst, dion3_stream_t stream);
 
 /*
+ * Log probabilities of given tokens under the softmax of each row of logits l:
+ *   p_j = exp(scale l_j) / sum_i exp(scale l_i),   logp = log p_target,
+ *   entropy = -sum_j p_j log p_j,   and the `top` largest p_j.
+ * One pass over the logits; sums and statistics in fp32, differences taken to the
+ * row's largest logit.
+ *   logits      [rows][vocab], any dtype.
+ *   scale       2^-20 <= scale <= 2^20 (an inverse temperature).
+ *   targets     [rows] token numbers (target_bytes 4 or 8), or NULL without logp; a
+ *               target outside [0, vocab) (-100 by custom) has logp 0.
+ *   logp, entropy  fp32 [rows], or NULL.
+ *   stats       fp32 [rows][3] for the backward pass, or NULL: the largest logit m,
+ *               log sum exp(scale (l - m)) and the entropy.
+ *   top         0 <= top <= 32, at most vocab: top_values fp32 [rows][top] are their
+ *               log probabilities, descending, top_ids int32 [rows][top] their
+ *               columns; equal logits in the order of their columns, NaN last.
+ *               Either may be NULL.
+ * A logit of -infinity has probability 0 and no part in the entropy.  In a row of
+ * nothing else logp is -infinity and the entropy 0.  A row that holds NaN or
+ * +infinity gives NaN (and the columns by the order above).
+ * rows <= 2^21, vocab <= 2^21.
+ */
+dion3_status dion3_log_probs(int32_t rows, int32_t vocab, const dion3_matrix* logits, float scale,
+                             const void* targets, int32_t target_bytes, float* logp,
+                             float* entropy, float* stats, int32_t top, float* top_values,
+                             int32_t* top_ids, dion3_stream_t stream);
+
+/*
+ * Gradient of dion3_log_probs for its logits from its stats:
+ *   dlogits_j = scale (dlogp ([j = target] - p_j) - dentropy p_j (log p_j + entropy)).
+ *   dlogp, dentropy  fp32 [rows], or NULL (0).  dlogp of a target outside
+ *               [0, vocab) is not used.
+ *   dlogits     the type of logits; may be logits (in place).
+ * A row with neither gradient, or whose logits are all -infinity, gets zeros.
+ */
+dion3_status dion3_log_probs_backward(int32_t rows, int32_t vocab, const dion3_matrix* logits,
+                                      float scale, const void* targets, int32_t target_bytes,
+                                      const float* stats, const float* dlogp,
+                                      const float* dentropy, const dion3_matrix* dlogits,
+                                      dion3_stream_t stream);
+
+/*
  * The bounded device-side wait of the tensor-core kernels, run on its own (a
  * diagnostic of the timeout path; the paper has no counterpart).  One thread
  * initialises an mbarrier in shared memory and waits for its first phase with

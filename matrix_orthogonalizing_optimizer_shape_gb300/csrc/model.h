@@ -57,4 +57,34 @@ struct RecurrenceArgs {
 };
 cudaError_t launch_recurrence(const RecurrenceArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Log probabilities (logprob.cu)
+// ---------------------------------------------------------------------------
+constexpr int kMaxTop = 32;  // alternatives: a list in a warp's lanes
+struct LogProbArgs {
+  int rows, vocab, dtype;
+  Mat logits;
+  float scale;
+  Ids targets;        // p null: none
+  float* logp;        // [rows], may be null
+  float* entropy;     // [rows], may be null
+  float* stats;       // [rows][3], may be null
+  int top;            // 0 .. kMaxTop
+  float* top_values;  // [rows][top], may be null
+  int* top_ids;       // [rows][top], may be null
+};
+cudaError_t launch_log_probs(const LogProbArgs& a, cudaStream_t s);
+
+struct LogProbGradArgs {
+  int rows, vocab, dtype;
+  Mat logits;
+  float scale;
+  Ids targets;
+  const float* stats;
+  const float* dlogp;     // [rows], may be null
+  const float* dentropy;  // [rows], may be null
+  Mat dlogits;            // may be logits
+};
+cudaError_t launch_log_probs_grad(const LogProbGradArgs& a, cudaStream_t s);
+
 }  // namespace dion3

@@ -12,6 +12,7 @@ constexpr int32_t kMaxGrouped = 1 << 27;    // tokens whose positions are groupe
 constexpr int32_t kMaxEmbedCols = 1 << 20;
 constexpr int32_t kMaxChannels = 1 << 20;
 constexpr int32_t kMaxSequences = 1 << 27;
+constexpr int32_t kMaxLogRows = 1 << 21, kMaxVocab = 1 << 21;
 
 dion3_status check_any(const char* name, const dion3_matrix* m, int32_t rows, int32_t cols) {
   if (m == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s is NULL", name);
@@ -40,6 +41,14 @@ dion3_status check_sequences(const int32_t* offsets, int32_t sequences) {
     return fail(DION3_ERR_INVALID_ARG, "offsets is NULL with %d sequences", sequences);
   if (reinterpret_cast<uintptr_t>(offsets) % 4) return fail(DION3_ERR_INVALID_ARG, "offsets is not aligned to its element");
   return DION3_OK;
+}
+dion3_status check_log_probs(int32_t rows, int32_t vocab, const dion3_matrix* logits, float scale, const void* targets,
+                             int32_t target_bytes) {
+  DION3_TRY(check_dims(rows, vocab, kMaxVocab));
+  if (rows > kMaxLogRows) return fail(DION3_ERR_UNSUPPORTED, "more than %d rows", kMaxLogRows);
+  DION3_TRY(check_any("logits", logits, rows, vocab));
+  if (!(scale >= 0x1p-20f && scale <= 0x1p20f)) return fail(DION3_ERR_INVALID_ARG, "scale must lie in [2^-20, 2^20]");
+  return targets != nullptr ? check_ids("targets", targets, target_bytes, rows) : DION3_OK;
 }
 // Whether two matrices of a call start at the same address.
 bool same(const dion3_matrix* a, const dion3_matrix* b) { return a->data != nullptr && a->data == b->data; }
@@ -201,6 +210,64 @@ dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const d
   DION3_CUDA(traced_launch("recurrence_backward", 0.0, 6.0 * tokens * channels * bytes_of(dh->dtype), s,
                            [&] { return launch_recurrence(a, s); }),
              "recurrence_backward launch");
+  return ok();
+}
+
+dion3_status dion3_log_probs(int32_t rows, int32_t vocab, const dion3_matrix* logits, float scale, const void* targets,
+                             int32_t target_bytes, float* logp, float* entropy, float* stats, int32_t top,
+                             float* top_values, int32_t* top_ids, dion3_stream_t stream) {
+  DION3_TRY(check_log_probs(rows, vocab, logits, scale, targets, target_bytes));
+  DION3_TRY(check_f32("logp", logp));
+  DION3_TRY(check_f32("entropy", entropy));
+  DION3_TRY(check_f32("stats", stats));
+  DION3_TRY(check_f32("top_values", top_values));
+  DION3_TRY(check_f32("top_ids", reinterpret_cast<const float*>(top_ids)));
+  if (rows > 0 && logp != nullptr && targets == nullptr) return fail(DION3_ERR_INVALID_ARG, "logp is given without targets");
+  if (top < 0 || top > kMaxTop || top > vocab)
+    return fail(DION3_ERR_INVALID_ARG, "top must lie in [0, %d] (got %d)", std::min(kMaxTop, vocab), top);
+  DION3_TRY(check_inject());
+  if (rows == 0) return ok();
+  LogProbArgs a{};
+  a.rows = rows;
+  a.vocab = vocab;
+  a.dtype = logits->dtype;
+  a.logits = mat(logits);
+  a.scale = scale;
+  a.targets = {targets, target_bytes};
+  a.logp = logp;
+  a.entropy = entropy;
+  a.stats = stats;
+  a.top = top_values != nullptr || top_ids != nullptr ? top : 0;
+  a.top_values = top_values;
+  a.top_ids = top_ids;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DION3_CUDA(traced_launch("log_probs", 0.0, 1.0 * rows * vocab * bytes_of(logits->dtype), s,
+                           [&] { return launch_log_probs(a, s); }),
+             "log_probs launch");
+  return ok();
+}
+
+dion3_status dion3_log_probs_backward(int32_t rows, int32_t vocab, const dion3_matrix* logits, float scale,
+                                      const void* targets, int32_t target_bytes, const float* stats,
+                                      const float* dlogp, const float* dentropy, const dion3_matrix* dlogits,
+                                      dion3_stream_t stream) {
+  DION3_TRY(check_log_probs(rows, vocab, logits, scale, targets, target_bytes));
+  DION3_TRY(check_mat_ptr("dlogits", dlogits, rows, vocab, logits->dtype));
+  DION3_TRY(check_f32("stats", stats));
+  DION3_TRY(check_f32("dlogp", dlogp));
+  DION3_TRY(check_f32("dentropy", dentropy));
+  if (rows > 0 && stats == nullptr) return fail(DION3_ERR_INVALID_ARG, "stats is NULL");
+  if (rows > 0 && dlogp != nullptr && targets == nullptr) return fail(DION3_ERR_INVALID_ARG, "dlogp is given without targets");
+  if (same(logits, dlogits) && logits->ld != dlogits->ld)
+    return fail(DION3_ERR_INVALID_ARG, "dlogits in the place of logits needs its pitch");
+  DION3_TRY(check_inject());
+  if (rows == 0) return ok();
+  LogProbGradArgs a{rows,  vocab, logits->dtype, mat(logits), scale, {targets, target_bytes},
+                    stats, dlogp, dentropy,      mat(dlogits)};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DION3_CUDA(traced_launch("log_probs_backward", 0.0, 2.0 * rows * vocab * bytes_of(logits->dtype), s,
+                           [&] { return launch_log_probs_grad(a, s); }),
+             "log_probs_backward launch");
   return ok();
 }
 

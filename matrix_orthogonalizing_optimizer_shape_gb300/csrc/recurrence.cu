@@ -18,6 +18,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "layer_math.cuh"
 #include "model.h"
 
@@ -31,29 +32,6 @@ constexpr int kRows = 8;                // rows of a warp in a step
 constexpr int kSpan = kWarps * kRows;   // rows of a block in a step
 constexpr int kMaxCluster = 8;
 constexpr int kSharedOffsets = 1024;
-
-// --------------------------------------------------------------------------
-// Clusters
-// --------------------------------------------------------------------------
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ int cluster_rank() {
-  int r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ int cluster_size() {
-  int r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void store_remote(void* shared, int rank, float4 v) {
-  const unsigned local = static_cast<unsigned>(__cvta_generic_to_shared(shared));
-  unsigned remote;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
 
 // --------------------------------------------------------------------------
 // Elements and maps.  VEC = 2 channels a lane where they are aligned, else 1.
@@ -256,10 +234,10 @@ __device__ __forceinline__ void enter(Maps& m, int step, int rank, int size, con
         const float4 v = m.warp[half][w][lane];
         all = make_float4(after(v.x, all.x), through(v.x, v.y, all.y), after(v.z, all.z), through(v.z, v.w, all.w));
       }
-      for (int r = 0; r < size; ++r) store_remote(&m.block[half][rank][lane], r, all);
+      for (int r = 0; r < size; ++r) cl::store(cl::peer(&m.block[half][rank][lane], r), all);
     }
-    cluster_arrive();
-    cluster_wait();
+    cl::arrive();
+    cl::wait();
     for (int r = 0; r < size; ++r) {
       if (r == rank) {
 #pragma unroll
@@ -285,9 +263,9 @@ __global__ void __launch_bounds__(kThreads) recurrence_kernel(RecurrenceArgs a) 
   pdl_wait();
   __shared__ Maps maps;
   __shared__ int shared_off[kSharedOffsets];
-  const int size = cluster_size(), rank = cluster_rank(), groups = gridDim.x / size;
+  const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
   const Span p = span_of(a, blockIdx.x / size, groups, shared_off);
-  if (size > 1) cluster_arrive(), cluster_wait();  // every block has begun before one writes to another
+  if (size > 1) cl::arrive(), cl::wait();  // every block has begun before one writes to another
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = (blockIdx.y * 32 + lane) * VEC;
   const bool in = c < a.channels;
@@ -391,9 +369,9 @@ __global__ void __launch_bounds__(kThreads) recurrence_grad_kernel(RecurrenceArg
   pdl_wait();
   __shared__ Maps maps;
   __shared__ int shared_off[kSharedOffsets];
-  const int size = cluster_size(), rank = cluster_rank(), groups = gridDim.x / size;
+  const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
   const Span p = span_of(a, blockIdx.x / size, groups, shared_off);
-  if (size > 1) cluster_arrive(), cluster_wait();
+  if (size > 1) cl::arrive(), cl::wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = (blockIdx.y * 32 + lane) * VEC;
   const bool in = c < a.channels;

@@ -9,6 +9,8 @@ current one) and returns without waiting::
     d3.embedding(ids, table, x)
     d3.recurrence(z, x, h, offsets=offsets, first=state, last=state)
     d3.recurrence_backward(dh, z, x, h, dz, dx, offsets=offsets)
+    d3.log_probs(logits, targets, logp, stats=stats, top_values=values, top_ids=ids)
+    d3.log_probs_backward(logits, targets, stats, dlogits, dlogp=dlogp)
     d3.embedding_backward(dx, ids, dtable, ws=ws)
 """
 from __future__ import annotations
@@ -19,7 +21,7 @@ from typing import Optional
 import matrix_orthogonalizing_optimizer_shape_gb300 as _d3
 
 from . import layer as _l
-from .layer import _MAT, _i32, _mat, _pm, _psz, _stream, _sz, _vp, _ws
+from .layer import _MAT, _i32, _mat, _pm, _psz, _stream, _sz, _vec, _vp, _ws
 
 _int, _f32 = ctypes.c_int, ctypes.c_float
 SIGS = {
@@ -28,6 +30,8 @@ SIGS = {
     "dion3_embedding_backward": (_int, [_i32, _i32, _i32, _pm, _vp, _i32, _f32, _pm, _i32, _vp, _sz, _vp]),
     "dion3_recurrence": (_int, [_i32, _i32, _pm, _pm, _vp, _i32, _vp, _pm, _vp, _vp]),
     "dion3_recurrence_backward": (_int, [_i32, _i32, _pm, _pm, _pm, _pm, _vp, _i32, _vp, _vp, _pm, _pm, _vp, _vp]),
+    "dion3_log_probs": (_int, [_i32, _i32, _pm, _f32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "dion3_log_probs_backward": (_int, [_i32, _i32, _pm, _f32, _vp, _i32, _vp, _vp, _vp, _pm, _vp]),
 }
 
 
@@ -123,3 +127,50 @@ def recurrence_backward(dh, z, x, h, dz, dx, *, offsets=None, first=None, dlast=
         tokens, channels, md, mz, mx, mh, p, n, _states("first", first, n, channels, dev),
         _states("dlast", dlast, n, channels, dev), mdz, mdx, _states("dfirst", dfirst, n, channels, dev),
         _stream(stream, dev)))
+
+
+def _row_values(name: str, t, rows: int, dev: int) -> Optional[int]:
+    return None if t is None else _vec(name, t, rows, dev, f32=True)
+
+
+def _table(name: str, t, rows: int, cols: int, dtype, dev: int) -> Optional[int]:
+    """Address of a dense [rows, cols] tensor of a type."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != dev:
+        _l._on(name, t, dev)
+    if t.dtype is not dtype or tuple(t.shape) != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {rows} x {cols}")
+    return t.data_ptr()
+
+
+def log_probs(logits, targets=None, logp=None, *, scale: float = 1.0, entropy=None, stats=None, top_values=None,
+              top_ids=None, stream=None):
+    """Log probabilities of the targets under softmax(scale * logits) of each row,
+    the entropy, and log probabilities and columns of the most probable tokens
+    (float32 and int32 [rows, n], n at most 32).  ``stats``, float32 [rows, 3], is
+    what :func:`log_probs_backward` needs.  Every result may be left out (see
+    dion3_log_probs)."""
+    ml = _MAT.pack(*_mat("logits", logits))
+    (rows, vocab), dev = logits.shape, logits.get_device()
+    p, b = (None, 8) if targets is None else _ids("targets", targets, rows, dev)
+    top = top_values.shape[-1] if top_values is not None else top_ids.shape[-1] if top_ids is not None else 0
+    torch = _l._load_torch()
+    _d3._check(_l._fn("dion3_log_probs")(
+        rows, vocab, ml, scale, p, b, _row_values("logp", logp, rows, dev), _row_values("entropy", entropy, rows, dev),
+        _table("stats", stats, rows, 3, torch.float32, dev), top,
+        _table("top_values", top_values, rows, top, torch.float32, dev),
+        _table("top_ids", top_ids, rows, top, torch.int32, dev), _stream(stream, dev)))
+
+
+def log_probs_backward(logits, targets, stats, dlogits, *, dlogp=None, dentropy=None, scale: float = 1.0, stream=None):
+    """Gradient of :func:`log_probs` for its logits, from its stats and the gradients
+    of the log probabilities and of the entropies; dlogits may be logits (see
+    dion3_log_probs_backward)."""
+    ml = _MAT.pack(*_mat("logits", logits))
+    (rows, vocab), dev = logits.shape, logits.get_device()
+    p, b = (None, 8) if targets is None else _ids("targets", targets, rows, dev)
+    _d3._check(_l._fn("dion3_log_probs_backward")(
+        rows, vocab, ml, scale, p, b, _table("stats", stats, rows, 3, _l._load_torch().float32, dev),
+        _row_values("dlogp", dlogp, rows, dev), _row_values("dentropy", dentropy, rows, dev),
+        _MAT.pack(*_mat("dlogits", dlogits, rows, vocab, dev)), _stream(stream, dev)))

@@ -100,3 +100,38 @@ def recurrence_grad_ref(dh, z, x, h, offsets, first, dlast):
             s, e = a[t] * g, a[t] * e
         dfirst[i], first_err[i] = s, e
     return dz, dx, dfirst, err, first_err
+
+
+def log_probs_ref(logits, targets, scale):
+    """logp, entropy, all log probabilities; a row of -inf has log probabilities of -inf and entropy 0."""
+    v = logits * scale
+    m = v.max(1, keepdims=True)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        d = np.where(np.isneginf(m), -np.inf, v - m)
+        e = np.exp(d)
+        lp = np.where(np.isneginf(m), -np.inf, d - np.log(e.sum(1, keepdims=True)))
+        p = np.exp(lp)
+        entropy = -np.where(p > 0, p * lp, 0.0).sum(1)
+    ok = (targets >= 0) & (targets < logits.shape[1])
+    logp = np.where(ok, lp[np.arange(len(lp)), np.where(ok, targets, 0)], 0.0)
+    return logp, entropy + 0.0, lp
+
+
+def log_probs_grad_ref(logits, targets, scale, dlogp, dentropy):
+    _, entropy, lp = log_probs_ref(logits, targets, scale)
+    p = np.exp(lp)
+    ok = (targets >= 0) & (targets < logits.shape[1]) & ~np.isneginf(logits).all(1)
+    g = np.where(ok, dlogp, 0.0)
+    d = -g[:, None] * p
+    d[np.arange(len(d))[ok], targets[ok]] += g[ok]
+    if dentropy is not None:
+        with np.errstate(invalid="ignore"):
+            d -= dentropy[:, None] * np.where(p > 0, p * (lp + entropy[:, None]), 0.0)
+    return d * scale
+
+
+def top_ref(logits, k):
+    """Columns of the k largest, equal ones in their order, NaN last."""
+    v = np.where(np.isnan(logits), -np.inf, logits)
+    order = np.lexsort((np.broadcast_to(np.arange(v.shape[1]), v.shape), np.isnan(logits), -v))
+    return order[:, :k]
