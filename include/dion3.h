@@ -729,6 +729,42 @@ dion3_status dion3_log_probs_backward(int32_t rows, int32_t vocab, const dion3_m
                                       dion3_stream_t stream);
 
 /*
+ * A gradient of any shape: `rows` rows of `cols` contiguous elements, `ld` apart
+ * (a dense tensor: one row of all its elements, or its own rows).
+ */
+typedef struct {
+  void* data;
+  int64_t rows, cols, ld;
+  int32_t dtype; /* dion3_dtype */
+} dion3_tensor;
+
+/*
+ * The norm over all elements of n tensors of any types and shapes (dion3_group.grads
+ * and the vectors beside them), norm = sqrt(sum g^2), into the device word norm;
+ * and clipping to it,
+ *   out = min(1, max_norm / (norm + 1e-6)) g,   each element rounded once.
+ * Squares are summed without overflow or underflow for every finite g (a norm past
+ * fp32's range reads infinity, and clips to 0); NaN and infinity reach norm (and,
+ * through the factor, every gradient).
+ *   tensors   HOST array [n], read during the call only.
+ *   out       HOST array [n] of tensors of the same rows and cols and any type and
+ *             pitch (gradients summed in fp32, clipped into the 16-bit ones that
+ *             dion3_step reads), or NULL: in place, where a factor of 1 writes
+ *             nothing.  out[i] may be tensors[i]; otherwise no two tensors of a
+ *             call that are written, or written and read, may share elements
+ *             (columns of one matrix interleave without doing so).
+ *   max_norm  >= 0; infinity clips nothing.
+ *   norm      device fp32, may be NULL when clipping.
+ * No host synchronisation: the factor stays on the device.
+ */
+dion3_status dion3_grad_norm_workspace_size(size_t* bytes);
+dion3_status dion3_grad_norm(const dion3_tensor* tensors, int32_t n, float* norm, void* ws,
+                             size_t ws_bytes, dion3_stream_t stream);
+dion3_status dion3_clip_grad_norm(const dion3_tensor* tensors, const dion3_tensor* out, int32_t n,
+                                  float max_norm, float* norm, void* ws, size_t ws_bytes,
+                                  dion3_stream_t stream);
+
+/*
  * The bounded device-side wait of the tensor-core kernels, run on its own (a
  * diagnostic of the timeout path; the paper has no counterpart).  One thread
  * initialises an mbarrier in shared memory and waits for its first phase with

@@ -45,6 +45,7 @@ EXPORTED = (
     "dion3_linear_backward_workspace_size", "dion3_linear_backward",
     "dion3_embedding", "dion3_embedding_backward_workspace_size", "dion3_embedding_backward",
     "dion3_recurrence", "dion3_recurrence_backward", "dion3_log_probs", "dion3_log_probs_backward",
+    "dion3_grad_norm_workspace_size", "dion3_grad_norm", "dion3_clip_grad_norm",
 )
 
 
@@ -478,8 +479,8 @@ from .layer import (  # noqa: E402,F401
     rms_norm_backward_workspace_size, unpack8)
 from . import model as _model  # noqa: E402
 from .model import (  # noqa: E402,F401
-    embedding, embedding_backward, embedding_backward_workspace_size, log_probs, log_probs_backward, recurrence,
-    recurrence_backward)
+    clip_grad_norm, embedding, embedding_backward, embedding_backward_workspace_size, grad_norm,
+    grad_norm_workspace_size, log_probs, log_probs_backward, recurrence, recurrence_backward)
 
 _SIGS.update(_layer.SIGS)
 _SIGS.update(_model.SIGS)

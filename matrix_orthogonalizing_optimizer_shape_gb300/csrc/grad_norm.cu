@@ -1,0 +1,334 @@
+// The norm over all gradients and their clipping, on sm_103a.  Bound by HBM: the
+// norm reads every gradient once, clipping reads and writes each once more (what
+// the norm read last still comes from L2, since clipping walks backwards).
+//
+// Tensors are divided into chunks of kChunk bytes, which the blocks of one launch
+// take in turn: a table of the tensors travels in the kernel's parameters.  Each
+// block leaves one partial sum, and every block that needs the norm adds them in
+// the same order.
+//
+// Squares are summed in fp32 over a thread's few pieces and those sums in fp64.  A
+// sum outside [2^-70, 2^110], where squares may have left fp32's range, is formed
+// again from scaled values, so the norm is right for every finite gradient.
+#include <algorithm>
+#include <type_traits>
+
+#include "layer_math.cuh"
+#include "model.h"
+
+namespace dion3 {
+namespace {
+
+using namespace lm;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kChunk = 32768;  // bytes of a chunk that is read
+constexpr int kSquareBlocks = 3, kScaleBlocks = 2;  // of an SM
+constexpr int kBatch = 4;      // pieces of 16 bytes a thread has in flight: a chunk in one go
+
+template <typename T>
+constexpr int kPer = 16 / sizeof(T);
+
+template <int N>
+struct Table {
+  GradTensor t[N];
+};
+
+template <typename T>
+__device__ __forceinline__ void piece_values(const uint4& u, float (&v)[kPer<T>]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      const float2 f = unpack2<std::is_same<T, __nv_bfloat16>::value>(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// A chunk: n elements from `in`, to `out`.
+struct Chunk {
+  const GradTensor* t;
+  long long row, at;  // its row and its first element's column
+  int n;
+};
+// Which one number c is: the last tensor whose first chunk is not behind it.
+template <int N>
+__device__ __forceinline__ Chunk chunk_of(const Table<N>& tab, int count, unsigned c) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.t[mid].first <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const GradTensor& t = tab.t[lo];
+  const unsigned k = c - t.first, row = k / t.per_row;
+  const int len = kChunk / (t.dtype == kF32 ? 4 : 2);
+  const long long at = static_cast<long long>(k - row * t.per_row) * len;
+  return {&t, static_cast<long long>(row), at, static_cast<int>(min(static_cast<long long>(len), t.cols - at))};
+}
+
+// Sum of squares of n values, as a double; s: their plain fp32 sum.
+template <int N>
+__device__ __forceinline__ double squares(const float (&v)[N]) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) s = fmaf(v[j], v[j], s);
+  if (s >= 0x1p-70f && s <= 0x1p110f) return static_cast<double>(s);
+  const float up = s < 1.f ? 0x1p90f : 0x1p-70f;  // too small, or too large (or NaN)
+  float r = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float x = v[j] * up;
+    r = fmaf(x, x, r);
+  }
+  return static_cast<double>(r) * (s < 1.f ? 0x1p-180 : 0x1p140);
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const Chunk& c) {
+  const T* p = static_cast<const T*>(c.t->in) + c.row * c.t->ld_in + c.at;
+  const int head = min(c.n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) % 16 / sizeof(T)));
+  const int pieces = (c.n - head) / kPer<T>, tail = c.n - head - pieces * kPer<T>;
+  const uint4* body = reinterpret_cast<const uint4*>(p + head);
+  float v[kBatch * kPer<T>];
+  static_assert(kBatch * 16 * kThreads == kChunk, "a chunk in one go");
+  uint4 u[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int i = threadIdx.x + b * kThreads;
+    u[b] = i < pieces ? body[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    float f[kPer<T>];
+    piece_values<T>(u[b], f);
+#pragma unroll
+    for (int j = 0; j < kPer<T>; ++j) v[b * kPer<T> + j] = f[j];
+  }
+  double sum = squares(v);
+  if (threadIdx.x < head + tail) {
+    const int at = threadIdx.x < head ? threadIdx.x : head + pieces * kPer<T> + threadIdx.x - head;
+    const float e[1] = {to_f32<T>(p[at])};
+    sum += squares(e);
+  }
+  return sum;
+}
+
+// The sum over a block's threads, in thread 0.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kWarps ? red[threadIdx.x] : 0.0;
+#pragma unroll
+    for (int d = kWarps / 2; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  }
+  return v;
+}
+
+// partials[block] = (of an earlier launch: +=) the block's sum; `kept`: partials that earlier launches left.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kSquareBlocks) grad_squares_kernel(const __grid_constant__ Table<N> tab, int count,
+                                                                  unsigned chunks, double* partials, int kept) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[kWarps];
+  double sum = 0.0;
+  for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const Chunk k = chunk_of(tab, count, c);
+    if (k.t->dtype == kF32)
+      sum += chunk_squares<float>(k);
+    else if (k.t->dtype == kBF16)
+      sum += chunk_squares<__nv_bfloat16>(k);
+    else
+      sum += chunk_squares<__half>(k);
+  }
+  sum = block_sum(sum, red);
+  if (threadIdx.x == 0) partials[blockIdx.x] = sum + (static_cast<int>(blockIdx.x) < kept ? partials[blockIdx.x] : 0.0);
+}
+
+// The norm from the partials, the same bits in every block (in thread 0).
+__device__ __forceinline__ float norm_of(const double* partials, int n, double* red) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) v += partials[i];
+  v = block_sum(v, red);
+  return static_cast<float>(sqrt(v));
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* partials, int n, float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[kWarps];
+  const float v = norm_of(partials, n, red);
+  if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename T, typename O>
+__device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
+  const T* p = static_cast<const T*>(c.t->in) + c.row * c.t->ld_in + c.at;
+  O* q = static_cast<O*>(c.t->out) + c.row * c.t->ld_out + c.at;
+  const int head = min(c.n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) % 16 / sizeof(T)));
+  constexpr int kBytes = kPer<T> * static_cast<int>(sizeof(O));  // what a piece becomes: 8, 16 or 32
+  const bool together = (reinterpret_cast<uintptr_t>(q + head) & (std::min(kBytes, 16) - 1)) == 0;
+  if (!together) {
+    for (int i = threadIdx.x; i < c.n; i += kThreads) q[i] = from_f32<O>(to_f32<T>(p[i]) * coef);
+    return;
+  }
+  const int pieces = (c.n - head) / kPer<T>, tail = c.n - head - pieces * kPer<T>;
+  const uint4* body = reinterpret_cast<const uint4*>(p + head);
+  O* to = q + head;
+  uint4 u[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int i = threadIdx.x + b * kThreads;
+    if (i < pieces) u[b] = body[i];
+  }
+  if (threadIdx.x < head + tail) {
+    const int at = threadIdx.x < head ? threadIdx.x : head + pieces * kPer<T> + threadIdx.x - head;
+    q[at] = from_f32<O>(to_f32<T>(p[at]) * coef);
+  }
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int i = threadIdx.x + b * kThreads;
+    if (i >= pieces) break;
+    float f[kPer<T>];
+    piece_values<T>(u[b], f);
+    uint32_t w[kBytes / 4];
+    constexpr bool kBf = std::is_same<O, __nv_bfloat16>::value;
+#pragma unroll
+    for (int j = 0; j < kBytes / 4; ++j) {
+      if constexpr (sizeof(O) == 4)
+        w[j] = __float_as_uint(f[j] * coef);
+      else
+        w[j] = pack2<kBf>(f[2 * j] * coef, f[2 * j + 1] * coef);
+    }
+    O* at = to + i * kPer<T>;
+    if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kBytes / 16; ++j)
+        reinterpret_cast<uint4*>(at)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+  }
+}
+
+// out = min(1, max_norm / (norm + 1e-6)) in.  In place a factor of 1 leaves everything as it is.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(const __grid_constant__ Table<N> tab, int count,
+                                                                unsigned chunks, const double* partials, int n,
+                                                                float max_norm, bool in_place, float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[kWarps];
+  __shared__ float coef_s;
+  const float total = norm_of(partials, n, red);
+  if (threadIdx.x == 0) {
+    const float r = max_norm / (total + 1e-6f);
+    coef_s = r > 1.f ? 1.f : r;  // NaN stays NaN
+    if (norm != nullptr && blockIdx.x == 0) *norm = total;
+  }
+  __syncthreads();
+  const float coef = coef_s;
+  if (in_place && coef == 1.f) return;
+  for (unsigned i = blockIdx.x; i < chunks; i += gridDim.x) {
+    const Chunk c = chunk_of(tab, count, chunks - 1 - i);
+    auto from = [&](auto* p) {
+      using T = std::remove_pointer_t<decltype(p)>;
+      if (c.t->out_dtype == kF32)
+        scale_chunk<T, float>(c, coef);
+      else if (c.t->out_dtype == kBF16)
+        scale_chunk<T, __nv_bfloat16>(c, coef);
+      else
+        scale_chunk<T, __half>(c, coef);
+    };
+    if (c.t->dtype == kF32)
+      from(static_cast<float*>(nullptr));
+    else if (c.t->dtype == kBF16)
+      from(static_cast<__nv_bfloat16*>(nullptr));
+    else
+      from(static_cast<__half*>(nullptr));
+  }
+}
+
+// Calls f(table, tensors, chunks) for groups of tensors that fit a launch's
+// parameters: 16 (a kilobyte) or kMany.
+constexpr int kFew = 16, kMany = 448;
+static_assert(sizeof(Table<kMany>) < 32000, "kernel parameters");
+
+template <class F>
+cudaError_t for_groups(const GradTensor* t, int n, F&& f) {
+  int i = 0;
+  while (i < n) {
+    // The tensors of a group have fewer than 2^31 chunks together.
+    Table<kMany> tab;
+    int k = 0;
+    unsigned long long chunks = 0;
+    for (; i < n && k < kMany; ++i) {
+      const long long len = kChunk / (t[i].dtype == kF32 ? 4 : 2), per = (t[i].cols + len - 1) / len;
+      const unsigned long long all = static_cast<unsigned long long>(per) * t[i].rows;
+      if (all == 0) continue;
+      if (chunks + all >= (1ull << 31)) {
+        if (k == 0) return cudaErrorInvalidValue;
+        break;
+      }
+      GradTensor& g = tab.t[k++] = t[i];
+      g.first = static_cast<unsigned>(chunks);
+      g.per_row = static_cast<unsigned>(per);
+      chunks += all;
+    }
+    if (k == 0) break;
+    cudaError_t e;
+    if (k <= kFew) {
+      Table<kFew> few;
+      std::copy(tab.t, tab.t + k, few.t);
+      e = f(few, k, static_cast<unsigned>(chunks));
+    } else {
+      e = f(tab, k, static_cast<unsigned>(chunks));
+    }
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+int blocks_for(unsigned chunks, int per_sm) {
+  return static_cast<int>(std::min<unsigned>(chunks, static_cast<unsigned>(std::min(per_sm * sm_count(), kMaxGradPartials))));
+}
+
+}  // namespace
+
+cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_norm, bool in_place, float* norm,
+                             double* partials, cudaStream_t s) {
+  int kept = 0;
+  cudaError_t e = for_groups(t, n, [&](const auto& tab, int count, unsigned chunks) {
+    constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
+    const int blocks = blocks_for(chunks, kSquareBlocks);
+    const cudaError_t r = launch_kernel(pdl_enabled(), grad_squares_kernel<N>, dim3(blocks), dim3(kThreads), 0, s, tab,
+                                        count, chunks, partials, kept);
+    kept = std::max(kept, blocks);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  if (!clip || kept == 0)
+    return norm == nullptr ? cudaSuccess
+                           : launch_kernel(pdl_enabled(), grad_norm_kernel, dim3(1), dim3(kThreads), 0, s,
+                                           static_cast<const double*>(partials), kept, norm);
+  bool first = true;
+  return for_groups(t, n, [&](const auto& tab, int count, unsigned chunks) {
+    constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
+    float* to = first ? norm : nullptr;
+    first = false;
+    return launch_kernel(pdl_enabled(), grad_scale_kernel<N>, dim3(blocks_for(chunks, kScaleBlocks)), dim3(kThreads), 0, s, tab,
+                         count, chunks, static_cast<const double*>(partials), kept, max_norm, in_place, to);
+  });
+}
+
+}  // namespace dion3

@@ -87,4 +87,21 @@ struct LogProbGradArgs {
 };
 cudaError_t launch_log_probs_grad(const LogProbGradArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping (grad_norm.cu)
+// ---------------------------------------------------------------------------
+struct GradTensor {
+  const void* in;
+  void* out;
+  long long ld_in, ld_out, cols;  // in elements
+  int rows;
+  unsigned first, per_row;        // chunks before the tensor, and of a row (set by the launcher)
+  short dtype, out_dtype;
+};
+constexpr int kMaxGradPartials = 1024;
+// The norm of n tensors (norm: may be null when clipping) and, with clip, out =
+// min(1, max_norm / (norm + 1e-6)) in.  partials: [kMaxGradPartials].
+cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_norm, bool in_place, float* norm,
+                             double* partials, cudaStream_t s);
+
 }  // namespace dion3

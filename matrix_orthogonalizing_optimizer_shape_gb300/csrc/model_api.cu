@@ -4,6 +4,8 @@
 #include "model.h"
 
 #include <algorithm>
+#include <memory>
+#include <new>
 
 namespace dion3 {
 namespace {
@@ -50,6 +52,100 @@ dion3_status check_log_probs(int32_t rows, int32_t vocab, const dion3_matrix* lo
   if (!(scale >= 0x1p-20f && scale <= 0x1p20f)) return fail(DION3_ERR_INVALID_ARG, "scale must lie in [2^-20, 2^20]");
   return targets != nullptr ? check_ids("targets", targets, target_bytes, rows) : DION3_OK;
 }
+dion3_status check_tensor(const char* name, int32_t i, const dion3_tensor& t) {
+  if (!known_dtype(t.dtype)) return fail(DION3_ERR_INVALID_ARG, "%s[%d]: unknown dtype %d", name, i, t.dtype);
+  if (t.rows < 0 || t.cols < 0) return fail(DION3_ERR_INVALID_ARG, "%s[%d]: negative size", name, i);
+  if (t.rows == 0 || t.cols == 0) return DION3_OK;
+  if (t.rows > kMaxRows || t.cols > (1ll << 40) || t.ld > (1ll << 40))
+    return fail(DION3_ERR_UNSUPPORTED, "%s[%d] is larger than 2^30 rows of 2^40", name, i);
+  if (t.data == nullptr) return fail(DION3_ERR_INVALID_ARG, "%s[%d] is NULL", name, i);
+  if (t.rows > 1 && t.ld < t.cols)
+    return fail(DION3_ERR_INVALID_ARG, "%s[%d]: pitch %lld is smaller than its row of %lld", name, i,
+                static_cast<long long>(t.ld), static_cast<long long>(t.cols));
+  if (reinterpret_cast<uintptr_t>(t.data) % bytes_of(t.dtype))
+    return fail(DION3_ERR_INVALID_ARG, "%s[%d] is not aligned to its element", name, i);
+  return DION3_OK;
+}
+
+// The memory of a tensor of a call that clips.
+struct Extent {
+  uintptr_t lo, hi;
+  unsigned long long pitch, row;  // bytes from row to row (0: one row) and of a row
+  int32_t i;
+  bool written;
+};
+Extent extent_of(const dion3_tensor& t, int32_t i, bool written) {
+  const unsigned long long es = bytes_of(t.dtype), row = t.cols * es, pitch = t.rows > 1 ? t.ld * es : 0;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data);
+  return {lo, static_cast<uintptr_t>(lo + (t.rows - 1) * pitch + row), pitch, row, i, written};
+}
+// Whether two that overlap are different columns of one matrix (a.lo <= b.lo).
+bool interleaved(const Extent& a, const Extent& b) {
+  if (a.pitch == 0 || a.pitch != b.pitch) return false;
+  const unsigned long long at = (b.lo - a.lo) % a.pitch;
+  return at >= a.row && at + b.row <= a.pitch;
+}
+// Refuses tensors whose elements several would write, or one write and another read.
+dion3_status check_apart(const dion3_tensor* in, const dion3_tensor* out, int32_t n) {
+  std::unique_ptr<Extent[]> all(new (std::nothrow) Extent[2 * static_cast<size_t>(n)]);
+  if (all == nullptr) return fail(DION3_ERR_UNSUPPORTED, "no host memory for %d tensors", n);
+  size_t m = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (in[i].rows == 0 || in[i].cols == 0) continue;
+    if (out == nullptr) {
+      all[m++] = extent_of(in[i], i, true);
+      continue;
+    }
+    const Extent a = extent_of(in[i], i, false), b = extent_of(out[i], i, true);
+    all[m++] = b;
+    if (a.lo != b.lo || in[i].dtype != out[i].dtype || (in[i].rows > 1 && in[i].ld != out[i].ld)) all[m++] = a;
+  }
+  std::sort(all.get(), all.get() + m, [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+  for (size_t j = 0; j < m; ++j)
+    for (size_t k = j + 1; k < m && all[k].lo < all[j].hi; ++k)
+      if ((all[j].written || all[k].written) && !interleaved(all[j], all[k]))
+        return fail(DION3_ERR_INVALID_ARG, "tensors %d and %d share elements", std::min(all[j].i, all[k].i),
+                    std::max(all[j].i, all[k].i));
+  return DION3_OK;
+}
+
+dion3_status grad_norm(const dion3_tensor* in, const dion3_tensor* out, int32_t n, bool clip, float max_norm, float* norm,
+                       void* ws, size_t ws_bytes, dion3_stream_t stream) {
+  if (n < 0) return fail(DION3_ERR_INVALID_ARG, "n must be >= 0 (got %d)", n);
+  if (n > 0 && in == nullptr) return fail(DION3_ERR_INVALID_ARG, "tensors is NULL");
+  if (!clip && norm == nullptr) return fail(DION3_ERR_INVALID_ARG, "norm is NULL");
+  if (clip && !(max_norm >= 0.f)) return fail(DION3_ERR_INVALID_ARG, "max_norm must be >= 0");
+  DION3_TRY(check_f32("norm", norm));
+  for (int32_t i = 0; i < n; ++i) {
+    DION3_TRY(check_tensor("tensors", i, in[i]));
+    if (out == nullptr) continue;
+    DION3_TRY(check_tensor("out", i, out[i]));
+    if (out[i].rows != in[i].rows || out[i].cols != in[i].cols)
+      return fail(DION3_ERR_INVALID_ARG, "out[%d] is not of the size of tensors[%d]", i, i);
+  }
+  if (clip) DION3_TRY(check_apart(in, out, n));
+  DION3_TRY(check_ws(ws, ws_bytes, kMaxGradPartials * sizeof(double)));
+  std::unique_ptr<GradTensor[]> t(new (std::nothrow) GradTensor[static_cast<size_t>(n) + 1]);
+  if (t == nullptr) return fail(DION3_ERR_UNSUPPORTED, "no host memory for %d tensors", n);
+  double bytes = 0.0;
+  for (int32_t i = 0; i < n; ++i) {
+    const dion3_tensor &a = in[i], &b = out != nullptr ? out[i] : in[i];
+    const bool dense = a.rows == 1 || (a.ld == a.cols && b.ld == b.cols);
+    t[i] = {a.data, b.data, a.ld, b.ld, dense ? a.rows * a.cols : a.cols, dense ? std::min<int>(a.rows, 1) : static_cast<int>(a.rows),
+            0u, 0u, static_cast<short>(a.dtype), static_cast<short>(b.dtype)};
+    bytes += static_cast<double>(a.rows) * a.cols * (bytes_of(a.dtype) * (clip ? 2 : 1) + (clip ? bytes_of(b.dtype) : 0));
+  }
+  DION3_TRY(check_inject());
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DION3_CUDA(traced_launch(clip ? "clip_grad_norm" : "grad_norm", 0.0, bytes, s,
+                           [&] {
+                             return launch_grad_norm(t.get(), n, clip, max_norm, out == nullptr, norm,
+                                                     static_cast<double*>(ws), s);
+                           }),
+             clip ? "clip_grad_norm launch" : "grad_norm launch");
+  return ok();
+}
+
 // Whether two matrices of a call start at the same address.
 bool same(const dion3_matrix* a, const dion3_matrix* b) { return a->data != nullptr && a->data == b->data; }
 
@@ -269,6 +365,22 @@ dion3_status dion3_log_probs_backward(int32_t rows, int32_t vocab, const dion3_m
                            [&] { return launch_log_probs_grad(a, s); }),
              "log_probs_backward launch");
   return ok();
+}
+
+dion3_status dion3_grad_norm_workspace_size(size_t* bytes) {
+  if (bytes == nullptr) return fail(DION3_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = kMaxGradPartials * sizeof(double);
+  return ok();
+}
+
+dion3_status dion3_grad_norm(const dion3_tensor* tensors, int32_t n, float* norm, void* ws, size_t ws_bytes,
+                             dion3_stream_t stream) {
+  return grad_norm(tensors, nullptr, n, false, 0.f, norm, ws, ws_bytes, stream);
+}
+
+dion3_status dion3_clip_grad_norm(const dion3_tensor* tensors, const dion3_tensor* out, int32_t n, float max_norm,
+                                  float* norm, void* ws, size_t ws_bytes, dion3_stream_t stream) {
+  return grad_norm(tensors, out, n, true, max_norm, norm, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

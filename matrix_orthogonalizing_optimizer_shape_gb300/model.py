@@ -11,12 +11,14 @@ current one) and returns without waiting::
     d3.recurrence_backward(dh, z, x, h, dz, dx, offsets=offsets)
     d3.log_probs(logits, targets, logp, stats=stats, top_values=values, top_ids=ids)
     d3.log_probs_backward(logits, targets, stats, dlogits, dlogp=dlogp)
+    d3.clip_grad_norm(grads, 1.0, norm, ws=ws)
     d3.embedding_backward(dx, ids, dtable, ws=ws)
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import struct
+from typing import Optional, Sequence
 
 import matrix_orthogonalizing_optimizer_shape_gb300 as _d3
 
@@ -32,7 +34,14 @@ SIGS = {
     "dion3_recurrence_backward": (_int, [_i32, _i32, _pm, _pm, _pm, _pm, _vp, _i32, _vp, _vp, _pm, _pm, _vp, _vp]),
     "dion3_log_probs": (_int, [_i32, _i32, _pm, _f32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
     "dion3_log_probs_backward": (_int, [_i32, _i32, _pm, _f32, _vp, _i32, _vp, _vp, _vp, _pm, _vp]),
+    "dion3_grad_norm_workspace_size": (_int, [_psz]),
+    "dion3_grad_norm": (_int, [_vp, _i32, _vp, _vp, _sz, _vp]),
+    "dion3_clip_grad_norm": (_int, [_vp, _vp, _i32, _f32, _vp, _vp, _sz, _vp]),
 }
+
+# dion3_tensor, as packed bytes (see the layer operators).
+_TENSOR = "Pqqqi4x"
+assert struct.calcsize("@" + _TENSOR) == 40
 
 
 def _ids(name: str, t, n: Optional[int], dev: int) -> tuple:
@@ -174,3 +183,82 @@ def log_probs_backward(logits, targets, stats, dlogits, *, dlogp=None, dentropy=
         rows, vocab, ml, scale, p, b, _table("stats", stats, rows, 3, _l._load_torch().float32, dev),
         _row_values("dlogp", dlogp, rows, dev), _row_values("dentropy", dentropy, rows, dev),
         _MAT.pack(*_mat("dlogits", dlogits, rows, vocab, dev)), _stream(stream, dev)))
+
+
+def grad_norm_workspace_size() -> int:
+    out = _sz(0)
+    _d3._check(_d3.load_library().dion3_grad_norm_workspace_size(ctypes.byref(out)))
+    return out.value
+
+
+def _tensors(name: str, ts: Sequence, dev: int) -> bytes:
+    """dion3_tensor of each: dense tensors of any shape, or matrices with contiguous rows."""
+    fields = []
+    dtypes = _l._DTYPES
+    for t in ts:
+        if t.get_device() != dev or dev < 0 or t.dtype not in dtypes:
+            _l._on(name, t, dev)
+            _l._dtype(t)
+        if t.is_contiguous():
+            n = t.numel()
+            fields += t.data_ptr(), 1, n, n, dtypes[t.dtype]
+        else:
+            p, ld, dtype = _mat(name, t, None, None, dev)
+            fields += p, t.shape[0], t.shape[1], ld, dtype
+    return struct.pack("@" + _TENSOR * len(ts), *fields)
+
+
+def _norm(t, dev: int) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != dev:
+        _l._on("norm", t, dev)
+    if t.numel() != 1 or t.dtype is not _l._load_torch().float32:
+        raise ValueError("norm must be one float32")
+    return t.data_ptr()
+
+
+def grad_norm(tensors: Sequence, norm, *, ws=None, ws_bytes: Optional[int] = None, stream=None):
+    """The norm over all elements of all tensors, of any types and shapes, into the
+    one-element float32 tensor norm (see dion3_grad_norm)."""
+    dev = norm.get_device()
+    p = _norm(norm, dev)
+    w, n = _ws(ws, ws_bytes, dev)
+    _l._load_torch()
+    _d3._check(_l._fn("dion3_grad_norm")(_tensors("tensors", tensors, dev), len(tensors), p, w, n, _stream(stream, dev)))
+
+
+def clip_grad_norm(tensors: Sequence, max_norm: float, norm=None, *, out: Optional[Sequence] = None, ws=None,
+                   ws_bytes: Optional[int] = None, stream=None):
+    """Scales all tensors by min(1, max_norm / (their norm + 1e-6)), in place or into
+    the tensors of ``out`` (same sizes, any types); norm receives the norm before
+    (see dion3_clip_grad_norm)."""
+    _l._load_torch()
+    dev = tensors[0].get_device() if len(tensors) else _l._device() if norm is None else norm.get_device()
+    if out is not None and len(out) != len(tensors):
+        raise ValueError(f"out has {len(out)} tensors, {len(tensors)} are wanted")
+    a, b = _tensors("tensors", tensors, dev), None
+    if out is not None:
+        for t, o in zip(tensors, out):
+            if t.shape != o.shape:
+                raise ValueError(f"out: a tensor of {tuple(o.shape)}, {tuple(t.shape)} is wanted")
+        if any(not (t.is_contiguous() and o.is_contiguous()) for t, o in zip(tensors, out)):
+            # The same rows on both sides: dense ones as rows too where the other has a pitch.
+            a, b = (_rows("tensors", tensors, out, dev), _rows("out", out, tensors, dev))
+        else:
+            b = _tensors("out", out, dev)
+    w, n = _ws(ws, ws_bytes, dev)
+    _d3._check(_l._fn("dion3_clip_grad_norm")(a, b, len(tensors), max_norm, _norm(norm, dev), w, n,
+                                              _stream(stream, dev)))
+
+
+def _rows(name: str, ts: Sequence, others: Sequence, dev: int) -> bytes:
+    """dion3_tensor of each, by rows where it or its counterpart is not dense."""
+    fields = []
+    for t, o in zip(ts, others):
+        if t.is_contiguous() and o.is_contiguous():
+            fields.append(_tensors(name, (t,), dev))
+        else:
+            p, ld, dtype = _mat(name, t, None, None, dev)
+            fields.append(struct.pack("@" + _TENSOR, p, t.shape[0], t.shape[1], ld, dtype))
+    return b"".join(fields)
