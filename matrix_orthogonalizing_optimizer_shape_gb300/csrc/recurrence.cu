@@ -4,13 +4,14 @@
 //
 // A step h -> a h + b is an affine map, and maps compose: (A, B) after (A', B')
 // is (A A', A B' + B).  A block takes a tile of channels (a lane VEC of them) and
-// kSpan consecutive rows, kRows a warp: each thread composes its rows' maps in
-// order, the warps' maps are composed through shared memory and those of a
-// cluster's blocks, which take the spans after one another, through the cluster's.
-// The cluster then walks down the rows, keeping the state; a row waits for one
-// block barrier and one cluster barrier, while the next rows' loads are in flight.
+// consecutive rows, R a warp: each thread composes its rows' maps in order; the
+// warps' maps are composed through shared memory by one thread a channel, and
+// those of a cluster's blocks, which take the rows after one another, through the
+// cluster's; then each thread runs through its rows again from the state before
+// them.  The cluster walks down the rows with the state, the next rows' loads in
+// flight.  Arithmetic is on pairs of channels (one instruction for two).
 //
-// Packed sequences: a map whose factor is set to 0 cuts, so that rows are divided
+// Packed sequences: a map that begins a sequence cuts, so that rows are divided
 // evenly whatever the sequences' lengths; nothing of the rows before a cut, NaN
 // included, passes it.  Where the channels are few, groups of whole sequences go
 // to different clusters.
@@ -28,110 +29,245 @@ namespace {
 using namespace lm;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRows = 8;                // rows of a warp in a step
-constexpr int kSpan = kWarps * kRows;   // rows of a block in a step
 constexpr int kMaxCluster = 8;
 constexpr int kSharedOffsets = 1024;
 
 // --------------------------------------------------------------------------
-// Elements and maps.  VEC = 2 channels a lane where they are aligned, else 1.
+// Vectors of VEC channels, 4 or 2 where they are aligned and else 1.
 // --------------------------------------------------------------------------
-template <typename T, int VEC>
-struct Word {
-  using type = std::conditional_t<sizeof(T) * VEC == 8, uint2, std::conditional_t<sizeof(T) * VEC == 4, uint32_t, uint16_t>>;
+template <int VEC>
+struct Vec {
+  float v[VEC];
+  __device__ __forceinline__ float& operator[](int j) { return v[j]; }
+  __device__ __forceinline__ float operator[](int j) const { return v[j]; }
 };
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(unsigned long long r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> fma(const Vec<VEC>& a, const Vec<VEC>& b, const Vec<VEC>& c) {
+  Vec<VEC> r;
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      unsigned long long d;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])),
+          "l"(pair(c[j], c[j + 1])));
+      unpair(d, r[j], r[j + 1]);
+    }
+  } else {
+    r[0] = fmaf(a[0], b[0], c[0]);
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> mul(const Vec<VEC>& a, const Vec<VEC>& b) {
+  Vec<VEC> r;
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      unsigned long long d;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])));
+      unpair(d, r[j], r[j + 1]);
+    }
+  } else {
+    r[0] = a[0] * b[0];
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> add(const Vec<VEC>& a, const Vec<VEC>& b) {
+  Vec<VEC> r;
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      unsigned long long d;
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])));
+      unpair(d, r[j], r[j + 1]);
+    }
+  } else {
+    r[0] = a[0] + b[0];
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> all(float x) {
+  Vec<VEC> r;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) r[j] = x;
+  return r;
+}
+
+// VEC elements as they lie in memory.
 template <typename T, int VEC>
 struct Cell {
-  typename Word<T, VEC>::type w;
-  __device__ __forceinline__ void load(const T* p, bool in) {
-    if (in)
-      w = *reinterpret_cast<const typename Word<T, VEC>::type*>(p);
-    else
-      w = {};
-  }
-  __device__ __forceinline__ void values(float (&v)[VEC]) const {
-    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    if constexpr (sizeof(T) == 4 && VEC == 2) {
-      v[0] = __uint_as_float(w.x);
-      v[1] = __uint_as_float(w.y);
-    } else if constexpr (sizeof(T) == 4) {
-      v[0] = __uint_as_float(w);
-    } else if constexpr (VEC == 2) {
-      const float2 f = unpack2<kBf>(w);
-      v[0] = f.x;
-      v[1] = f.y;
+  static constexpr int kWords = (VEC * static_cast<int>(sizeof(T)) + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC * sizeof(T) == 16) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else if constexpr (VEC * sizeof(T) == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x, w[1] = u.y;
+    } else if constexpr (VEC * sizeof(T) == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
-      v[0] = unpack1<kBf>(w);
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ Vec<VEC> values() const {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    Vec<VEC> v;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(w[j]);
+    } else if constexpr (VEC == 1) {
+      v[0] = unpack1<kBf>(static_cast<uint16_t>(w[0]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; j += 2) {
+        const float2 f = unpack2<kBf>(w[j / 2]);
+        v[j] = f.x;
+        v[j + 1] = f.y;
+      }
+    }
+    return v;
+  }
+};
+// What a thread has in flight: R cells of each of N matrices, for kAhead steps.
+// Copied into shared memory by cp.async, a place of its own for each thread, where
+// a cell has 4 bytes or more; else held in registers, for one step.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+template <typename T, int VEC, int R, int N>
+struct Flight {
+  static constexpr bool kAsync = VEC * sizeof(T) >= 4;
+  static constexpr int kAhead = kAsync ? 2 : 1;
+  static constexpr int kCell = VEC * static_cast<int>(sizeof(T));
+  static constexpr size_t kBytes = kAsync ? static_cast<size_t>(kAhead) * N * R * kThreads * kCell : 0;
+  Cell<T, VEC> reg[kAsync ? 1 : N][kAsync ? 1 : R];
+  char* mem;
+  uint32_t at;
+  __device__ __forceinline__ explicit Flight(char* shared)
+      : mem(shared + threadIdx.x * kCell), at(static_cast<uint32_t>(__cvta_generic_to_shared(mem))) {}
+  // Cell i of matrix n for step `step`.
+  __device__ __forceinline__ void load(int step, int n, int i, const T* p) {
+    if constexpr (kAsync)
+      copy_async(at + (((step % kAhead) * N + n) * R + i) * kThreads * kCell, p, kCell);
+    else
+      reg[n][i].load(p);
+  }
+  __device__ __forceinline__ void loaded() const {  // after the loads of a step
+    if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() const {  // for the oldest step's
+    if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+  }
+  __device__ __forceinline__ Vec<VEC> values(int step, int n, int i) const {
+    if constexpr (kAsync) {
+      Cell<T, VEC> c;
+      c.load(reinterpret_cast<const T*>(mem + (((step % kAhead) * N + n) * R + i) * kThreads * kCell));
+      return c.values();
+    } else {
+      return reg[n][i].values();
     }
   }
 };
+
 template <typename T, int VEC>
-__device__ __forceinline__ void store_cell(T* p, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_cell(T* p, const Vec<VEC>& v) {
   constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-  if constexpr (sizeof(T) == 4 && VEC == 2)
-    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-  else if constexpr (sizeof(T) == 2 && VEC == 2)
-    *reinterpret_cast<uint32_t*>(p) = pack2<kBf>(v[0], v[1]);
-  else
+  if constexpr (VEC == 1)
     *p = from_f32<T>(v[0]);
+  else if constexpr (sizeof(T) == 4 && VEC == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  else if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<kBf>(v[0], v[1]), pack2<kBf>(v[2], v[3]));
+  else
+    *reinterpret_cast<uint32_t*>(p) = pack2<kBf>(v[0], v[1]);
 }
 // State vectors are fp32 with the channels' alignment unknown: element by element.
 template <int VEC>
-__device__ __forceinline__ void load_state(const float* p, float (&v)[VEC]) {
+__device__ __forceinline__ Vec<VEC> load_state(const float* p) {
+  Vec<VEC> v;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) v[j] = p[j];
+  return v;
 }
 template <int VEC>
-__device__ __forceinline__ void store_state(float* p, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_state(float* p, const Vec<VEC>& v) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) p[j] = v[j];
 }
 
-// Maps h -> A h + B.  Where A is at least a half, F holds -(1 - A) with its sign
-// bit set, else A itself: a factor near 1 that were rounded would decay the state
-// at a rate that is off in every one of thousands of rows.  F = +0 cuts: nothing
-// of h passes, NaN and infinity included.
+// --------------------------------------------------------------------------
+// Gates.  a = 1 / (1 + u) and 1 - a = u a with u = e^-z: each accurate relative
+// to itself, by two special function instructions.  u stops at 2^126, where the
+// product is still 1, and 2^-126 taken off a makes a 0 there (nowhere else does
+// it change a): z = -infinity forgets.
+// --------------------------------------------------------------------------
+template <int VEC>
+struct Gate {
+  Vec<VEC> a, na;
+  __device__ __forceinline__ explicit Gate(const Vec<VEC>& z) {
+    const Vec<VEC> e = mul(z, all<VEC>(-kLog2E));
+    Vec<VEC> u, r;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u[j]) : "f"(e[j]));
+      asm("min.NaN.f32 %0, %1, 0f7E800000;" : "=f"(u[j]) : "f"(u[j]));
+    }
+    const Vec<VEC> s = add(u, all<VEC>(1.f));
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[j]) : "f"(s[j]));
+    na = mul(u, r);
+    a = add(r, all<VEC>(-0x1p-126f));
+  }
+};
+
+// --------------------------------------------------------------------------
+// Maps h -> A h + B.  Where A is above a half, F holds -(1 - A) with its sign bit
+// set, else A itself: a factor near 1 that were rounded would decay the state at a
+// rate that is off in every one of thousands of rows.  kCut: nothing passes.
+// --------------------------------------------------------------------------
+constexpr float kCut = 2.f;
 __device__ __forceinline__ bool near_one(float F) { return static_cast<int>(__float_as_uint(F)) < 0; }
 __device__ __forceinline__ float through(float F, float B, float h) {
   const float r = fmaf(F, h, B) + (near_one(F) ? h : 0.f);
-  return __float_as_uint(F) == 0u ? B : r;
+  return F == kCut ? B : r;
 }
 // The factor of F2 after F1: with both below 1 by D, D1 + D2 - D1 D2.
 __device__ __forceinline__ float after(float F2, float F1) {
+  if (F2 == kCut || F1 == kCut) return kCut;
   const bool n1 = near_one(F1), n2 = near_one(F2);
   const float r = fmaf(F2, F1, (n2 ? F1 : 0.f) + (n1 ? F2 : 0.f));
   if (!(n1 && n2)) return r;
   return r < -0.5f ? 1.f + r : -fabsf(r);
 }
-__device__ __forceinline__ float encode(float A, float D) { return D < 0.5f ? -D : A; }
-// A row's state from its thread's map up to it: not passed on, so a plain factor.
-__device__ __forceinline__ float reach(float A, float B, float h) { return A == 0.f ? B : fmaf(A, h, B); }
-
-// w = the smaller of a = sigmoid(z) and 1 - a, computed without cancellation;
-// the larger is 1 - w.  A state that is nearly kept or nearly replaced is then
-// h + w (x - h) or x + w (h - x), off by a rounding of the result, where a rounded
-// factor a near 1 would change the decay over thousands of rows.
-struct Gate {
-  float w, big;  // small and large of a, 1 - a
-  bool keep;     // a is the larger
-  __device__ __forceinline__ explicit Gate(float z) : keep(z >= 0.f) {
-    float u;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u) : "f"(-kLog2E * fabsf(z)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(big) : "f"(1.f + u));
-    w = u * big;
+// A thread's map: its factor A, D = 1 - A summed for itself, and B.
+template <int VEC>
+struct Map {
+  Vec<VEC> A = all<VEC>(1.f), D = all<VEC>(0.f), B = all<VEC>(0.f);
+  __device__ __forceinline__ void factor(const Gate<VEC>& g) {
+    D = fma(g.na, A, D);
+    A = mul(g.a, A);
   }
-  __device__ __forceinline__ float step(float h, float x) const {
-    const float p = keep ? h : x, q = keep ? x : h;
-    return fmaf(w, q - p, p);
-  }
-  __device__ __forceinline__ float decay(float A) const {  // a A
-    const float t = w * A;
-    return keep ? A - t : t;
-  }
-  __device__ __forceinline__ void decay(float& A, float& D) const {  // and D = 1 - A
-    const float t = w * A;
-    A = keep ? A - t : t;
-    D = keep ? D + t : 1.f - t;
+  __device__ __forceinline__ float2 channel(int j, bool cut) const {
+    return make_float2(cut ? kCut : D[j] < 0.5f ? -D[j] : A[j], B[j]);
   }
 };
 
@@ -155,7 +291,7 @@ struct Sequences {
     return lo;
   }
   // The sequence that holds a row of the sequences' rows.
-  __device__ __forceinline__ int of(int row) const { return max(starts_below(row, true) - 1, 0); }
+  __device__ __forceinline__ int of(int row) const { return n == 1 ? 0 : max(starts_below(row, true) - 1, 0); }
   // The next and the previous one that has rows.
   __device__ __forceinline__ int next(int q) const {
     q = min(q + 1, n - 1);
@@ -201,157 +337,183 @@ template <int VEC>
 __device__ __forceinline__ void copy_empty(const Span& p, const float* from, float* to, int channels, int c, bool in) {
   for (int q = p.s0 + static_cast<int>(threadIdx.x) / 32; q < p.s1; q += kWarps) {
     if (p.seq.off[q + 1] > p.seq.off[q] || !in) continue;
-    float v[VEC] = {};
-    if (from != nullptr) load_state<VEC>(from + static_cast<long long>(q) * channels + c, v);
-    store_state<VEC>(to + static_cast<long long>(q) * channels + c, v);
+    const long long at = static_cast<long long>(q) * channels + c;
+    store_state<VEC>(to + at, from != nullptr ? load_state<VEC>(from + at) : all<VEC>(0.f));
   }
 }
 
-// The maps of a block's warps and a cluster's blocks, in turn in two halves.
-struct Maps {
-  float4 warp[2][kWarps][32];
-  float4 block[2][kMaxCluster][32];
+// The sequence of a warp's row, kept from step to step.
+struct Place {
+  int q = 0, begin = INT_MAX, end = INT_MIN;
+  __device__ __forceinline__ void set(const Sequences& s, int to) { q = to, begin = s.off[to], end = s.off[to + 1]; }
+  __device__ __forceinline__ void find(const Sequences& s, int row) {
+    if (row < begin || row >= end) set(s, s.of(row));
+  }
 };
 
-// From the map (F, B) of this warp's rows and the state before the cluster's rows
-// (which becomes the state after them): the state before this warp's rows.  A
-// thread's call number is `step`.
+// --------------------------------------------------------------------------
+// The states before each warp's rows, from the maps of all and the state before
+// the cluster's rows.  One thread a channel keeps that state.
+// --------------------------------------------------------------------------
 template <int VEC>
-__device__ __forceinline__ void enter(Maps& m, int step, int rank, int size, const float (&F)[VEC], const float (&B)[VEC],
-                                      float (&carry)[VEC], float (&h)[VEC]) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, half = step & 1;
-  m.warp[half][warp][lane] = make_float4(F[0], B[0], F[VEC - 1], B[VEC - 1]);
-  __syncthreads();
-  auto apply = [&](const float4& v, float (&to)[VEC]) {
-    to[0] = through(v.x, v.y, to[0]);
-    if constexpr (VEC == 2) to[1] = through(v.z, v.w, to[1]);
-  };
-  if (size > 1) {
-    if (warp == kWarps - 1) {
-      float4 all = m.warp[half][0][lane];
+struct Shared {
+  static constexpr int kTile = 32 * VEC;
+  float2 warp[kWarps][kTile];                 // maps of the block's warps
+  float2 block[2][kMaxCluster][kTile];        // of the cluster's blocks, in turn in two halves
+  float enter[kWarps][kTile];                 // the states
+  int off[kSharedOffsets];
+};
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, int size, const Map<VEC>& m, bool cut,
+                                          float& carry) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, half = step & 1, t = threadIdx.x;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 v = m.warp[half][w][lane];
-        all = make_float4(after(v.x, all.x), through(v.x, v.y, all.y), after(v.z, all.z), through(v.z, v.w, all.w));
-      }
-      for (int r = 0; r < size; ++r) cl::store(cl::peer(&m.block[half][rank][lane], r), all);
+  for (int j = 0; j < VEC; ++j) sh.warp[warp][lane * VEC + j] = m.channel(j, cut);
+  __syncthreads();
+  float2 f[kWarps];
+  if (t < 32 * VEC) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) f[w] = sh.warp[w][t];
+  }
+  float h = carry;
+  if (size > 1) {
+    if (t < 32 * VEC) {
+      float2 all = f[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) all = make_float2(after(f[w].x, all.x), through(f[w].x, f[w].y, all.y));
+      for (int r = 0; r < size; ++r) cl::store(cl::peer(&sh.block[half][rank][t], r), all);
     }
     cl::arrive();
     cl::wait();
-    for (int r = 0; r < size; ++r) {
-      if (r == rank) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = carry[j];
+    if (t < 32 * VEC) {
+      for (int r = 0; r < size; ++r) {
+        if (r == rank) h = carry;
+        const float2 b = sh.block[half][r][t];
+        carry = through(b.x, b.y, carry);
       }
-      apply(m.block[half][r][lane], carry);
-    }
-    for (int w = 0; w < warp; ++w) apply(m.warp[half][w][lane], h);
-  } else {
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = carry[j];
-      }
-      apply(m.warp[half][w][lane], carry);
     }
   }
+  if (t < 32 * VEC) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      sh.enter[w][t] = h;
+      h = through(f[w].x, f[w].y, h);
+    }
+    if (size == 1) carry = h;
+  }
+  __syncthreads();
+  Vec<VEC> v;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = sh.enter[warp][lane * VEC + j];
+  return v;
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) recurrence_kernel(RecurrenceArgs a) {
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ Maps maps;
-  __shared__ int shared_off[kSharedOffsets];
+  __shared__ __align__(16) Shared<VEC> sh;
   const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
-  const Span p = span_of(a, blockIdx.x / size, groups, shared_off);
+  const Span p = span_of(a, blockIdx.x / size, groups, sh.off);
   if (size > 1) cl::arrive(), cl::wait();  // every block has begun before one writes to another
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int c = (blockIdx.y * 32 + lane) * VEC;
+  const int c = (blockIdx.y * 32 + lane) * VEC, cr = c < a.channels ? c : 0;
   const bool in = c < a.channels;
   if (a.last != nullptr && rank == 0) copy_empty<VEC>(p, a.first, a.last, a.channels, c, in);
 
-  const T* pz = static_cast<const T*>(a.z.p) + c;
-  const T* px = static_cast<const T*>(a.x.p) + c;
-  T* ph = static_cast<T*>(a.h.p) + c;
-  Cell<T, VEC> z[kRows], x[kRows];
-  auto load = [&](long long row0) {
+  const T* pz = static_cast<const T*>(a.z.p) + cr;
+  const T* px = static_cast<const T*>(a.x.p) + cr;
+  T* ph = static_cast<T*>(a.h.p) + cr;
+  extern __shared__ __align__(16) char flight_mem[];
+  using F = Flight<T, VEC, R, 2>;
+  F in_flight(flight_mem);
+  auto load = [&](int step, long long row0) {
+    const T *qz = pz + row0 * a.z.ld, *qx = px + row0 * a.x.ld;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const bool ok = in && row0 + i < p.r1;
-      z[i].load(pz + (row0 + i) * a.z.ld, ok);
-      x[i].load(px + (row0 + i) * a.x.ld, ok);
+    for (int i = 0; i < R; ++i, qz += a.z.ld, qx += a.x.ld) {
+      if (row0 + i >= p.r1) break;
+      in_flight.load(step, 0, i, qz);
+      in_flight.load(step, 1, i, qx);
     }
+    in_flight.loaded();
   };
-  float carry[VEC] = {};
-  const int stride = size * kSpan;
-  long long base = p.r0 + (rank * kWarps + warp) * kRows;
-  load(base);
+  float carry = 0.f;
+  const int stride = size * kWarps * R;
+  long long base = p.r0 + (rank * kWarps + warp) * R;
+#pragma unroll
+  for (int i = 0; i < F::kAhead; ++i) load(i, base + i * stride);
+  Place at;
   int step = 0;
   for (long long top = p.r0; top < p.r1; top += stride, base += stride, ++step) {
-    const int row0 = static_cast<int>(min(base, static_cast<long long>(INT_MAX - kRows)));
-    // Which rows begin a sequence, and the states that those begin with.
+    const int row0 = static_cast<int>(min(base, static_cast<long long>(INT_MAX - R)));
+    in_flight.wait();
+    Map<VEC> m;
+    Vec<VEC> f[R];  // a and (1 - a) x of the rows
+    Vec<VEC> g[R];
     unsigned begins = 0, ends = 0;
-    float f[kRows][VEC];
     int q0 = 0;
+    bool whole = false;  // whole rows of one sequence, neither its first nor (where that is asked for) its last
     if (row0 < p.r1) {
-      int q = q0 = p.seq.of(row0);
-      int begin = p.seq.off[q], end = p.seq.off[q + 1];
+      at.find(p.seq, row0);
+      q0 = at.q;
+      whole = row0 + R <= p.r1 && row0 != at.begin && (a.last == nullptr ? row0 + R <= at.end : row0 + R < at.end);
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (row0 + i == begin) {
-          begins |= 1u << i;
-          if (a.first != nullptr && in) load_state<VEC>(a.first + static_cast<long long>(q) * a.channels + c, f[i]);
+        for (int i = 0; i < R; ++i) {
+          const Gate<VEC> k(in_flight.values(step, 0, i));
+          f[i] = k.a;
+          g[i] = mul(k.na, in_flight.values(step, 1, i));
+          m.factor(k);
+          m.B = fma(f[i], m.B, g[i]);
         }
-        if (row0 + i + 1 == end && row0 + i < p.r1) {
-          ends |= 1u << i;
-          q = p.seq.next(q);
-          begin = p.seq.off[q], end = p.seq.off[q + 1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (row0 + i >= p.r1) break;
+          if (row0 + i == at.begin) {
+            begins |= 1u << i;
+            g[i] = a.first != nullptr ? load_state<VEC>(a.first + static_cast<long long>(at.q) * a.channels + cr)
+                                      : all<VEC>(0.f);
+          }
+          if (row0 + i + 1 == at.end) {
+            ends |= 1u << i;
+            at.set(p.seq, p.seq.next(at.q));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (row0 + i >= p.r1) break;
+          const Gate<VEC> k(in_flight.values(step, 0, i));
+          f[i] = k.a;
+          const Vec<VEC> b = mul(k.na, in_flight.values(step, 1, i));
+          if (begins >> i & 1) {  // the state before it is in g
+            m.B = g[i] = fma(f[i], g[i], b);
+          } else {
+            g[i] = b;
+            m.B = fma(f[i], m.B, b);
+          }
+          m.factor(k);
         }
       }
     }
-    float A[kRows][VEC], B[kRows][VEC], F[VEC];
+    load(step + F::kAhead, base + F::kAhead * stride);
+    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry);
+    T* q = ph + row0 * a.h.ld;
+    if (whole) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      float ra = 1.f, rd = 0.f, rb = 0.f;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (begins >> i & 1) {
-          ra = 0.f;
-          rd = 1.f;
-          rb = a.first != nullptr ? f[i][j] : 0.f;
-        }
-        float zv[VEC], xv[VEC];
-        z[i].values(zv);
-        x[i].values(xv);
-        if (row0 + i < p.r1) {
-          const Gate g(zv[j]);
-          rb = g.step(rb, xv[j]);
-          g.decay(ra, rd);
-        }
-        A[i][j] = ra;
-        B[i][j] = rb;
+      for (int i = 0; i < R; ++i, q += a.h.ld) {
+        h = fma(f[i], h, g[i]);
+        if (in) store_cell<T, VEC>(q, h);
       }
-      F[j] = encode(ra, rd);
-    }
-    load(base + stride);
-    float h[VEC];
-    enter<VEC>(maps, step, rank, size, F, B[kRows - 1], carry, h);
-    if (!in || row0 >= p.r1) continue;
+    } else {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (row0 + i >= p.r1) break;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) B[i][j] = reach(A[i][j], B[i][j], h[j]);
-      store_cell<T, VEC>(ph + static_cast<long long>(row0 + i) * a.h.ld, B[i]);
-    }
-    if (a.last != nullptr && ends != 0u) {
-      int q = q0;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
+      for (int i = 0; i < R; ++i, q += a.h.ld) {
+        if (row0 + i >= p.r1) break;
+        h = begins >> i & 1 ? g[i] : fma(f[i], h, g[i]);
+        if (in) store_cell<T, VEC>(q, h);
         if (ends >> i & 1) {
-          store_state<VEC>(a.last + static_cast<long long>(q) * a.channels + c, B[i]);
-          q = p.seq.next(q);
+          if (a.last != nullptr && in) store_state<VEC>(a.last + static_cast<long long>(q0) * a.channels + c, h);
+          q0 = p.seq.next(q0);
         }
       }
     }
@@ -360,118 +522,126 @@ __global__ void __launch_bounds__(kThreads) recurrence_kernel(RecurrenceArgs a) 
 
 // --------------------------------------------------------------------------
 // Gradient: g_t = dh_t + s_{t+1}, s_t = a_t g_t, dx = (1 - a) g and
-// dz = g (h_{t-1} - x) a (1 - a).  The scan runs from the last row to the first;
-// a row's map is s -> a s + a dh.  Row i of a warp is the i-th from its end.
+// dz = dx a (h_{t-1} - x).  The scan runs from the last row to the first; a row's
+// map is s -> a s + a dh.  Row i of a warp is the i-th from its end.
 // --------------------------------------------------------------------------
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) recurrence_grad_kernel(RecurrenceArgs a) {
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(RecurrenceArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ Maps maps;
-  __shared__ int shared_off[kSharedOffsets];
+  __shared__ __align__(16) Shared<VEC> sh;
   const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
-  const Span p = span_of(a, blockIdx.x / size, groups, shared_off);
+  const Span p = span_of(a, blockIdx.x / size, groups, sh.off);
   if (size > 1) cl::arrive(), cl::wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int c = (blockIdx.y * 32 + lane) * VEC;
+  const int c = (blockIdx.y * 32 + lane) * VEC, cr = c < a.channels ? c : 0;
   const bool in = c < a.channels;
   if (a.dfirst != nullptr && rank == 0) copy_empty<VEC>(p, a.dlast, a.dfirst, a.channels, c, in);
 
-  const T* pz = static_cast<const T*>(a.z.p) + c;
-  const T* px = static_cast<const T*>(a.x.p) + c;
-  const T* ph = static_cast<const T*>(a.h.p) + c;
-  const T* pd = static_cast<const T*>(a.dh.p) + c;
-  T* pdz = static_cast<T*>(a.dz.p) + c;
-  T* pdx = static_cast<T*>(a.dx.p) + c;
-  float carry[VEC] = {};
-  const int stride = size * kSpan;
-  long long base = static_cast<long long>(p.r1) - 1 - (rank * kWarps + warp) * kRows;
+  const T* pz = static_cast<const T*>(a.z.p) + cr;
+  const T* px = static_cast<const T*>(a.x.p) + cr;
+  const T* ph = static_cast<const T*>(a.h.p) + cr;
+  const T* pd = static_cast<const T*>(a.dh.p) + cr;
+  T* pdz = static_cast<T*>(a.dz.p) + cr;
+  T* pdx = static_cast<T*>(a.dx.p) + cr;
+  extern __shared__ __align__(16) char flight_mem[];
+  using F = Flight<T, VEC, R, 4>;
+  F in_flight(flight_mem);
+  auto load = [&](int step, long long row0) {  // of h the row before, where there is one
+    const T *qz = pz + row0 * a.z.ld, *qx = px + row0 * a.x.ld, *qh = ph + (row0 - 1) * a.h.ld, *qd = pd + row0 * a.dh.ld;
+#pragma unroll
+    for (int i = 0; i < R; ++i, qz -= a.z.ld, qx -= a.x.ld, qh -= a.h.ld, qd -= a.dh.ld) {
+      if (row0 - i < p.r0) break;
+      in_flight.load(step, 0, i, qz);
+      in_flight.load(step, 1, i, qx);
+      if (row0 - i > p.r0) in_flight.load(step, 2, i, qh);
+      in_flight.load(step, 3, i, qd);
+    }
+    in_flight.loaded();
+  };
+  float carry = 0.f;
+  const int stride = size * kWarps * R;
+  long long base = static_cast<long long>(p.r1) - 1 - (rank * kWarps + warp) * R;
+#pragma unroll
+  for (int i = 0; i < F::kAhead; ++i) load(i, base - i * stride);
+  Place at;
   int step = 0;
   for (long long top = p.r1; top > p.r0; top -= stride, base -= stride, ++step) {
-    Cell<T, VEC> z[kRows], x[kRows], hp[kRows], d[kRows];
     const bool any = base >= p.r0;
+    in_flight.wait();
     const int row0 = any ? static_cast<int>(base) : p.r0;
+    Map<VEC> m;
+    Vec<VEC> ga[R], gn[R], dv[R], diff[R];  // a, 1 - a, dh and h_{t-1} - x of the rows
     unsigned begins = 0, ends = 0;
-    float f[kRows][VEC], dl[kRows][VEC];
     int q0 = 0;
+    bool whole = false;
     if (any) {
-      int q = q0 = p.seq.of(row0);
-      int begin = p.seq.off[q], end = p.seq.off[q + 1];
+      at.find(p.seq, row0);
+      q0 = at.q;
+      whole = row0 - R >= p.r0 && row0 + 1 != at.end && row0 - R >= at.begin;
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = row0 - i;
-        if (row + 1 == end) {
-          ends |= 1u << i;
-          if (a.dlast != nullptr && in) load_state<VEC>(a.dlast + static_cast<long long>(q) * a.channels + c, dl[i]);
+        for (int i = 0; i < R; ++i) {
+          const Gate<VEC> k(in_flight.values(step, 0, i));
+          ga[i] = k.a;
+          gn[i] = k.na;
+          dv[i] = in_flight.values(step, 3, i);
+          diff[i] = fma(in_flight.values(step, 1, i), all<VEC>(-1.f), in_flight.values(step, 2, i));
+          m.factor(k);
+          m.B = mul(ga[i], add(dv[i], m.B));
         }
-        if (row == begin) {
-          begins |= 1u << i;
-          if (a.first != nullptr && in) load_state<VEC>(a.first + static_cast<long long>(q) * a.channels + c, f[i]);
-          q = p.seq.prev(q);
-          begin = p.seq.off[q], end = p.seq.off[q + 1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (row0 - i < p.r0) break;
+          if (row0 - i + 1 == at.end) {
+            ends |= 1u << i;
+            dv[i] = a.dlast != nullptr ? load_state<VEC>(a.dlast + static_cast<long long>(at.q) * a.channels + cr)
+                                       : all<VEC>(0.f);
+          }
+          if (row0 - i == at.begin) {
+            begins |= 1u << i;
+            diff[i] = a.first != nullptr ? load_state<VEC>(a.first + static_cast<long long>(at.q) * a.channels + cr)
+                                         : all<VEC>(0.f);
+            at.set(p.seq, p.seq.prev(at.q));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (row0 - i < p.r0) break;
+          const Gate<VEC> k(in_flight.values(step, 0, i));
+          ga[i] = k.a;
+          gn[i] = k.na;
+          if (ends >> i & 1) {  // dlast is in dv
+            dv[i] = add(in_flight.values(step, 3, i), dv[i]);
+            m.B = all<VEC>(0.f);
+          } else {
+            dv[i] = in_flight.values(step, 3, i);
+          }
+          if (!(begins >> i & 1)) diff[i] = in_flight.values(step, 2, i);  // else the state before it is there
+          diff[i] = fma(in_flight.values(step, 1, i), all<VEC>(-1.f), diff[i]);
+          m.factor(k);
+          m.B = mul(ga[i], add(dv[i], m.B));
         }
       }
     }
+    load(step + F::kAhead, base - F::kAhead * stride);
+    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry);
+    if (!any) continue;
+    T *qz = pdz + row0 * a.dz.ld, *qx = pdx + row0 * a.dx.ld;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const long long row = row0 - i;
-      const bool ok = in && any && row >= p.r0;
-      z[i].load(pz + row * a.z.ld, ok);
-      d[i].load(pd + row * a.dh.ld, ok);
-      x[i].load(px + row * a.x.ld, ok);
-      hp[i].load(ph + (row - 1) * a.h.ld, ok && row > p.r0 && !(begins >> i & 1));
-    }
-    float A[VEC], D[VEC], B[VEC], dv[kRows][VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) A[j] = 1.f, D[j] = B[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      d[i].values(dv[i]);
-      float zv[VEC];
-      z[i].values(zv);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (ends >> i & 1) {
-          A[j] = B[j] = 0.f;
-          D[j] = 1.f;
-          if (a.dlast != nullptr) dv[i][j] += dl[i][j];
-        }
-        if (any && row0 - i >= p.r0) {
-          const Gate g(zv[j]);
-          B[j] = g.decay(dv[i][j] + B[j]);
-          g.decay(A[j], D[j]);
-        }
+    for (int i = 0; i < R; ++i, qz -= a.dz.ld, qx -= a.dx.ld) {
+      if (!whole && row0 - i < p.r0) break;
+      const Vec<VEC> g = ends >> i & 1 ? dv[i] : add(dv[i], s);
+      const Vec<VEC> dx = mul(gn[i], g);
+      s = mul(ga[i], g);
+      if (in) {
+        store_cell<T, VEC>(qx, dx);
+        store_cell<T, VEC>(qz, mul(mul(dx, ga[i]), diff[i]));
       }
-    }
-    float F[VEC], s[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) F[j] = encode(A[j], D[j]);
-    enter<VEC>(maps, step, rank, size, F, B, carry, s);
-    if (!in || !any) continue;
-    int q = q0;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const long long row = row0 - i;
-      if (row < p.r0) break;
-      float zv[VEC], xv[VEC], hv[VEC], dz[VEC], dx[VEC];
-      z[i].values(zv);
-      x[i].values(xv);
-      hp[i].values(hv);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (ends >> i & 1) s[j] = 0.f;
-        if ((begins >> i & 1) && a.first != nullptr) hv[j] = f[i][j];
-        const Gate g(zv[j]);
-        const float gr = dv[i][j] + s[j], t = g.w * gr;
-        dx[j] = g.keep ? t : gr - t;
-        dz[j] = t * g.big * (hv[j] - xv[j]);
-        s[j] = g.keep ? gr - t : t;
-      }
-      store_cell<T, VEC>(pdz + row * a.dz.ld, dz);
-      store_cell<T, VEC>(pdx + row * a.dx.ld, dx);
       if (begins >> i & 1) {
-        if (a.dfirst != nullptr) store_state<VEC>(a.dfirst + static_cast<long long>(q) * a.channels + c, s);
-        q = p.seq.prev(q);
+        if (a.dfirst != nullptr && in) store_state<VEC>(a.dfirst + static_cast<long long>(q0) * a.channels + c, s);
+        q0 = p.seq.prev(q0);
       }
     }
   }
@@ -480,21 +650,30 @@ __global__ void __launch_bounds__(kThreads) recurrence_grad_kernel(RecurrenceArg
 // --------------------------------------------------------------------------
 // Host side
 // --------------------------------------------------------------------------
-bool pairs(const Mat& m, int dtype) {  // two channels at an aligned address in every row
+// Channels at an aligned address in every row: 4, 2 or 1.
+int aligned_channels(const Mat& m, int dtype) {
+  if (m.p == nullptr) return 4;
   const int es = dtype == kF32 ? 4 : 2;
-  return m.p == nullptr || (m.ld % 2 == 0 && reinterpret_cast<uintptr_t>(m.p) % (2 * es) == 0);
+  for (int v : {4, 2})
+    if (m.ld % v == 0 && reinterpret_cast<uintptr_t>(m.p) % (v * es) == 0) return v;
+  return 1;
 }
 
 template <class K>
-cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, cudaStream_t s) {
+cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, int rows, size_t shared, cudaStream_t s) {
+  if (shared > 0) {  // with the static part past what a kernel has without asking
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+    if (e != cudaSuccess) return e;
+  }
   const int tiles = (a.channels + 32 * vec - 1) / (32 * vec);
   const int want = 2 * sm_count();  // blocks
   int size = 1;
-  while (size < kMaxCluster && 2 * size * tiles <= want && size * kSpan < a.tokens) size *= 2;
+  while (size < kMaxCluster && 2 * size * tiles <= want && size * kWarps * rows < a.tokens) size *= 2;
   const int groups = std::max(1, std::min({a.sequences, want / (tiles * size), 65535 / kMaxCluster}));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size * groups, tiles);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -506,21 +685,30 @@ cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename T>
-cudaError_t launch_typed(const RecurrenceArgs& a, bool vec2, cudaStream_t s) {
+template <typename T, int VEC>
+cudaError_t launch_vec(const RecurrenceArgs& a, cudaStream_t s) {
+  // Rows of a warp: what fits in registers with the next ones' loads.
+  constexpr int kForward = sizeof(T) * VEC > 8 ? 4 : 8, kBackward = sizeof(T) * VEC > 8 ? 2 : 4;
   if (a.grad)
-    return launch_scan(vec2 ? recurrence_grad_kernel<T, 2> : recurrence_grad_kernel<T, 1>, a, vec2 ? 2 : 1, s);
-  return launch_scan(vec2 ? recurrence_kernel<T, 2> : recurrence_kernel<T, 1>, a, vec2 ? 2 : 1, s);
+    return launch_scan(recurrence_grad_kernel<T, VEC, kBackward>, a, VEC, kBackward, Flight<T, VEC, kBackward, 4>::kBytes,
+                       s);
+  return launch_scan(recurrence_kernel<T, VEC, kForward>, a, VEC, kForward, Flight<T, VEC, kForward, 2>::kBytes, s);
+}
+template <typename T>
+cudaError_t launch_typed(const RecurrenceArgs& a, int vec, cudaStream_t s) {
+  // Narrower tiles where wide ones would not give every SM a block.
+  if (vec == 4 && (a.channels + 127) / 128 * kMaxCluster < sm_count()) vec = 2;
+  return vec == 4 ? launch_vec<T, 4>(a, s) : vec == 2 ? launch_vec<T, 2>(a, s) : launch_vec<T, 1>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_recurrence(const RecurrenceArgs& a, cudaStream_t s) {
-  bool vec2 = a.channels % 2 == 0;
-  for (const Mat* m : {&a.z, &a.x, &a.h, &a.dh, &a.dz, &a.dx}) vec2 = vec2 && pairs(*m, a.dtype);
-  if (a.dtype == kF32) return launch_typed<float>(a, vec2, s);
-  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, vec2, s);
-  return launch_typed<__half>(a, vec2, s);
+  int vec = a.channels % 4 == 0 ? 4 : a.channels % 2 == 0 ? 2 : 1;
+  for (const Mat* m : {&a.z, &a.x, &a.h, &a.dh, &a.dz, &a.dx}) vec = std::min(vec, aligned_channels(*m, a.dtype));
+  if (a.dtype == kF32) return launch_typed<float>(a, vec, s);
+  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, vec, s);
+  return launch_typed<__half>(a, vec, s);
 }
 
 }  // namespace dion3
