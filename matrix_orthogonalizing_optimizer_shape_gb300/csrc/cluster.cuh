@@ -29,8 +29,11 @@ __device__ __forceinline__ void store(uint32_t at, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
 }
-__device__ __forceinline__ void store(uint32_t at, float2 v) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+// Counts its bytes on the mbarrier `bar` of the same block when they are there.
+__device__ __forceinline__ void store_async(uint32_t at, float2 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at), "f"(v.x),
+               "f"(v.y), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void store(uint32_t at, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");

@@ -54,6 +54,7 @@ struct RecurrenceArgs {
   const float* dlast;  // may be null
   float* dfirst;       // may be null
   bool grad;
+  unsigned* status;    // device status word
 };
 cudaError_t launch_recurrence(const RecurrenceArgs& a, cudaStream_t s);
 

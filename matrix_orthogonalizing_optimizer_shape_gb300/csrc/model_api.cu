@@ -253,6 +253,8 @@ dion3_status dion3_recurrence(int32_t tokens, int32_t channels, const dion3_matr
   a.sequences = sequences;
   a.first = first;
   a.last = last;
+  a.status = device_status_ptr();
+  if (a.status == nullptr) return fail(DION3_ERR_CUDA, "cannot resolve the device status word");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DION3_CUDA(traced_launch("recurrence", 0.0, 3.0 * tokens * channels * bytes_of(z->dtype), s,
                            [&] { return launch_recurrence(a, s); }),
@@ -302,6 +304,8 @@ dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const d
   a.dlast = dlast;
   a.dfirst = dfirst;
   a.grad = true;
+  a.status = device_status_ptr();
+  if (a.status == nullptr) return fail(DION3_ERR_CUDA, "cannot resolve the device status word");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DION3_CUDA(traced_launch("recurrence_backward", 0.0, 6.0 * tokens * channels * bytes_of(dh->dtype), s,
                            [&] { return launch_recurrence(a, s); }),

@@ -22,6 +22,7 @@
 #include "cluster.cuh"
 #include "layer_math.cuh"
 #include "model.h"
+#include "tc_ops.cuh"
 
 namespace dion3 {
 namespace {
@@ -240,34 +241,30 @@ struct Gate {
 };
 
 // --------------------------------------------------------------------------
-// Maps h -> A h + B.  Where A is above a half, F holds -(1 - A) with its sign bit
-// set, else A itself: a factor near 1 that were rounded would decay the state at a
-// rate that is off in every one of thousands of rows.  kCut: nothing passes.
+// Maps h -> A h + B, with D = 1 - A summed for itself: where A is above a half a
+// map is applied as h - D h + B, since a factor near 1 that were rounded would decay
+// the state at a rate that is off in every one of thousands of rows.  D = 2 cuts:
+// nothing passes.  Between blocks a map's factor is one number: A up to a half, else
+// -D with its sign bit set, or 2.
 // --------------------------------------------------------------------------
 constexpr float kCut = 2.f;
-__device__ __forceinline__ bool near_one(float F) { return static_cast<int>(__float_as_uint(F)) < 0; }
-__device__ __forceinline__ float through(float F, float B, float h) {
-  const float r = fmaf(F, h, B) + (near_one(F) ? h : 0.f);
+__device__ __forceinline__ float through(float A, float D, float B, float h) {
+  const bool near = D < 0.5f;
+  const float r = fmaf(near ? -D : A, h, B) + (near ? h : 0.f);
+  return D == kCut ? B : r;
+}
+__device__ __forceinline__ float encode(float A, float D) { return D == kCut ? kCut : D < 0.5f ? -D : A; }
+__device__ __forceinline__ float pass_block(float F, float B, float h) {
+  const float r = fmaf(F, h, B) + (static_cast<int>(__float_as_uint(F)) < 0 ? h : 0.f);
   return F == kCut ? B : r;
 }
-// The factor of F2 after F1: with both below 1 by D, D1 + D2 - D1 D2.
-__device__ __forceinline__ float after(float F2, float F1) {
-  if (F2 == kCut || F1 == kCut) return kCut;
-  const bool n1 = near_one(F1), n2 = near_one(F2);
-  const float r = fmaf(F2, F1, (n2 ? F1 : 0.f) + (n1 ? F2 : 0.f));
-  if (!(n1 && n2)) return r;
-  return r < -0.5f ? 1.f + r : -fabsf(r);
-}
-// A thread's map: its factor A, D = 1 - A summed for itself, and B.
+// A thread's map.
 template <int VEC>
 struct Map {
   Vec<VEC> A = all<VEC>(1.f), D = all<VEC>(0.f), B = all<VEC>(0.f);
   __device__ __forceinline__ void factor(const Gate<VEC>& g) {
     D = fma(g.na, A, D);
     A = mul(g.a, A);
-  }
-  __device__ __forceinline__ float2 channel(int j, bool cut) const {
-    return make_float2(cut ? kCut : D[j] < 0.5f ? -D[j] : A[j], B[j]);
   }
 };
 
@@ -353,59 +350,99 @@ struct Place {
 
 // --------------------------------------------------------------------------
 // The states before each warp's rows, from the maps of all and the state before
-// the cluster's rows.  One thread a channel keeps that state.
+// the cluster's rows.  One thread a channel keeps that state.  A block's map goes to
+// the others of the cluster by stores that complete on an mbarrier of theirs, so
+// that no fence waits for this block's own stores of rows.
 // --------------------------------------------------------------------------
 template <int VEC>
 struct Shared {
   static constexpr int kTile = 32 * VEC;
-  float2 warp[kWarps][kTile];                 // maps of the block's warps
-  float2 block[2][kMaxCluster][kTile];        // of the cluster's blocks, in turn in two halves
-  float enter[kWarps][kTile];                 // the states
+  float A[kWarps][kTile], D[kWarps][kTile], B[kWarps][kTile];  // maps of the block's warps
+  float2 block[2][kMaxCluster][kTile];                         // of the cluster's blocks, in turn in two halves
+  float enter[kWarps][kTile];                                  // the states
+  unsigned long long bar[2];                                   // of the halves
+  int stop;                                                    // a wait ran out
   int off[kSharedOffsets];
 };
 template <int VEC>
-__device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, int size, const Map<VEC>& m, bool cut,
-                                          float& carry) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, half = step & 1, t = threadIdx.x;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) sh.warp[warp][lane * VEC + j] = m.channel(j, cut);
-  __syncthreads();
-  float2 f[kWarps];
-  if (t < 32 * VEC) {
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) f[w] = sh.warp[w][t];
+__device__ __forceinline__ void put(float* p, const Vec<VEC>& v) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (VEC == 2)
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  else
+    *p = v[0];
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> get(const float* p) {
+  Vec<VEC> v;
+  if constexpr (VEC == 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  } else if constexpr (VEC == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    v[0] = f.x, v[1] = f.y;
+  } else {
+    v[0] = *p;
   }
-  float h = carry;
-  if (size > 1) {
-    if (t < 32 * VEC) {
-      float2 all = f[0];
+  return v;
+}
+// Before the first step, by all threads.
+template <int VEC>
+__device__ __forceinline__ void begin_steps(Shared<VEC>& sh, int size) {
+  if (threadIdx.x == 0) {
+    sh.stop = 0;
+    for (unsigned long long& b : sh.bar) tc::mbar_init(tc::smem_u32(&b), 1);
+    tc::mbar_init_fence();
+  }
+  __syncthreads();
+  if (size > 1) cl::arrive(), cl::wait();  // every block has begun before one writes to another
+}
+// After the last: no block leaves while another may write to it.
+__device__ __forceinline__ void end_steps(int size) {
+  __syncwarp();
+  if (size > 1) cl::arrive(), cl::wait();
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, int size, const Map<VEC>& m, bool cut,
+                                          float& carry, unsigned* status) {
+  constexpr int kTile = 32 * VEC;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, half = step & 1, t = threadIdx.x;
+  put<VEC>(&sh.A[warp][lane * VEC], cut ? all<VEC>(0.f) : m.A);
+  put<VEC>(&sh.D[warp][lane * VEC], cut ? all<VEC>(kCut) : m.D);
+  put<VEC>(&sh.B[warp][lane * VEC], m.B);
+  __syncthreads();
+  if (t < kTile) {  // whole warps
+    float h = carry;
+    if (size > 1) {
+      float A = sh.A[0][t], D = sh.D[0][t], B = sh.B[0][t];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) all = make_float2(after(f[w].x, all.x), through(f[w].x, f[w].y, all.y));
-      for (int r = 0; r < size; ++r) cl::store(cl::peer(&sh.block[half][rank][t], r), all);
-    }
-    cl::arrive();
-    cl::wait();
-    if (t < 32 * VEC) {
+      for (int w = 1; w < kWarps; ++w) {
+        const float a = sh.A[w][t], d = sh.D[w][t];
+        B = through(a, d, sh.B[w][t], B);
+        D = d == kCut ? kCut : fmaf(d, A, D);
+        A = d == kCut ? 0.f : A * a;  // whatever was before a cut, NaN too
+      }
+      const float2 mine = make_float2(encode(A, D), B);
+      if (t == 0) tc::mbar_expect(tc::smem_u32(&sh.bar[half]), size * kTile * sizeof(float2));
+      for (int r = 0; r < size; ++r)
+        cl::store_async(cl::peer(&sh.block[half][rank][t], r), mine, cl::peer(&sh.bar[half], r));
+      if (!tc::mbar_wait_warp(tc::smem_u32(&sh.bar[half]), (step >> 1) & 1, status)) sh.stop = 1;
       for (int r = 0; r < size; ++r) {
         if (r == rank) h = carry;
         const float2 b = sh.block[half][r][t];
-        carry = through(b.x, b.y, carry);
+        carry = pass_block(b.x, b.y, carry);
       }
     }
-  }
-  if (t < 32 * VEC) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       sh.enter[w][t] = h;
-      h = through(f[w].x, f[w].y, h);
+      if (w < kWarps - 1 || size == 1) h = through(sh.A[w][t], sh.D[w][t], sh.B[w][t], h);
     }
     if (size == 1) carry = h;
   }
   __syncthreads();
-  Vec<VEC> v;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) v[j] = sh.enter[warp][lane * VEC + j];
-  return v;
+  return get<VEC>(&sh.enter[warp][lane * VEC]);
 }
 
 template <typename T, int VEC, int R>
@@ -415,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
   __shared__ __align__(16) Shared<VEC> sh;
   const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
   const Span p = span_of(a, blockIdx.x / size, groups, sh.off);
-  if (size > 1) cl::arrive(), cl::wait();  // every block has begun before one writes to another
+  begin_steps<VEC>(sh, size);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = (blockIdx.y * 32 + lane) * VEC, cr = c < a.channels ? c : 0;
   const bool in = c < a.channels;
@@ -427,25 +464,33 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
   extern __shared__ __align__(16) char flight_mem[];
   using F = Flight<T, VEC, R, 2>;
   F in_flight(flight_mem);
-  auto load = [&](int step, long long row0) {
+  auto load = [&](int step, int row0) {
+    const int n = min(p.r1 - row0, R);
     const T *qz = pz + row0 * a.z.ld, *qx = px + row0 * a.x.ld;
+    if (n == R) {
 #pragma unroll
-    for (int i = 0; i < R; ++i, qz += a.z.ld, qx += a.x.ld) {
-      if (row0 + i >= p.r1) break;
-      in_flight.load(step, 0, i, qz);
-      in_flight.load(step, 1, i, qx);
+      for (int i = 0; i < R; ++i, qz += a.z.ld, qx += a.x.ld) {
+        in_flight.load(step, 0, i, qz);
+        in_flight.load(step, 1, i, qx);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i, qz += a.z.ld, qx += a.x.ld) {
+        if (i >= n) break;
+        in_flight.load(step, 0, i, qz);
+        in_flight.load(step, 1, i, qx);
+      }
     }
     in_flight.loaded();
   };
   float carry = 0.f;
   const int stride = size * kWarps * R;
-  long long base = p.r0 + (rank * kWarps + warp) * R;
+  int row0 = p.r0 + (rank * kWarps + warp) * R;
 #pragma unroll
-  for (int i = 0; i < F::kAhead; ++i) load(i, base + i * stride);
+  for (int i = 0; i < F::kAhead; ++i) load(i, row0 + i * stride);
   Place at;
   int step = 0;
-  for (long long top = p.r0; top < p.r1; top += stride, base += stride, ++step) {
-    const int row0 = static_cast<int>(min(base, static_cast<long long>(INT_MAX - R)));
+  for (int top = p.r0; top < p.r1; top += stride, row0 += stride, ++step) {
     in_flight.wait();
     Map<VEC> m;
     Vec<VEC> f[R];  // a and (1 - a) x of the rows
@@ -496,9 +541,10 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
         }
       }
     }
-    load(step + F::kAhead, base + F::kAhead * stride);
-    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry);
-    T* q = ph + row0 * a.h.ld;
+    load(step + F::kAhead, row0 + F::kAhead * stride);
+    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry, a.status);
+    if (sh.stop) break;
+    T* q = ph + static_cast<long long>(row0) * a.h.ld;
     if (whole) {
 #pragma unroll
       for (int i = 0; i < R; ++i, q += a.h.ld) {
@@ -518,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
       }
     }
   }
+  end_steps(size);
 }
 
 // --------------------------------------------------------------------------
@@ -532,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
   __shared__ __align__(16) Shared<VEC> sh;
   const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
   const Span p = span_of(a, blockIdx.x / size, groups, sh.off);
-  if (size > 1) cl::arrive(), cl::wait();
+  begin_steps<VEC>(sh, size);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int c = (blockIdx.y * 32 + lane) * VEC, cr = c < a.channels ? c : 0;
   const bool in = c < a.channels;
@@ -547,29 +594,40 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
   extern __shared__ __align__(16) char flight_mem[];
   using F = Flight<T, VEC, R, 4>;
   F in_flight(flight_mem);
-  auto load = [&](int step, long long row0) {  // of h the row before, where there is one
+  auto load = [&](int step, int row0) {  // of h the row before, where there is one
+    const int n = min(row0 - p.r0 + 1, R + 1);
     const T *qz = pz + row0 * a.z.ld, *qx = px + row0 * a.x.ld, *qh = ph + (row0 - 1) * a.h.ld, *qd = pd + row0 * a.dh.ld;
+    if (n > R) {
 #pragma unroll
-    for (int i = 0; i < R; ++i, qz -= a.z.ld, qx -= a.x.ld, qh -= a.h.ld, qd -= a.dh.ld) {
-      if (row0 - i < p.r0) break;
-      in_flight.load(step, 0, i, qz);
-      in_flight.load(step, 1, i, qx);
-      if (row0 - i > p.r0) in_flight.load(step, 2, i, qh);
-      in_flight.load(step, 3, i, qd);
+      for (int i = 0; i < R; ++i, qz -= a.z.ld, qx -= a.x.ld, qh -= a.h.ld, qd -= a.dh.ld) {
+        in_flight.load(step, 0, i, qz);
+        in_flight.load(step, 1, i, qx);
+        in_flight.load(step, 2, i, qh);
+        in_flight.load(step, 3, i, qd);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i, qz -= a.z.ld, qx -= a.x.ld, qh -= a.h.ld, qd -= a.dh.ld) {
+        if (i >= n) break;
+        in_flight.load(step, 0, i, qz);
+        in_flight.load(step, 1, i, qx);
+        if (i + 1 < n) in_flight.load(step, 2, i, qh);
+        in_flight.load(step, 3, i, qd);
+      }
     }
     in_flight.loaded();
   };
   float carry = 0.f;
   const int stride = size * kWarps * R;
-  long long base = static_cast<long long>(p.r1) - 1 - (rank * kWarps + warp) * R;
+  int base = p.r1 - 1 - (rank * kWarps + warp) * R;
 #pragma unroll
   for (int i = 0; i < F::kAhead; ++i) load(i, base - i * stride);
   Place at;
   int step = 0;
-  for (long long top = p.r1; top > p.r0; top -= stride, base -= stride, ++step) {
+  for (int top = p.r1; top > p.r0; top -= stride, base -= stride, ++step) {
     const bool any = base >= p.r0;
     in_flight.wait();
-    const int row0 = any ? static_cast<int>(base) : p.r0;
+    const int row0 = any ? base : p.r0;
     Map<VEC> m;
     Vec<VEC> ga[R], gn[R], dv[R], diff[R];  // a, 1 - a, dh and h_{t-1} - x of the rows
     unsigned begins = 0, ends = 0;
@@ -626,9 +684,10 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
       }
     }
     load(step + F::kAhead, base - F::kAhead * stride);
-    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry);
+    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry, a.status);
+    if (sh.stop) break;
     if (!any) continue;
-    T *qz = pdz + row0 * a.dz.ld, *qx = pdx + row0 * a.dx.ld;
+    T *qz = pdz + static_cast<long long>(row0) * a.dz.ld, *qx = pdx + static_cast<long long>(row0) * a.dx.ld;
 #pragma unroll
     for (int i = 0; i < R; ++i, qz -= a.dz.ld, qx -= a.dx.ld) {
       if (!whole && row0 - i < p.r0) break;
@@ -645,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
       }
     }
   }
+  end_steps(size);
 }
 
 // --------------------------------------------------------------------------
