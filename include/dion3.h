@@ -661,7 +661,7 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
  *              sequence (those before it where it has no rows), or NULL.  May be
  *              first.
  * z = -infinity forgets (h_t = x_t), z = +infinity keeps (h_t = h_{t-1}).
- * channels <= 2^20, sequences <= 2^27.  Offsets that do not ascend give undefined
+ * channels <= 2^19, sequences <= 2^27.  Offsets that do not ascend give undefined
  * values in the rows, but no access outside the matrices.
  */
 dion3_status dion3_recurrence(int32_t tokens, int32_t channels, const dion3_matrix* z,

@@ -12,7 +12,7 @@ namespace {
 
 constexpr int32_t kMaxGrouped = 1 << 27;    // tokens whose positions are grouped
 constexpr int32_t kMaxEmbedCols = 1 << 20;
-constexpr int32_t kMaxChannels = 1 << 20;
+constexpr int32_t kMaxChannels = 1 << 19;
 constexpr int32_t kMaxSequences = 1 << 27;
 constexpr int32_t kMaxLogRows = 1 << 21, kMaxVocab = 1 << 21;
 

@@ -3,13 +3,14 @@
 // once and written once, the scan happens in registers.
 //
 // A step h -> a h + b is an affine map, and maps compose: (A, B) after (A', B')
-// is (A A', A B' + B).  A block takes a tile of channels (a lane VEC of them) and
-// consecutive rows, R a warp: each thread composes its rows' maps in order; the
-// warps' maps are composed through shared memory by one thread a channel, and
-// those of a cluster's blocks, which take the rows after one another, through the
-// cluster's; then each thread runs through its rows again from the state before
-// them.  The cluster walks down the rows with the state, the next rows' loads in
-// flight.  Arithmetic is on pairs of channels (one instruction for two).
+// is (A A', A B' + B).  A block takes 16 channels, a sector of 16-bit memory, and
+// walks down the rows: each thread composes the maps of R rows of VEC channels, 16
+// lanes a channel compose those of the block's threads, and each thread runs through
+// its rows again from the state before them, the next rows' loads in flight.  Wider
+// tiles, whose rows the blocks of larger clusters have to share out, wait for one
+// another at every step: 120 us for 16384 x 4096 bf16 at 128 channels and clusters
+// of 8.  Clusters remain for few channels.  Arithmetic is on pairs of channels (one
+// instruction for two).
 //
 // Packed sequences: a map that begins a sequence cuts, so that rows are divided
 // evenly whatever the sequences' lengths; nothing of the rows before a cut, NaN
@@ -31,6 +32,8 @@ using namespace lm;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
+constexpr int kAcross = 16;                    // threads along a block's channels
+constexpr int kGroups = kThreads / kAcross;    // groups of rows
 constexpr int kSharedOffsets = 1024;
 
 // --------------------------------------------------------------------------
@@ -266,6 +269,14 @@ struct Map {
     D = fma(g.na, A, D);
     A = mul(g.a, A);
   }
+  // The product's factors are rounded numbers near 1, the same in row after row of a
+  // steady gate: taken from D, A is off by less than one of those roundings.
+  __device__ __forceinline__ Vec<VEC> kept() const {
+    Vec<VEC> r;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r[j] = D[j] < 0.875f ? 1.f - D[j] : A[j];
+    return r;
+  }
 };
 
 // --------------------------------------------------------------------------
@@ -331,8 +342,9 @@ __device__ __forceinline__ Span span_of(const RecurrenceArgs& a, int group, int 
 
 // to[i] = from[i] (0 without one) for the sequences without rows.
 template <int VEC>
-__device__ __forceinline__ void copy_empty(const Span& p, const float* from, float* to, int channels, int c, bool in) {
-  for (int q = p.s0 + static_cast<int>(threadIdx.x) / 32; q < p.s1; q += kWarps) {
+__device__ __forceinline__ void copy_empty(const Span& p, const float* from, float* to, int channels, int c, int group,
+                                           bool in) {
+  for (int q = p.s0 + group; q < p.s1; q += kGroups) {
     if (p.seq.off[q + 1] > p.seq.off[q] || !in) continue;
     const long long at = static_cast<long long>(q) * channels + c;
     store_state<VEC>(to + at, from != nullptr ? load_state<VEC>(from + at) : all<VEC>(0.f));
@@ -349,20 +361,24 @@ struct Place {
 };
 
 // --------------------------------------------------------------------------
-// The states before each warp's rows, from the maps of all and the state before
-// the cluster's rows.  One thread a channel keeps that state.  A block's map goes to
-// the others of the cluster by stores that complete on an mbarrier of theirs, so
-// that no fence waits for this block's own stores of rows.
+// The states before each thread's rows, from the maps of all and the state before
+// the cluster's rows, which kLanes neighbouring lanes a channel keep.  A block's map
+// goes to the others of the cluster by stores that complete on an mbarrier of theirs,
+// so that no fence waits for this block's own stores of rows.
 // --------------------------------------------------------------------------
 template <int VEC>
 struct Shared {
-  static constexpr int kTile = 32 * VEC;
-  float A[kWarps][kTile], D[kWarps][kTile], B[kWarps][kTile];  // maps of the block's warps
-  float2 block[2][kMaxCluster][kTile];                         // of the cluster's blocks, in turn in two halves
-  float enter[kWarps][kTile];                                  // the states
-  unsigned long long bar[2];                                   // of the halves
-  int stop;                                                    // a wait ran out
+  static constexpr int kTile = kAcross * VEC;        // channels of a block
+  static constexpr int kLanes = kThreads / kTile;    // that compose a channel's maps
+  static constexpr int kMaps = kGroups / kLanes;     // of each of them
+  float A[kGroups][kTile], D[kGroups][kTile], B[kGroups][kTile];  // the groups' maps, columns by at()
+  float enter[kGroups][kTile];                                    // the states
+  float2 block[2][kMaxCluster][kTile];                            // of the cluster's blocks, in turn in two halves
+  unsigned long long bar[2];                                      // of the halves
+  int stop;                                                       // a wait ran out
   int off[kSharedOffsets];
+  // A warp reads 32 / kLanes channels of kLanes groups at once: each from other banks.
+  static __device__ __forceinline__ int at(int group, int c) { return (c + group / kMaps * (32 / kLanes)) % kTile; }
 };
 template <int VEC>
 __device__ __forceinline__ void put(float* p, const Vec<VEC>& v) {
@@ -403,46 +419,69 @@ __device__ __forceinline__ void end_steps(int size) {
   __syncwarp();
   if (size > 1) cl::arrive(), cl::wait();
 }
+// (A, D, B) after (A1, D1, B1).
+__device__ __forceinline__ void compose(float& A, float& D, float& B, float A1, float D1, float B1) {
+  const bool cut = D == kCut;
+  B = through(A, D, B, B1);
+  D = cut ? kCut : fmaf(D, A1, D1);
+  A = cut ? 0.f : A * A1;  // whatever was before a cut, NaN too
+}
 template <int VEC>
 __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, int size, const Map<VEC>& m, bool cut,
                                           float& carry, unsigned* status) {
-  constexpr int kTile = 32 * VEC;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, half = step & 1, t = threadIdx.x;
-  put<VEC>(&sh.A[warp][lane * VEC], cut ? all<VEC>(0.f) : m.A);
-  put<VEC>(&sh.D[warp][lane * VEC], cut ? all<VEC>(kCut) : m.D);
-  put<VEC>(&sh.B[warp][lane * VEC], m.B);
+  using S = Shared<VEC>;
+  constexpr int kTile = S::kTile, kLanes = S::kLanes;
+  const int group = threadIdx.x / kAcross, own = S::at(group, threadIdx.x % kAcross * VEC), half = step & 1;
+  put<VEC>(&sh.A[group][own], cut ? all<VEC>(0.f) : m.kept());
+  put<VEC>(&sh.D[group][own], cut ? all<VEC>(kCut) : m.D);
+  put<VEC>(&sh.B[group][own], m.B);
   __syncthreads();
-  if (t < kTile) {  // whole warps
-    float h = carry;
-    if (size > 1) {
-      float A = sh.A[0][t], D = sh.D[0][t], B = sh.B[0][t];
+  const int c = threadIdx.x / kLanes, k = threadIdx.x % kLanes;
+  float a[S::kMaps], d[S::kMaps], b[S::kMaps];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float a = sh.A[w][t], d = sh.D[w][t];
-        B = through(a, d, sh.B[w][t], B);
-        D = d == kCut ? kCut : fmaf(d, A, D);
-        A = d == kCut ? 0.f : A * a;  // whatever was before a cut, NaN too
-      }
-      const float2 mine = make_float2(encode(A, D), B);
-      if (t == 0) tc::mbar_expect(tc::smem_u32(&sh.bar[half]), size * kTile * sizeof(float2));
-      for (int r = 0; r < size; ++r)
-        cl::store_async(cl::peer(&sh.block[half][rank][t], r), mine, cl::peer(&sh.bar[half], r));
-      if (!tc::mbar_wait_warp(tc::smem_u32(&sh.bar[half]), (step >> 1) & 1, status)) sh.stop = 1;
-      for (int r = 0; r < size; ++r) {
-        if (r == rank) h = carry;
-        const float2 b = sh.block[half][r][t];
-        carry = pass_block(b.x, b.y, carry);
-      }
-    }
+  for (int i = 0; i < S::kMaps; ++i) {
+    const int w = k * S::kMaps + i;
+    a[i] = sh.A[w][S::at(w, c)], d[i] = sh.D[w][S::at(w, c)], b[i] = sh.B[w][S::at(w, c)];
+  }
+  float A = a[0], D = d[0], B = b[0];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      sh.enter[w][t] = h;
-      if (w < kWarps - 1 || size == 1) h = through(sh.A[w][t], sh.D[w][t], sh.B[w][t], h);
+  for (int i = 1; i < S::kMaps; ++i) {
+    float A2 = a[i], D2 = d[i], B2 = b[i];
+    compose(A2, D2, B2, A, D, B);
+    A = A2, D = D2, B = B2;
+  }
+#pragma unroll
+  for (int n = 1; n < kLanes; n *= 2) {  // of the channel's lanes up to this one
+    const float A1 = __shfl_up_sync(0xffffffffu, A, n, kLanes), D1 = __shfl_up_sync(0xffffffffu, D, n, kLanes),
+                B1 = __shfl_up_sync(0xffffffffu, B, n, kLanes);
+    if (k >= n) compose(A, D, B, A1, D1, B1);
+  }
+  const float F = encode(A, D);
+  const float allF = __shfl_sync(0xffffffffu, F, kLanes - 1, kLanes);
+  const float allB = __shfl_sync(0xffffffffu, B, kLanes - 1, kLanes);
+  const float F1 = __shfl_up_sync(0xffffffffu, F, 1, kLanes), B1 = __shfl_up_sync(0xffffffffu, B, 1, kLanes);
+  float h = carry;
+  if (size > 1) {
+    if (threadIdx.x == 0) tc::mbar_expect(tc::smem_u32(&sh.bar[half]), size * kTile * sizeof(float2));
+    for (int r = k; r < size; r += kLanes)
+      cl::store_async(cl::peer(&sh.block[half][rank][c], r), make_float2(allF, allB), cl::peer(&sh.bar[half], r));
+    if (!tc::mbar_wait_warp(tc::smem_u32(&sh.bar[half]), (step >> 1) & 1, status)) sh.stop = 1;
+    for (int r = 0; r < size; ++r) {
+      if (r == rank) h = carry;
+      const float2 f = sh.block[half][r][c];
+      carry = pass_block(f.x, f.y, carry);
     }
-    if (size == 1) carry = h;
+  } else {
+    carry = pass_block(allF, allB, carry);
+  }
+  if (k > 0) h = pass_block(F1, B1, h);
+#pragma unroll
+  for (int i = 0; i < S::kMaps; ++i) {
+    sh.enter[k * S::kMaps + i][S::at(k * S::kMaps + i, c)] = h;
+    if (i + 1 < S::kMaps) h = through(a[i], d[i], b[i], h);
   }
   __syncthreads();
-  return get<VEC>(&sh.enter[warp][lane * VEC]);
+  return get<VEC>(&sh.enter[group][own]);
 }
 
 template <typename T, int VEC, int R>
@@ -453,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
   const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
   const Span p = span_of(a, blockIdx.x / size, groups, sh.off);
   begin_steps<VEC>(sh, size);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int c = (blockIdx.y * 32 + lane) * VEC, cr = c < a.channels ? c : 0;
+  const int group = threadIdx.x / kAcross;
+  const int c = (blockIdx.y * kAcross + threadIdx.x % kAcross) * VEC, cr = c < a.channels ? c : 0;
   const bool in = c < a.channels;
-  if (a.last != nullptr && rank == 0) copy_empty<VEC>(p, a.first, a.last, a.channels, c, in);
+  if (a.last != nullptr && rank == 0) copy_empty<VEC>(p, a.first, a.last, a.channels, c, group, in);
 
   const T* pz = static_cast<const T*>(a.z.p) + cr;
   const T* px = static_cast<const T*>(a.x.p) + cr;
@@ -484,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
     in_flight.loaded();
   };
   float carry = 0.f;
-  const int stride = size * kWarps * R;
-  int row0 = p.r0 + (rank * kWarps + warp) * R;
+  const int stride = size * kGroups * R;
+  int row0 = p.r0 + (rank * kGroups + group) * R;
 #pragma unroll
   for (int i = 0; i < F::kAhead; ++i) load(i, row0 + i * stride);
   Place at;
@@ -502,6 +541,9 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
       at.find(p.seq, row0);
       q0 = at.q;
       whole = row0 + R <= p.r1 && row0 != at.begin && (a.last == nullptr ? row0 + R <= at.end : row0 + R < at.end);
+    }
+    whole = __all_sync(0xffffffffu, whole);
+    if (row0 < p.r1) {
       if (whole) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -580,10 +622,10 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
   const int size = cl::size(), rank = cl::rank(), groups = gridDim.x / size;
   const Span p = span_of(a, blockIdx.x / size, groups, sh.off);
   begin_steps<VEC>(sh, size);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int c = (blockIdx.y * 32 + lane) * VEC, cr = c < a.channels ? c : 0;
+  const int group = threadIdx.x / kAcross;
+  const int c = (blockIdx.y * kAcross + threadIdx.x % kAcross) * VEC, cr = c < a.channels ? c : 0;
   const bool in = c < a.channels;
-  if (a.dfirst != nullptr && rank == 0) copy_empty<VEC>(p, a.dlast, a.dfirst, a.channels, c, in);
+  if (a.dfirst != nullptr && rank == 0) copy_empty<VEC>(p, a.dlast, a.dfirst, a.channels, c, group, in);
 
   const T* pz = static_cast<const T*>(a.z.p) + cr;
   const T* px = static_cast<const T*>(a.x.p) + cr;
@@ -618,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
     in_flight.loaded();
   };
   float carry = 0.f;
-  const int stride = size * kWarps * R;
-  int base = p.r1 - 1 - (rank * kWarps + warp) * R;
+  const int stride = size * kGroups * R;
+  int base = p.r1 - 1 - (rank * kGroups + group) * R;
 #pragma unroll
   for (int i = 0; i < F::kAhead; ++i) load(i, base - i * stride);
   Place at;
@@ -637,6 +679,9 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
       at.find(p.seq, row0);
       q0 = at.q;
       whole = row0 - R >= p.r0 && row0 + 1 != at.end && row0 - R >= at.begin;
+    }
+    whole = __all_sync(0xffffffffu, whole);
+    if (any) {
       if (whole) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -720,15 +765,15 @@ int aligned_channels(const Mat& m, int dtype) {
 }
 
 template <class K>
-cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, int rows, size_t shared, cudaStream_t s) {
+cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, int rows, size_t shared, cudaStream_t s) {  // rows of a block's step
   if (shared > 0) {  // with the static part past what a kernel has without asking
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
     if (e != cudaSuccess) return e;
   }
-  const int tiles = (a.channels + 32 * vec - 1) / (32 * vec);
+  const int tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
   const int want = 2 * sm_count();  // blocks
   int size = 1;
-  while (size < kMaxCluster && 2 * size * tiles <= want && size * kWarps * rows < a.tokens) size *= 2;
+  while (size < kMaxCluster && 2 * size * tiles <= want && size * rows < a.tokens) size *= 2;
   const int groups = std::max(1, std::min({a.sequences, want / (tiles * size), 65535 / kMaxCluster}));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size * groups, tiles);
@@ -750,14 +795,12 @@ cudaError_t launch_vec(const RecurrenceArgs& a, cudaStream_t s) {
   // Rows of a warp: what fits in registers with the next ones' loads.
   constexpr int kForward = sizeof(T) * VEC > 8 ? 4 : 8, kBackward = sizeof(T) * VEC > 8 ? 2 : 4;
   if (a.grad)
-    return launch_scan(recurrence_grad_kernel<T, VEC, kBackward>, a, VEC, kBackward, Flight<T, VEC, kBackward, 4>::kBytes,
-                       s);
-  return launch_scan(recurrence_kernel<T, VEC, kForward>, a, VEC, kForward, Flight<T, VEC, kForward, 2>::kBytes, s);
+    return launch_scan(recurrence_grad_kernel<T, VEC, kBackward>, a, VEC, kGroups * kBackward,
+                       Flight<T, VEC, kBackward, 4>::kBytes, s);
+  return launch_scan(recurrence_kernel<T, VEC, kForward>, a, VEC, kGroups * kForward, Flight<T, VEC, kForward, 2>::kBytes, s);
 }
 template <typename T>
 cudaError_t launch_typed(const RecurrenceArgs& a, int vec, cudaStream_t s) {
-  // Narrower tiles where wide ones would not give every SM a block.
-  if (vec == 4 && (a.channels + 127) / 128 * kMaxCluster < sm_count()) vec = 2;
   return vec == 4 ? launch_vec<T, 4>(a, s) : vec == 2 ? launch_vec<T, 2>(a, s) : launch_vec<T, 1>(a, s);
 }
 
