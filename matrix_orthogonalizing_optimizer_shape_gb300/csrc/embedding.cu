@@ -22,6 +22,45 @@ __device__ __forceinline__ long long id_at(const Ids& ids, long long i) {
   return ids.bytes == 8 ? static_cast<const long long*>(ids.p)[i] : static_cast<const int*>(ids.p)[i];
 }
 
+// VEC elements as they lie in memory: loads of several are in flight before the
+// first is unpacked (unpacking each behind its own condition made them wait for one
+// another, 72 us instead of 25 for the sums of 16384 x 4096).
+template <typename T, int VEC>
+struct Raw {
+  static constexpr int kPieces = VEC == 8 ? static_cast<int>(sizeof(T)) / 2 : 1;
+  std::conditional_t<VEC == 8, uint4, T> w[kPieces];
+  __device__ __forceinline__ void load(const T* p, bool in = true) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if constexpr (VEC == 8)
+        w[i] = in ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
+      else
+        w[i] = in ? *p : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[VEC]) const {
+    if constexpr (VEC == 1) {
+      v[0] = to_f32<T>(w[0]);
+    } else {
+      constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            v[4 * i + j] = __uint_as_float(x[j]);
+          } else {
+            const float2 f = unpack2<kBf>(x[j]);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+          }
+        }
+      }
+    }
+  }
+};
+
 // --------------------------------------------------------------------------
 // Lookup.  blockDim = (lanes along a row, rows); a thread keeps its columns and
 // walks kWalk rows, all their loads issued before the first is used.  VEC = 8
@@ -38,24 +77,20 @@ __global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a) {
   const long long step = static_cast<long long>(gridDim.y) * blockDim.y;
   for (long long t = static_cast<long long>(blockIdx.y) * blockDim.y + threadIdx.y; t < a.tokens; t += kWalk * step) {
     long long id[kWalk];
-    float v[kWalk][VEC];
+    Raw<W, VEC> raw[kWalk];
 #pragma unroll
     for (int i = 0; i < kWalk; ++i) id[i] = t + i * step < a.tokens ? id_at(a.ids, t + i * step) : -1;
 #pragma unroll
-    for (int i = 0; i < kWalk; ++i) {
-      if (id[i] >= 0 && id[i] < a.vocab) {
-        load_vec<W, VEC>(static_cast<const W*>(a.table.p) + id[i] * a.table.ld + c, v[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
-      }
-    }
+    for (int i = 0; i < kWalk; ++i)
+      raw[i].load(static_cast<const W*>(a.table.p) + id[i] * a.table.ld + c, id[i] >= 0 && id[i] < a.vocab);
 #pragma unroll
     for (int i = 0; i < kWalk; ++i) {
       if (t + i * step >= a.tokens) break;
+      float v[VEC];
+      raw[i].values(v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] *= a.scale;
-      store_vec<T, VEC>(static_cast<T*>(a.y.p) + (t + i * step) * a.y.ld + c, v[i]);
+      for (int j = 0; j < VEC; ++j) v[j] *= a.scale;
+      store_vec<T, VEC>(static_cast<T*>(a.y.p) + (t + i * step) * a.y.ld + c, v);
     }
   }
 }
@@ -66,12 +101,17 @@ __global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a) {
 // different blocks.  Every block reads all ids (from L2: 64 kB at 16384 tokens),
 // counts its own by token and warp, and lays their positions out behind those of
 // the blocks before it, which it counts on the way.  A warp takes a contiguous
-// part of the positions in order, so a token's positions end up ascending.
-// Rows of tokens that do not occur are zeroed here too.
+// part of the positions in order, so a token's positions end up ascending; it
+// keeps those of its block in shared memory, and reads the ids again only where
+// they are too many.  Rows of tokens that do not occur are zeroed here too.
 // --------------------------------------------------------------------------
 constexpr int kGroupWarps = 16, kGroupThreads = 32 * kGroupWarps;
 constexpr int kMaxLocals = 512;  // tokens of a block: counters in 34 kB of shared memory
 constexpr int kMinGroups = 256;
+
+constexpr int kIdsAhead = 8;     // ids a lane has in flight
+constexpr int kListed = 64;      // of a warp's own positions kept from the first walk
+constexpr int kZeros = 4096;     // bytes of shared zeros, which bulk copies lay into rows
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
@@ -79,34 +119,46 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
   pdl_trigger();
   pdl_wait();
   extern __shared__ int cnt[];  // [kGroupWarps][locals], then [locals] totals
+  __shared__ __align__(128) uint4 zeros[kZeros / 16];
+  __shared__ int2 listed[kGroupWarps][kListed];  // position, token
   __shared__ int before_s, wsum[kGroupWarps];
   int* total = cnt + kGroupWarps * locals;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int mine = blockIdx.x, mask = (1 << log_groups) - 1;
   for (int i = threadIdx.x; i < kGroupWarps * locals; i += kGroupThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < kZeros / 16; i += kGroupThreads) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (threadIdx.x == 0) before_s = 0;
   __syncthreads();
 
-  const int slice = ((a.tokens + kGroupWarps - 1) / kGroupWarps + 127) / 128 * 128;
+  constexpr int kStep = 32 * kIdsAhead;
+  const int slice = ((a.tokens + kGroupWarps - 1) / kGroupWarps + kStep - 1) / kStep * kStep;
   const long long lo = static_cast<long long>(warp) * slice, hi = min(lo + slice, static_cast<long long>(a.tokens));
   int* own = cnt + warp * locals;
-  int before = 0;
-  auto load = [&](long long i0, int (&id)[4]) {
+  auto load = [&](long long i0, int (&id)[kIdsAhead]) {
+    long long v[kIdsAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const long long i = i0 + 32 * u + lane, v = i < hi ? id_at(a.ids, i) : -1;
-      id[u] = v >= 0 && v < a.vocab ? static_cast<int>(v) : -1;
-    }
+    for (int u = 0; u < kIdsAhead; ++u) v[u] = i0 + 32 * u + lane < hi ? id_at(a.ids, i0 + 32 * u + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < kIdsAhead; ++u) id[u] = v[u] >= 0 && v[u] < a.vocab ? static_cast<int>(v[u]) : -1;
   };
-  for (long long i0 = lo; i0 < hi; i0 += 128) {
-    int id[4];
+  int before = 0, found = 0;
+  for (long long i0 = lo; i0 < hi; i0 += kStep) {
+    int id[kIdsAhead];
     load(i0, id);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (id[u] < 0) continue;
+    for (int u = 0; u < kIdsAhead; ++u) {
       const int g = id[u] & mask;
-      before += g < mine;
-      if (g == mine) atomicAdd(own + (id[u] >> log_groups), 1);
+      before += id[u] >= 0 && g < mine;
+      const bool hit = id[u] >= 0 && g == mine;
+      const unsigned hits = __ballot_sync(0xffffffffu, hit);
+      if (hits == 0u) continue;
+      if (hit) {
+        atomicAdd(own + (id[u] >> log_groups), 1);
+        const int at = found + __popc(hits & ((1u << lane) - 1u));
+        if (at < kListed) listed[warp][at] = make_int2(static_cast<int>(i0) + 32 * u + lane, id[u]);
+      }
+      found += __popc(hits);
     }
   }
   before = warp_sum(before);
@@ -138,38 +190,62 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
   if (threadIdx.x == kGroupThreads - 1 && mine == mask) *a.count = base + sum;
   __syncthreads();
 
-  for (long long i0 = lo; i0 < hi; i0 += 128) {
-    int id[4];
-    load(i0, id);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool hit = id[u] >= 0 && (id[u] & mask) == mine;
-      const unsigned hits = __ballot_sync(0xffffffffu, hit);
-      if (hits == 0u) continue;
-      if (hit) {
-        const int local = id[u] >> log_groups;
-        const unsigned same = __match_any_sync(hits, local);
-        const int at = own[local] + __popc(same & ((1u << lane) - 1u));
-        a.order[at] = static_cast<int>(i0) + 32 * u + lane;
-        a.token[at] = id[u];
-        __syncwarp(hits);
-        if ((same >> lane) == 1u) own[local] = at + 1;  // the last of them
-      }
-      __syncwarp();
-    }
-  }
-  if (a.accumulate) return;
+  // Rows of tokens that do not occur, written while the positions are laid out.
   const int es = a.table_dtype == kF32 ? 4 : 2;
   const long long bytes = static_cast<long long>(a.cols) * es, pitch = a.dtable.ld * es;
   uint8_t* out = static_cast<uint8_t*>(a.dtable.p);
   const bool pieces = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(bytes) | static_cast<uintptr_t>(pitch)) & 15u) == 0;
+  if (!a.accumulate && pieces) {
+    const uint32_t from = static_cast<uint32_t>(__cvta_generic_to_shared(zeros));
+    for (int l = threadIdx.x; l < locals; l += kGroupThreads) {
+      const long long row = (static_cast<long long>(l) << log_groups) + mine;
+      if (row >= a.vocab || total[l] != 0) continue;
+      for (long long i = 0; i < bytes; i += kZeros)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out + row * pitch + i), "r"(from),
+                     "r"(static_cast<int>(min(bytes - i, static_cast<long long>(kZeros))))
+                     : "memory");
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+
+  auto lay = [&](bool hit, int position, int id) {
+    const unsigned hits = __ballot_sync(0xffffffffu, hit);
+    if (hits == 0u) return;
+    if (hit) {
+      const int local = id >> log_groups;
+      const unsigned same = __match_any_sync(hits, local);
+      const int at = own[local] + __popc(same & ((1u << lane) - 1u));
+      a.order[at] = position;
+      a.token[at] = id;
+      __syncwarp(hits);
+      if ((same >> lane) == 1u) own[local] = at + 1;  // the last of them
+    }
+    __syncwarp();
+  };
+  if (found <= kListed) {
+    for (int i = 0; i < found; i += 32) {
+      const int2 e = i + lane < found ? listed[warp][i + lane] : make_int2(0, 0);
+      lay(i + lane < found, e.x, e.y);
+    }
+  } else {
+    for (long long i0 = lo; i0 < hi; i0 += kStep) {
+      int id[kIdsAhead];
+      load(i0, id);
+#pragma unroll
+      for (int u = 0; u < kIdsAhead; ++u)
+        lay(id[u] >= 0 && (id[u] & mask) == mine, static_cast<int>(i0) + 32 * u + lane, id[u]);
+    }
+  }
+  if (a.accumulate) return;
+  if (pieces) {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    return;
+  }
   for (int l = warp; l < locals; l += kGroupWarps) {
     const long long row = (static_cast<long long>(l) << log_groups) + mine;
     if (row >= a.vocab || total[l] != 0) continue;
     uint8_t* p = out + row * pitch;
-    if (pieces) {
-      for (long long i = 16 * lane; i < bytes; i += 512) *reinterpret_cast<uint4*>(p + i) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (es == 4) {
+    if (es == 4) {
       for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint32_t*>(p)[i] = 0u;
     } else {
       for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0u;
@@ -229,15 +305,16 @@ __global__ void __launch_bounds__(256) window_kernel(EmbedGradArgs a, int window
   float sum[VEC] = {};
   const int len = s1 - s0;
   for (int i0 = 0; i0 < len; i0 += kBatch) {
-    float v[kBatch][VEC];
+    Raw<T, VEC> raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (i0 + i < len) load_vec<T, VEC>(dy + static_cast<long long>(pos[i0 + i]) * a.dy.ld, v[i]);
+    for (int i = 0; i < kBatch; ++i) raw[i].load(dy + static_cast<long long>(pos[min(i0 + i, len - 1)]) * a.dy.ld);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (i0 + i >= len) break;
+      float v[VEC];
+      raw[i].values(v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sum[j] += v[i][j];
+      for (int j = 0; j < VEC; ++j) sum[j] += v[j];
       const int t = tok[i0 + i + 1];
       const bool last = i0 + i == len - 1, goes_on = t == tok[i0 + i + 2];
       if (goes_on && !last) continue;
@@ -253,15 +330,15 @@ __global__ void __launch_bounds__(256) window_kernel(EmbedGradArgs a, int window
 }
 
 // A run that begins in window w and reaches over its end: its sums in slot 1 of w
-// and slot 0 of the windows after it, added by 8 rows of threads that take every
-// eighth and then in order.
-constexpr int kJoinRows = 8;
+// and slot 0 of the windows after it, added by rows of threads that take every
+// fourth and then in order.
+constexpr int kJoinLanes = 64, kJoinRows = 4;
 
 template <int VEC>
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(EmbedGradArgs a, int window) {
+__global__ void __launch_bounds__(kJoinLanes * kJoinRows) join_kernel(EmbedGradArgs a, int window) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float red[kJoinRows][32][VEC + 1];
+  __shared__ float red[kJoinRows][kJoinLanes][VEC + 1];
   const int n = *a.count;
   const int s0 = blockIdx.x * window, s1 = s0 + window;
   if (s1 >= n) return;
@@ -270,15 +347,16 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(EmbedGradArgs a, i
   const int windows = (n + window - 1) / window;
   int more = 0;  // windows after this one that the run reaches
   for (;;) {
-    const int w = blockIdx.x + 1 + more + threadIdx.y * 32 + threadIdx.x;
+    const int w = blockIdx.x + 1 + more + threadIdx.y * kJoinLanes + threadIdx.x;
     const int got = __syncthreads_count(w < windows && a.token[min(w, windows - 1) * window] == t);
     more += got;
-    if (got < 32 * kJoinRows) break;
+    if (got < kJoinLanes * kJoinRows) break;
   }
-  const int c = (blockIdx.y * 32 + threadIdx.x) * VEC;
+  const int c = (blockIdx.y * kJoinLanes + threadIdx.x) * VEC;
   const bool in = c < a.cols;
   float sum[VEC] = {};
   if (in) {
+#pragma unroll 4
     for (int i = threadIdx.y; i <= more; i += kJoinRows) {
       float v[VEC];
       load_vec<float, VEC>(a.partials + (2ll * (static_cast<int>(blockIdx.x) + i) + (i == 0)) * a.cols + c, v);
@@ -332,10 +410,10 @@ cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s) {
   });
 }
 
-// Windows enough for every SM, sums of several rows each: 32 positions at 16384.
+// Windows enough for every SM, sums of several rows each: 64 positions at 16384.
 int embed_window(int tokens) {
   int w = 8;
-  while (w < kMaxWindow && w < (tokens + 511) / 512) w *= 2;
+  while (w < kMaxWindow && w < (tokens + 255) / 256) w *= 2;
   return w;
 }
 
@@ -357,8 +435,8 @@ cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s) {
                          dim3(windows, ceil_div(pieces, threads)), dim3(threads), 0, s, a, window);
   });
   if (e != cudaSuccess || windows == 1) return e;
-  return launch_kernel(pdl_enabled(), vec ? join_kernel<8> : join_kernel<1>, dim3(windows, ceil_div(pieces, 32)),
-                       dim3(32, kJoinRows), 0, s, a, window);
+  return launch_kernel(pdl_enabled(), vec ? join_kernel<8> : join_kernel<1>, dim3(windows, ceil_div(pieces, kJoinLanes)),
+                       dim3(kJoinLanes, kJoinRows), 0, s, a, window);
 }
 
 }  // namespace dion3

@@ -21,9 +21,9 @@ namespace {
 
 using namespace lm;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kChunk = 32768;  // bytes of a chunk that is read
-constexpr int kSquareBlocks = 3, kScaleBlocks = 2;  // of an SM
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kChunk = 16384;  // bytes of a chunk that is read
+constexpr int kSquareBlocks = 6, kScaleBlocks = 5;  // of an SM
 constexpr int kBatch = 4;      // pieces of 16 bytes a thread has in flight: a chunk in one go
 
 template <typename T>
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* parti
   if (threadIdx.x == 0) *norm = v;
 }
 
-template <typename T, typename O>
+// Scales a chunk, BATCH pieces of a thread in flight.
+template <typename T, typename O, int BATCH>
 __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
   const T* p = static_cast<const T*>(c.t->in) + c.row * c.t->ld_in + c.at;
   O* q = static_cast<O*>(c.t->out) + c.row * c.t->ld_out + c.at;
@@ -185,70 +186,153 @@ __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
   const int pieces = (c.n - head) / kPer<T>, tail = c.n - head - pieces * kPer<T>;
   const uint4* body = reinterpret_cast<const uint4*>(p + head);
   O* to = q + head;
-  uint4 u[kBatch];
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    const int i = threadIdx.x + b * kThreads;
-    if (i < pieces) u[b] = body[i];
-  }
   if (threadIdx.x < head + tail) {
     const int at = threadIdx.x < head ? threadIdx.x : head + pieces * kPer<T> + threadIdx.x - head;
     q[at] = from_f32<O>(to_f32<T>(p[at]) * coef);
   }
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < pieces; i0 += BATCH * kThreads) {
+    uint4 u[BATCH];
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    const int i = threadIdx.x + b * kThreads;
-    if (i >= pieces) break;
-    float f[kPer<T>];
-    piece_values<T>(u[b], f);
-    uint32_t w[kBytes / 4];
-    constexpr bool kBf = std::is_same<O, __nv_bfloat16>::value;
+    for (int b = 0; b < BATCH; ++b)
+      if (i0 + b * kThreads < pieces) u[b] = body[i0 + b * kThreads];
 #pragma unroll
-    for (int j = 0; j < kBytes / 4; ++j) {
-      if constexpr (sizeof(O) == 4)
-        w[j] = __float_as_uint(f[j] * coef);
-      else
-        w[j] = pack2<kBf>(f[2 * j] * coef, f[2 * j + 1] * coef);
-    }
-    O* at = to + i * kPer<T>;
-    if constexpr (kBytes == 8) {
-      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-    } else {
+    for (int b = 0; b < BATCH; ++b) {
+      const int i = i0 + b * kThreads;
+      if (i >= pieces) break;
+      uint4* at = reinterpret_cast<uint4*>(to + i * kPer<T>);
+      float f[kPer<T>];
+      piece_values<T>(u[b], f);
 #pragma unroll
-      for (int j = 0; j < kBytes / 16; ++j)
-        reinterpret_cast<uint4*>(at)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      for (int j = 0; j < kPer<T>; ++j) f[j] *= coef;
+      constexpr bool kBf = std::is_same<O, __nv_bfloat16>::value;
+      if constexpr (kBytes == 8) {
+        *reinterpret_cast<uint2*>(at) = make_uint2(pack2<kBf>(f[0], f[1]), pack2<kBf>(f[2], f[3]));
+      } else if constexpr (sizeof(O) == 4) {
+#pragma unroll
+        for (int j = 0; j < kPer<T> / 4; ++j)
+          at[j] = make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
+                             __float_as_uint(f[4 * j + 3]));
+      } else {
+        *at = make_uint4(pack2<kBf>(f[0], f[1]), pack2<kBf>(f[2], f[3]), pack2<kBf>(f[4], f[5]), pack2<kBf>(f[6], f[7]));
+      }
     }
   }
 }
 
-// out = min(1, max_norm / (norm + 1e-6)) in.  In place a factor of 1 leaves everything as it is.
-template <int N>
-__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(const __grid_constant__ Table<N> tab, int count,
-                                                                unsigned chunks, const double* partials, int n,
-                                                                float max_norm, bool in_place, float* norm) {
-  pdl_trigger();
-  pdl_wait();
+// The factor from the partials, the same bits in every block and thread.
+__device__ __forceinline__ float factor_of(const double* partials, int n, float max_norm, float* norm) {
   __shared__ double red[kWarps];
-  __shared__ float coef_s;
+  __shared__ float coef;
   const float total = norm_of(partials, n, red);
   if (threadIdx.x == 0) {
     const float r = max_norm / (total + 1e-6f);
-    coef_s = r > 1.f ? 1.f : r;  // NaN stays NaN
+    coef = r > 1.f ? 1.f : r;  // NaN stays NaN
     if (norm != nullptr && blockIdx.x == 0) *norm = total;
   }
   __syncthreads();
-  const float coef = coef_s;
+  return coef;
+}
+
+// Clipping, out = min(1, max_norm / (norm + 1e-6)) in; in place a factor of 1 leaves
+// everything as it is.  Chunks run from the last to the first.  Tensors whose rows are
+// aligned pieces that keep their type go through this kernel, the next chunk's loads in
+// flight while one is scaled; the others through the one below (both in one kernel
+// needed more registers than its blocks have: 1.05 ms for the 1B-shaped set).
+template <typename T>
+__device__ __forceinline__ uint4 scaled(const uint4& u, float coef) {
+  float f[kPer<T>];
+  piece_values<T>(u, f);
+#pragma unroll
+  for (int j = 0; j < kPer<T>; ++j) f[j] *= coef;
+  if constexpr (sizeof(T) == 4) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  } else {
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    return make_uint4(pack2<kBf>(f[0], f[1]), pack2<kBf>(f[2], f[3]), pack2<kBf>(f[4], f[5]), pack2<kBf>(f[6], f[7]));
+  }
+}
+struct Pieces {
+  const char* in;
+  char* out;
+  int bytes, dtype;
+  __device__ __forceinline__ explicit Pieces(const Chunk& c) : dtype(c.t->dtype) {
+    const int es = dtype == kF32 ? 4 : 2;
+    in = static_cast<const char*>(c.t->in) + (c.row * c.t->ld_in + c.at) * es;
+    out = static_cast<char*>(c.t->out) + (c.row * c.t->ld_out + c.at) * es;
+    bytes = c.n * es;
+  }
+  __device__ __forceinline__ void load(uint4 (&u)[kBatch]) const {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int at = 16 * (threadIdx.x + b * kThreads);
+      u[b] = at + 16 <= bytes ? *reinterpret_cast<const uint4*>(in + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(const uint4 (&u)[kBatch], float coef) const {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int at = 16 * (threadIdx.x + b * kThreads);
+      if (at + 16 <= bytes) *reinterpret_cast<uint4*>(out + at) = scaled<T>(u[b], coef);
+    }
+    const int tail = bytes / 16 * 16 + static_cast<int>(threadIdx.x * sizeof(T));
+    if (tail < bytes)
+      *reinterpret_cast<T*>(out + tail) = from_f32<T>(to_f32<T>(*reinterpret_cast<const T*>(in + tail)) * coef);
+  }
+};
+template <int N>
+__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(const __grid_constant__ Table<N> tab,
+                                                                           int count, unsigned chunks,
+                                                                           const double* partials, int n, float max_norm,
+                                                                           bool in_place, float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  const float coef = factor_of(partials, n, max_norm, norm);
+  if (in_place && coef == 1.f) return;
+  unsigned i = blockIdx.x;
+  Pieces p(chunk_of(tab, count, chunks - 1 - i));
+  uint4 u[kBatch];
+  p.load(u);
+  for (;;) {
+    i += gridDim.x;
+    const bool more = i < chunks;
+    Pieces next = p;
+    uint4 v[kBatch];
+    if (more) {
+      next = Pieces(chunk_of(tab, count, chunks - 1 - i));
+      next.load(v);
+    }
+    if (p.dtype == kF32)
+      p.store<float>(u, coef);
+    else if (p.dtype == kBF16)
+      p.store<__nv_bfloat16>(u, coef);
+    else
+      p.store<__half>(u, coef);
+    if (!more) return;
+    p = next;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) u[b] = v[b];
+  }
+}
+template <int N>
+__global__ void __launch_bounds__(kThreads, 2) grad_scale_other_kernel(const __grid_constant__ Table<N> tab, int count,
+                                                                    unsigned chunks, const double* partials, int n,
+                                                                    float max_norm, bool in_place, float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  const float coef = factor_of(partials, n, max_norm, norm);
   if (in_place && coef == 1.f) return;
   for (unsigned i = blockIdx.x; i < chunks; i += gridDim.x) {
     const Chunk c = chunk_of(tab, count, chunks - 1 - i);
     auto from = [&](auto* p) {
       using T = std::remove_pointer_t<decltype(p)>;
       if (c.t->out_dtype == kF32)
-        scale_chunk<T, float>(c, coef);
+        scale_chunk<T, float, 4>(c, coef);
       else if (c.t->out_dtype == kBF16)
-        scale_chunk<T, __nv_bfloat16>(c, coef);
+        scale_chunk<T, __nv_bfloat16, 4>(c, coef);
       else
-        scale_chunk<T, __half>(c, coef);
+        scale_chunk<T, __half, 4>(c, coef);
     };
     if (c.t->dtype == kF32)
       from(static_cast<float*>(nullptr));
@@ -258,14 +342,20 @@ __global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(cons
       from(static_cast<__half*>(nullptr));
   }
 }
+// Whether a tensor goes through the first of the two.
+bool keeps_pieces(const GradTensor& t) {
+  const int es = t.dtype == kF32 ? 4 : 2;
+  return t.dtype == t.out_dtype && ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0 &&
+         (t.rows == 1 || (t.ld_in * es % 16 == 0 && t.ld_out * es % 16 == 0));
+}
 
-// Calls f(table, tensors, chunks) for groups of tensors that fit a launch's
+// Calls f(table, tensors, chunks) for groups of the wanted tensors that fit a launch's
 // parameters: 16 (a kilobyte) or kMany.
 constexpr int kFew = 16, kMany = 448;
 static_assert(sizeof(Table<kMany>) < 32000, "kernel parameters");
 
-template <class F>
-cudaError_t for_groups(const GradTensor* t, int n, F&& f) {
+template <class P, class F>
+cudaError_t for_groups(const GradTensor* t, int n, P&& wanted, F&& f) {
   int i = 0;
   while (i < n) {
     // The tensors of a group have fewer than 2^31 chunks together.
@@ -275,7 +365,7 @@ cudaError_t for_groups(const GradTensor* t, int n, F&& f) {
     for (; i < n && k < kMany; ++i) {
       const long long len = kChunk / (t[i].dtype == kF32 ? 4 : 2), per = (t[i].cols + len - 1) / len;
       const unsigned long long all = static_cast<unsigned long long>(per) * t[i].rows;
-      if (all == 0) continue;
+      if (all == 0 || !wanted(t[i])) continue;
       if (chunks + all >= (1ull << 31)) {
         if (k == 0) return cudaErrorInvalidValue;
         break;
@@ -308,7 +398,7 @@ int blocks_for(unsigned chunks, int per_sm) {
 cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_norm, bool in_place, float* norm,
                              double* partials, cudaStream_t s) {
   int kept = 0;
-  cudaError_t e = for_groups(t, n, [&](const auto& tab, int count, unsigned chunks) {
+  cudaError_t e = for_groups(t, n, [](const GradTensor&) { return true; }, [&](const auto& tab, int count, unsigned chunks) {
     constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
     const int blocks = blocks_for(chunks, kSquareBlocks);
     const cudaError_t r = launch_kernel(pdl_enabled(), grad_squares_kernel<N>, dim3(blocks), dim3(kThreads), 0, s, tab,
@@ -321,14 +411,20 @@ cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_no
     return norm == nullptr ? cudaSuccess
                            : launch_kernel(pdl_enabled(), grad_norm_kernel, dim3(1), dim3(kThreads), 0, s,
                                            static_cast<const double*>(partials), kept, norm);
-  bool first = true;
-  return for_groups(t, n, [&](const auto& tab, int count, unsigned chunks) {
-    constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
-    float* to = first ? norm : nullptr;
-    first = false;
-    return launch_kernel(pdl_enabled(), grad_scale_kernel<N>, dim3(blocks_for(chunks, kScaleBlocks)), dim3(kThreads), 0, s, tab,
-                         count, chunks, static_cast<const double*>(partials), kept, max_norm, in_place, to);
-  });
+  for (bool pieces : {true, false}) {
+    e = for_groups(t, n, [&](const GradTensor& g) { return keeps_pieces(g) == pieces; },
+                   [&](const auto& tab, int count, unsigned chunks) {
+                     constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
+                     const cudaError_t r = launch_kernel(
+                         pdl_enabled(), pieces ? grad_scale_kernel<N> : grad_scale_other_kernel<N>,
+                         dim3(blocks_for(chunks, kScaleBlocks)), dim3(kThreads), 0, s, tab, count, chunks,
+                         static_cast<const double*>(partials), kept, max_norm, in_place, norm);
+                     norm = nullptr;  // written by the first launch
+                     return r;
+                   });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace dion3
