@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256) embedding_kernel(EmbedArgs a) {
 // the blocks before it, which it counts on the way.  A warp takes a contiguous
 // part of the positions in order, so a token's positions end up ascending; it
 // keeps those of its block in shared memory, and reads the ids again only where
-// they are too many.  Rows of tokens that do not occur are zeroed here too.
+// they are too many.
 // --------------------------------------------------------------------------
 constexpr int kGroupWarps = 16, kGroupThreads = 32 * kGroupWarps;
 constexpr int kMaxLocals = 512;  // tokens of a block: counters in 34 kB of shared memory
@@ -111,23 +111,18 @@ constexpr int kMinGroups = 256;
 
 constexpr int kIdsAhead = 8;     // ids a lane has in flight
 constexpr int kListed = 64;      // of a warp's own positions kept from the first walk
-constexpr int kZeros = 4096;     // bytes of shared zeros, which bulk copies lay into rows
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, int log_groups, int locals) {
   pdl_trigger();
   pdl_wait();
-  extern __shared__ int cnt[];  // [kGroupWarps][locals], then [locals] totals
-  __shared__ __align__(128) uint4 zeros[kZeros / 16];
+  extern __shared__ int cnt[];  // [kGroupWarps][locals]
   __shared__ int2 listed[kGroupWarps][kListed];  // position, token
   __shared__ int before_s, wsum[kGroupWarps];
-  int* total = cnt + kGroupWarps * locals;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int mine = blockIdx.x, mask = (1 << log_groups) - 1;
   for (int i = threadIdx.x; i < kGroupWarps * locals; i += kGroupThreads) cnt[i] = 0;
-  for (int i = threadIdx.x; i < kZeros / 16; i += kGroupThreads) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (threadIdx.x == 0) before_s = 0;
   __syncthreads();
 
@@ -173,7 +168,6 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
       cnt[w * locals + threadIdx.x] = sum;
       sum += n;
     }
-    total[threadIdx.x] = sum;
   }
   int incl = sum;
 #pragma unroll
@@ -190,23 +184,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
   if (threadIdx.x == kGroupThreads - 1 && mine == mask) *a.count = base + sum;
   __syncthreads();
 
-  // Rows of tokens that do not occur, written while the positions are laid out.
-  const int es = a.table_dtype == kF32 ? 4 : 2;
-  const long long bytes = static_cast<long long>(a.cols) * es, pitch = a.dtable.ld * es;
-  uint8_t* out = static_cast<uint8_t*>(a.dtable.p);
-  const bool pieces = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(bytes) | static_cast<uintptr_t>(pitch)) & 15u) == 0;
-  if (!a.accumulate && pieces) {
-    const uint32_t from = static_cast<uint32_t>(__cvta_generic_to_shared(zeros));
-    for (int l = threadIdx.x; l < locals; l += kGroupThreads) {
-      const long long row = (static_cast<long long>(l) << log_groups) + mine;
-      if (row >= a.vocab || total[l] != 0) continue;
-      for (long long i = 0; i < bytes; i += kZeros)
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out + row * pitch + i), "r"(from),
-                     "r"(static_cast<int>(min(bytes - i, static_cast<long long>(kZeros))))
-                     : "memory");
-    }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
+  if (threadIdx.x < locals && !a.accumulate) a.occurs[static_cast<long long>(mine) * locals + threadIdx.x] = sum != 0;
 
   auto lay = [&](bool hit, int position, int id) {
     const unsigned hits = __ballot_sync(0xffffffffu, hit);
@@ -236,31 +214,81 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
         lay(id[u] >= 0 && (id[u] & mask) == mine, static_cast<int>(i0) + 32 * u + lane, id[u]);
     }
   }
-  if (a.accumulate) return;
-  if (pieces) {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    return;
-  }
-  for (int l = warp; l < locals; l += kGroupWarps) {
-    const long long row = (static_cast<long long>(l) << log_groups) + mine;
-    if (row >= a.vocab || total[l] != 0) continue;
-    uint8_t* p = out + row * pitch;
-    if (es == 4) {
-      for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint32_t*>(p)[i] = 0u;
-    } else {
-      for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0u;
-    }
-  }
 }
 
 // --------------------------------------------------------------------------
 // Sums.  A window is `window` grouped positions; a block takes one window of one
 // strip of columns, walks its rows kBatch at a time with all their loads in
-// flight, and writes a token's row when its run ends.  A run that reaches over
+// flight, and writes a token's row when its run ends.  Each warp also writes
+// zeros to its share of the rows of tokens that do not occur, some at every batch: the
+// memory takes no more than 6.4 TB/s of writes alone, and reads wait behind as many as
+// are sent ahead of them (all at once: 400 us instead of 210; in a launch of their own
+// before the sums: 260).  A run that reaches over
 // the window's first or last position leaves its sum in fp32 instead: slot 0 of
 // the window if it began before, else slot 1.
 // --------------------------------------------------------------------------
-constexpr int kBatch = 8, kMaxWindow = 512;
+constexpr int kMaxWindow = 512;
+constexpr int kZeros = 8192;    // bytes of shared zeros
+constexpr int kZerosAhead = 4;  // rows of a warp being written
+
+// A warp's share of the rows of tokens that do not occur, written by bulk copies of
+// shared zeros, some at a time.
+struct ZeroRows {
+  const EmbedGradArgs& a;
+  int log_groups, locals, lane;
+  long long r0, hi;   // the rows whose bits are in todo begin at r0; all end at hi
+  unsigned todo = 0;
+  long long bytes, pitch;
+  uint8_t* out;
+  uint32_t from;
+  bool pieces;
+  __device__ __forceinline__ ZeroRows(const EmbedGradArgs& args, int log_g, int l, const uint4* zeros)
+      : a(args), log_groups(log_g), locals(l), lane(threadIdx.x % 32) {
+    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
+    const long long warp = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
+    hi = a.accumulate ? 0 : a.vocab * (warp + 1) / warps;
+    r0 = (a.accumulate ? 0 : a.vocab * warp / warps) - 32;
+    const int es = a.table_dtype == kF32 ? 4 : 2;
+    bytes = static_cast<long long>(a.cols) * es, pitch = a.dtable.ld * es;
+    out = static_cast<uint8_t*>(a.dtable.p);
+    from = static_cast<uint32_t>(__cvta_generic_to_shared(zeros));
+    pieces = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(bytes) | static_cast<uintptr_t>(pitch)) & 15u) == 0;
+  }
+  // Up to `most` rows; false: none is left.
+  __device__ __forceinline__ bool some(int most) {
+    while (most > 0) {
+      while (todo == 0u) {
+        r0 += 32;
+        if (r0 >= hi) return false;
+        const long long row = r0 + lane, slot = (row & ((1 << log_groups) - 1)) * locals + (row >> log_groups);
+        todo = __ballot_sync(0xffffffffu, row < hi && a.occurs[row < hi ? slot : 0] == 0);
+      }
+      uint8_t* p = out + (r0 + __ffs(todo) - 1) * pitch;
+      todo &= todo - 1;
+      --most;
+      if (pieces) {
+        if (lane == 0) {
+          for (long long i = 0; i < bytes; i += kZeros)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p + i), "r"(from),
+                         "r"(static_cast<int>(min(bytes - i, static_cast<long long>(kZeros))))
+                         : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group %0;" ::"n"(kZerosAhead - 1) : "memory");
+        }
+      } else if (a.table_dtype == kF32) {
+        for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint32_t*>(p)[i] = 0u;
+      } else {
+        for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0u;
+      }
+    }
+    return true;
+  }
+  __device__ __forceinline__ void finish() {
+    while (some(kZerosAhead)) {
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+};
 
 template <int VEC>
 __device__ __forceinline__ void put_row(const EmbedGradArgs& a, int token, int c, const float (&sum)[VEC]) {
@@ -287,29 +315,38 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs& a, int token, int c
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) window_kernel(EmbedGradArgs a, int window) {
+constexpr int kBatch = VEC == 8 && sizeof(T) == 4 ? 4 : 8;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(VEC == 8 ? 128 : 256, VEC == 8 ? 7 : 4) window_kernel(EmbedGradArgs a, int window, int strips, int log_groups,
+                                                                                   int locals) {
   pdl_trigger();
   pdl_wait();
+  __shared__ __align__(128) uint4 zeros[kZeros / 16];
   __shared__ int pos[kMaxWindow], tok[kMaxWindow + 2];
-  const int n = *a.count, s0 = blockIdx.x * window, s1 = min(s0 + window, n);
-  if (s0 >= n) return;
-  for (int i = threadIdx.x; i < s1 - s0; i += blockDim.x) pos[i] = a.order[s0 + i];
-  for (int i = static_cast<int>(threadIdx.x) - 1; i <= s1 - s0; i += blockDim.x)
+  const int index = static_cast<int>(blockIdx.x) / strips, strip = static_cast<int>(blockIdx.x) % strips;
+  const int n = *a.count, s0 = min(index * window, n), s1 = min(s0 + window, n), len = s1 - s0;
+  for (int i = threadIdx.x; i < kZeros / 16; i += blockDim.x) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  for (int i = threadIdx.x; i < len; i += blockDim.x) pos[i] = a.order[s0 + i];
+  for (int i = static_cast<int>(threadIdx.x) - 1; i <= len; i += blockDim.x)
     tok[i + 1] = s0 + i >= 0 && s0 + i < n ? a.token[s0 + i] : -1;
   __syncthreads();
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-  if (c >= a.cols) return;
-  const T* dy = static_cast<const T*>(a.dy.p) + c;
-  float* part = a.partials + 2ll * blockIdx.x * a.cols + c;
+  ZeroRows zero(a, log_groups, locals, zeros);
+  const int each = static_cast<int>(min((zero.hi - zero.r0 - 32) * kBatch<T, VEC> / window + 1, 1ll << 20));  // at a batch
+  const int c = (strip * blockDim.x + threadIdx.x) * VEC;
+  const bool in = c < a.cols;
+  const T* dy = static_cast<const T*>(a.dy.p) + (in ? c : 0);
+  float* part = a.partials + 2ll * index * a.cols + c;
   bool began_before = tok[0] == tok[1];
   float sum[VEC] = {};
-  const int len = s1 - s0;
-  for (int i0 = 0; i0 < len; i0 += kBatch) {
-    Raw<T, VEC> raw[kBatch];
+  for (int i0 = 0; i0 < len; i0 += kBatch<T, VEC>) {
+    Raw<T, VEC> raw[kBatch<T, VEC>];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) raw[i].load(dy + static_cast<long long>(pos[min(i0 + i, len - 1)]) * a.dy.ld);
+    for (int i = 0; i < kBatch<T, VEC>; ++i) raw[i].load(dy + static_cast<long long>(pos[min(i0 + i, len - 1)]) * a.dy.ld);
+    zero.some(each);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kBatch<T, VEC>; ++i) {
       if (i0 + i >= len) break;
       float v[VEC];
       raw[i].values(v);
@@ -318,15 +355,18 @@ __global__ void __launch_bounds__(256) window_kernel(EmbedGradArgs a, int window
       const int t = tok[i0 + i + 1];
       const bool last = i0 + i == len - 1, goes_on = t == tok[i0 + i + 2];
       if (goes_on && !last) continue;
-      if (!goes_on && !began_before)
-        put_row<VEC>(a, t, c, sum);
-      else
-        store_vec<float, VEC>(part + (began_before ? 0 : a.cols), sum);
+      if (in) {
+        if (!goes_on && !began_before)
+          put_row<VEC>(a, t, c, sum);
+        else
+          store_vec<float, VEC>(part + (began_before ? 0 : a.cols), sum);
+      }
       began_before = false;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) sum[j] = 0.f;
     }
   }
+  zero.finish();
 }
 
 // A run that begins in window w and reaches over its end: its sums in slot 1 of w
@@ -417,22 +457,33 @@ int embed_window(int tokens) {
   return w;
 }
 
-cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s) {
-  int log_groups = 8;
+static int log_groups_of(int vocab) {
+  int n = 8;
   static_assert(kMinGroups == 1 << 8, "256 blocks");
-  while (ceil_div(a.vocab, 1ll << log_groups) > kMaxLocals) ++log_groups;
-  const int locals = ceil_div(a.vocab, 1ll << log_groups);
+  while (ceil_div(vocab, 1ll << n) > kMaxLocals) ++n;
+  return n;
+}
+int embed_slots(int vocab) {
+  const int n = log_groups_of(vocab);
+  return ceil_div(vocab, 1ll << n) << n;
+}
+
+cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s) {
+  const int log_groups = log_groups_of(a.vocab), locals = ceil_div(a.vocab, 1ll << log_groups);
   cudaError_t e = launch_kernel(pdl_enabled(), group_kernel, dim3(1u << log_groups), dim3(kGroupThreads),
-                                (kGroupWarps + 1) * locals * sizeof(int), s, a, log_groups, locals);
+                                kGroupWarps * locals * sizeof(int), s, a, log_groups, locals);
   if (e != cudaSuccess) return e;
   const bool vec = pieces_of(a.dy, a.dtype, a.cols) && pieces_of(a.dtable, a.table_dtype, a.cols);
   const int window = embed_window(a.tokens), windows = ceil_div(a.tokens, window);
   const int pieces = vec ? a.cols / 8 : a.cols;
   const int threads = vec ? 128 : 256;
+  // Enough blocks for the zeros of a large vocabulary, too.
+  const int strips = ceil_div(pieces, threads);
+  const int blocks = a.accumulate ? windows * strips : std::max(windows * strips, 4 * sm_count());
   e = with_type(a.dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_kernel(pdl_enabled(), vec ? window_kernel<T, 8> : window_kernel<T, 1>,
-                         dim3(windows, ceil_div(pieces, threads)), dim3(threads), 0, s, a, window);
+    return launch_kernel(pdl_enabled(), vec ? window_kernel<T, 8> : window_kernel<T, 1>, dim3(blocks), dim3(threads),
+                         0, s, a, window, strips, log_groups, locals);
   });
   if (e != cudaSuccess || windows == 1) return e;
   return launch_kernel(pdl_enabled(), vec ? join_kernel<8> : join_kernel<1>, dim3(windows, ceil_div(pieces, kJoinLanes)),

@@ -36,8 +36,10 @@ struct EmbedGradArgs {
   int* order;       // [tokens] positions, grouped by token
   int* token;       // [tokens] their tokens
   int* count;       // [1] positions that have a token
+  uint8_t* occurs;  // [embed_slots(vocab)] whether a token does, by its group
   float* partials;  // [2 windows][cols]
 };
+int embed_slots(int vocab);
 cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
