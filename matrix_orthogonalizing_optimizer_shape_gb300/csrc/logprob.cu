@@ -26,6 +26,7 @@ using namespace lm;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBatch = 4;  // pieces of 16 bytes that a thread has in flight
 constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster <= kWarps, "a warp a block");
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = -1e30f;  // of a masked logit: its exponential is 0, and 0 times it too
 
@@ -169,6 +170,21 @@ __device__ __forceinline__ void insert(Key key, int k, Key& list) {
   }
 }
 
+// The lists of a block's warps, written and waited for, into one in warp 0: by halves.
+template <typename K>
+__device__ __forceinline__ K merge_warps(K (&lists)[kWarps][32], K mine) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int n = kWarps / 2; n > 0; n /= 2) {
+    if (warp < n) {
+      mine = merge_lists(mine, lists[warp + n][31 - lane]);
+      lists[warp][lane] = mine;
+    }
+    __syncthreads();
+  }
+  return mine;
+}
+
 struct Shared {
   Stat warp[kWarps];
   float4 block[kMaxCluster];          // of the cluster's blocks, in block 0
@@ -177,7 +193,7 @@ struct Shared {
   int ncand;
   short cand[kThreads];
   Key list[kWarps][32];
-  Key lists[kMaxCluster][32];         // of the cluster's blocks, in block 0
+  Key lists[kWarps][32];              // of the cluster's blocks, in block 0; others empty
 };
 
 // The block's k largest elements of its slice, in warp 0's lanes.
@@ -189,12 +205,8 @@ __device__ __forceinline__ Key block_top(Shared& sh, const Slice<T>& sl, int c0,
   sh.order[warp][lane] = sort_lanes(order);
   if (tid == 0) sh.ncand = 0;
   __syncthreads();
-  if (warp == 0) {
-    uint32_t top = sh.order[0][lane];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = merge_lists(top, sh.order[w][31 - lane]);
-    if (lane == k - 1) sh.least = max(top, 1u);
-  }
+  const uint32_t top = merge_warps(sh.order, sh.order[warp][lane]);
+  if (warp == 0 && lane == k - 1) sh.least = max(top, 1u);
   __syncthreads();
   const uint32_t least = sh.least;
   if (any && order >= least) sh.cand[atomicAdd(&sh.ncand, 1)] = static_cast<short>(tid);
@@ -227,11 +239,7 @@ __device__ __forceinline__ Key block_top(Shared& sh, const Slice<T>& sl, int c0,
   }
   sh.list[warp][lane] = list;
   __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) list = merge_lists(list, sh.list[w][31 - lane]);
-  }
-  return list;
+  return merge_warps(sh.list, list);
 }
 
 template <typename T, bool TOP>
@@ -241,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprob_kernel(LogProbA
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int size = cl::size(), rank = cl::rank();
+  if constexpr (TOP) sh.lists[warp][lane] = 0;
+  __syncwarp();
   if (size > 1) cl::arrive();  // waited for before the first store to another block
   const long long row = blockIdx.x / size;
   const T* p = static_cast<const T*>(a.logits.p) + row * a.logits.ld;
@@ -296,15 +306,16 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprob_kernel(LogProbA
     __syncwarp();
     cl::arrive();
     cl::wait();
-    if (rank != 0 || warp != 0) return;
+    if (rank != 0) return;
+    if constexpr (TOP) {
+      list = warp < size ? sh.lists[warp][lane] : 0;  // a warp a block
+      list = merge_warps(sh.lists, list);
+    }
+    if (warp != 0) return;
     st = Stat{};
     if (lane < size) st.m = sh.block[lane].x, st.s = sh.block[lane].y, st.q = sh.block[lane].z;
 #pragma unroll
     for (int d = kMaxCluster / 2; d > 0; d /= 2) st.join(st.shuffled(d), c);
-    if constexpr (TOP) {
-      list = sh.lists[0][lane];
-      for (int r = 1; r < size; ++r) list = merge_lists(list, sh.lists[r][31 - lane]);
-    }
   }
   if (warp != 0) return;
   // Lane 0 has them all.  A row without a logit above -infinity has no distribution.

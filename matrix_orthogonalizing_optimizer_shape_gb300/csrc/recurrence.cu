@@ -17,6 +17,7 @@
 // included, passes it.  Where the channels are few, groups of whole sequences go
 // to different clusters.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -764,11 +765,19 @@ int aligned_channels(const Mat& m, int dtype) {
   return 1;
 }
 
-template <class K>
-cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, int rows, size_t shared, cudaStream_t s) {  // rows of a block's step
-  if (shared > 0) {  // with the static part past what a kernel has without asking
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+template <auto kernel>
+cudaError_t launch_scan(const RecurrenceArgs& a, int vec, int rows, size_t shared, cudaStream_t s) {  // rows of a block's step
+  if (shared > 0) {  // with the static part past what a kernel has without asking; once a device
+    static std::atomic<unsigned long long> asked{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (bit == 0 || !(asked.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+      if (e != cudaSuccess) return e;
+      asked.fetch_or(bit, std::memory_order_release);
+    }
   }
   const int tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
   const int want = 2 * sm_count();  // blocks
@@ -792,12 +801,15 @@ cudaError_t launch_scan(K kernel, const RecurrenceArgs& a, int vec, int rows, si
 
 template <typename T, int VEC>
 cudaError_t launch_vec(const RecurrenceArgs& a, cudaStream_t s) {
-  // Rows of a warp: what fits in registers with the next ones' loads.
-  constexpr int kForward = sizeof(T) * VEC > 8 ? 4 : 8, kBackward = sizeof(T) * VEC > 8 ? 2 : 4;
+  // Rows of a thread: 32 (forward) and 16 elements of each matrix fill the registers,
+  // half of them where the next rows' wait there too, or where fp32 cells of 4 would
+  // not leave two blocks the shared memory.
+  constexpr int kElements = sizeof(T) * VEC > 8 || sizeof(T) * VEC < 4 ? 16 : 32;
+  constexpr int kForward = kElements / VEC, kBackward = kForward / 2;
   if (a.grad)
-    return launch_scan(recurrence_grad_kernel<T, VEC, kBackward>, a, VEC, kGroups * kBackward,
+    return launch_scan<recurrence_grad_kernel<T, VEC, kBackward>>(a, VEC, kGroups * kBackward,
                        Flight<T, VEC, kBackward, 4>::kBytes, s);
-  return launch_scan(recurrence_kernel<T, VEC, kForward>, a, VEC, kGroups * kForward, Flight<T, VEC, kForward, 2>::kBytes, s);
+  return launch_scan<recurrence_kernel<T, VEC, kForward>>(a, VEC, kGroups * kForward, Flight<T, VEC, kForward, 2>::kBytes, s);
 }
 template <typename T>
 cudaError_t launch_typed(const RecurrenceArgs& a, int vec, cudaStream_t s) {

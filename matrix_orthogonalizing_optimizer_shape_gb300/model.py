@@ -17,6 +17,7 @@ current one) and returns without waiting::
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from typing import Optional, Sequence
 
@@ -191,21 +192,52 @@ def grad_norm_workspace_size() -> int:
     return out.value
 
 
+_device_of, _dense, _numel, _address, _type = (
+    *map(operator.methodcaller, ("get_device", "is_contiguous", "numel", "data_ptr")), operator.attrgetter("dtype"))
+_shape = operator.attrgetter("shape")
+_packers: dict = {}
+
+
+def _pack_tensors(fields: list) -> bytes:
+    """dion3_tensor of each five fields."""
+    n = len(fields) // 5
+    s = _packers.get(n)
+    if s is None:
+        s = _packers[n] = struct.Struct("@" + _TENSOR * n)
+    return s.pack(*fields)
+
+
+def _dense_tensors(ts: Sequence, dev: int, sizes: Optional[list] = None) -> Optional[bytes]:
+    """dion3_tensor of each if all are dense, of known types and on device `dev`."""
+    n = len(ts)
+    if dev < 0 or not all(map(_dense, ts)) or [dev] * n != [*map(_device_of, ts)]:
+        return None
+    try:
+        fields = [1] * (5 * n)
+        fields[4::5] = map(_l._DTYPES.__getitem__, map(_type, ts))
+    except KeyError:
+        return None
+    fields[0::5] = map(_address, ts)
+    fields[2::5] = fields[3::5] = [*map(_numel, ts)] if sizes is None else sizes
+    return _pack_tensors(fields)
+
+
 def _tensors(name: str, ts: Sequence, dev: int) -> bytes:
     """dion3_tensor of each: dense tensors of any shape, or matrices with contiguous rows."""
+    packed = _dense_tensors(ts, dev)
+    if packed is not None:
+        return packed
     fields = []
-    dtypes = _l._DTYPES
     for t in ts:
-        if t.get_device() != dev or dev < 0 or t.dtype not in dtypes:
+        if t.get_device() != dev or dev < 0:
             _l._on(name, t, dev)
-            _l._dtype(t)
         if t.is_contiguous():
             n = t.numel()
-            fields += t.data_ptr(), 1, n, n, dtypes[t.dtype]
+            fields += t.data_ptr(), 1, n, n, _l._dtype(t)
         else:
             p, ld, dtype = _mat(name, t, None, None, dev)
             fields += p, t.shape[0], t.shape[1], ld, dtype
-    return struct.pack("@" + _TENSOR * len(ts), *fields)
+    return _pack_tensors(fields)
 
 
 def _norm(t, dev: int) -> Optional[int]:
@@ -237,16 +269,17 @@ def clip_grad_norm(tensors: Sequence, max_norm: float, norm=None, *, out: Option
     dev = tensors[0].get_device() if len(tensors) else _l._device() if norm is None else norm.get_device()
     if out is not None and len(out) != len(tensors):
         raise ValueError(f"out has {len(out)} tensors, {len(tensors)} are wanted")
-    a, b = _tensors("tensors", tensors, dev), None
-    if out is not None:
-        for t, o in zip(tensors, out):
-            if t.shape != o.shape:
-                raise ValueError(f"out: a tensor of {tuple(o.shape)}, {tuple(t.shape)} is wanted")
-        if any(not (t.is_contiguous() and o.is_contiguous()) for t, o in zip(tensors, out)):
+    if out is None:
+        a, b = _tensors("tensors", tensors, dev), None
+    else:
+        if [*map(_shape, tensors)] != [*map(_shape, out)]:
+            t, o = next((t, o) for t, o in zip(tensors, out) if t.shape != o.shape)
+            raise ValueError(f"out: a tensor of {tuple(o.shape)}, {tuple(t.shape)} is wanted")
+        sizes = [*map(_numel, tensors)]
+        a, b = _dense_tensors(tensors, dev, sizes), _dense_tensors(out, dev, sizes)
+        if a is None or b is None:
             # The same rows on both sides: dense ones as rows too where the other has a pitch.
-            a, b = (_rows("tensors", tensors, out, dev), _rows("out", out, tensors, dev))
-        else:
-            b = _tensors("out", out, dev)
+            a, b = _rows("tensors", tensors, out, dev), _rows("out", out, tensors, dev)
     w, n = _ws(ws, ws_bytes, dev)
     _d3._check(_l._fn("dion3_clip_grad_norm")(a, b, len(tensors), max_norm, _norm(norm, dev), w, n,
                                               _stream(stream, dev)))
@@ -260,5 +293,5 @@ def _rows(name: str, ts: Sequence, others: Sequence, dev: int) -> bytes:
             fields.append(_tensors(name, (t,), dev))
         else:
             p, ld, dtype = _mat(name, t, None, None, dev)
-            fields.append(struct.pack("@" + _TENSOR, p, t.shape[0], t.shape[1], ld, dtype))
+            fields.append(_pack_tensors([p, t.shape[0], t.shape[1], ld, dtype]))
     return b"".join(fields)
