@@ -22,6 +22,7 @@
 #include <mutex>
 
 #include "layer_math.cuh"
+#include "model.h"
 #include "tc_ops.cuh"
 
 namespace dion3 {
@@ -1138,6 +1139,21 @@ cudaError_t run_product(const Product& g, const Epilogue& e, unsigned* status, c
 }
 
 }  // namespace
+
+bool plain_box_map(CUtensorMap* map, const Mat& m, int rows, int cols, int dtype, int box_rows, int box_cols) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int bytes = dtype == kF32 ? 4 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.ld) * bytes};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUtensorMapDataType dt = dtype == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(map, dt, 2, m.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_product(const Product& g, unsigned* status, cudaStream_t s) {
   Epilogue e{};

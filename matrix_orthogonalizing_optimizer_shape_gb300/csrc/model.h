@@ -2,6 +2,8 @@
 // log probabilities, gradient norm).  Nothing here crosses the C ABI.
 #pragma once
 
+#include <cuda.h>
+
 #include "layer.h"
 
 namespace dion3 {
@@ -59,6 +61,9 @@ struct RecurrenceArgs {
   unsigned* status;    // device status word
 };
 cudaError_t launch_recurrence(const RecurrenceArgs& a, cudaStream_t s);
+// Boxes of box_rows x box_cols of a matrix [rows][cols] whose base and pitch are
+// multiples of 16 bytes, as they lie in memory, zeros outside (layer_gemm.cu).
+bool plain_box_map(CUtensorMap* map, const Mat& m, int rows, int cols, int dtype, int box_rows, int box_cols);
 
 // ---------------------------------------------------------------------------
 // Log probabilities (logprob.cu)

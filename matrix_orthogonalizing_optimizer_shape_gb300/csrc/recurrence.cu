@@ -145,9 +145,14 @@ struct Cell {
     return v;
   }
 };
-// What a thread has in flight: R cells of each of N matrices, for kAhead steps.
-// Copied into shared memory by cp.async, a place of its own for each thread, where
-// a cell has 4 bytes or more; else held in registers, for one step.
+// What a block has in flight: R cells a thread of each of N matrices, for kAhead steps.
+//   kTma    the block's rows as one box of a matrix, where bases and pitches are
+//           multiples of 16 bytes and there are steps enough to pay for the maps;
+//   kCells  cells of 4 bytes or more by cp.async, to a place of its own for each thread
+//           (8 instructions a row and matrix with their addresses);
+//   kRegs   in registers, for one step.
+// DOWN: a thread's row i is the i-th from its last (the gradient).
+enum Way { kTma, kCells, kRegs };
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
   if (bytes == 16)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -156,37 +161,61 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from, int by
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
-template <typename T, int VEC, int R, int N>
+struct TileMaps {
+  CUtensorMap m[4];
+};
+struct NoMaps {};
+template <Way WAY>
+using MapsOf = std::conditional_t<WAY == kTma, TileMaps, NoMaps>;
+
+template <typename T, int VEC, int R, int N, Way WAY, bool DOWN>
 struct Flight {
-  static constexpr bool kAsync = VEC * sizeof(T) >= 4;
-  static constexpr int kAhead = kAsync ? 2 : 1;
+  static constexpr int kAhead = WAY == kRegs ? 1 : 2;
   static constexpr int kCell = VEC * static_cast<int>(sizeof(T));
-  static constexpr size_t kBytes = kAsync ? static_cast<size_t>(kAhead) * N * R * kThreads * kCell : 0;
-  Cell<T, VEC> reg[kAsync ? 1 : N][kAsync ? 1 : R];
+  static constexpr int kBox = R * kThreads * kCell;  // bytes of a step's cells of a matrix
+  static constexpr size_t kBytes = WAY == kRegs ? 0 : static_cast<size_t>(kAhead) * N * kBox;
+  Cell<T, VEC> reg[WAY == kRegs ? N : 1][WAY == kRegs ? R : 1];
   char* mem;
-  uint32_t at;
-  __device__ __forceinline__ explicit Flight(char* shared)
-      : mem(shared + threadIdx.x * kCell), at(static_cast<uint32_t>(__cvta_generic_to_shared(mem))) {}
+  uint32_t at, bar;
+  __device__ __forceinline__ Flight(char* shared, const unsigned long long* full) {
+    const int group = threadIdx.x / kAcross, first = DOWN ? kGroups * R - 1 - group * R : group * R;
+    mem = shared + (WAY == kTma ? (first * kAcross + threadIdx.x % kAcross) * kCell : threadIdx.x * kCell);
+    at = static_cast<uint32_t>(__cvta_generic_to_shared(WAY == kTma ? shared : mem));
+    bar = static_cast<uint32_t>(__cvta_generic_to_shared(full));
+  }
   // Cell i of matrix n for step `step`.
   __device__ __forceinline__ void load(int step, int n, int i, const T* p) {
-    if constexpr (kAsync)
-      copy_async(at + (((step % kAhead) * N + n) * R + i) * kThreads * kCell, p, kCell);
-    else
+    if constexpr (WAY == kCells)
+      copy_async(at + ((step % kAhead) * N + n) * kBox + i * kThreads * kCell, p, kCell);
+    else if constexpr (WAY == kRegs)
       reg[n][i].load(p);
   }
   __device__ __forceinline__ void loaded() const {  // after the loads of a step
-    if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (WAY == kCells) asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  __device__ __forceinline__ void wait() const {  // for the oldest step's
-    if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+  // kTma, by one thread: the boxes of a step, from row y and channel x (of matrix 2 from the row before).
+  __device__ __forceinline__ void issue(int step, const MapsOf<WAY>& maps, int x, int y) const {
+    if constexpr (WAY == kTma) {
+      const uint32_t b = bar + 8 * (step % kAhead);
+      tc::mbar_expect(b, N * kBox);
+#pragma unroll
+      for (int n = 0; n < N; ++n) tc::tma_load(at + ((step % kAhead) * N + n) * kBox, &maps.m[n], b, x, n == 2 ? y - 1 : y);
+    }
+  }
+  // For a step's cells; false: the wait ran out.
+  __device__ __forceinline__ bool wait(int step, unsigned* status) const {
+    if constexpr (WAY == kTma) return tc::mbar_wait_warp(bar + 8 * (step % kAhead), step / kAhead & 1, status);
+    if constexpr (WAY == kCells) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    return true;
   }
   __device__ __forceinline__ Vec<VEC> values(int step, int n, int i) const {
-    if constexpr (kAsync) {
-      Cell<T, VEC> c;
-      c.load(reinterpret_cast<const T*>(mem + (((step % kAhead) * N + n) * R + i) * kThreads * kCell));
-      return c.values();
-    } else {
+    if constexpr (WAY == kRegs) {
       return reg[n][i].values();
+    } else {
+      constexpr int kRow = WAY == kTma ? (DOWN ? -1 : 1) * kAcross * kCell : kThreads * kCell;  // from row to row of a thread
+      Cell<T, VEC> c;
+      c.load(reinterpret_cast<const T*>(mem + ((step % kAhead) * N + n) * kBox + i * kRow));
+      return c.values();
     }
   }
 };
@@ -376,6 +405,7 @@ struct Shared {
   float enter[kGroups][kTile];                                    // the states
   float2 block[2][kMaxCluster][kTile];                            // of the cluster's blocks, in turn in two halves
   unsigned long long bar[2];                                      // of the halves
+  unsigned long long full[2];                                     // of the boxes in flight
   int stop;                                                       // a wait ran out
   int off[kSharedOffsets];
   // A warp reads 32 / kLanes channels of kLanes groups at once: each from other banks.
@@ -410,6 +440,7 @@ __device__ __forceinline__ void begin_steps(Shared<VEC>& sh, int size) {
   if (threadIdx.x == 0) {
     sh.stop = 0;
     for (unsigned long long& b : sh.bar) tc::mbar_init(tc::smem_u32(&b), 1);
+    for (unsigned long long& b : sh.full) tc::mbar_init(tc::smem_u32(&b), 1);
     tc::mbar_init_fence();
   }
   __syncthreads();
@@ -427,9 +458,9 @@ __device__ __forceinline__ void compose(float& A, float& D, float& B, float A1, 
   D = cut ? kCut : fmaf(D, A1, D1);
   A = cut ? 0.f : A * A1;  // whatever was before a cut, NaN too
 }
-template <int VEC>
+template <int VEC, class Then>
 __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, int size, const Map<VEC>& m, bool cut,
-                                          float& carry, unsigned* status) {
+                                          float& carry, unsigned* status, Then&& then) {  // once all have their rows
   using S = Shared<VEC>;
   constexpr int kTile = S::kTile, kLanes = S::kLanes;
   const int group = threadIdx.x / kAcross, own = S::at(group, threadIdx.x % kAcross * VEC), half = step & 1;
@@ -437,6 +468,7 @@ __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, i
   put<VEC>(&sh.D[group][own], cut ? all<VEC>(kCut) : m.D);
   put<VEC>(&sh.B[group][own], m.B);
   __syncthreads();
+  then();
   const int c = threadIdx.x / kLanes, k = threadIdx.x % kLanes;
   float a[S::kMaps], d[S::kMaps], b[S::kMaps];
 #pragma unroll
@@ -485,8 +517,8 @@ __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, i
   return get<VEC>(&sh.enter[group][own]);
 }
 
-template <typename T, int VEC, int R>
-__global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs a) {
+template <typename T, int VEC, int R, Way WAY>
+__global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs a, const __grid_constant__ MapsOf<WAY> boxes) {
   pdl_trigger();
   pdl_wait();
   __shared__ __align__(16) Shared<VEC> sh;
@@ -501,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
   const T* pz = static_cast<const T*>(a.z.p) + cr;
   const T* px = static_cast<const T*>(a.x.p) + cr;
   T* ph = static_cast<T*>(a.h.p) + cr;
-  extern __shared__ __align__(16) char flight_mem[];
-  using F = Flight<T, VEC, R, 2>;
-  F in_flight(flight_mem);
+  extern __shared__ __align__(128) char flight_mem[];
+  using F = Flight<T, VEC, R, 2, WAY, false>;
+  F in_flight(flight_mem, sh.full);
   auto load = [&](int step, int row0) {
     const int n = min(p.r1 - row0, R);
     const T *qz = pz + row0 * a.z.ld, *qx = px + row0 * a.x.ld;
@@ -526,12 +558,19 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
   float carry = 0.f;
   const int stride = size * kGroups * R;
   int row0 = p.r0 + (rank * kGroups + group) * R;
+  const int start = row0, x = blockIdx.y * kAcross * VEC;
+  auto fetch = [&](int to) {  // what step `to` reads
+    if constexpr (WAY != kTma)
+      load(to, start + to * stride);
+    else if (threadIdx.x == 0 && p.r0 + to * stride < p.r1)
+      in_flight.issue(to, boxes, x, p.r0 + rank * kGroups * R + to * stride);
+  };
 #pragma unroll
-  for (int i = 0; i < F::kAhead; ++i) load(i, row0 + i * stride);
+  for (int i = 0; i < F::kAhead; ++i) fetch(i);
   Place at;
   int step = 0;
   for (int top = p.r0; top < p.r1; top += stride, row0 += stride, ++step) {
-    in_flight.wait();
+    if (!in_flight.wait(step, a.status)) sh.stop = 1;
     Map<VEC> m;
     Vec<VEC> f[R];  // a and (1 - a) x of the rows
     Vec<VEC> g[R];
@@ -584,9 +623,14 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
         }
       }
     }
-    load(step + F::kAhead, row0 + F::kAhead * stride);
-    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry, a.status);
-    if (sh.stop) break;
+    if constexpr (WAY != kTma) fetch(step + F::kAhead);
+    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry, a.status, [&] {
+      if constexpr (WAY == kTma) fetch(step + F::kAhead);
+    });
+    if (sh.stop) {
+      for (int i = 1; i <= F::kAhead && WAY == kTma && top + i * stride < p.r1; ++i) in_flight.wait(step + i, a.status);
+      break;
+    }
     T* q = ph + static_cast<long long>(row0) * a.h.ld;
     if (whole) {
 #pragma unroll
@@ -615,8 +659,9 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
 // dz = dx a (h_{t-1} - x).  The scan runs from the last row to the first; a row's
 // map is s -> a s + a dh.  Row i of a warp is the i-th from its end.
 // --------------------------------------------------------------------------
-template <typename T, int VEC, int R>
-__global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(RecurrenceArgs a) {
+template <typename T, int VEC, int R, Way WAY>
+__global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(RecurrenceArgs a,
+                                                                    const __grid_constant__ MapsOf<WAY> boxes) {
   pdl_trigger();
   pdl_wait();
   __shared__ __align__(16) Shared<VEC> sh;
@@ -634,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
   const T* pd = static_cast<const T*>(a.dh.p) + cr;
   T* pdz = static_cast<T*>(a.dz.p) + cr;
   T* pdx = static_cast<T*>(a.dx.p) + cr;
-  extern __shared__ __align__(16) char flight_mem[];
-  using F = Flight<T, VEC, R, 4>;
-  F in_flight(flight_mem);
+  extern __shared__ __align__(128) char flight_mem[];
+  using F = Flight<T, VEC, R, 4, WAY, true>;
+  F in_flight(flight_mem, sh.full);
   auto load = [&](int step, int row0) {  // of h the row before, where there is one
     const int n = min(row0 - p.r0 + 1, R + 1);
     const T *qz = pz + row0 * a.z.ld, *qx = px + row0 * a.x.ld, *qh = ph + (row0 - 1) * a.h.ld, *qd = pd + row0 * a.dh.ld;
@@ -663,13 +708,20 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
   float carry = 0.f;
   const int stride = size * kGroups * R;
   int base = p.r1 - 1 - (rank * kGroups + group) * R;
+  const int start = base, x = blockIdx.y * kAcross * VEC;
+  auto fetch = [&](int to) {  // what step `to` reads
+    if constexpr (WAY != kTma)
+      load(to, start - to * stride);
+    else if (threadIdx.x == 0 && p.r1 - to * stride > p.r0)
+      in_flight.issue(to, boxes, x, p.r1 - (rank + 1) * kGroups * R - to * stride);
+  };
 #pragma unroll
-  for (int i = 0; i < F::kAhead; ++i) load(i, base - i * stride);
+  for (int i = 0; i < F::kAhead; ++i) fetch(i);
   Place at;
   int step = 0;
   for (int top = p.r1; top > p.r0; top -= stride, base -= stride, ++step) {
     const bool any = base >= p.r0;
-    in_flight.wait();
+    if (!in_flight.wait(step, a.status)) sh.stop = 1;
     const int row0 = any ? base : p.r0;
     Map<VEC> m;
     Vec<VEC> ga[R], gn[R], dv[R], diff[R];  // a, 1 - a, dh and h_{t-1} - x of the rows
@@ -729,9 +781,14 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
         }
       }
     }
-    load(step + F::kAhead, base - F::kAhead * stride);
-    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry, a.status);
-    if (sh.stop) break;
+    if constexpr (WAY != kTma) fetch(step + F::kAhead);
+    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry, a.status, [&] {
+      if constexpr (WAY == kTma) fetch(step + F::kAhead);
+    });
+    if (sh.stop) {
+      for (int i = 1; i <= F::kAhead && WAY == kTma && top - i * stride > p.r0; ++i) in_flight.wait(step + i, a.status);
+      break;
+    }
     if (!any) continue;
     T *qz = pdz + static_cast<long long>(row0) * a.dz.ld, *qx = pdx + static_cast<long long>(row0) * a.dx.ld;
 #pragma unroll
@@ -765,8 +822,22 @@ int aligned_channels(const Mat& m, int dtype) {
   return 1;
 }
 
-template <auto kernel>
-cudaError_t launch_scan(const RecurrenceArgs& a, int vec, int rows, size_t shared, cudaStream_t s) {  // rows of a block's step
+// Blocks of a cluster, and clusters side by side for groups of sequences.
+struct Plan {
+  int tiles, size, groups;
+};
+Plan plan_scan(const RecurrenceArgs& a, int vec, int rows) {  // rows of a block's step
+  Plan p;
+  p.tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
+  const int want = 2 * sm_count();  // blocks
+  p.size = 1;
+  while (p.size < kMaxCluster && 2 * p.size * p.tiles <= want && p.size * rows < a.tokens) p.size *= 2;
+  p.groups = std::max(1, std::min({a.sequences, want / (p.tiles * p.size), 65535 / kMaxCluster}));
+  return p;
+}
+
+template <auto kernel, class M>
+cudaError_t launch_scan(const RecurrenceArgs& a, const M& boxes, const Plan& p, size_t shared, cudaStream_t s) {
   if (shared > 0) {  // with the static part past what a kernel has without asking; once a device
     static std::atomic<unsigned long long> asked{0};
     int device = 0;
@@ -779,41 +850,57 @@ cudaError_t launch_scan(const RecurrenceArgs& a, int vec, int rows, size_t share
       asked.fetch_or(bit, std::memory_order_release);
     }
   }
-  const int tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
-  const int want = 2 * sm_count();  // blocks
-  int size = 1;
-  while (size < kMaxCluster && 2 * size * tiles <= want && size * rows < a.tokens) size *= 2;
-  const int groups = std::max(1, std::min({a.sequences, want / (tiles * size), 65535 / kMaxCluster}));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(size * groups, tiles);
+  cfg.gridDim = dim3(p.size * p.groups, p.tiles);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = shared;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {static_cast<unsigned>(size), 1u, 1u};
+  attr[0].val.clusterDim = {static_cast<unsigned>(p.size), 1u, 1u};
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a, boxes);
 }
 
-template <typename T, int VEC>
-cudaError_t launch_vec(const RecurrenceArgs& a, cudaStream_t s) {
+// Boxes of all matrices that are read; false where TMA cannot read one.
+bool boxes_of(const RecurrenceArgs& a, int rows, int cols, TileMaps* boxes) {
+  const Mat* m[4] = {&a.z, &a.x, &a.h, &a.dh};
+  const int es = a.dtype == kF32 ? 4 : 2;
+  for (int i = 0; i < (a.grad ? 4 : 2); ++i) {
+    if (reinterpret_cast<uintptr_t>(m[i]->p) % 16 != 0 || m[i]->ld * es % 16 != 0) return false;
+    if (!plain_box_map(&boxes->m[i], *m[i], a.tokens, a.channels, a.dtype, rows, cols)) return false;
+  }
+  return true;
+}
+
+template <typename T, int VEC, Way WAY>
+cudaError_t launch_way(const RecurrenceArgs& a, cudaStream_t s) {
   // Rows of a thread: 32 (forward) and 16 elements of each matrix fill the registers,
   // half of them where the next rows' wait there too, or where fp32 cells of 4 would
   // not leave two blocks the shared memory.
-  constexpr int kElements = sizeof(T) * VEC > 8 || sizeof(T) * VEC < 4 ? 16 : 32;
+  constexpr int kElements = sizeof(T) * VEC > 8 || WAY == kRegs ? 16 : 32;
   constexpr int kForward = kElements / VEC, kBackward = kForward / 2;
+  const int rows = kGroups * (a.grad ? kBackward : kForward);
+  const Plan p = plan_scan(a, VEC, rows);
+  MapsOf<WAY> boxes;
+  if constexpr (WAY == kTma) {
+    // A map costs the host half a microsecond: for some steps of the clusters at least.
+    if (a.tokens < 4 * rows * p.size || !boxes_of(a, rows, kAcross * VEC, &boxes)) return launch_way<T, VEC, kCells>(a, s);
+  }
   if (a.grad)
-    return launch_scan<recurrence_grad_kernel<T, VEC, kBackward>>(a, VEC, kGroups * kBackward,
-                       Flight<T, VEC, kBackward, 4>::kBytes, s);
-  return launch_scan<recurrence_kernel<T, VEC, kForward>>(a, VEC, kGroups * kForward, Flight<T, VEC, kForward, 2>::kBytes, s);
+    return launch_scan<recurrence_grad_kernel<T, VEC, kBackward, WAY>>(
+        a, boxes, p, Flight<T, VEC, kBackward, 4, WAY, true>::kBytes, s);
+  return launch_scan<recurrence_kernel<T, VEC, kForward, WAY>>(a, boxes, p, Flight<T, VEC, kForward, 2, WAY, false>::kBytes,
+                                                               s);
 }
 template <typename T>
 cudaError_t launch_typed(const RecurrenceArgs& a, int vec, cudaStream_t s) {
-  return vec == 4 ? launch_vec<T, 4>(a, s) : vec == 2 ? launch_vec<T, 2>(a, s) : launch_vec<T, 1>(a, s);
+  if (vec == 4) return launch_way<T, 4, kTma>(a, s);
+  if (vec == 2) return launch_way<T, 2, kCells>(a, s);
+  return launch_way<T, 1, sizeof(T) == 4 ? kCells : kRegs>(a, s);
 }
 
 }  // namespace
