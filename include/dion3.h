@@ -637,7 +637,7 @@ dion3_status dion3_embedding(int32_t tokens, int32_t vocab, int32_t cols, const 
  * instead, and the rows of tokens that do not occur are not touched.
  *   dy      [tokens][cols], dtable [vocab][cols], any two dtypes.  dtable may not
  *           be dy.
- *   tokens  at most 2^27.
+ *   tokens  at most 2^27, vocab at most 2^24.
  */
 dion3_status dion3_embedding_backward_workspace_size(int32_t tokens, int32_t vocab, int32_t cols,
                                                      size_t* bytes);

@@ -11,6 +11,7 @@ namespace dion3 {
 namespace {
 
 constexpr int32_t kMaxGrouped = 1 << 27;    // tokens whose positions are grouped
+constexpr int32_t kMaxGroupedVocab = 1 << 24;  // every group's block reads all ids
 constexpr int32_t kMaxEmbedCols = 1 << 20;
 constexpr int32_t kMaxChannels = 1 << 19;
 constexpr int32_t kMaxSequences = 1 << 27;
@@ -181,6 +182,7 @@ dion3_status dion3_embedding_backward_workspace_size(int32_t tokens, int32_t voc
   DION3_TRY(check_dims(tokens, cols, kMaxEmbedCols));
   DION3_TRY(check_dims(vocab, cols, kMaxEmbedCols));
   if (tokens > kMaxGrouped) return fail(DION3_ERR_UNSUPPORTED, "more than %d tokens", kMaxGrouped);
+  if (vocab > kMaxGroupedVocab) return fail(DION3_ERR_UNSUPPORTED, "a vocabulary of more than %d", kMaxGroupedVocab);
   Carve c{nullptr};
   if (tokens > 0) {
     const size_t n = tokens, w = embed_window(tokens);

@@ -24,7 +24,9 @@ UNIT = 32 * 2.0 ** -23
 # tokens, channels, offsets (None: one sequence)
 CASES = [(1, 1, None), (1, 64, None), (7, 33, [0, 3, 7]), (64, 96, list(range(65))), (65, 64, [0, 0, 1, 1, 64, 65, 65]),
          (130, 5, [0, 60, 130]), (1000, 2047, [0, 1, 9, 500, 500, 990, 1000]), (2500, 66, None), (700, 40, [3, 10, 600]),
-         (3000, 8, [0, 1000, 1001, 2000, 2999]), (513, 128, None)]
+         (3000, 8, [0, 1000, 1001, 2000, 2999]), (513, 128, None),
+         # Long enough for whole boxes of rows: a part of a tile, several tiles, a start and an end inside a box.
+         (9000, 72, [5, 77, 4000, 4000, 8989]), (4500, 520, None)]
 
 
 def offsets_of(tokens, offsets):
@@ -282,3 +284,24 @@ def test_equal_bits_on_other_streams_and_in_a_graph(cuda_lib):
         d3.recurrence_backward(x, z, x, h, dz, dx, offsets=off)
         torch.cuda.synchronize()
         assert torch.equal(h, h2) and torch.equal(dz, dz2) and torch.equal(dx, dx2)
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls that share nothing but their inputs, side by side."""
+    rng = np.random.default_rng(4)
+    z, x, _ = make(rng, 6000, 512, 1, "bf16", 0, 0)
+    want, wz, wx = (torch.empty_like(x) for _ in range(3))
+    d3.recurrence(z, x, want)
+    d3.recurrence_backward(x, z, x, want, wz, wx)
+    outs = [[torch.empty_like(x) for _ in range(3)] for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in outs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (h, dz, dx) in zip(streams, outs):
+            with torch.cuda.stream(s):
+                d3.recurrence(z, x, h)
+                d3.recurrence_backward(x, z, x, h, dz, dx)
+    torch.cuda.synchronize()
+    for h, dz, dx in outs:
+        assert torch.equal(h, want) and torch.equal(dz, wz) and torch.equal(dx, wx)
+    d3.device_status()

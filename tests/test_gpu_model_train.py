@@ -2,6 +2,8 @@
 program and a generating one call them."""
 import importlib.util
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -114,3 +116,42 @@ def test_a_step_captured_in_a_graph(cuda_lib, ex):
         assert torch.equal(loss, want)
         assert all(torch.equal(x, y) for x, y in zip(eager.grads, graph.grads))
         assert torch.equal(eager.blocks[1].w_in, graph.blocks[1].w_in)
+
+
+def test_first_calls_inside_a_capture(cuda_lib, ex):
+    """A process whose very first calls are captured: nothing in them needs an earlier one."""
+    code = """
+import torch
+import matrix_orthogonalizing_optimizer_shape_gb300 as d3
+T, D, V = 5000, 64, 300
+x = torch.randn(T, D, device="cuda").bfloat16()
+ids = torch.randint(0, V, (T,), device="cuda")
+h, dz, dx, logits, dl = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.randn(T, V, device="cuda"), torch.empty(T, V, device="cuda")
+table, y = torch.empty(V, D, device="cuda"), torch.empty_like(x)
+logp, stats, norm = torch.empty(T, device="cuda"), torch.empty(T, 3, device="cuda"), torch.empty(1, device="cuda")
+ws = d3.alloc_workspace(max(d3.embedding_backward_workspace_size(T, V, D), d3.grad_norm_workspace_size()))
+top = torch.empty(T, 4, device="cuda", dtype=torch.int32)
+def go():
+    d3.recurrence(x, x, h)
+    d3.recurrence_backward(x, x, x, h, dz, dx)
+    d3.embedding_backward(x, ids, table, ws=ws)
+    d3.embedding(ids, table, y)
+    d3.log_probs(logits, ids, logp, stats=stats, top_ids=top)
+    d3.log_probs_backward(logits, ids, stats, dl, dlogp=logp)
+    d3.clip_grad_norm([dl, y], 1.0, norm, ws=ws)
+outs = (h, dz, dx, table, y, logp, stats, top, dl, norm)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    go()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs]
+go()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, outs))
+d3.device_status()
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

@@ -87,11 +87,12 @@ def clip(lib, ts=(T(),), out=None, max_norm=1.0, norm=B, ws=C, ws_bytes=1 << 20,
     (embedding, dict(y=M(ld=63)), INV, b"pitch"), (embedding, dict(y=M(data=A)), INV, b"y may not be table"),
     (embedding, dict(scale=NAN), INV, b"scale"), (embedding, dict(scale=INF), INV, b"scale"),
     (embedding_backward, dict(tokens=-1), INV, b"rows"), (embedding_backward, dict(tokens=1 << 28), UNS, b"tokens"),
+    (embedding_backward, dict(vocab=(1 << 24) + 1), UNS, b"vocabulary"),
     (embedding_backward, dict(dy=M(data=B)), INV, b"dtable may not be dy"),
     (embedding_backward, dict(dtable=M(data=B + 1)), INV, b"aligned"), (embedding_backward, dict(dy=None), INV, b"dy"),
     (embedding_backward, dict(ws=None), WS, b"NULL"), (embedding_backward, dict(ws_bytes=64), WS, b"small"),
     (embedding_backward, dict(ws=C + 8), INV, b"256"), (embedding_backward, dict(scale=NAN), INV, b"scale"),
-    (recurrence, dict(tokens=-1), INV, b"rows"), (recurrence, dict(channels=1 << 21), UNS, b"larger"),
+    (recurrence, dict(tokens=-1), INV, b"rows"), (recurrence, dict(channels=1 << 20, z=M(ld=1 << 20)), UNS, b"larger"),
     (recurrence, dict(sequences=-1), INV, b"sequences"), (recurrence, dict(sequences=1 << 28), UNS, b"sequences"),
     (recurrence, dict(offsets=None), INV, b"offsets is NULL"), (recurrence, dict(offsets=FAKE + 2), INV, b"offsets"),
     (recurrence, dict(x=M(dtype=d3.F16)), INV, b"x has dtype"), (recurrence, dict(h=None), INV, b"h is NULL"),
