@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
 // flight, and writes a token's row when its run ends.  Each warp also writes
 // zeros to its share of the rows of tokens that do not occur, some at every batch: the
 // memory takes no more than 6.4 TB/s of writes alone, and reads wait behind as many as
-// are sent ahead of them (all at once: 400 us instead of 210; in a launch of their own
-// before the sums: 260).  A run that reaches over
+// are sent ahead of them (16384 x 4096 under 131072 tokens: 217 us; with all zeros sent
+// at once 400, in a launch of their own before the sums 260).  A run that reaches over
 // the window's first or last position leaves its sum in fp32 instead: slot 0 of
 // the window if it began before, else slot 1.
 // --------------------------------------------------------------------------
@@ -318,7 +318,7 @@ template <typename T, int VEC>
 constexpr int kBatch = VEC == 8 && sizeof(T) == 4 ? 4 : 8;
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(VEC == 8 ? 128 : 256, VEC == 8 ? 7 : 4) window_kernel(EmbedGradArgs a, int window, int strips, int log_groups,
+__global__ void __launch_bounds__(VEC == 8 ? 128 : 256, VEC == 8 ? 5 : 4) window_kernel(EmbedGradArgs a, int window, int strips, int log_groups,
                                                                                    int locals) {
   pdl_trigger();
   pdl_wait();
@@ -370,9 +370,9 @@ __global__ void __launch_bounds__(VEC == 8 ? 128 : 256, VEC == 8 ? 7 : 4) window
 }
 
 // A run that begins in window w and reaches over its end: its sums in slot 1 of w
-// and slot 0 of the windows after it, added by rows of threads that take every
-// fourth and then in order.
-constexpr int kJoinLanes = 64, kJoinRows = 4;
+// and slot 0 of the windows after it, added by two rows of threads that
+// take every other one, and then in order.
+constexpr int kJoinLanes = 128, kJoinRows = 2;
 
 template <int VEC>
 __global__ void __launch_bounds__(kJoinLanes * kJoinRows) join_kernel(EmbedGradArgs a, int window) {
@@ -450,10 +450,10 @@ cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s) {
   });
 }
 
-// Windows enough for every SM, sums of several rows each: 64 positions at 16384.
+// Windows enough for every SM, sums of several rows each: 32 positions at 16384.
 int embed_window(int tokens) {
   int w = 8;
-  while (w < kMaxWindow && w < (tokens + 255) / 256) w *= 2;
+  while (w < kMaxWindow && w < (tokens + 511) / 512) w *= 2;
   return w;
 }
 

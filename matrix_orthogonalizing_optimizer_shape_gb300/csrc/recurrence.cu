@@ -3,14 +3,16 @@
 // once and written once, the scan happens in registers.
 //
 // A step h -> a h + b is an affine map, and maps compose: (A, B) after (A', B')
-// is (A A', A B' + B).  A block takes 16 channels, a sector of 16-bit memory, and
-// walks down the rows: each thread composes the maps of R rows of VEC channels, 16
-// lanes a channel compose those of the block's threads, and each thread runs through
-// its rows again from the state before them, the next rows' loads in flight.  Wider
-// tiles, whose rows the blocks of larger clusters have to share out, wait for one
-// another at every step: 120 us for 16384 x 4096 bf16 at 128 channels and clusters
-// of 8.  Clusters remain for few channels.  Arithmetic is on pairs of channels (one
-// instruction for two).
+// is (A A', A B' + B).  The blocks of a cluster take 16 VEC channels and walk down the
+// rows together, one span of rows behind the other: each thread composes the maps of R
+// rows of VEC channels, a few lanes a channel compose those of a block's threads, the
+// blocks exchange theirs, and each thread runs through its rows again from the state
+// before them, the next rows' loads in flight.  Arithmetic is on pairs of channels
+// (one instruction for two).  Tiles of 64 channels in clusters of four were the best
+// for 16384 x 4096 bf16: 95 us (86 by boxes); 128 channels in clusters of eight, where
+// more blocks wait for one another, 120; 16 channels in none, whose rows are sectors
+// of 32 bytes, 157.  What bounds it is instructions (20 to 25 an element, at two
+// blocks an SM on two thirds of the SMs): 70 % of HBM's time; the gradient 80 %.
 //
 // Packed sequences: a map that begins a sequence cuts, so that rows are divided
 // evenly whatever the sequences' lengths; nothing of the rows before a cut, NaN
@@ -32,7 +34,7 @@ namespace {
 using namespace lm;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;                // past 8 a kernel has to ask
 constexpr int kAcross = 16;                    // threads along a block's channels
 constexpr int kGroups = kThreads / kAcross;    // groups of rows
 constexpr int kSharedOffsets = 1024;
@@ -831,14 +833,18 @@ Plan plan_scan(const RecurrenceArgs& a, int vec, int rows) {  // rows of a block
   p.tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
   const int want = 2 * sm_count();  // blocks
   p.size = 1;
-  while (p.size < kMaxCluster && 2 * p.size * p.tiles <= want && p.size * rows < a.tokens) p.size *= 2;
+  // 16 blocks wait for one another longer than 8: where they have four steps at least
+  // (16384 x 256: 16 us for 23; 2048 x 512, gradient: 12.9 for 10.5).
+  while (p.size < kMaxCluster && 2 * p.size * p.tiles <= want &&
+         (p.size < 8 ? p.size * rows < a.tokens : 8ll * p.size * rows <= a.tokens))
+    p.size *= 2;
   p.groups = std::max(1, std::min({a.sequences, want / (p.tiles * p.size), 65535 / kMaxCluster}));
   return p;
 }
 
 template <auto kernel, class M>
 cudaError_t launch_scan(const RecurrenceArgs& a, const M& boxes, const Plan& p, size_t shared, cudaStream_t s) {
-  if (shared > 0) {  // with the static part past what a kernel has without asking; once a device
+  {  // shared memory past what a kernel has without asking, and large clusters; once a device
     static std::atomic<unsigned long long> asked{0};
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
@@ -846,6 +852,7 @@ cudaError_t launch_scan(const RecurrenceArgs& a, const M& boxes, const Plan& p, 
     const unsigned long long bit = device < 64 ? 1ull << device : 0;
     if (bit == 0 || !(asked.load(std::memory_order_acquire) & bit)) {
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       asked.fetch_or(bit, std::memory_order_release);
     }
@@ -898,8 +905,10 @@ cudaError_t launch_way(const RecurrenceArgs& a, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t launch_typed(const RecurrenceArgs& a, int vec, cudaStream_t s) {
-  if (vec == 4) return launch_way<T, 4, kTma>(a, s);
-  if (vec == 2) return launch_way<T, 2, kCells>(a, s);
+  // Tiles of half the channels where whole ones in clusters of 8 would not give every
+  // SM a block (16384 x 1024: 28 us for 46).
+  if (vec == 4 && (a.channels + 4 * kAcross - 1) / (4 * kAcross) * 8 >= sm_count()) return launch_way<T, 4, kTma>(a, s);
+  if (vec >= 2) return launch_way<T, 2, kTma>(a, s);
   return launch_way<T, 1, sizeof(T) == 4 ? kCells : kRegs>(a, s);
 }
 

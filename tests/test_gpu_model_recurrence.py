@@ -7,8 +7,9 @@ product: for |z| <= 20 that is 20 units of w itself, and w |z| < 0.3 brings it
 under 8 of the state), the difference, the product and the sum by one each, and a
 composition by as many again, so that a step is off by at most 32 units of
 |h_{t-1}| + |x_t|; what a step is off decays with the state (`err` of the reference).
-Factors of maps are products of up to 512 decays, each off by 12 units relative at
-most: another 12 units a step of what they carry, within the same 32.
+A factor that spans n rows is composed of min(n, 39) others at most (a thread's rows, a
+channel's lanes, a cluster's blocks), each within 3 units of itself, and what it carries
+has 32 n units in the bound: n terms |h_k| that decay alike.
 """
 import numpy as np
 import pytest
@@ -26,7 +27,8 @@ CASES = [(1, 1, None), (1, 64, None), (7, 33, [0, 3, 7]), (64, 96, list(range(65
          (130, 5, [0, 60, 130]), (1000, 2047, [0, 1, 9, 500, 500, 990, 1000]), (2500, 66, None), (700, 40, [3, 10, 600]),
          (3000, 8, [0, 1000, 1001, 2000, 2999]), (513, 128, None),
          # Long enough for whole boxes of rows: a part of a tile, several tiles, a start and an end inside a box.
-         (9000, 72, [5, 77, 4000, 4000, 8989]), (4500, 520, None)]
+         (9000, 72, [5, 77, 4000, 4000, 8989]), (4500, 520, None),
+         (33000, 8, [0, 16500, 33000])]
 
 
 def offsets_of(tokens, offsets):
