@@ -8,6 +8,7 @@
 // cross windows are joined in order (join_kernel).  No atomic touches a sum: the
 // result's bits depend on the ids alone.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "layer_math.cuh"
@@ -109,7 +110,7 @@ constexpr int kGroupWarps = 16, kGroupThreads = 32 * kGroupWarps;
 constexpr int kMaxLocals = 512;  // tokens of a block: counters in 34 kB of shared memory
 constexpr int kMinGroups = 256;
 
-constexpr int kIdsAhead = 8;     // ids a lane has in flight
+constexpr int kIdsAhead = 16;    // ids a lane has in flight
 constexpr int kListed = 64;      // of a warp's own positions kept from the first walk
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
@@ -128,30 +129,43 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
 
   constexpr int kStep = 32 * kIdsAhead;
   const int slice = ((a.tokens + kGroupWarps - 1) / kGroupWarps + kStep - 1) / kStep * kStep;
-  const long long lo = static_cast<long long>(warp) * slice, hi = min(lo + slice, static_cast<long long>(a.tokens));
+  const int lo = static_cast<int>(min(static_cast<long long>(warp) * slice, static_cast<long long>(a.tokens)));
+  const int hi = static_cast<int>(min(static_cast<long long>(lo) + slice, static_cast<long long>(a.tokens)));
   int* own = cnt + warp * locals;
-  auto load = [&](long long i0, int (&id)[kIdsAhead]) {
-    long long v[kIdsAhead];
+  // The tokens at i0 + 32 u + lane, -1 where there is none.
+  auto load = [&](int i0, int (&id)[kIdsAhead]) {
+    if (a.ids.bytes == 8) {
+      int2 v[kIdsAhead];
 #pragma unroll
-    for (int u = 0; u < kIdsAhead; ++u) v[u] = i0 + 32 * u + lane < hi ? id_at(a.ids, i0 + 32 * u + lane) : -1;
+      for (int u = 0; u < kIdsAhead; ++u)
+        v[u] = i0 + 32 * u + lane < hi ? static_cast<const int2*>(a.ids.p)[i0 + 32 * u + lane] : make_int2(-1, -1);
 #pragma unroll
-    for (int u = 0; u < kIdsAhead; ++u) id[u] = v[u] >= 0 && v[u] < a.vocab ? static_cast<int>(v[u]) : -1;
+      for (int u = 0; u < kIdsAhead; ++u)
+        id[u] = v[u].y == 0 && static_cast<unsigned>(v[u].x) < static_cast<unsigned>(a.vocab) ? v[u].x : -1;
+    } else {
+      int v[kIdsAhead];
+#pragma unroll
+      for (int u = 0; u < kIdsAhead; ++u)
+        v[u] = i0 + 32 * u + lane < hi ? static_cast<const int*>(a.ids.p)[i0 + 32 * u + lane] : -1;
+#pragma unroll
+      for (int u = 0; u < kIdsAhead; ++u) id[u] = static_cast<unsigned>(v[u]) < static_cast<unsigned>(a.vocab) ? v[u] : -1;
+    }
   };
   int before = 0, found = 0;
-  for (long long i0 = lo; i0 < hi; i0 += kStep) {
+  for (int i0 = lo; i0 < hi; i0 += kStep) {
     int id[kIdsAhead];
     load(i0, id);
 #pragma unroll
     for (int u = 0; u < kIdsAhead; ++u) {
-      const int g = id[u] & mask;
-      before += id[u] >= 0 && g < mine;
-      const bool hit = id[u] >= 0 && g == mine;
+      const int g = id[u] < 0 ? INT_MAX : id[u] & mask;
+      before += g < mine;
+      const bool hit = g == mine;
       const unsigned hits = __ballot_sync(0xffffffffu, hit);
       if (hits == 0u) continue;
       if (hit) {
         atomicAdd(own + (id[u] >> log_groups), 1);
         const int at = found + __popc(hits & ((1u << lane) - 1u));
-        if (at < kListed) listed[warp][at] = make_int2(static_cast<int>(i0) + 32 * u + lane, id[u]);
+        if (at < kListed) listed[warp][at] = make_int2(i0 + 32 * u + lane, id[u]);
       }
       found += __popc(hits);
     }
@@ -206,12 +220,11 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
       lay(i + lane < found, e.x, e.y);
     }
   } else {
-    for (long long i0 = lo; i0 < hi; i0 += kStep) {
+    for (int i0 = lo; i0 < hi; i0 += kStep) {
       int id[kIdsAhead];
       load(i0, id);
 #pragma unroll
-      for (int u = 0; u < kIdsAhead; ++u)
-        lay(id[u] >= 0 && (id[u] & mask) == mine, static_cast<int>(i0) + 32 * u + lane, id[u]);
+      for (int u = 0; u < kIdsAhead; ++u) lay(id[u] >= 0 && (id[u] & mask) == mine, i0 + 32 * u + lane, id[u]);
     }
   }
 }
