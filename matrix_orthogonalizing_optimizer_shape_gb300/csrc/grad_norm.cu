@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* parti
   if (threadIdx.x == 0) *norm = v;
 }
 
-// Scales a chunk, BATCH pieces of a thread in flight.
-template <typename T, typename O, int BATCH>
+// Scales a chunk, kBatch pieces of a thread (or eight elements) in flight.
+template <typename T, typename O>
 __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
   const T* p = static_cast<const T*>(c.t->in) + c.row * c.t->ld_in + c.at;
   O* q = static_cast<O*>(c.t->out) + c.row * c.t->ld_out + c.at;
@@ -180,7 +180,16 @@ __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
   constexpr int kBytes = kPer<T> * static_cast<int>(sizeof(O));  // what a piece becomes: 8, 16 or 32
   const bool together = (reinterpret_cast<uintptr_t>(q + head) & (std::min(kBytes, 16) - 1)) == 0;
   if (!together) {
-    for (int i = threadIdx.x; i < c.n; i += kThreads) q[i] = from_f32<O>(to_f32<T>(p[i]) * coef);
+    constexpr int kAhead = 8;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < c.n; i0 += kAhead * kThreads) {
+      T v[kAhead];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) v[b] = p[min(i0 + b * kThreads, c.n - 1)];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b)
+        if (i0 + b * kThreads < c.n) q[i0 + b * kThreads] = from_f32<O>(to_f32<T>(v[b]) * coef);
+    }
     return;
   }
   const int pieces = (c.n - head) / kPer<T>, tail = c.n - head - pieces * kPer<T>;
@@ -190,15 +199,14 @@ __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
     const int at = threadIdx.x < head ? threadIdx.x : head + pieces * kPer<T> + threadIdx.x - head;
     q[at] = from_f32<O>(to_f32<T>(p[at]) * coef);
   }
-#pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < pieces; i0 += BATCH * kThreads) {
-    uint4 u[BATCH];
+  {
+    uint4 u[kBatch];
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b)
-      if (i0 + b * kThreads < pieces) u[b] = body[i0 + b * kThreads];
+    for (int b = 0; b < kBatch; ++b)
+      u[b] = threadIdx.x + b * kThreads < pieces ? body[threadIdx.x + b * kThreads] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      const int i = i0 + b * kThreads;
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = threadIdx.x + b * kThreads;
       if (i >= pieces) break;
       uint4* at = reinterpret_cast<uint4*>(to + i * kPer<T>);
       float f[kPer<T>];
@@ -237,8 +245,8 @@ __device__ __forceinline__ float factor_of(const double* partials, int n, float 
 // Clipping, out = min(1, max_norm / (norm + 1e-6)) in; in place a factor of 1 leaves
 // everything as it is.  Chunks run from the last to the first.  Tensors whose rows are
 // aligned pieces that keep their type go through this kernel, the next chunk's loads in
-// flight while one is scaled; the others through the one below (both in one kernel
-// needed more registers than its blocks have: 1.05 ms for the 1B-shaped set).
+// flight while one is scaled; the others through the kernels below, one a pair of types
+// (all in one needed more registers than its blocks have).
 template <typename T>
 __device__ __forceinline__ uint4 scaled(const uint4& u, float coef) {
   float f[kPer<T>];
@@ -315,32 +323,16 @@ __global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(cons
     for (int b = 0; b < kBatch; ++b) u[b] = v[b];
   }
 }
-template <int N>
-__global__ void __launch_bounds__(kThreads, 2) grad_scale_other_kernel(const __grid_constant__ Table<N> tab, int count,
-                                                                    unsigned chunks, const double* partials, int n,
-                                                                    float max_norm, bool in_place, float* norm) {
+template <int N, typename T, typename O>
+__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_other_kernel(const __grid_constant__ Table<N> tab,
+                                                                                 int count, unsigned chunks,
+                                                                                 const double* partials, int n,
+                                                                                 float max_norm, bool in_place, float* norm) {
   pdl_trigger();
   pdl_wait();
   const float coef = factor_of(partials, n, max_norm, norm);
   if (in_place && coef == 1.f) return;
-  for (unsigned i = blockIdx.x; i < chunks; i += gridDim.x) {
-    const Chunk c = chunk_of(tab, count, chunks - 1 - i);
-    auto from = [&](auto* p) {
-      using T = std::remove_pointer_t<decltype(p)>;
-      if (c.t->out_dtype == kF32)
-        scale_chunk<T, float, 4>(c, coef);
-      else if (c.t->out_dtype == kBF16)
-        scale_chunk<T, __nv_bfloat16, 4>(c, coef);
-      else
-        scale_chunk<T, __half, 4>(c, coef);
-    };
-    if (c.t->dtype == kF32)
-      from(static_cast<float*>(nullptr));
-    else if (c.t->dtype == kBF16)
-      from(static_cast<__nv_bfloat16*>(nullptr));
-    else
-      from(static_cast<__half*>(nullptr));
-  }
+  for (unsigned i = blockIdx.x; i < chunks; i += gridDim.x) scale_chunk<T, O>(chunk_of(tab, count, chunks - 1 - i), coef);
 }
 // Whether a tensor goes through the first of the two.
 bool keeps_pieces(const GradTensor& t) {
@@ -389,6 +381,10 @@ cudaError_t for_groups(const GradTensor* t, int n, P&& wanted, F&& f) {
   return cudaSuccess;
 }
 
+template <typename T>
+int dtype_of() {
+  return std::is_same<T, float>::value ? kF32 : std::is_same<T, __nv_bfloat16>::value ? kBF16 : kF16;
+}
 int blocks_for(unsigned chunks, int per_sm) {
   return static_cast<int>(std::min<unsigned>(chunks, static_cast<unsigned>(std::min(per_sm * sm_count(), kMaxGradPartials))));
 }
@@ -411,20 +407,31 @@ cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_no
     return norm == nullptr ? cudaSuccess
                            : launch_kernel(pdl_enabled(), grad_norm_kernel, dim3(1), dim3(kThreads), 0, s,
                                            static_cast<const double*>(partials), kept, norm);
-  for (bool pieces : {true, false}) {
-    e = for_groups(t, n, [&](const GradTensor& g) { return keeps_pieces(g) == pieces; },
-                   [&](const auto& tab, int count, unsigned chunks) {
-                     constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
-                     const cudaError_t r = launch_kernel(
-                         pdl_enabled(), pieces ? grad_scale_kernel<N> : grad_scale_other_kernel<N>,
-                         dim3(blocks_for(chunks, kScaleBlocks)), dim3(kThreads), 0, s, tab, count, chunks,
-                         static_cast<const double*>(partials), kept, max_norm, in_place, norm);
-                     norm = nullptr;  // written by the first launch
-                     return r;
-                   });
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  // One launch for the tensors whose pieces keep their type, and one for each pair of
+  // types among the others.
+  auto launch = [&](auto wanted, auto kernel_of) {
+    return for_groups(t, n, wanted, [&](const auto& tab, int count, unsigned chunks) {
+      constexpr int N = sizeof(tab.t) / sizeof(GradTensor);
+      const cudaError_t r = launch_kernel(pdl_enabled(), kernel_of(std::integral_constant<int, N>{}),
+                                          dim3(blocks_for(chunks, kScaleBlocks)), dim3(kThreads), 0, s, tab, count,
+                                          chunks, static_cast<const double*>(partials), kept, max_norm, in_place, norm);
+      norm = nullptr;  // written by the first launch
+      return r;
+    });
+  };
+  e = launch([](const GradTensor& g) { return keeps_pieces(g); }, [](auto N) { return grad_scale_kernel<N()>; });
+  auto pair = [&](auto* from, auto* to) {
+    using T = std::remove_pointer_t<decltype(from)>;
+    using O = std::remove_pointer_t<decltype(to)>;
+    if (e == cudaSuccess)
+      e = launch([](const GradTensor& g) { return !keeps_pieces(g) && g.dtype == dtype_of<T>() && g.out_dtype == dtype_of<O>(); },
+                 [](auto N) { return grad_scale_other_kernel<N(), T, O>; });
+  };
+  float* f = nullptr;
+  __nv_bfloat16* b = nullptr;
+  __half* h = nullptr;
+  pair(f, f), pair(f, b), pair(f, h), pair(b, f), pair(b, b), pair(b, h), pair(h, f), pair(h, b), pair(h, h);
+  return e;
 }
 
 }  // namespace dion3

@@ -150,6 +150,26 @@ def test_special_rows(cuda_lib, vocab):
     check(host(d)[fine], wd, 8 * adds(vocab) * (np.abs(wd) + 2.0 / vocab) + 1.001 * U["bf16"] * np.abs(wd) + 2.0 ** -120, "dlogits")
 
 
+@pytest.mark.parametrize("rows,vocab", [(3, 131072), (2, 5003), (1300, 40007)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_alternatives_among_equal_logits(cuda_lib, dtype, rows, vocab):
+    """Few values, so that equal logits reach far along a row: masked ones, the type's lowest, one value, NaN."""
+    rng = np.random.default_rng(vocab)
+    low = float(torch.finfo(torch.float16).min)
+    for values, p in (([-np.inf, 1.0, 2.0], [0.9999, 0.00005, 0.00005]), ([-np.inf, low, 3.0], [0.5, 0.4999, 0.0001]),
+                      ([0.0, -0.0, 1.0], [0.5, 0.4999, 0.0001]), ([5.0, 4.0, 3.0], [0.001, 0.01, 0.989]),
+                      ([-np.inf, np.nan, 1.0], [0.01, 0.989, 0.001]), ([np.nan, np.nan, -np.inf], [0.5, 0.4999, 0.0001])):
+        logits = dev(rng.choice(values, size=(min(rows, 40), vocab), p=p), dtype, 3, 1)
+        if rows > 40:
+            logits = logits.repeat(rows // 40 + 1, 1)[:rows]
+        for k in (1, 20, 32):
+            ids = torch.empty(rows, k, dtype=torch.int32, device="cuda")
+            d3.log_probs(logits, top_ids=ids)
+            want = top_ref(host(logits[:40]), k)
+            got = ids.cpu().numpy()
+            assert np.array_equal(got[:len(want)], want) and np.array_equal(got, want[np.arange(rows) % len(want)])
+
+
 def test_each_result_alone(cuda_lib):
     """A result does not depend on which others are asked for, and each may be left out."""
     rng = np.random.default_rng(0)
