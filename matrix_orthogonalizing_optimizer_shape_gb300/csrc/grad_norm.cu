@@ -11,8 +11,10 @@
 // sum outside [2^-70, 2^110], where squares may have left fp32's range, is formed
 // again from scaled values, so the norm is right for every finite gradient.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "layer_math.cuh"
 #include "model.h"
 
@@ -33,6 +35,8 @@ template <int N>
 struct Table {
   GradTensor t[N];
 };
+constexpr int kFew = 16, kMany = 448;
+static_assert(sizeof(Table<kMany>) < 32000, "kernel parameters");
 
 template <typename T>
 __device__ __forceinline__ void piece_values(const uint4& u, float (&v)[kPer<T>]) {
@@ -134,13 +138,9 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return v;
 }
 
-// partials[block] = (of an earlier launch: +=) the block's sum; `kept`: partials that earlier launches left.
+// A thread's part of the squares of the chunks that its block takes.
 template <int N>
-__global__ void __launch_bounds__(kThreads, kSquareBlocks) grad_squares_kernel(const __grid_constant__ Table<N> tab, int count,
-                                                                  unsigned chunks, double* partials, int kept) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ double red[kWarps];
+__device__ __forceinline__ double squares_of_chunks(const Table<N>& tab, int count, unsigned chunks) {
   double sum = 0.0;
   for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
     const Chunk k = chunk_of(tab, count, c);
@@ -151,7 +151,17 @@ __global__ void __launch_bounds__(kThreads, kSquareBlocks) grad_squares_kernel(c
     else
       sum += chunk_squares<__half>(k);
   }
-  sum = block_sum(sum, red);
+  return sum;
+}
+
+// partials[block] = (of an earlier launch: +=) the block's sum; `kept`: partials that earlier launches left.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kSquareBlocks) grad_squares_kernel(const __grid_constant__ Table<N> tab, int count,
+                                                                  unsigned chunks, double* partials, int kept) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[kWarps];
+  const double sum = block_sum(squares_of_chunks(tab, count, chunks), red);
   if (threadIdx.x == 0) partials[blockIdx.x] = sum + (static_cast<int>(blockIdx.x) < kept ? partials[blockIdx.x] : 0.0);
 }
 
@@ -228,14 +238,17 @@ __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
   }
 }
 
+__device__ __forceinline__ float factor(float norm, float max_norm) {
+  const float r = max_norm / (norm + 1e-6f);
+  return r > 1.f ? 1.f : r;  // NaN stays NaN
+}
 // The factor from the partials, the same bits in every block and thread.
 __device__ __forceinline__ float factor_of(const double* partials, int n, float max_norm, float* norm) {
   __shared__ double red[kWarps];
   __shared__ float coef;
   const float total = norm_of(partials, n, red);
   if (threadIdx.x == 0) {
-    const float r = max_norm / (total + 1e-6f);
-    coef = r > 1.f ? 1.f : r;  // NaN stays NaN
+    coef = factor(total, max_norm);
     if (norm != nullptr && blockIdx.x == 0) *norm = total;
   }
   __syncthreads();
@@ -289,16 +302,11 @@ struct Pieces {
       *reinterpret_cast<T*>(out + tail) = from_f32<T>(to_f32<T>(*reinterpret_cast<const T*>(in + tail)) * coef);
   }
 };
+// A thread's part of chunk after chunk of its block, from the last to the first.
 template <int N>
-__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(const __grid_constant__ Table<N> tab,
-                                                                           int count, unsigned chunks,
-                                                                           const double* partials, int n, float max_norm,
-                                                                           bool in_place, float* norm) {
-  pdl_trigger();
-  pdl_wait();
-  const float coef = factor_of(partials, n, max_norm, norm);
-  if (in_place && coef == 1.f) return;
+__device__ __forceinline__ void scale_chunks(const Table<N>& tab, int count, unsigned chunks, float coef) {
   unsigned i = blockIdx.x;
+  if (i >= chunks) return;
   Pieces p(chunk_of(tab, count, chunks - 1 - i));
   uint4 u[kBatch];
   p.load(u);
@@ -323,6 +331,47 @@ __global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(cons
     for (int b = 0; b < kBatch; ++b) u[b] = v[b];
   }
 }
+template <int N>
+__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(const __grid_constant__ Table<N> tab,
+                                                                           int count, unsigned chunks,
+                                                                           const double* partials, int n, float max_norm,
+                                                                           bool in_place, float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  const float coef = factor_of(partials, n, max_norm, norm);
+  if (in_place && coef == 1.f) return;
+  scale_chunks(tab, count, chunks, coef);
+}
+
+// Norm and clipping of a few chunks by one cluster: one launch, whose second reads come
+// from cache.  Seven matrices and two vectors of a small layer: 21 us a call for 24 with
+// two launches, where the host's side is what counts (on the device 7.7 for 5.8).
+constexpr int kSmallCluster = 16, kSmallChunks = 4 * kSmallCluster;
+__global__ void __launch_bounds__(kThreads) grad_clip_small_kernel(const __grid_constant__ Table<kFew> tab, int count,
+                                                                   unsigned chunks, float max_norm, bool in_place,
+                                                                   float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[kWarps];
+  __shared__ unsigned long long sums[kSmallCluster];  // of the cluster's blocks
+  cl::arrive();  // waited for before the first store to another block
+  const int rank = cl::rank();
+  const double sum = block_sum(squares_of_chunks(tab, count, chunks), red);
+  cl::wait();
+  if (threadIdx.x == 0)
+    for (int r = 0; r < kSmallCluster; ++r)
+      cl::store(cl::peer(&sums[rank], r), static_cast<unsigned long long>(__double_as_longlong(sum)));
+  __syncwarp();
+  cl::arrive();
+  cl::wait();
+  double all = 0.0;
+  for (int r = 0; r < kSmallCluster; ++r) all += __longlong_as_double(static_cast<long long>(sums[r]));
+  const float total = static_cast<float>(sqrt(all)), coef = factor(total, max_norm);
+  if (norm != nullptr && rank == 0 && threadIdx.x == 0) *norm = total;
+  if (in_place && coef == 1.f) return;
+  scale_chunks(tab, count, chunks, coef);
+}
+
 template <int N, typename T, typename O>
 __global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_other_kernel(const __grid_constant__ Table<N> tab,
                                                                                  int count, unsigned chunks,
@@ -342,9 +391,7 @@ bool keeps_pieces(const GradTensor& t) {
 }
 
 // Calls f(table, tensors, chunks) for groups of the wanted tensors that fit a launch's
-// parameters: 16 (a kilobyte) or kMany.
-constexpr int kFew = 16, kMany = 448;
-static_assert(sizeof(Table<kMany>) < 32000, "kernel parameters");
+// parameters: kFew (a kilobyte) or kMany.
 
 template <class P, class F>
 cudaError_t for_groups(const GradTensor* t, int n, P&& wanted, F&& f) {
@@ -393,6 +440,41 @@ int blocks_for(unsigned chunks, int per_sm) {
 
 cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_norm, bool in_place, float* norm,
                              double* partials, cudaStream_t s) {
+  if (clip && n <= kFew) {  // all in one launch?
+    bool done = false;
+    const bool plain = std::all_of(t, t + n, keeps_pieces);
+    const cudaError_t e = !plain ? cudaSuccess : for_groups(t, n, [](const GradTensor&) { return true; },
+                                                           [&](const auto& tab, int count, unsigned chunks) {
+      if constexpr (sizeof(tab.t) == sizeof(Table<kFew>)) {
+        if (chunks > kSmallChunks) return cudaSuccess;
+        done = true;
+        static std::atomic<unsigned long long> asked{0};  // a cluster past 8 blocks; once a device
+        int device = 0;
+        cudaError_t r = cudaGetDevice(&device);
+        if (r != cudaSuccess) return r;
+        const unsigned long long bit = device < 64 ? 1ull << device : 0;
+        if (bit == 0 || !(asked.load(std::memory_order_acquire) & bit)) {
+          r = cudaFuncSetAttribute(grad_clip_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+          if (r != cudaSuccess) return r;
+          asked.fetch_or(bit, std::memory_order_release);
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSmallCluster);
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {kSmallCluster, 1u, 1u};
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_enabled() ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, grad_clip_small_kernel, tab, count, chunks, max_norm, in_place, norm);
+      }
+      return cudaSuccess;
+    });
+    if (e != cudaSuccess || done) return e;
+  }
   int kept = 0;
   cudaError_t e = for_groups(t, n, [](const GradTensor&) { return true; }, [&](const auto& tab, int count, unsigned chunks) {
     constexpr int N = sizeof(tab.t) / sizeof(GradTensor);

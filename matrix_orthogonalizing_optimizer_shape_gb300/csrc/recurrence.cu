@@ -1,6 +1,6 @@
 // Gated linear recurrence on sm_103a, h_t = a_t h_{t-1} + (1 - a_t) x_t with
-// a = sigmoid(z), and its gradient.  Both are bound by HBM: every row is read
-// once and written once, the scan happens in registers.
+// a = sigmoid(z), and its gradient.  Every row is read once and written once; the
+// scan happens in registers.
 //
 // A step h -> a h + b is an affine map, and maps compose: (A, B) after (A', B')
 // is (A A', A B' + B).  The blocks of a cluster take 16 VEC channels and walk down the
@@ -833,10 +833,13 @@ Plan plan_scan(const RecurrenceArgs& a, int vec, int rows) {  // rows of a block
   p.tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
   const int want = 2 * sm_count();  // blocks
   p.size = 1;
-  // 16 blocks wait for one another longer than 8: where they have four steps at least
+  // Clusters for the length that two sequences have on the average, groups of sequences
+  // beyond that (16384 x 512 in 64 sequences: 22 us for 44 in clusters of 16).  16
+  // blocks wait for one another longer than 8: where they have four steps at least
   // (16384 x 256: 16 us for 23; 2048 x 512, gradient: 12.9 for 10.5).
+  const long long length = std::min<long long>(a.tokens, 2ll * a.tokens / a.sequences);
   while (p.size < kMaxCluster && 2 * p.size * p.tiles <= want &&
-         (p.size < 8 ? p.size * rows < a.tokens : 8ll * p.size * rows <= a.tokens))
+         (p.size < 8 ? p.size * rows < length : 8ll * p.size * rows <= length))
     p.size *= 2;
   p.groups = std::max(1, std::min({a.sequences, want / (p.tiles * p.size), 65535 / kMaxCluster}));
   return p;
@@ -886,9 +889,9 @@ bool boxes_of(const RecurrenceArgs& a, int rows, int cols, TileMaps* boxes) {
 template <typename T, int VEC, Way WAY>
 cudaError_t launch_way(const RecurrenceArgs& a, cudaStream_t s) {
   // Rows of a thread: 32 (forward) and 16 elements of each matrix fill the registers,
-  // half of them where the next rows' wait there too, or where fp32 cells of 4 would
-  // not leave two blocks the shared memory.
-  constexpr int kElements = sizeof(T) * VEC > 8 || WAY == kRegs ? 16 : 32;
+  // half of them where the next rows' wait there too, and half in fp32, whose cells
+  // would not leave two blocks the shared memory.
+  constexpr int kElements = sizeof(T) == 4 || WAY == kRegs ? 16 : 32;
   constexpr int kForward = kElements / VEC, kBackward = kForward / 2;
   const int rows = kGroups * (a.grad ? kBackward : kForward);
   const Plan p = plan_scan(a, VEC, rows);
