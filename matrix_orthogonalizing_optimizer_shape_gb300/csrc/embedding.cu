@@ -4,9 +4,9 @@
 // are is found without a sort of the whole vocabulary: the tokens are grouped by
 // the low bits of their number, a block a group (group_kernel), then summed in
 // windows of equal numbers of positions (window_kernel), so that a token that
-// makes up a tenth of the batch costs no block more than any other, and runs that
-// cross windows are joined in order (join_kernel).  No atomic touches a sum: the
-// result's bits depend on the ids alone.
+// makes up a tenth of the batch costs no block more than any other; runs that cross
+// windows are joined in order by the last block of them.  No atomic touches a sum:
+// the result's bits depend on the ids alone.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -127,7 +127,7 @@ constexpr int kListed = 64;      // of a warp's own positions kept from the firs
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-__global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, int log_groups, int locals) {
+__global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, int log_groups, int locals, int counters) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ int cnt[];  // [kGroupWarps][locals]
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int mine = blockIdx.x, mask = (1 << log_groups) - 1;
   for (int i = threadIdx.x; i < kGroupWarps * locals; i += kGroupThreads) cnt[i] = 0;
+  for (int i = blockIdx.x * kGroupThreads + threadIdx.x; i < counters; i += gridDim.x * kGroupThreads) a.arrived[i] = 0;
   if (threadIdx.x == 0) before_s = 0;
   __syncthreads();
 
@@ -247,14 +248,15 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(EmbedGradArgs a, i
 // flight, and writes a token's row when its run ends.  Each warp also writes
 // zeros to its share of the rows of tokens that do not occur, some at every batch: the
 // memory takes no more than 6.4 TB/s of writes alone, and reads wait behind as many as
-// are sent ahead of them (16384 x 4096 under 131072 tokens: 217 us; with all zeros sent
+// are sent ahead of them (16384 x 4096 under 131072 tokens: 212 us; with all zeros sent
 // at once 400, in a launch of their own before the sums 260).  A run that reaches over
 // the window's first or last position leaves its sum in fp32 instead: slot 0 of
-// the window if it began before, else slot 1.
+// the window if it began before, else slot 1 (joined in a launch of its own the
+// gradient of 216 x 1054 took 13.4 us on the device).
 // --------------------------------------------------------------------------
 constexpr int kMaxWindow = 512;
 constexpr int kZeros = 8192;    // bytes of shared zeros
-constexpr int kZerosAhead = 4;  // rows of a warp being written
+constexpr int kZerosAhead = 16;  // rows of a warp being written: enough of short ones
 
 // A warp's share of the rows of tokens that do not occur, written by bulk copies of
 // shared zeros, some at a time.
@@ -300,10 +302,19 @@ struct ZeroRows {
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           asm volatile("cp.async.bulk.wait_group %0;" ::"n"(kZerosAhead - 1) : "memory");
         }
-      } else if (a.table_dtype == kF32) {
-        for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint32_t*>(p)[i] = 0u;
-      } else {
-        for (int i = lane; i < a.cols; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0u;
+      } else {  // elements up to an aligned piece, pieces, elements
+        const int es = a.table_dtype == kF32 ? 4 : 2;
+        const long long head = min(bytes, static_cast<long long>(-reinterpret_cast<uintptr_t>(p) & 15u));
+        const long long body = (bytes - head) / 16, tail = head + 16 * body;
+        for (long long i = lane; i < body; i += 32) reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+        const int i = lane * es, j = i - static_cast<int>(head);  // of the head, else of the tail
+        uint8_t* e = i < head ? p + i : tail + j < bytes ? p + tail + j : nullptr;
+        if (e != nullptr) {
+          if (es == 4)
+            *reinterpret_cast<uint32_t*>(e) = 0u;
+          else
+            *reinterpret_cast<uint16_t*>(e) = 0u;
+        }
       }
     }
     return true;
@@ -339,6 +350,65 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs& a, int token, int c
     put(static_cast<__half*>(a.dtable.p));
 }
 
+// A run over several windows: each of them that has left its sum counts itself at the
+// first one's counter, and the last to do so adds them all, in the windows' order
+// whichever it is.  Called by all threads of a block, `index` being its window.
+template <int VEC>
+__device__ __forceinline__ void contribute(const EmbedGradArgs& a, int window, int n, int index, int strips, int strip,
+                                           int t, bool began_before, bool goes_on, int c) {
+  __shared__ int last;
+  int first = index, end = index;  // windows of the run
+  if (began_before) {
+    for (first = index - 1;;) {
+      const int w = first - static_cast<int>(threadIdx.x);  // a window that the run may have come into from before
+      const int got = __syncthreads_count(w > 0 && a.token[max(w, 1) * window - 1] == t);
+      first -= got;
+      if (got < static_cast<int>(blockDim.x)) break;
+    }
+  }
+  if (goes_on) {
+    for (;;) {
+      const int w = end + 1 + static_cast<int>(threadIdx.x);
+      const long long at = static_cast<long long>(w) * window;
+      const int got = __syncthreads_count(at < n && a.token[min(at, n - 1ll)] == t);
+      end += got;
+      if (got < static_cast<int>(blockDim.x)) break;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.arrived + static_cast<long long>(first) * strips + strip, 1) == end - first;
+  __syncthreads();
+  const bool mine = last != 0;
+  __syncthreads();
+  if (!mine || c >= a.cols) return;
+  __threadfence();
+  float sum[VEC] = {};
+  constexpr int kParts = 8;  // in flight
+  for (int w0 = first; w0 <= end; w0 += kParts) {
+    float v[kParts][VEC];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const int w = min(w0 + i, end);
+      const float* p = a.partials + (2ll * w + (w == first)) * a.cols + c;
+      if constexpr (VEC == 8) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p)), y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
+      } else {
+        v[i][0] = __ldcg(p);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      if (w0 + i > end) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum[j] += v[i][j];
+    }
+  }
+  put_row<VEC>(a, t, c, sum);
+}
+
 template <typename T, int VEC>
 constexpr int kBatch = VEC == 8 && sizeof(T) == 4 ? 4 : 8;
 
@@ -364,6 +434,7 @@ __global__ void __launch_bounds__(VEC == 8 ? 128 : 256, VEC == 8 ? 5 : 4) window
   const T* dy = static_cast<const T*>(a.dy.p) + (in ? c : 0);
   float* part = a.partials + 2ll * index * a.cols + c;
   bool began_before = tok[0] == tok[1];
+  const bool head = len > 0 && began_before, tail = len > 0 && tok[len] == tok[len + 1];
   float sum[VEC] = {};
   for (int i0 = 0; i0 < len; i0 += kBatch<T, VEC>) {
     Raw<T, VEC> raw[kBatch<T, VEC>];
@@ -391,53 +462,14 @@ __global__ void __launch_bounds__(VEC == 8 ? 128 : 256, VEC == 8 ? 5 : 4) window
       for (int j = 0; j < VEC; ++j) sum[j] = 0.f;
     }
   }
+  if (head || tail) {
+    const bool through = tail && tok[1] == tok[len];  // one run takes the whole window
+    if (head) contribute<VEC>(a, window, n, index, strips, strip, tok[1], true, through, c);
+    if (tail && !(head && through)) contribute<VEC>(a, window, n, index, strips, strip, tok[len], false, true, c);
+  }
   zero.finish();
 }
 
-// A run that begins in window w and reaches over its end: its sums in slot 1 of w
-// and slot 0 of the windows after it, added by two rows of threads that
-// take every other one, and then in order.
-constexpr int kJoinLanes = 128, kJoinRows = 2;
-
-template <int VEC>
-__global__ void __launch_bounds__(kJoinLanes * kJoinRows) join_kernel(EmbedGradArgs a, int window) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ float red[kJoinRows][kJoinLanes][VEC + 1];
-  const int n = *a.count;
-  const int s0 = blockIdx.x * window, s1 = s0 + window;
-  if (s1 >= n) return;
-  const int t = a.token[s1 - 1];
-  if (a.token[s1] != t || (s0 > 0 && a.token[s0 - 1] == t)) return;
-  const int windows = (n + window - 1) / window;
-  int more = 0;  // windows after this one that the run reaches
-  for (;;) {
-    const int w = blockIdx.x + 1 + more + threadIdx.y * kJoinLanes + threadIdx.x;
-    const int got = __syncthreads_count(w < windows && a.token[min(w, windows - 1) * window] == t);
-    more += got;
-    if (got < kJoinLanes * kJoinRows) break;
-  }
-  const int c = (blockIdx.y * kJoinLanes + threadIdx.x) * VEC;
-  const bool in = c < a.cols;
-  float sum[VEC] = {};
-  if (in) {
-#pragma unroll 4
-    for (int i = threadIdx.y; i <= more; i += kJoinRows) {
-      float v[VEC];
-      load_vec<float, VEC>(a.partials + (2ll * (static_cast<int>(blockIdx.x) + i) + (i == 0)) * a.cols + c, v);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) sum[j] += v[j];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) red[threadIdx.y][threadIdx.x][j] = sum[j];
-  __syncthreads();
-  if (threadIdx.y != 0 || !in) return;
-  for (int r = 1; r < kJoinRows; ++r)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sum[j] += red[r][threadIdx.x][j];
-  put_row<VEC>(a, t, c, sum);
-}
 
 // --------------------------------------------------------------------------
 // Host side
@@ -475,7 +507,9 @@ cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s) {
   });
 }
 
-// Windows enough for every SM, sums of several rows each: 32 positions at 16384.
+// Windows enough for every SM, sums of several rows each: 32 positions at 16384 (more and
+// shorter ones leave more partial sums of frequent tokens to add: 14136 x 448 in 39 us,
+// in 55 with windows of 8).
 int embed_window(int tokens) {
   int w = 8;
   while (w < kMaxWindow && w < (tokens + 511) / 512) w *= 2;
@@ -488,6 +522,7 @@ static int log_groups_of(int vocab) {
   while (ceil_div(vocab, 1ll << n) > kMaxLocals) ++n;
   return n;
 }
+int embed_counters(int tokens, int cols) { return ceil_div(tokens, embed_window(tokens)) * ceil_div(cols, 256); }
 int embed_slots(int vocab) {
   const int n = log_groups_of(vocab);
   return ceil_div(vocab, 1ll << n) << n;
@@ -495,24 +530,20 @@ int embed_slots(int vocab) {
 
 cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s) {
   const int log_groups = log_groups_of(a.vocab), locals = ceil_div(a.vocab, 1ll << log_groups);
-  cudaError_t e = launch_kernel(pdl_enabled(), group_kernel, dim3(1u << log_groups), dim3(kGroupThreads),
-                                kGroupWarps * locals * sizeof(int), s, a, log_groups, locals);
-  if (e != cudaSuccess) return e;
   const bool vec = pieces_of(a.dy, a.dtype, a.cols) && pieces_of(a.dtable, a.table_dtype, a.cols);
   const int window = embed_window(a.tokens), windows = ceil_div(a.tokens, window);
   const int pieces = vec ? a.cols / 8 : a.cols;
-  const int threads = vec ? 128 : 256;
+  const int threads = vec ? 128 : 256, strips = ceil_div(pieces, threads);
+  cudaError_t e = launch_kernel(pdl_enabled(), group_kernel, dim3(1u << log_groups), dim3(kGroupThreads),
+                                kGroupWarps * locals * sizeof(int), s, a, log_groups, locals, windows * strips);
+  if (e != cudaSuccess) return e;
   // Enough blocks for the zeros of a large vocabulary, too.
-  const int strips = ceil_div(pieces, threads);
-  const int blocks = a.accumulate ? windows * strips : std::max(windows * strips, 4 * sm_count());
-  e = with_type(a.dtype, [&](auto* t) {
+  const int blocks = a.accumulate ? windows * strips : std::max(windows * strips, 5 * sm_count());
+  return with_type(a.dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     return launch_kernel(pdl_enabled(), vec ? window_kernel<T, 8> : window_kernel<T, 1>, dim3(blocks), dim3(threads),
                          0, s, a, window, strips, log_groups, locals);
   });
-  if (e != cudaSuccess || windows == 1) return e;
-  return launch_kernel(pdl_enabled(), vec ? join_kernel<8> : join_kernel<1>, dim3(windows, ceil_div(pieces, kJoinLanes)),
-                       dim3(kJoinLanes, kJoinRows), 0, s, a, window);
 }
 
 }  // namespace dion3

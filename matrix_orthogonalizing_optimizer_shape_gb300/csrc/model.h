@@ -40,8 +40,10 @@ struct EmbedGradArgs {
   int* count;       // [1] positions that have a token
   uint8_t* occurs;  // [embed_slots(vocab)] whether a token does, by its group
   float* partials;  // [2 windows][cols]
+  int* arrived;     // [windows][strips of columns] of the runs that begin there
 };
 int embed_slots(int vocab);
+int embed_counters(int tokens, int cols);  // at most
 cudaError_t launch_embedding_grad(const EmbedGradArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

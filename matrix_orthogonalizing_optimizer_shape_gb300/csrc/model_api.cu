@@ -191,6 +191,7 @@ dion3_status dion3_embedding_backward_workspace_size(int32_t tokens, int32_t voc
     c.take(4);
     c.take(embed_slots(vocab));
     c.take(2 * ((n + w - 1) / w) * cols * 4);
+    c.take(4 * static_cast<size_t>(embed_counters(tokens, cols)));
   }
   *bytes = c.off;
   return ok();
@@ -225,6 +226,7 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
   a.count = static_cast<int*>(c.take(4));
   a.occurs = static_cast<uint8_t*>(c.take(embed_slots(vocab)));
   a.partials = static_cast<float*>(c.take(2 * ((n + w - 1) / w) * cols * 4));
+  a.arrived = static_cast<int*>(c.take(4 * static_cast<size_t>(embed_counters(tokens, cols))));
   DION3_CUDA(traced_launch("embedding_backward", 0.0,
                            1.0 * tokens * cols * bytes_of(dy->dtype) + 1.0 * vocab * cols * bytes_of(dtable->dtype), s,
                            [&] { return launch_embedding_grad(a, s); }),
