@@ -171,3 +171,24 @@ def test_equal_bits_on_other_streams_and_in_a_graph(cuda_lib):
         d3.embedding(v, first, x)
         torch.cuda.synchronize()
         assert torch.equal(first, again) and torch.equal(x, y)
+
+
+def test_frequent_tokens_give_equal_bits_whoever_joins_them(cuda_lib):
+    """Runs over many windows are added by whichever block is last: in the same order."""
+    rng = np.random.default_rng(2)
+    tokens, vocab, cols = 16000, 200, 2048
+    ids = numbers(np.minimum((vocab * rng.random(tokens) ** 3).astype(int), vocab - 1))
+    dy = dev(rng.standard_normal((tokens, cols)), "bf16")
+    ws, first = workspace(tokens, vocab, cols), None
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [(out(vocab, cols, "f32")[0], workspace(tokens, vocab, cols)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, (dtable, own) in zip(streams, outs):  # side by side, a workspace each
+            with torch.cuda.stream(s):
+                d3.embedding_backward(dy, ids, dtable, ws=own)
+        torch.cuda.synchronize()
+        dtable, _ = out(vocab, cols, "f32")
+        d3.embedding_backward(dy, ids, dtable, ws=ws)
+        first = dtable if first is None else first
+        assert torch.equal(first, dtable) and all(torch.equal(first, d) for d, _ in outs)

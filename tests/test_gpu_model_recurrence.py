@@ -307,3 +307,37 @@ def test_two_streams_at_once(cuda_lib):
     for h, dz, dx in outs:
         assert torch.equal(h, want) and torch.equal(dz, wz) and torch.equal(dx, wx)
     d3.device_status()
+
+
+@pytest.mark.parametrize("dtype,tokens,channels", [("bf16", 700, 128), ("f16", 9000, 64), ("f32", 300, 33)])
+def test_states_and_places_in_every_combination(cuda_lib, dtype, tokens, channels):
+    """Each state alone, and each result in the place of each input."""
+    rng = np.random.default_rng(tokens)
+    seqs = [0, tokens // 3, tokens // 3, tokens - 1]
+    off = numbers(seqs, 32)
+    z, x, state = make(rng, tokens, channels, 3, dtype, 0, 0)
+    z.clamp_(-5, 5)
+    first, dlast, zero = state(), state(), torch.zeros(3, channels, device="cuda")
+    h0, last0, h1, last1 = torch.zeros_like(x), torch.empty_like(first), torch.zeros_like(x), torch.empty_like(first)
+    d3.recurrence(z, x, h0, offsets=off, first=first, last=last0)
+    d3.recurrence(z, x, h1, offsets=off, first=zero, last=last1)
+    for f, want, end in ((first, h0, last0), (None, h1, last1)):
+        for ask in (False, True):
+            for place in ("z", "x", "new"):
+                zi, xi = z.clone(), x.clone()
+                h = {"z": zi, "x": xi, "new": torch.empty_like(x)}[place]
+                last = torch.empty_like(first) if ask else None
+                d3.recurrence(zi, xi, h, offsets=off, first=f, last=last)
+                assert torch.equal(h[:-1], want[:-1]) and (not ask or torch.equal(last, end))
+    dh = dev(rng.standard_normal((tokens, channels)), dtype)
+    for f, dl in ((first, dlast), (first, None), (None, dlast), (None, None)):
+        dz0, dx0, df0 = torch.zeros_like(x), torch.zeros_like(x), torch.empty_like(first)
+        d3.recurrence_backward(dh, z, x, h0, dz0, dx0, offsets=off, first=zero if f is None else f,
+                               dlast=zero if dl is None else dl, dfirst=df0)
+        for ask in (False, True):
+            for pz, px in (("z", "x"), ("x", "z"), ("dh", "z"), ("x", "dh"), ("new", "x")):
+                t = {"z": z.clone(), "x": x.clone(), "dh": dh.clone(), "new": torch.empty_like(x)}
+                df = torch.empty_like(first) if ask else None
+                d3.recurrence_backward(t["dh"], t["z"], t["x"], h0, t[pz], t[px], offsets=off, first=f, dlast=dl, dfirst=df)
+                assert torch.equal(t[pz][:-1], dz0[:-1]) and torch.equal(t[px][:-1], dx0[:-1])
+                assert not ask or torch.equal(df, df0)
