@@ -262,6 +262,8 @@ def clip_grad_norm(tensors: Sequence, max_norm: float, norm=None, *, out: Option
     norm receives the norm before (see dion3_clip_grad_norm)."""
     _l._load_torch()
     dev = tensors[0].get_device() if len(tensors) else _l._device() if norm is None else norm.get_device()
+    if dev < 0 and len(tensors):
+        _l._on("tensors", tensors[0], dev)
     if out is not None and len(out) != len(tensors):
         raise ValueError(f"out has {len(out)} tensors, {len(tensors)} are wanted")
     if out is None:

@@ -273,3 +273,17 @@ def test_binding_refuses_layouts_types_and_other_devices(calls):
     assert not calls
 
 
+
+
+def test_clipping_refuses_strided_tensors_without_a_device(calls):
+    """Rows of a CPU matrix into rows of another: dense ones are refused on another way."""
+    class Host(Fake):
+        is_cuda = False
+
+    t, o = Host((5, 6), stride=(7, 1), device=-1), Host((5, 6), stride=(9, 1), device=-1, address=A)
+    for out in (None, [o], [Fake((5, 6))]):
+        with pytest.raises(ValueError, match="not a CUDA tensor"):
+            d3.clip_grad_norm([t], 1.0, out=out, stream=1)
+    with pytest.raises(ValueError):
+        d3.clip_grad_norm([Fake((5, 6), stride=(7, 1))], 1.0, out=[o], stream=1)
+    assert not calls
