@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <memory>
 #include <new>
+#include <numeric>
 
 namespace dion3 {
 namespace {
@@ -80,11 +81,13 @@ Extent extent_of(const dion3_tensor& t, int32_t i, bool written) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data);
   return {lo, static_cast<uintptr_t>(lo + (t.rows - 1) * pitch + row), pitch, row, i, written};
 }
-// Whether two that overlap are different columns of one matrix (a.lo <= b.lo).
+// Whether two that overlap are different columns or rows of one matrix (a.lo <= b.lo):
+// apart modulo what both pitches are multiples of.
 bool interleaved(const Extent& a, const Extent& b) {
-  if (a.pitch == 0 || a.pitch != b.pitch) return false;
-  const unsigned long long at = (b.lo - a.lo) % a.pitch;
-  return at >= a.row && at + b.row <= a.pitch;
+  const unsigned long long pitch = std::gcd(a.pitch, b.pitch);
+  if (pitch == 0) return false;
+  const unsigned long long at = (b.lo - a.lo) % pitch;
+  return at >= a.row && at + b.row <= pitch;
 }
 // Refuses tensors whose elements several would write, or one write and another read.
 dion3_status check_apart(const dion3_tensor* in, const dion3_tensor* out, int32_t n) {

@@ -3,6 +3,7 @@ what the binding hands to the library.  No call here launches GPU work."""
 import ctypes
 import struct
 
+import numpy as np
 import pytest
 import torch
 
@@ -287,3 +288,28 @@ def test_clipping_refuses_strided_tensors_without_a_device(calls):
     with pytest.raises(ValueError):
         d3.clip_grad_norm([Fake((5, 6), stride=(7, 1))], 1.0, out=[o], stream=1)
     assert not calls
+
+
+def test_rows_and_columns_of_one_matrix_are_apart(lib, monkeypatch):  # noqa: F811
+    """Against the sets of elements: matrices of one base pitch, its multiples and single rows."""
+    monkeypatch.setenv("DION3_INJECT", "launch_fail")
+    rng = np.random.default_rng(0)
+    seen = set()
+    for _ in range(4000):
+        ts, sets = [], []
+        for _ in range(2):
+            rows, cols, start = int(rng.integers(1, 5)), int(rng.integers(1, 8)), int(rng.integers(0, 40))
+            ld = 8 * int(rng.integers(1, 4))
+            ts.append(T(data=A + 2 * start, rows=rows, cols=cols, ld=ld))
+            sets.append({start + r * ld + c for r in range(rows) for c in range(cols)})
+        status, meet = clip(lib, ts=tuple(ts)), bool(sets[0] & sets[1])
+        if meet:
+            assert status == INV and b"share" in lib.dion3_last_error(), (ts, sets)
+        seen.add((meet, status))
+    assert seen == {(True, INV), (False, d3.ERR_CUDA), (False, INV)}  # (wrapping around a pitch may be refused)
+    view = lambda i, rows, cols, ld: T(data=A + 2 * i, rows=rows, cols=cols, ld=ld)  # noqa: E731
+    for ts in ((view(0, 9, 32, 96), view(4 * 96 + 32, 1, 64, 64)),    # columns, and a single row of the others
+               (view(0, 5, 96, 192), view(96, 5, 96, 192)),           # every other row
+               (view(0, 5, 32, 192), view(32, 9, 64, 96)),            # every other row of some columns, all of others
+               (view(32, 1, 64, 64), view(0, 9, 32, 96))):
+        assert clip(lib, ts=ts) == d3.ERR_CUDA, lib.dion3_last_error()
