@@ -660,7 +660,8 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
  *   last       fp32 [sequences][channels], dense: receives the states after each
  *              sequence (those before it where it has no rows), or NULL.  May be
  *              first.
- * z = -infinity forgets (h_t = x_t), z = +infinity keeps (h_t = h_{t-1}).
+ * z = -infinity forgets (h_t = x_t), z = +infinity keeps (h_t = h_{t-1}, of a finite
+ * x_t: 0 times another is NaN).
  * channels <= 2^19, sequences <= 2^27.  Offsets that do not ascend give undefined
  * values in the rows, but no access outside the matrices.
  */
@@ -753,7 +754,7 @@ typedef struct {
  *             nothing.  out[i] may be tensors[i]; otherwise no two tensors of a
  *             call that are written, or written and read, may share elements
  *             (columns of one matrix interleave without doing so).
- *   max_norm  >= 0; infinity clips nothing.
+ *   max_norm  >= 0; infinity clips nothing: the factor is 1 whatever the norm.
  *   norm      device fp32, may be NULL when clipping.
  * No host synchronisation: the factor stays on the device.
  */

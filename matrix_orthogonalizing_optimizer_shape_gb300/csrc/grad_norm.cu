@@ -239,6 +239,7 @@ __device__ __forceinline__ void scale_chunk(const Chunk& c, float coef) {
 }
 
 __device__ __forceinline__ float factor(float norm, float max_norm) {
+  if (max_norm == INFINITY) return 1.f;  // clips nothing, though a norm may be infinite too
   const float r = max_norm / (norm + 1e-6f);
   return r > 1.f ? 1.f : r;  // NaN stays NaN
 }

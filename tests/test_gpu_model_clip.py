@@ -163,3 +163,18 @@ def test_equal_bits_on_other_streams_and_in_a_graph(cuda_lib):
         d3.clip_grad_norm(ts, 1.0, norm, out=outs, ws=ws)
         torch.cuda.synchronize()
         assert torch.equal(norm, n2) and all(torch.equal(a, b) for a, b in zip(outs, again))
+
+
+def test_no_limit_clips_nothing(cuda_lib):
+    """A max_norm of infinity leaves gradients as they are whose norm is infinite or NaN, too."""
+    for value in (3e38, float("inf"), float("nan")):
+        for n in (1000, 3000000):  # one launch, and several
+            ts = [torch.full((n,), 1.0, device="cuda"), torch.ones(7, 9, device="cuda", dtype=torch.bfloat16)]
+            ts[0][:5] = value
+            before, norm = [t.clone() for t in ts], torch.zeros(1, device="cuda")
+            outs = [torch.zeros_like(ts[0], dtype=torch.float32), torch.zeros_like(ts[1], dtype=torch.float32)]
+            d3.clip_grad_norm(ts, math.inf, norm, out=outs, ws=workspace())
+            d3.clip_grad_norm(ts, math.inf, norm, ws=workspace())
+            assert not torch.isfinite(norm).any()
+            for t, b, o in zip(ts, before, outs):
+                assert torch.equal(t.nan_to_num(7), b.nan_to_num(7)) and torch.equal(o.nan_to_num(7), b.float().nan_to_num(7))
