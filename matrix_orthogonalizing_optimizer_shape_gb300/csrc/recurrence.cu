@@ -8,16 +8,18 @@
 // rows of VEC channels, a few lanes a channel compose those of a block's threads, the
 // blocks exchange theirs, and each thread runs through its rows again from the state
 // before them, the next rows' loads in flight.  Arithmetic is on pairs of channels
-// (one instruction for two).  Tiles of 64 channels in clusters of four were the best
-// for 16384 x 4096 bf16: 95 us (86 by boxes); 128 channels in clusters of eight, where
-// more blocks wait for one another, 120; 16 channels in none, whose rows are sectors
-// of 32 bytes, 157.  What bounds it is instructions (20 to 25 an element, at two
-// blocks an SM on two thirds of the SMs): 70 % of HBM's time; the gradient 80 %.
+// (one instruction for two).  16384 x 4096 bf16: 78 us by boxes of 32 channels in
+// clusters of two (by cp.async of 64 channels in clusters of four 95; of 128 in clusters
+// of eight, where more blocks wait for one another, 120; of 16 in none, whose rows are
+// sectors of 32 bytes, 157), the gradient 147.  What bounds it is instructions (about 20
+// and 45 an element, at two blocks an SM on two thirds of the SMs) and the steps' waits:
+// 75 % of HBM's time; the gradient 80 %.  Four rows a thread with three blocks an SM: 125.
 //
 // Packed sequences: a map that begins a sequence cuts, so that rows are divided
 // evenly whatever the sequences' lengths; nothing of the rows before a cut, NaN
-// included, passes it.  Where the channels are few, groups of whole sequences go
-// to different clusters.
+// included, passes it.  Warps whose rows hold a boundary pick by it in each row, without
+// a branch (64 sequences: 103 us; row by row behind conditions 120).  Where the
+// channels are few, groups of whole sequences go to different clusters.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -184,6 +186,12 @@ struct Flight {
     mem = shared + (WAY == kTma ? (first * kAcross + threadIdx.x % kAcross) * kCell : threadIdx.x * kCell);
     at = static_cast<uint32_t>(__cvta_generic_to_shared(WAY == kTma ? shared : mem));
     bar = static_cast<uint32_t>(__cvta_generic_to_shared(full));
+    if constexpr (WAY == kRegs) {
+#pragma unroll
+      for (auto& r : reg)
+#pragma unroll
+        for (auto& cell : r) cell = {};
+    }
   }
   // Cell i of matrix n for step `step`.
   __device__ __forceinline__ void load(int step, int n, int i, const T* p) {
@@ -248,6 +256,28 @@ template <int VEC>
 __device__ __forceinline__ void store_state(float* p, const Vec<VEC>& v) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) p[j] = v[j];
+}
+
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> pick(bool first, const Vec<VEC>& a, const Vec<VEC>& b) {
+  Vec<VEC> r;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) r[j] = first ? a[j] : b[j];
+  return r;
+}
+// to[i] = the state of a sequence at the rows whose bits are in `at`, else 0; the first
+// is q's, and bits of `past` step to the next one.
+template <int VEC, int R, class Next>
+__device__ __forceinline__ void load_states(Vec<VEC> (&to)[R], const float* from, unsigned at, unsigned past, int q,
+                                            Next&& next, int channels, int c) {
+#pragma unroll
+  for (int i = 0; i < R; ++i) to[i] = all<VEC>(0.f);
+  if (from == nullptr || at == 0u) return;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (at >> i & 1) to[i] = load_state<VEC>(from + static_cast<long long>(q) * channels + c);
+    if (past >> i & 1) q = next(q);
+  }
 }
 
 // --------------------------------------------------------------------------
@@ -596,31 +626,22 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
           m.B = fma(f[i], m.B, g[i]);
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if (row0 + i >= p.r1) break;
-          if (row0 + i == at.begin) {
-            begins |= 1u << i;
-            g[i] = a.first != nullptr ? load_state<VEC>(a.first + static_cast<long long>(at.q) * a.channels + cr)
-                                      : all<VEC>(0.f);
-          }
-          if (row0 + i + 1 == at.end) {
-            ends |= 1u << i;
-            at.set(p.seq, p.seq.next(at.q));
-          }
+        for (int n = 0; n < R; ++n) {  // the sequences of the rows
+          if (static_cast<unsigned>(at.begin) - row0 < R) begins |= 1u << (at.begin - row0);
+          if (static_cast<unsigned>(at.end) - 1 - row0 >= R) break;
+          ends |= 1u << (at.end - 1 - row0);
+          if (at.end >= p.r1) break;
+          at.set(p.seq, p.seq.next(at.q));
         }
+        load_states<VEC, R>(g, a.first, begins, ends, q0, [&](int q) { return p.seq.next(q); }, a.channels, cr);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if (row0 + i >= p.r1) break;
+        for (int i = 0; i < R; ++i) {  // rows behind the last are nobody's past
           const Gate<VEC> k(in_flight.values(step, 0, i));
-          f[i] = k.a;
+          const bool cut = begins >> i & 1;
           const Vec<VEC> b = mul(k.na, in_flight.values(step, 1, i));
-          if (begins >> i & 1) {  // the state before it is in g
-            m.B = g[i] = fma(f[i], g[i], b);
-          } else {
-            g[i] = b;
-            m.B = fma(f[i], m.B, b);
-          }
+          f[i] = k.a;
+          m.B = fma(f[i], pick(cut, g[i], m.B), b);  // the state before a sequence is in g
+          g[i] = pick(cut, m.B, b);
           m.factor(k);
         }
       }
@@ -643,11 +664,10 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i, q += a.h.ld) {
-        if (row0 + i >= p.r1) break;
-        h = begins >> i & 1 ? g[i] : fma(f[i], h, g[i]);
-        if (in) store_cell<T, VEC>(q, h);
-        if (ends >> i & 1) {
-          if (a.last != nullptr && in) store_state<VEC>(a.last + static_cast<long long>(q0) * a.channels + c, h);
+        h = pick(begins >> i & 1, g[i], fma(f[i], h, g[i]));
+        if (in && row0 + i < p.r1) store_cell<T, VEC>(q, h);
+        if (a.last != nullptr && (ends >> i & 1)) {
+          if (in) store_state<VEC>(a.last + static_cast<long long>(q0) * a.channels + c, h);
           q0 = p.seq.next(q0);
         }
       }
@@ -749,37 +769,26 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
           m.B = mul(ga[i], add(dv[i], m.B));
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if (row0 - i < p.r0) break;
-          if (row0 - i + 1 == at.end) {
-            ends |= 1u << i;
-            dv[i] = a.dlast != nullptr ? load_state<VEC>(a.dlast + static_cast<long long>(at.q) * a.channels + cr)
-                                       : all<VEC>(0.f);
-          }
-          if (row0 - i == at.begin) {
-            begins |= 1u << i;
-            diff[i] = a.first != nullptr ? load_state<VEC>(a.first + static_cast<long long>(at.q) * a.channels + cr)
-                                         : all<VEC>(0.f);
-            at.set(p.seq, p.seq.prev(at.q));
-          }
+        for (int n = 0; n < R; ++n) {  // the sequences of the rows
+          if (static_cast<unsigned>(row0) - at.end + 1 < R) ends |= 1u << (row0 - at.end + 1);
+          if (static_cast<unsigned>(row0) - at.begin >= R) break;
+          begins |= 1u << (row0 - at.begin);
+          if (at.begin <= p.r0) break;
+          at.set(p.seq, p.seq.prev(at.q));
         }
+        const auto prev = [&](int q) { return p.seq.prev(q); };
+        load_states<VEC, R>(dv, a.dlast, ends, begins, q0, prev, a.channels, cr);
+        load_states<VEC, R>(diff, a.first, begins, begins, q0, prev, a.channels, cr);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          if (row0 - i < p.r0) break;
+        for (int i = 0; i < R; ++i) {  // rows before the first are nobody's future
           const Gate<VEC> k(in_flight.values(step, 0, i));
           ga[i] = k.a;
           gn[i] = k.na;
-          if (ends >> i & 1) {  // dlast is in dv
-            dv[i] = add(in_flight.values(step, 3, i), dv[i]);
-            m.B = all<VEC>(0.f);
-          } else {
-            dv[i] = in_flight.values(step, 3, i);
-          }
-          if (!(begins >> i & 1)) diff[i] = in_flight.values(step, 2, i);  // else the state before it is there
-          diff[i] = fma(in_flight.values(step, 1, i), all<VEC>(-1.f), diff[i]);
+          dv[i] = add(in_flight.values(step, 3, i), dv[i]);
+          diff[i] = fma(in_flight.values(step, 1, i), all<VEC>(-1.f),
+                        pick(begins >> i & 1, diff[i], in_flight.values(step, 2, i)));
           m.factor(k);
-          m.B = mul(ga[i], add(dv[i], m.B));
+          m.B = mul(ga[i], add(dv[i], pick(ends >> i & 1, all<VEC>(0.f), m.B)));
         }
       }
     }
@@ -795,16 +804,14 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
     T *qz = pdz + static_cast<long long>(row0) * a.dz.ld, *qx = pdx + static_cast<long long>(row0) * a.dx.ld;
 #pragma unroll
     for (int i = 0; i < R; ++i, qz -= a.dz.ld, qx -= a.dx.ld) {
-      if (!whole && row0 - i < p.r0) break;
-      const Vec<VEC> g = ends >> i & 1 ? dv[i] : add(dv[i], s);
-      const Vec<VEC> dx = mul(gn[i], g);
+      const Vec<VEC> g = add(dv[i], pick(ends >> i & 1, all<VEC>(0.f), s)), dx = mul(gn[i], g);
       s = mul(ga[i], g);
-      if (in) {
+      if (in && row0 - i >= p.r0) {
         store_cell<T, VEC>(qx, dx);
         store_cell<T, VEC>(qz, mul(mul(dx, ga[i]), diff[i]));
       }
-      if (begins >> i & 1) {
-        if (a.dfirst != nullptr && in) store_state<VEC>(a.dfirst + static_cast<long long>(q0) * a.channels + c, s);
+      if (a.dfirst != nullptr && (begins >> i & 1)) {
+        if (in) store_state<VEC>(a.dfirst + static_cast<long long>(q0) * a.channels + c, s);
         q0 = p.seq.prev(q0);
       }
     }
@@ -824,55 +831,86 @@ int aligned_channels(const Mat& m, int dtype) {
   return 1;
 }
 
+// Channels of a thread that the matrices allow.
+int vector_of(const RecurrenceArgs& a) {
+  int vec = a.channels % 4 == 0 ? 4 : a.channels % 2 == 0 ? 2 : 1;
+  for (const Mat* m : {&a.z, &a.x, &a.h, &a.dh, &a.dz, &a.dx}) vec = std::min(vec, aligned_channels(*m, a.dtype));
+  return vec;
+}
+// Tiles of 64 channels, where they give every SM a block in clusters of 8 (16384 x 1024 in
+// tiles of 32: 28 us for 46).
+bool wide(const RecurrenceArgs& a) {
+  return vector_of(a) == 4 && (a.channels + 4 * kAcross - 1) / (4 * kAcross) * 8 >= sm_count();
+}
+
+// A launch of clusters.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  Launch(dim3 grid, int size, size_t shared, cudaStream_t s) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(size), 1u, 1u};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  }
+  Launch(const Launch&) = delete;
+};
+
+// How many clusters of each size run side by side (0: none): what the groups of SMs that
+// hold a cluster leave of two blocks an SM, 296 blocks in clusters of 4 and 266 of 7 on
+// 152 SMs.  Asked once a kernel and device, with the attributes that its launches need.
+template <auto kernel>
+cudaError_t resident_of(size_t shared, int (&clusters)[kMaxCluster + 1]) {
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];  // [0]: 1 when the others are there
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* r = device < kDevices ? known[device] : nullptr;
+  if (r != nullptr && r[0].load(std::memory_order_acquire)) {
+    for (int n = 1; n <= kMaxCluster; ++n) clusters[n] = r[n].load(std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int n = 1; n <= kMaxCluster && e == cudaSuccess; ++n) {
+    Launch l(dim3(n), n, shared, nullptr);
+    l.cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&clusters[n], kernel, &l.cfg);
+    if (r != nullptr) r[n].store(clusters[n], std::memory_order_relaxed);
+  }
+  if (r != nullptr && e == cudaSuccess) r[0].store(1, std::memory_order_release);
+  return e;
+}
+
 // Blocks of a cluster, and clusters side by side for groups of sequences.
 struct Plan {
   int tiles, size, groups;
 };
-Plan plan_scan(const RecurrenceArgs& a, int vec, int rows) {  // rows of a block's step
+Plan plan_scan(const RecurrenceArgs& a, int vec, int rows, const int (&clusters)[kMaxCluster + 1]) {  // rows of a block's step
   Plan p;
   p.tiles = (a.channels + kAcross * vec - 1) / (kAcross * vec);
-  const int want = 2 * sm_count();  // blocks
-  p.size = 1;
   // Clusters for the length that two sequences have on the average, groups of sequences
   // beyond that (16384 x 512 in 64 sequences: 22 us for 44 in clusters of 16).  16
   // blocks wait for one another longer than 8: where they have four steps at least
-  // (16384 x 256: 16 us for 23; 2048 x 512, gradient: 12.9 for 10.5).
+  // (16384 x 256: 16 us for 23; 2048 x 512, gradient: 12.9 for 10.5).  All clusters run
+  // at once: a second wave costs as much as the first.
   const long long length = std::min<long long>(a.tokens, 2ll * a.tokens / a.sequences);
-  while (p.size < kMaxCluster && 2 * p.size * p.tiles <= want &&
-         (p.size < 8 ? p.size * rows < length : 8ll * p.size * rows <= length))
-    p.size *= 2;
-  p.groups = std::max(1, std::min({a.sequences, want / (p.tiles * p.size), 65535 / kMaxCluster}));
-  return p;
-}
-
-template <auto kernel, class M>
-cudaError_t launch_scan(const RecurrenceArgs& a, const M& boxes, const Plan& p, size_t shared, cudaStream_t s) {
-  {  // shared memory past what a kernel has without asking, and large clusters; once a device
-    static std::atomic<unsigned long long> asked{0};
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = device < 64 ? 1ull << device : 0;
-    if (bit == 0 || !(asked.load(std::memory_order_acquire) & bit)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-      asked.fetch_or(bit, std::memory_order_release);
-    }
+  for (p.size = kMaxCluster; p.size > 1; --p.size) {
+    int half = 1;  // of the next power of two
+    while (2 * half < p.size) half *= 2;
+    if (p.tiles <= clusters[p.size] &&
+        (half < 8 ? static_cast<long long>(half) * rows < length : 8ll * half * rows <= length))
+      break;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.size * p.groups, p.tiles);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {static_cast<unsigned>(p.size), 1u, 1u};
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, boxes);
+  p.groups = std::max(1, std::min({a.sequences, clusters[p.size] / p.tiles, 65535 / kMaxCluster}));
+  return p;
 }
 
 // Boxes of all matrices that are read; false where TMA cannot read one.
@@ -886,43 +924,57 @@ bool boxes_of(const RecurrenceArgs& a, int rows, int cols, TileMaps* boxes) {
   return true;
 }
 
-template <typename T, int VEC, Way WAY>
+template <typename T, int VEC, Way WAY, bool GRAD>
 cudaError_t launch_way(const RecurrenceArgs& a, cudaStream_t s) {
   // Rows of a thread: 32 (forward) and 16 elements of each matrix fill the registers,
   // half of them where the next rows' wait there too, and half in fp32, whose cells
   // would not leave two blocks the shared memory.
   constexpr int kElements = sizeof(T) == 4 || WAY == kRegs ? 16 : 32;
-  constexpr int kForward = kElements / VEC, kBackward = kForward / 2;
-  const int rows = kGroups * (a.grad ? kBackward : kForward);
-  const Plan p = plan_scan(a, VEC, rows);
+  constexpr int R = kElements / VEC / (GRAD ? 2 : 1), kRows = kGroups * R;
+  constexpr size_t kBytes = Flight<T, VEC, R, GRAD ? 4 : 2, WAY, GRAD>::kBytes;
+  constexpr auto kernel = [] {
+    if constexpr (GRAD)
+      return recurrence_grad_kernel<T, VEC, R, WAY>;
+    else
+      return recurrence_kernel<T, VEC, R, WAY>;
+  }();
+  int clusters[kMaxCluster + 1];
+  const cudaError_t e = resident_of<kernel>(kBytes, clusters);
+  if (e != cudaSuccess) return e;
+  const Plan p = plan_scan(a, VEC, kRows, clusters);
   MapsOf<WAY> boxes;
   if constexpr (WAY == kTma) {
     // A map costs the host half a microsecond: for some steps of the clusters at least.
-    if (a.tokens < 4 * rows * p.size || !boxes_of(a, rows, kAcross * VEC, &boxes)) return launch_way<T, VEC, kCells>(a, s);
+    if (a.tokens < 4 * kRows * p.size || !boxes_of(a, kRows, kAcross * VEC, &boxes)) {
+      // Cells of two channels are copied by twice the instructions.
+      constexpr int kWide = VEC == 2 && !GRAD && sizeof(T) == 2 ? 4 : VEC;
+      if (kWide != VEC && wide(a)) return launch_way<T, kWide, kCells, GRAD>(a, s);
+      return launch_way<T, VEC, kCells, GRAD>(a, s);
+    }
   }
-  if (a.grad)
-    return launch_scan<recurrence_grad_kernel<T, VEC, kBackward, WAY>>(
-        a, boxes, p, Flight<T, VEC, kBackward, 4, WAY, true>::kBytes, s);
-  return launch_scan<recurrence_kernel<T, VEC, kForward, WAY>>(a, boxes, p, Flight<T, VEC, kForward, 2, WAY, false>::kBytes,
-                                                               s);
+  const Launch l(dim3(p.size * p.groups, p.tiles), p.size, kBytes, s);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a, boxes);
 }
-template <typename T>
-cudaError_t launch_typed(const RecurrenceArgs& a, int vec, cudaStream_t s) {
-  // Tiles of half the channels where whole ones in clusters of 8 would not give every
-  // SM a block (16384 x 1024: 28 us for 46).
-  if (vec == 4 && (a.channels + 4 * kAcross - 1) / (4 * kAcross) * 8 >= sm_count()) return launch_way<T, 4, kTma>(a, s);
-  if (vec >= 2) return launch_way<T, 2, kTma>(a, s);
-  return launch_way<T, 1, sizeof(T) == 4 ? kCells : kRegs>(a, s);
+template <typename T, bool GRAD>
+cudaError_t launch_typed(const RecurrenceArgs& a, cudaStream_t s) {
+  // Boxes of 32 channels and 16 rows a thread compose half as many maps as 64 and 8, by
+  // as many blocks in smaller clusters: 16384 x 4096 bf16 83 us for 87, x 8192 138 for
+  // 158.  The gradient has no registers for that (157 for 148), fp32 loads halve (65 for
+  // 64).
+  if (wide(a) && (GRAD || sizeof(T) == 4)) return launch_way<T, 4, kTma, GRAD>(a, s);
+  if (vector_of(a) >= 2) return launch_way<T, 2, kTma, GRAD>(a, s);
+  return launch_way<T, 1, sizeof(T) == 4 ? kCells : kRegs, GRAD>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_recurrence(const RecurrenceArgs& a, cudaStream_t s) {
-  int vec = a.channels % 4 == 0 ? 4 : a.channels % 2 == 0 ? 2 : 1;
-  for (const Mat* m : {&a.z, &a.x, &a.h, &a.dh, &a.dz, &a.dx}) vec = std::min(vec, aligned_channels(*m, a.dtype));
-  if (a.dtype == kF32) return launch_typed<float>(a, vec, s);
-  if (a.dtype == kBF16) return launch_typed<__nv_bfloat16>(a, vec, s);
-  return launch_typed<__half>(a, vec, s);
+  const auto launch = [&](auto grad) {
+    if (a.dtype == kF32) return launch_typed<float, grad()>(a, s);
+    if (a.dtype == kBF16) return launch_typed<__nv_bfloat16, grad()>(a, s);
+    return launch_typed<__half, grad()>(a, s);
+  };
+  return a.grad ? launch(std::true_type{}) : launch(std::false_type{});
 }
 
 }  // namespace dion3
