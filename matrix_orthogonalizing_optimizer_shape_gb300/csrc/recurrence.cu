@@ -843,6 +843,16 @@ bool wide(const RecurrenceArgs& a) {
   return vector_of(a) == 4 && (a.channels + 4 * kAcross - 1) / (4 * kAcross) * 8 >= sm_count();
 }
 
+// Whether one row a thread takes all of it in a step (the gradient) or two: single tokens
+// of many sequences.  With eight, a thread walks through the boundaries of as many rows
+// while others have none: 64 tokens x 4096 in as many sequences 4.1 us for 6.8, one token
+// 2.7 for 3.9; 256 tokens, in four steps, 9.5 for 7.8.
+bool is_short(const RecurrenceArgs& a) {
+  const int vec = wide(a) ? 4 : std::min(2, vector_of(a)), tiles = (a.channels + vec * kAcross - 1) / (vec * kAcross);
+  const int groups = std::max(1, std::min(a.sequences, 2 * sm_count() / tiles));
+  return a.tokens <= (a.grad ? 1 : 2) * kGroups * groups;
+}
+
 // A launch of clusters.
 struct Launch {
   cudaLaunchConfig_t cfg = {};
@@ -924,13 +934,13 @@ bool boxes_of(const RecurrenceArgs& a, int rows, int cols, TileMaps* boxes) {
   return true;
 }
 
-template <typename T, int VEC, Way WAY, bool GRAD>
+template <typename T, int VEC, Way WAY, bool GRAD, bool SHORT = false>
 cudaError_t launch_way(const RecurrenceArgs& a, cudaStream_t s) {
-  // Rows of a thread: 32 (forward) and 16 elements of each matrix fill the registers,
+  // Rows of a thread, one or: 32 (forward) and 16 elements of each matrix fill the registers,
   // half of them where the next rows' wait there too, and half in fp32, whose cells
   // would not leave two blocks the shared memory.
   constexpr int kElements = sizeof(T) == 4 || WAY == kRegs ? 16 : 32;
-  constexpr int R = kElements / VEC / (GRAD ? 2 : 1), kRows = kGroups * R;
+  constexpr int R = SHORT ? 1 : kElements / VEC / (GRAD ? 2 : 1), kRows = kGroups * R;
   constexpr size_t kBytes = Flight<T, VEC, R, GRAD ? 4 : 2, WAY, GRAD>::kBytes;
   constexpr auto kernel = [] {
     if constexpr (GRAD)
@@ -961,6 +971,11 @@ cudaError_t launch_typed(const RecurrenceArgs& a, cudaStream_t s) {
   // as many blocks in smaller clusters: 16384 x 4096 bf16 83 us for 87, x 8192 138 for
   // 158.  The gradient has no registers for that (157 for 148), fp32 loads halve (65 for
   // 64).
+  if (is_short(a)) {
+    if (wide(a)) return launch_way<T, 4, kRegs, GRAD, true>(a, s);
+    if (vector_of(a) >= 2) return launch_way<T, 2, kRegs, GRAD, true>(a, s);
+    return launch_way<T, 1, kRegs, GRAD, true>(a, s);
+  }
   if (wide(a) && (GRAD || sizeof(T) == 4)) return launch_way<T, 4, kTma, GRAD>(a, s);
   if (vector_of(a) >= 2) return launch_way<T, 2, kTma, GRAD>(a, s);
   return launch_way<T, 1, sizeof(T) == 4 ? kCells : kRegs, GRAD>(a, s);

@@ -341,3 +341,42 @@ def test_states_and_places_in_every_combination(cuda_lib, dtype, tokens, channel
                 d3.recurrence_backward(t["dh"], t["z"], t["x"], h0, t[pz], t[px], offsets=off, first=f, dlast=dl, dfirst=df)
                 assert torch.equal(t[pz][:-1], dz0[:-1]) and torch.equal(t[px][:-1], dx0[:-1])
                 assert not ask or torch.equal(df, df0)
+
+
+# Short calls: each on both sides of one and of two rows a thread, sequences of one row, of
+# several and of none; and channels whose tiles take clusters of 3, 5, 7 and more blocks.
+SHORT = [(1, 4096, 1), (5, 4096, 5), (64, 4096, 64), (65, 4096, 65), (128, 4096, 100), (129, 4096, 129), (30, 4096, 3),
+         (16, 1024, 16), (300, 1024, 300), (33, 520, 33), (17, 4096, 1), (32, 4100, 2), (70, 1023, 70), (9, 66, 20)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,channels,n", SHORT + [(2600, 2560, 2), (1500, 1536, 1), (2100, 4864, 3), (900, 700, 1)])
+def test_short_calls_and_clusters_of_every_size(cuda_lib, dtype, tokens, channels, n):
+    rng = np.random.default_rng(tokens * n)
+    cuts = np.sort(rng.integers(0, tokens + 1, n - 1)) if n < tokens else np.arange(1, n).clip(max=tokens)
+    seqs = np.concatenate([[0], cuts, [tokens]])
+    off = numbers(seqs, 32)
+    for states in (True, False):
+        z, x, state = make(rng, tokens, channels, n, dtype, 0, 0)
+        h, dh = dev(rng.standard_normal((tokens, channels)), dtype), dev(rng.standard_normal((tokens, channels)), dtype)
+        first, dlast = (state(), state()) if states else (None, None)
+        last, dfirst = (torch.empty(n, channels, device="cuda") for _ in range(2)) if states else (None, None)
+        y, dz, dx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        d3.recurrence(z, x, y, offsets=off, first=first, last=last)
+        want, want_last, err, last_err = recurrence_ref(host(z), host(x), seqs, host(first) if states else None)
+        check(host(y), want, UNIT * err + 1.001 * U[dtype] * np.abs(want) + TINY[dtype], "h")
+        if states:
+            check(host(last), want_last, UNIT * last_err, "last")
+        d3.recurrence_backward(dh, z, x, h, dz, dx, offsets=off, first=first, dlast=dlast, dfirst=dfirst)
+        hz, hx, prev = host(z), host(x), np.concatenate([np.zeros((1, channels)), host(h)[:-1]])
+        wz, wx, wf, err, first_err = recurrence_grad_ref(host(dh), hz, hx, host(h), seqs, host(first) if states else None,
+                                                         host(dlast) if states else None)
+        for i in range(n):
+            if seqs[i + 1] > seqs[i]:
+                prev[seqs[i]] = host(first)[i] if states else 0.0
+        slope = np.exp(-np.abs(hz)) / (1 + np.exp(-np.abs(hz))) ** 2
+        check(host(dx), wx, UNIT * err + 1.001 * U[dtype] * np.abs(wx) + TINY[dtype], "dx")
+        check(host(dz), wz, UNIT * err * (np.abs(prev) + np.abs(hx)) * slope + 1.001 * U[dtype] * np.abs(wz) + TINY[dtype],
+              "dz")
+        if states:
+            check(host(dfirst), wf, UNIT * first_err, "dfirst")
