@@ -11,8 +11,8 @@
 // (one instruction for two).  16384 x 4096 bf16: 78 us by boxes of 32 channels in
 // clusters of two (by cp.async of 64 channels in clusters of four 95; of 128 in clusters
 // of eight, where more blocks wait for one another, 120; of 16 in none, whose rows are
-// sectors of 32 bytes, 157), the gradient 147.  What bounds it is instructions (about 20
-// and 45 an element, at two blocks an SM on two thirds of the SMs) and the steps' waits:
+// sectors of 32 bytes, 157), the gradient 147.  What bounds it is instructions (22 and
+// 45 an element, at two blocks an SM on two thirds of the SMs) and the steps' waits:
 // 75 % of HBM's time; the gradient 80 %.  Four rows a thread with three blocks an SM: 125.
 //
 // Packed sequences: a map that begins a sequence cuts, so that rows are divided
