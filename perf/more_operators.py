@@ -136,7 +136,7 @@ def _plain_scan(c, s):
     prev = torch.cat([torch.zeros_like(h[:1]), h[:-1]])
     prev[begin] = s["first"][at] if c["states"] else 0
     if c["states"]:
-        dh[end] += s["dlast"][at]
+        dh = dh.index_add(0, end, s["dlast"][at])
     down = torch.cat([a[1:], torch.zeros_like(a[:1])])  # what a row's gradient takes from the next row's
     down[end] = 0
     g = _scan32(down.flip(0), dh.flip(0)).flip(0)
