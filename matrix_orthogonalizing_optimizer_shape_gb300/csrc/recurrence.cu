@@ -438,7 +438,11 @@ struct Shared {
   float2 block[2][kMaxCluster][kTile];                            // of the cluster's blocks, in turn in two halves
   unsigned long long bar[2];                                      // of the halves
   unsigned long long full[2];                                     // of the boxes in flight
-  int stop;                                                       // a wait ran out
+  // Waits that ran out: for rows, written before a step's first barrier and read behind
+  // it, and for maps, written between its two barriers and read behind the second.  No
+  // warp can write one while another of the block has yet to read it, so that all threads
+  // leave at the same step.
+  int late, stop;
   int off[kSharedOffsets];
   // A warp reads 32 / kLanes channels of kLanes groups at once: each from other banks.
   static __device__ __forceinline__ int at(int group, int c) { return (c + group / kMaps * (32 / kLanes)) % kTile; }
@@ -470,7 +474,7 @@ __device__ __forceinline__ Vec<VEC> get(const float* p) {
 template <int VEC>
 __device__ __forceinline__ void begin_steps(Shared<VEC>& sh, int size) {
   if (threadIdx.x == 0) {
-    sh.stop = 0;
+    sh.late = sh.stop = 0;
     for (unsigned long long& b : sh.bar) tc::mbar_init(tc::smem_u32(&b), 1);
     for (unsigned long long& b : sh.full) tc::mbar_init(tc::smem_u32(&b), 1);
     tc::mbar_init_fence();
@@ -492,7 +496,8 @@ __device__ __forceinline__ void compose(float& A, float& D, float& B, float A1, 
 }
 template <int VEC, class Then>
 __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, int size, const Map<VEC>& m, bool cut,
-                                          float& carry, unsigned* status, Then&& then) {  // once all have their rows
+                                          float& carry, unsigned* status, bool& stop,
+                                          Then&& then) {  // once all have their rows
   using S = Shared<VEC>;
   constexpr int kTile = S::kTile, kLanes = S::kLanes;
   const int group = threadIdx.x / kAcross, own = S::at(group, threadIdx.x % kAcross * VEC), half = step & 1;
@@ -500,6 +505,7 @@ __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, i
   put<VEC>(&sh.D[group][own], cut ? all<VEC>(kCut) : m.D);
   put<VEC>(&sh.B[group][own], m.B);
   __syncthreads();
+  const bool late = sh.late;
   then();
   const int c = threadIdx.x / kLanes, k = threadIdx.x % kLanes;
   float a[S::kMaps], d[S::kMaps], b[S::kMaps];
@@ -546,6 +552,7 @@ __device__ __forceinline__ Vec<VEC> enter(Shared<VEC>& sh, int step, int rank, i
     if (i + 1 < S::kMaps) h = through(a[i], d[i], b[i], h);
   }
   __syncthreads();
+  stop = late || sh.stop;
   return get<VEC>(&sh.enter[group][own]);
 }
 
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
   Place at;
   int step = 0;
   for (int top = p.r0; top < p.r1; top += stride, row0 += stride, ++step) {
-    if (!in_flight.wait(step, a.status)) sh.stop = 1;
+    if (!in_flight.wait(step, a.status)) sh.late = 1;
     Map<VEC> m;
     Vec<VEC> f[R];  // a and (1 - a) x of the rows
     Vec<VEC> g[R];
@@ -647,10 +654,11 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_kernel(RecurrenceArgs 
       }
     }
     if constexpr (WAY != kTma) fetch(step + F::kAhead);
-    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry, a.status, [&] {
+    bool stop;
+    Vec<VEC> h = enter<VEC>(sh, step, rank, size, m, begins != 0u, carry, a.status, stop, [&] {
       if constexpr (WAY == kTma) fetch(step + F::kAhead);
     });
-    if (sh.stop) {
+    if (stop) {
       for (int i = 1; i <= F::kAhead && WAY == kTma && top + i * stride < p.r1; ++i) in_flight.wait(step + i, a.status);
       break;
     }
@@ -743,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
   int step = 0;
   for (int top = p.r1; top > p.r0; top -= stride, base -= stride, ++step) {
     const bool any = base >= p.r0;
-    if (!in_flight.wait(step, a.status)) sh.stop = 1;
+    if (!in_flight.wait(step, a.status)) sh.late = 1;
     const int row0 = any ? base : p.r0;
     Map<VEC> m;
     Vec<VEC> ga[R], gn[R], dv[R], diff[R];  // a, 1 - a, dh and h_{t-1} - x of the rows
@@ -793,10 +801,11 @@ __global__ void __launch_bounds__(kThreads, 2) recurrence_grad_kernel(Recurrence
       }
     }
     if constexpr (WAY != kTma) fetch(step + F::kAhead);
-    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry, a.status, [&] {
+    bool stop;
+    Vec<VEC> s = enter<VEC>(sh, step, rank, size, m, ends != 0u, carry, a.status, stop, [&] {
       if constexpr (WAY == kTma) fetch(step + F::kAhead);
     });
-    if (sh.stop) {
+    if (stop) {
       for (int i = 1; i <= F::kAhead && WAY == kTma && top - i * stride > p.r0; ++i) in_flight.wait(step + i, a.status);
       break;
     }

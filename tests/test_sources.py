@@ -46,3 +46,22 @@ def test_every_wrapper_is_used():
     for name in (a or b for a, b in names):
         uses = sum(len(re.findall(rf"\b{name}\b", t)) for t in users)
         assert uses > 1, f"{name} is not used"
+
+
+def test_flags_of_waits_that_ran_out_are_read_between_barriers():
+    """A thread that leaves a loop of block barriers alone hangs its block: the recurrence's
+    flags are read where a barrier stands between every write and every read.  `late` is
+    written by the kernels before a step (the call of enter) and read behind enter's first
+    barrier; `stop` is written between enter's barriers and read behind the second."""
+    text = re.sub(r"//[^\n]*", "", sources()["recurrence.cu"])
+    start = text.index("enter(Shared<VEC>& sh")
+    end = text.index("\n}\n", start)
+    enter, others = text[start:end], text[:start] + text[end:]
+    assert not re.search(r"sh\.(late|stop)\b(?! = )", others)  # written, never read
+    assert not re.search(r"sh\.stop = 1", others) and len(re.findall(r"sh\.late = 1", others)) == 2
+    before, between, behind = enter.split("__syncthreads();")
+    assert not re.search(r"sh\.(late|stop)\b", before)
+    assert re.findall(r"sh\.(?:late|stop)\b(?: = 1)?", between) == ["sh.late", "sh.stop = 1"]
+    assert re.findall(r"sh\.(?:late|stop)\b(?: = 1)?", behind) == ["sh.stop"]
+    for call in re.finditer(r"= enter<VEC>\(", others):  # each step's writes of `late` stand before its call
+        assert "sh.late = 1" in others[others.rindex("in_flight.wait(step,", 0, call.start()):call.start()]
