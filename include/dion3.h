@@ -615,7 +615,10 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* args, void* ws,
  * The conventions of the layer operators hold: matrices of any row pitch and
  * element-aligned base, fp32 sums and statistics, the same bits from call to
  * call.  Token numbers (ids, targets) are device vectors of 4- or 8-byte signed
- * integers (id_bytes).
+ * integers (id_bytes).  A result may take the place of another argument (the same
+ * memory at the same pitch) where its page says so, and shares no element with one
+ * otherwise (columns of one matrix interleave without doing so); calls whose
+ * matrices, states or row values do are refused.
  * ------------------------------------------------------------------------ */
 
 /*

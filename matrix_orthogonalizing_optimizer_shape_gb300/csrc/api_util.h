@@ -4,6 +4,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <numeric>
 
 #include "../../include/dion3.h"
 #include "layer.h"
@@ -84,6 +85,35 @@ inline dion3_status check_inject() {
 
 inline Mat mat(const dion3_matrix& m) { return {m.data, m.ld}; }
 inline Mat mat(const dion3_matrix* m) { return m == nullptr ? Mat{} : mat(*m); }
+
+// The memory of an argument: rows of `row` bytes, `pitch` bytes apart (0: one row).
+struct Extent {
+  uintptr_t lo = 0, hi = 0;  // both 0: nothing
+  unsigned long long pitch = 0, row = 0;
+};
+inline Extent extent_of(const void* p, long long rows, long long cols, long long ld, int bytes) {
+  if (p == nullptr || rows <= 0 || cols <= 0) return {};
+  const unsigned long long row = cols * bytes, pitch = rows > 1 ? ld * bytes : 0;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, static_cast<uintptr_t>(lo + (rows - 1) * pitch + row), pitch, row};
+}
+inline Extent extent_of(const dion3_matrix* m, int32_t rows, int32_t cols) {
+  return m == nullptr ? Extent{} : extent_of(m->data, rows, cols, m->ld, bytes_of(m->dtype));
+}
+inline Extent extent_of(const float* p, int32_t rows, int32_t cols) { return extent_of(p, rows, cols, cols, 4); }
+// Whether two may share elements: they overlap and are not different columns or rows of
+// one matrix, apart modulo what both pitches are multiples of.
+inline bool meet(const Extent& a, const Extent& b) {
+  if (a.lo > b.lo) return meet(b, a);
+  if (b.lo >= a.hi || b.lo == b.hi) return false;
+  const unsigned long long pitch = std::gcd(a.pitch, b.pitch);
+  if (pitch == 0) return true;
+  const unsigned long long at = (b.lo - a.lo) % pitch;
+  return !(at >= a.row && at + b.row <= pitch);
+}
+inline bool same_place(const Extent& a, const Extent& b) {
+  return a.lo == b.lo && a.hi == b.hi && a.pitch == b.pitch && a.row == b.row;
+}
 
 // Hands out 256-byte aligned pieces of a workspace (base NULL: sizes only).
 struct Carve {

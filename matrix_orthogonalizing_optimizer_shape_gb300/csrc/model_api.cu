@@ -6,7 +6,6 @@
 #include <algorithm>
 #include <memory>
 #include <new>
-#include <numeric>
 
 namespace dion3 {
 namespace {
@@ -69,45 +68,52 @@ dion3_status check_tensor(const char* name, int32_t i, const dion3_tensor& t) {
   return DION3_OK;
 }
 
-// The memory of a tensor of a call that clips.
-struct Extent {
-  uintptr_t lo, hi;
-  unsigned long long pitch, row;  // bytes from row to row (0: one row) and of a row
+// What a call reads or writes.  `may`: bits of the arguments before this one whose place
+// (all of their memory, at the same pitch) it may take.
+struct Arg {
+  const char* name;
+  Extent e;
+  bool written;
+  unsigned may = 0;
+};
+// Refuses results that share memory with other arguments: some rows would be read behind
+// the writes of others.
+template <size_t N>
+dion3_status check_args_apart(const Arg (&a)[N]) {
+  for (size_t j = 1; j < N; ++j)
+    for (size_t i = 0; i < j; ++i)
+      if ((a[i].written || a[j].written) && meet(a[i].e, a[j].e) && !((a[j].may >> i & 1) && same_place(a[i].e, a[j].e)))
+        return fail(DION3_ERR_INVALID_ARG, "%s and %s share memory", a[i].name, a[j].name);
+  return DION3_OK;
+}
+
+// A tensor of a call that clips.
+struct Part : Extent {
   int32_t i;
   bool written;
 };
-Extent extent_of(const dion3_tensor& t, int32_t i, bool written) {
-  const unsigned long long es = bytes_of(t.dtype), row = t.cols * es, pitch = t.rows > 1 ? t.ld * es : 0;
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data);
-  return {lo, static_cast<uintptr_t>(lo + (t.rows - 1) * pitch + row), pitch, row, i, written};
-}
-// Whether two that overlap are different columns or rows of one matrix (a.lo <= b.lo):
-// apart modulo what both pitches are multiples of.
-bool interleaved(const Extent& a, const Extent& b) {
-  const unsigned long long pitch = std::gcd(a.pitch, b.pitch);
-  if (pitch == 0) return false;
-  const unsigned long long at = (b.lo - a.lo) % pitch;
-  return at >= a.row && at + b.row <= pitch;
+Part part_of(const dion3_tensor& t, int32_t i, bool written) {
+  return {extent_of(t.data, t.rows, t.cols, t.ld, bytes_of(t.dtype)), i, written};
 }
 // Refuses tensors whose elements several would write, or one write and another read.
 dion3_status check_apart(const dion3_tensor* in, const dion3_tensor* out, int32_t n) {
-  std::unique_ptr<Extent[]> all(new (std::nothrow) Extent[2 * static_cast<size_t>(n)]);
+  std::unique_ptr<Part[]> all(new (std::nothrow) Part[2 * static_cast<size_t>(n)]);
   if (all == nullptr) return fail(DION3_ERR_UNSUPPORTED, "no host memory for %d tensors", n);
   size_t m = 0;
   for (int32_t i = 0; i < n; ++i) {
     if (in[i].rows == 0 || in[i].cols == 0) continue;
     if (out == nullptr) {
-      all[m++] = extent_of(in[i], i, true);
+      all[m++] = part_of(in[i], i, true);
       continue;
     }
-    const Extent a = extent_of(in[i], i, false), b = extent_of(out[i], i, true);
+    const Part a = part_of(in[i], i, false), b = part_of(out[i], i, true);
     all[m++] = b;
     if (a.lo != b.lo || in[i].dtype != out[i].dtype || (in[i].rows > 1 && in[i].ld != out[i].ld)) all[m++] = a;
   }
-  std::sort(all.get(), all.get() + m, [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+  std::sort(all.get(), all.get() + m, [](const Part& a, const Part& b) { return a.lo < b.lo; });
   for (size_t j = 0; j < m; ++j)
     for (size_t k = j + 1; k < m && all[k].lo < all[j].hi; ++k)
-      if ((all[j].written || all[k].written) && !interleaved(all[j], all[k]))
+      if ((all[j].written || all[k].written) && meet(all[j], all[k]))
         return fail(DION3_ERR_INVALID_ARG, "tensors %d and %d share elements", std::min(all[j].i, all[k].i),
                     std::max(all[j].i, all[k].i));
   return DION3_OK;
@@ -169,6 +175,10 @@ dion3_status dion3_embedding(int32_t tokens, int32_t vocab, int32_t cols, const 
   DION3_TRY(check_any("y", y, tokens, cols));
   DION3_TRY(check_finite("scale", scale));
   if (tokens > 0 && y->data == table->data) return fail(DION3_ERR_INVALID_ARG, "y may not be table");
+  const Arg args[] = {{"ids", extent_of(ids, 1, tokens, tokens, id_bytes), false},
+                      {"table", extent_of(table, vocab, cols), false},
+                      {"y", extent_of(y, tokens, cols), true}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (tokens == 0) return ok();
   EmbedArgs a{tokens, vocab, cols, {ids, id_bytes}, mat(table), table->dtype, mat(y), y->dtype, scale};
@@ -211,6 +221,11 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
   DION3_TRY(check_finite("scale", scale));
   if (tokens > 0 && dtable->data != nullptr && dy->data == dtable->data)
     return fail(DION3_ERR_INVALID_ARG, "dtable may not be dy");
+  const Arg args[] = {{"ids", extent_of(ids, 1, tokens, tokens, id_bytes), false},
+                      {"dy", extent_of(dy, tokens, cols), false},
+                      {"dtable", extent_of(dtable, vocab, cols), true},
+                      {"workspace", extent_of(ws, 1, need, need, 1), true}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_ws(ws, ws_bytes, need));
   DION3_TRY(check_inject());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -249,6 +264,12 @@ dion3_status dion3_recurrence(int32_t tokens, int32_t channels, const dion3_matr
   DION3_TRY(check_f32("last", last));
   if ((same(h, z) && h->ld != z->ld) || (same(h, x) && h->ld != x->ld))
     return fail(DION3_ERR_INVALID_ARG, "h in the place of z or x needs its pitch");
+  const Arg args[] = {{"z", extent_of(z, tokens, channels), false},
+                      {"x", extent_of(x, tokens, channels), false},
+                      {"first", extent_of(first, sequences, channels), false},
+                      {"h", extent_of(h, tokens, channels), true, 3u},
+                      {"last", extent_of(last, sequences, channels), true, 4u}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (sequences == 0 || (tokens == 0 && last == nullptr)) return ok();
   RecurrenceArgs a{};
@@ -295,6 +316,16 @@ dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const d
         return fail(DION3_ERR_INVALID_ARG, "dz or dx in the place of an input needs its pitch");
   if (first != nullptr && (first == dfirst))
     return fail(DION3_ERR_INVALID_ARG, "dfirst may not be first");
+  const Arg args[] = {{"dh", extent_of(dh, tokens, channels), false},
+                      {"z", extent_of(z, tokens, channels), false},
+                      {"x", extent_of(x, tokens, channels), false},
+                      {"h", extent_of(h, tokens, channels), false},
+                      {"first", extent_of(first, sequences, channels), false},
+                      {"dlast", extent_of(dlast, sequences, channels), false},
+                      {"dz", extent_of(dz, tokens, channels), true, 7u},
+                      {"dx", extent_of(dx, tokens, channels), true, 7u},
+                      {"dfirst", extent_of(dfirst, sequences, channels), true, 1u << 5}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (sequences == 0 || (tokens == 0 && dfirst == nullptr)) return ok();
   RecurrenceArgs a{};
@@ -334,6 +365,13 @@ dion3_status dion3_log_probs(int32_t rows, int32_t vocab, const dion3_matrix* lo
   if (rows > 0 && logp != nullptr && targets == nullptr) return fail(DION3_ERR_INVALID_ARG, "logp is given without targets");
   if (top < 0 || top > kMaxTop || top > vocab)
     return fail(DION3_ERR_INVALID_ARG, "top must lie in [0, %d] (got %d)", std::min(kMaxTop, vocab), top);
+  const Arg args[] = {{"logits", extent_of(logits, rows, vocab), false},
+                      {"logp", extent_of(logp, rows, 1), true},
+                      {"entropy", extent_of(entropy, rows, 1), true},
+                      {"stats", extent_of(stats, rows, 3), true},
+                      {"top_values", extent_of(top_values, rows, top), true},
+                      {"top_ids", extent_of(top_ids, rows, top, top, 4), true}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (rows == 0) return ok();
   LogProbArgs a{};
@@ -369,6 +407,13 @@ dion3_status dion3_log_probs_backward(int32_t rows, int32_t vocab, const dion3_m
   if (rows > 0 && dlogp != nullptr && targets == nullptr) return fail(DION3_ERR_INVALID_ARG, "dlogp is given without targets");
   if (same(logits, dlogits) && logits->ld != dlogits->ld)
     return fail(DION3_ERR_INVALID_ARG, "dlogits in the place of logits needs its pitch");
+  const Arg args[] = {{"logits", extent_of(logits, rows, vocab), false},
+                      {"targets", targets == nullptr ? Extent{} : extent_of(targets, 1, rows, rows, target_bytes), false},
+                      {"stats", extent_of(stats, rows, 3), false},
+                      {"dlogp", extent_of(dlogp, rows, 1), false},
+                      {"dentropy", extent_of(dentropy, rows, 1), false},
+                      {"dlogits", extent_of(dlogits, rows, vocab), true, 1u}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (rows == 0) return ok();
   LogProbGradArgs a{rows,  vocab, logits->dtype, mat(logits), scale, {targets, target_bytes},
