@@ -456,7 +456,10 @@ dion3_status dion3_flush_row_scale(int32_t rows, int32_t cols, int32_t batch,
  * and are the same bits from call to call.  A matrix with zero rows (tokens)
  * is valid and may have a NULL base: forward calls then enqueue nothing, and a
  * gradient summed over the tokens is zero (or unchanged, when accumulated).
- * Sums and norms are fp32.  NaN and infinity propagate as in the formulas.
+ * Sums and norms are fp32.  NaN and infinity propagate as in the formulas.  A
+ * result may take the place of an argument (the same memory at the same pitch)
+ * where its page says so; one that shares some elements otherwise (one row behind
+ * it, say) of a matrix over the tokens that a kernel reads beside it is refused.
  * ------------------------------------------------------------------------ */
 
 /* A row-major matrix: rows and columns come from the call. data NULL: absent. */

@@ -115,6 +115,25 @@ inline bool same_place(const Extent& a, const Extent& b) {
   return a.lo == b.lo && a.hi == b.hi && a.pitch == b.pitch && a.row == b.row;
 }
 
+// What a call reads or writes.  `may`: bits of the arguments before this one whose place
+// (all of their memory, at the same pitch) it may take.
+struct Arg {
+  const char* name;
+  Extent e;
+  bool written;
+  unsigned may = 0;
+};
+// Refuses results that share memory with other arguments: some rows would be read behind
+// the writes of others.
+template <size_t N>
+inline dion3_status check_args_apart(const Arg (&a)[N]) {
+  for (size_t j = 1; j < N; ++j)
+    for (size_t i = 0; i < j; ++i)
+      if ((a[i].written || a[j].written) && meet(a[i].e, a[j].e) && !((a[j].may >> i & 1) && same_place(a[i].e, a[j].e)))
+        return fail(DION3_ERR_INVALID_ARG, "%s and %s share memory", a[i].name, a[j].name);
+  return DION3_OK;
+}
+
 // Hands out 256-byte aligned pieces of a workspace (base NULL: sizes only).
 struct Carve {
   char* base;

@@ -63,6 +63,9 @@ struct Staging {
   }
 };
 
+// Results of the layer operators may take any place that no check by name refuses.
+constexpr unsigned kAnyPlace = ~0u;
+
 dion3_status check_act(int32_t act) {
   return act < DION3_ACT_NONE || act > DION3_ACT_SILU ? fail(DION3_ERR_INVALID_ARG, "unknown activation %d", act)
                                                       : DION3_OK;
@@ -129,6 +132,11 @@ dion3_status dion3_rms_norm(int32_t rows, int32_t cols, const dion3_matrix* x, c
   if (present(y8)) DION3_TRY(check_pack("y8", *y8, rows, cols));
   if (rows > 0 && (y == nullptr || y->data == nullptr) && !present(y8))
     return fail(DION3_ERR_INVALID_ARG, "neither y nor y8 is given");
+  const Arg args[] = {{"x", extent_of(x, rows, cols), false},
+                      {"residual", extent_of(residual, rows, cols), false},
+                      {"h", extent_of(h, rows, cols), true, kAnyPlace},
+                      {"y", extent_of(y, rows, cols), true, kAnyPlace}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (rows == 0) return ok();
   NormArgs a{};
@@ -174,6 +182,11 @@ dion3_status dion3_rms_norm_backward(int32_t rows, int32_t cols, const dion3_mat
   DION3_TRY(check_f32("rstd", rstd));
   DION3_TRY(check_f32("dw", dw));
   if (rows > 0 && rstd == nullptr) return fail(DION3_ERR_INVALID_ARG, "rstd is NULL");
+  const Arg args[] = {{"dy", extent_of(dy, rows, cols), false},
+                      {"h", extent_of(h, rows, cols), false},
+                      {"dh", extent_of(dh, rows, cols), false},
+                      {"dx", extent_of(dx, rows, cols), true, kAnyPlace}};
+  DION3_TRY(check_args_apart(args));
   size_t need = 0;
   DION3_TRY(dion3_rms_norm_backward_workspace_size(rows, cols, &need));
   DION3_TRY(check_ws(ws, ws_bytes, dw != nullptr ? need : 0));
@@ -244,6 +257,11 @@ dion3_status dion3_linear(const dion3_linear_args* g, void* ws, size_t ws_bytes,
     if (T <= N && worth_copy(x, T, K, N)) x = copies.add(c, x, T, K, true);
     if (T > N && worth_copy(w, N, K, T)) w = copies.add(c, w, N, K, true);
   }
+  const Arg args[] = {{"x", extent_of(x.p, T, K, x.ld, 2), false},  // what the product reads: x or its copy
+                      {"residual", extent_of(&g->residual, T, N), false},
+                      {"y", extent_of(&g->y, T, N), true, kAnyPlace},
+                      {"z", extent_of(&g->z, T, N), true, kAnyPlace}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   if (T == 0) return ok();
   unsigned* st = device_status_ptr();
@@ -337,6 +355,10 @@ dion3_status dion3_linear_backward(const dion3_linear_grad_args* g, void* ws, si
   }
   if (want_dx) w = copies.add(c, mat(g->w), N, K);
   DION3_TRY(check_ws(ws, ws_bytes, T > 0 ? c.off : 0));
+  const Arg args[] = {{"dy", extent_of(dz.p, T, N, dz.ld, 2), false},  // what the products read, each or its copy
+                      {"x", extent_of(x.p, T, K, x.ld, 2), false},
+                      {"dx", extent_of(&g->dx, T, K), true, kAnyPlace}};
+  DION3_TRY(check_args_apart(args));
   DION3_TRY(check_inject());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) {
