@@ -89,6 +89,22 @@ __device__ __forceinline__ Vec<VEC> mul(const Vec<VEC>& a, const Vec<VEC>& b) {
   }
   return r;
 }
+// a / 2, 0 where that is below 2^-126.
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> half_of(const Vec<VEC>& a) {
+  Vec<VEC> r;
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      unsigned long long d;
+      asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a[j], a[j + 1])), "l"(pair(0.5f, 0.5f)));
+      unpair(d, r[j], r[j + 1]);
+    }
+  } else {
+    asm("mul.rn.ftz.f32 %0, %1, 0f3F000000;" : "=f"(r[0]) : "f"(a[0]));
+  }
+  return r;
+}
 template <int VEC>
 __device__ __forceinline__ Vec<VEC> add(const Vec<VEC>& a, const Vec<VEC>& b) {
   Vec<VEC> r;
@@ -281,27 +297,29 @@ __device__ __forceinline__ void load_states(Vec<VEC> (&to)[R], const float* from
 }
 
 // --------------------------------------------------------------------------
-// Gates.  a = 1 / (1 + u) and 1 - a = u a with u = e^-z: each accurate relative
-// to itself, by two special function instructions.  u stops at 2^126, where the
-// product is still 1, and 2^-126 taken off a makes a 0 there (nowhere else does
-// it change a): z = -infinity forgets.
+// Gates.  With u = e^-z / 2 and r = 1 / (u + 1/2), by two special function
+// instructions, a = r / 2 and 1 - a = u r: each accurate relative to itself, to some
+// units of 2^-23 for small |z| and to 6e-6 at |z| = 87, where the exponent's argument is
+// rounded at 2^-18.  u stops at 2^126, where r is 2^-126 and the product still 1; halving
+// flushes, so that a is 0 there (as everywhere below 2^-126; 1 - a is below 2^-125):
+// z = -infinity forgets.
 // --------------------------------------------------------------------------
 template <int VEC>
 struct Gate {
   Vec<VEC> a, na;
   __device__ __forceinline__ explicit Gate(const Vec<VEC>& z) {
-    const Vec<VEC> e = mul(z, all<VEC>(-kLog2E));
+    const Vec<VEC> e = fma(z, all<VEC>(-kLog2E), all<VEC>(-1.f));
     Vec<VEC> u, r;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u[j]) : "f"(e[j]));
       asm("min.NaN.f32 %0, %1, 0f7E800000;" : "=f"(u[j]) : "f"(u[j]));
     }
-    const Vec<VEC> s = add(u, all<VEC>(1.f));
+    const Vec<VEC> s = add(u, all<VEC>(0.5f));
 #pragma unroll
     for (int j = 0; j < VEC; ++j) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[j]) : "f"(s[j]));
     na = mul(u, r);
-    a = add(r, all<VEC>(-0x1p-126f));
+    a = half_of(r);
   }
 };
 
