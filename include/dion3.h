@@ -666,8 +666,10 @@ dion3_status dion3_embedding_backward(int32_t tokens, int32_t vocab, int32_t col
  *   last       fp32 [sequences][channels], dense: receives the states after each
  *              sequence (those before it where it has no rows), or NULL.  May be
  *              first.
- * z = -infinity forgets (h_t = x_t), z = +infinity keeps (h_t = h_{t-1}, of a finite
- * x_t: 0 times another is NaN).
+ * z = -infinity forgets (h_t = x_t, of a finite h_{t-1}), z = +infinity keeps (h_t =
+ * h_{t-1}, of a finite x_t): 0 times another is NaN.  After a state that is not finite
+ * no later one of its channel and sequence is; whether one reads infinity or NaN
+ * depends on how the rows are divided.  Other sequences and channels are not affected.
  * channels <= 2^19, sequences <= 2^27.  Offsets that do not ascend give undefined
  * values in the rows, but no access outside the matrices.
  */
@@ -686,6 +688,7 @@ dion3_status dion3_recurrence(int32_t tokens, int32_t channels, const dion3_matr
  *              or dh (in place), but not h nor one another.
  *   first, dlast, dfirst  fp32 [sequences][channels], dense, or NULL (first: 0,
  *              dlast: 0).  dfirst may be dlast.
+ * A g_t that is not finite leaves none that is in the rows before it, as above.
  */
 dion3_status dion3_recurrence_backward(int32_t tokens, int32_t channels, const dion3_matrix* dh,
                                        const dion3_matrix* z, const dion3_matrix* x,

@@ -328,7 +328,9 @@ struct Gate {
 // map is applied as h - D h + B, since a factor near 1 that were rounded would decay
 // the state at a rate that is off in every one of thousands of rows.  D = 2 cuts:
 // nothing passes.  Between blocks a map's factor is one number: A up to a half, else
-// -D with its sign bit set, or 2.
+// -D with its sign bit set, or 2.  An infinite h stays infinite by A and becomes NaN by
+// -D, and by an A that has underflowed: never finite, which is all that is promised (a
+// select by |h| could not tell an underflowed A from a gate of 0).
 // --------------------------------------------------------------------------
 constexpr float kCut = 2.f;
 __device__ __forceinline__ float through(float A, float D, float B, float h) {

@@ -117,7 +117,8 @@ def recurrence(z, x, h, *, offsets=None, first=None, last=None, stream=None):
     """h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(z), along the rows of each
     sequence: rows offsets[i] to offsets[i + 1], int32 (None: all rows are one).
     ``first`` and ``last`` are the states before and after each sequence, float32
-    [sequences, channels] (see dion3_recurrence)."""
+    [sequences, channels].  After a state that is not finite no later one of its channel
+    and sequence is (see dion3_recurrence)."""
     mz = _MAT.pack(*_mat("z", z))
     (tokens, channels), dev = z.shape, z.get_device()
     mx, mh = (_MAT.pack(*_mat(name, t, tokens, channels, dev)) for name, t in (("x", x), ("h", h)))
