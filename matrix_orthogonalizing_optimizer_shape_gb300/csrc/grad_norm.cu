@@ -437,6 +437,24 @@ int blocks_for(unsigned chunks, int per_sm) {
   return static_cast<int>(std::min<unsigned>(chunks, static_cast<unsigned>(std::min(per_sm * sm_count(), kMaxGradPartials))));
 }
 
+// Whether the current device holds a cluster past 8 blocks of the kernel for small sets: a
+// part of a device may not, and takes the other launches.  Asked once a device, with the
+// attribute that its launches need.
+bool holds_small_cluster(const cudaLaunchConfig_t& cfg) {
+  constexpr int kDevices = 64;
+  static std::atomic<signed char> known[kDevices];  // 0: not asked, 1: yes, -1: no
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return false;
+  if (device < kDevices && known[device].load(std::memory_order_acquire) != 0) return known[device].load() > 0;
+  int clusters = 0;
+  const bool holds =
+      cudaFuncSetAttribute(grad_clip_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, grad_clip_small_kernel, &cfg) == cudaSuccess && clusters > 0;
+  if (!holds) cudaGetLastError();
+  if (device < kDevices) known[device].store(holds ? 1 : -1, std::memory_order_release);
+  return holds;
+}
+
 }  // namespace
 
 cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_norm, bool in_place, float* norm,
@@ -448,17 +466,6 @@ cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_no
                                                            [&](const auto& tab, int count, unsigned chunks) {
       if constexpr (sizeof(tab.t) == sizeof(Table<kFew>)) {
         if (chunks > kSmallChunks) return cudaSuccess;
-        done = true;
-        static std::atomic<unsigned long long> asked{0};  // a cluster past 8 blocks; once a device
-        int device = 0;
-        cudaError_t r = cudaGetDevice(&device);
-        if (r != cudaSuccess) return r;
-        const unsigned long long bit = device < 64 ? 1ull << device : 0;
-        if (bit == 0 || !(asked.load(std::memory_order_acquire) & bit)) {
-          r = cudaFuncSetAttribute(grad_clip_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-          if (r != cudaSuccess) return r;
-          asked.fetch_or(bit, std::memory_order_release);
-        }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kSmallCluster);
         cfg.blockDim = dim3(kThreads);
@@ -469,7 +476,10 @@ cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, float max_no
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (!holds_small_cluster(cfg)) return cudaSuccess;
         cfg.numAttrs = pdl_enabled() ? 2 : 1;
+        done = true;
         return cudaLaunchKernelEx(&cfg, grad_clip_small_kernel, tab, count, chunks, max_norm, in_place, norm);
       }
       return cudaSuccess;

@@ -65,3 +65,14 @@ def test_flags_of_waits_that_ran_out_are_read_between_barriers():
     assert re.findall(r"sh\.(?:late|stop)\b(?: = 1)?", behind) == ["sh.stop"]
     for call in re.finditer(r"= enter<VEC>\(", others):  # each step's writes of `late` stand before its call
         assert "sh.late = 1" in others[others.rindex("in_flight.wait(step,", 0, call.start()):call.start()]
+
+
+def test_large_clusters_are_asked_for():
+    """A kernel that may run in clusters past the 8 blocks that every device holds asks
+    whether this one (or the part of it that the process has) holds them."""
+    found = 0
+    for name, text in sources().items():
+        for m in re.finditer(r"cudaFuncAttributeNonPortableClusterSizeAllowed", text):
+            found += 1
+            assert "cudaOccupancyMaxActiveClusters" in text[m.start():m.start() + 600], name
+    assert found == 2
