@@ -73,6 +73,16 @@ assert (_MAT.size, _PACK.size, _LINEAR.size, _LINEAR_GRAD.size) == tuple(
     map(ctypes.sizeof, (_Matrix, _Packed8, _LinearArgs, _LinearGradArgs)))
 _NO_MAT, _NO_PACK = (0, 0, 0), (0, 0, 0, 0)
 
+#: The largest size that a call can name: ctypes keeps the low 32 bits of a larger one.
+_MOST = 2 ** 31 - 1
+
+
+def _sizes(*sizes: int):
+    """Refuses sizes that a call cannot name."""
+    if max(sizes) > _MOST:
+        raise ValueError(f"a size of {max(sizes)} is larger than any operator takes")
+
+
 _FNS = {}
 _torch = _I8 = _U8 = None
 _DTYPES = {}
@@ -140,15 +150,16 @@ def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None, d
     try:
         (r, c), (ld, inner) = t.shape, t.stride()
         if ((t.is_cuda if dev is None else t.get_device() == dev) and inner == 1 and ld >= c
-                and (rows is None or r == rows) and (cols is None or c == cols)):
+                and (r <= _MOST if rows is None else r == rows) and (c <= _MOST if cols is None else c == cols)):
             return t.data_ptr(), ld, _DTYPES[t.dtype]
     except (ValueError, KeyError):
         pass
     return _mat_checked(name, t, rows, cols, dev)
 
 
-def _mat_checked(name: str, t, rows, cols, dev) -> tuple:
-    """The same, case by case: what is wrong, or the layouts whose strides say nothing."""
+def _mat_checked(name: str, t, rows, cols, dev, named: bool = True) -> tuple:
+    """The same, case by case: what is wrong, or the layouts whose strides say nothing.
+    `named`: the call names the sizes in 32 bits."""
     _on(name, t, dev)
     shape = t.shape
     if len(shape) != 2:
@@ -157,6 +168,8 @@ def _mat_checked(name: str, t, rows, cols, dev) -> tuple:
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} is {r} x {c}, {rows if rows is not None else r} x "
                          f"{cols if cols is not None else c} is wanted")
+    if named:
+        _sizes(r, c)
     ld, inner = t.stride()
     if inner != 1 and c > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -264,6 +277,7 @@ def unpack8(src: Packed8, out, stream=None):
     """The values that 8-bit blocks stand for, in out's dtype (see dion3_unpack8)."""
     p = _PACK.pack(*_packed("src", src))
     (rows, cols), dev = src.codes.shape, src.codes.get_device()
+    _sizes(rows, cols)
     _d3._check(_fn("dion3_unpack8")(rows, cols, p, _MAT.pack(*_mat("out", out, rows, cols, dev)),
                                     _stream(stream, dev)))
 
@@ -287,6 +301,7 @@ def rms_norm(x, weight, y=None, *, residual=None, h=None, y8: Optional[Packed8] 
 
 
 def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    _sizes(rows, cols)
     out = _sz(0)
     _d3._check(_d3.load_library().dion3_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)))
     return out.value
@@ -309,6 +324,7 @@ def rms_norm_backward(dy, h, weight, rstd, dx, *, dh=None, dw=None, accumulate: 
 def _ws_size(fn: str, tokens, in_features, out_features, dtype, strided) -> int:
     import torch
     code = {torch.float32: _d3.F32, torch.bfloat16: _d3.BF16, torch.float16: _d3.F16}.get(dtype, -1)
+    _sizes(tokens, in_features, out_features)
     out = _sz(0)
     _d3._check(getattr(_d3.load_library(), fn)(tokens, in_features, out_features, code, int(strided),
                                                ctypes.byref(out)))

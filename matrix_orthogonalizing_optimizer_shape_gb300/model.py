@@ -72,6 +72,7 @@ def embedding(ids, table, y, *, scale: float = 1.0, stream=None):
 
 
 def embedding_backward_workspace_size(tokens: int, vocab: int, cols: int) -> int:
+    _l._sizes(tokens, vocab, cols)
     out = _sz(0)
     _d3._check(_d3.load_library().dion3_embedding_backward_workspace_size(tokens, vocab, cols, ctypes.byref(out)))
     return out.value
@@ -100,6 +101,7 @@ def _offsets(t, dev: int) -> tuple:
         raise ValueError("offsets must be int32")
     if t.shape[0] < 1:
         raise ValueError("offsets must hold one number more than there are sequences")
+    _l._sizes(t.shape[0])
     return p, t.shape[0] - 1
 
 
@@ -231,7 +233,7 @@ def _tensors(name: str, ts: Sequence, dev: int) -> bytes:
             n = t.numel()
             fields += t.data_ptr(), 1, n, n, _l._dtype(t)
         else:
-            p, ld, dtype = _mat(name, t, None, None, dev)
+            p, ld, dtype = _l._mat_checked(name, t, None, None, dev, named=False)
             fields += p, t.shape[0], t.shape[1], ld, dtype
     return _pack_tensors(fields)
 
@@ -291,6 +293,6 @@ def _rows(name: str, ts: Sequence, others: Sequence, dev: int) -> bytes:
         if t.is_contiguous() and o.is_contiguous():
             fields.append(_tensors(name, (t,), dev))
         else:
-            p, ld, dtype = _mat(name, t, None, None, dev)
+            p, ld, dtype = _l._mat_checked(name, t, None, None, dev, named=False)
             fields.append(_pack_tensors([p, t.shape[0], t.shape[1], ld, dtype]))
     return b"".join(fields)
