@@ -8,17 +8,19 @@
 // rows of VEC channels, a few lanes a channel compose those of a block's threads, the
 // blocks exchange theirs, and each thread runs through its rows again from the state
 // before them, the next rows' loads in flight.  Arithmetic is on pairs of channels
-// (one instruction for two).  16384 x 4096 bf16: 78 us by boxes of 32 channels in
+// (one instruction for two).  16384 x 4096 bf16: 80 us by boxes of 32 channels in
 // clusters of two (by cp.async of 64 channels in clusters of four 95; of 128 in clusters
 // of eight, where more blocks wait for one another, 120; of 16 in none, whose rows are
-// sectors of 32 bytes, 157), the gradient 147.  What bounds it is instructions (22 and
-// 45 an element, at two blocks an SM on two thirds of the SMs) and the steps' waits:
-// 75 % of HBM's time; the gradient 80 %.  Four rows a thread with three blocks an SM: 125.
+// sectors of 32 bytes, 157), the gradient 148: 74 and 80 % of what their bytes take.
+// What bounds both is latency: 128 registers leave two blocks, 16 warps, an SM (on two
+// thirds of the SMs), which stand at two barriers and an exchange a step; 23 and 45
+// instructions an element keep the issue slots 53 and 58 % and DRAM 56 and 66 % busy.
+// Four rows a thread with three blocks an SM: 125.
 //
 // Packed sequences: a map that begins a sequence cuts, so that rows are divided
 // evenly whatever the sequences' lengths; nothing of the rows before a cut, NaN
 // included, passes it.  Warps whose rows hold a boundary pick by it in each row, without
-// a branch (64 sequences: 103 us; row by row behind conditions 120).  Where the
+// a branch (64 sequences: 98 us; row by row behind conditions 120).  Where the
 // channels are few, groups of whole sequences go to different clusters.
 #include <algorithm>
 #include <atomic>
