@@ -86,14 +86,17 @@ inline dion3_status check_inject() {
 inline Mat mat(const dion3_matrix& m) { return {m.data, m.ld}; }
 inline Mat mat(const dion3_matrix* m) { return m == nullptr ? Mat{} : mat(*m); }
 
-// The memory of an argument: rows of `row` bytes, `pitch` bytes apart (0: one row).
+// The memory of an argument: rows of `row` bytes, `pitch` bytes apart (0: one row, as
+// dense ones are together).
 struct Extent {
   uintptr_t lo = 0, hi = 0;  // both 0: nothing
   unsigned long long pitch = 0, row = 0;
 };
 inline Extent extent_of(const void* p, long long rows, long long cols, long long ld, int bytes) {
   if (p == nullptr || rows <= 0 || cols <= 0) return {};
-  const unsigned long long row = cols * bytes, pitch = rows > 1 ? ld * bytes : 0;
+  using ull = unsigned long long;
+  const bool one = rows == 1 || ld == cols;
+  const ull row = static_cast<ull>(cols) * bytes * (one ? rows : 1), pitch = one ? 0 : static_cast<ull>(ld) * bytes;
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   return {lo, static_cast<uintptr_t>(lo + (rows - 1) * pitch + row), pitch, row};
 }

@@ -88,3 +88,19 @@ def test_against_the_sets_of_elements(status):
             assert got == "z and h share memory", (rows, cols, ld, start)
         seen.add((meets, same, got))
     assert len(seen) >= 3
+
+
+@pytest.mark.parametrize("call,kw,meets", [
+    # Dense results in the gaps between the rows of a matrix with a pitch: row values, states, whole matrices.
+    (log_probs, dict(logits=M(ld=192), targets=D, logp=FAKE + 128), False),
+    (log_probs, dict(logits=M(ld=192), targets=D, logp=FAKE + 128, stats=FAKE + 144), False),
+    (log_probs, dict(logits=M(ld=192), targets=D, logp=FAKE + 384 - 12), True),
+    (log_probs, dict(logits=M(ld=192), targets=D, logp=FAKE + 384 - 16), False),
+    (recurrence, dict(z=M(data=A, ld=1024), last=A + 128), False), (recurrence, dict(z=M(data=A, ld=1024), last=A + 2048 - 508), True),
+    (recurrence, dict(z=M(data=A, ld=1024), h=M(data=A + 128)), False), (recurrence, dict(z=M(data=A, ld=1024), h=M(data=A + 126)), True),
+    (recurrence, dict(z=M(data=A, ld=1024), h=M(data=A + 2048 - 512)), False),
+    (recurrence, dict(z=M(data=A, ld=1024), h=M(data=A + 2048 - 510)), True),
+    (embedding, dict(y=M(data=A - 512)), False), (embedding, dict(y=M(data=A - 510)), True),
+])
+def test_dense_results_between_rows(status, call, kw, meets):
+    assert ("share memory" in status(call, **kw)) == meets
