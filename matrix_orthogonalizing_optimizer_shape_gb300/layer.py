@@ -157,9 +157,8 @@ def _mat(name: str, t, rows: Optional[int] = None, cols: Optional[int] = None, d
     return _mat_checked(name, t, rows, cols, dev)
 
 
-def _mat_checked(name: str, t, rows, cols, dev, named: bool = True) -> tuple:
-    """The same, case by case: what is wrong, or the layouts whose strides say nothing.
-    `named`: the call names the sizes in 32 bits."""
+def _mat_checked(name: str, t, rows, cols, dev) -> tuple:
+    """The same, case by case: what is wrong, or the layouts whose strides say nothing."""
     _on(name, t, dev)
     shape = t.shape
     if len(shape) != 2:
@@ -168,8 +167,7 @@ def _mat_checked(name: str, t, rows, cols, dev, named: bool = True) -> tuple:
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} is {r} x {c}, {rows if rows is not None else r} x "
                          f"{cols if cols is not None else c} is wanted")
-    if named:
-        _sizes(r, c)
+    _sizes(r if rows is None else 0, c if cols is None else 0)
     ld, inner = t.stride()
     if inner != 1 and c > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")

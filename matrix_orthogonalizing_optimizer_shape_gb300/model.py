@@ -220,6 +220,12 @@ def _dense_tensors(ts: Sequence, dev: int) -> Optional[tuple]:
     return _pack_tensors(fields), sizes
 
 
+def _wide_mat(name: str, t, dev: int) -> tuple:
+    """(data, ld, dtype) of a matrix whose sizes the call names in 64 bits."""
+    shape = t.shape
+    return _mat(name, t, shape[0], shape[1], dev) if len(shape) == 2 else _l._mat_checked(name, t, None, None, dev)
+
+
 def _tensors(name: str, ts: Sequence, dev: int) -> bytes:
     """dion3_tensor of each: dense tensors of any shape, or matrices with contiguous rows."""
     packed = _dense_tensors(ts, dev)
@@ -233,7 +239,7 @@ def _tensors(name: str, ts: Sequence, dev: int) -> bytes:
             n = t.numel()
             fields += t.data_ptr(), 1, n, n, _l._dtype(t)
         else:
-            p, ld, dtype = _l._mat_checked(name, t, None, None, dev, named=False)
+            p, ld, dtype = _wide_mat(name, t, dev)
             fields += p, t.shape[0], t.shape[1], ld, dtype
     return _pack_tensors(fields)
 
@@ -293,6 +299,6 @@ def _rows(name: str, ts: Sequence, others: Sequence, dev: int) -> bytes:
         if t.is_contiguous() and o.is_contiguous():
             fields.append(_tensors(name, (t,), dev))
         else:
-            p, ld, dtype = _l._mat_checked(name, t, None, None, dev, named=False)
+            p, ld, dtype = _wide_mat(name, t, dev)
             fields.append(_pack_tensors([p, t.shape[0], t.shape[1], ld, dtype]))
     return b"".join(fields)
